@@ -27,7 +27,8 @@ __all__ = [
     "csa2_index_topk_fp4_workspace_size", "csa2_index_topk_fp4",
     "csa2_topk_scores", "csa2_attn_workspace_size", "csa2_sparse_attn", "csa2_reuse_attn",
     "csa2_sparse_attn_rope", "csa2_reuse_attn_rope", "csa2_plane_fp4_bytes", "csa2_plane_fp4",
-    "csa2_sparse_attn_fp4", "csa2_selftest_wait_timeout",
+    "csa2_sparse_attn_fp4", "csa2_selftest_wait_timeout", "Paged", "csa2_paged_append",
+    "csa2_paged_attn_workspace_size", "csa2_paged_attn",
 ]
 
 STATUS = {0: "CSA2_OK", 1: "CSA2_EINVAL", 2: "CSA2_ECUDA", 3: "CSA2_ETIMEOUT", 4: "CSA2_EBOUNDS",
@@ -46,6 +47,14 @@ class _SwaC(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("dtype", ctypes.c_int32), ("data", ctypes.c_void_p),
                 ("n_rows", ctypes.c_int64), ("lin_base", ctypes.c_void_p),
                 ("lin_pos0", ctypes.c_void_p)]
+
+
+class _PagedC(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+                ("data", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("table_ld", ctypes.c_int64),
+                ("table_cols", ctypes.c_int64)]
 
 
 _vp, _i32, _i64, _f32, _sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
@@ -97,6 +106,14 @@ _SIGS = {
     "csa2_reuse_attn_rope": ([_vp, _i32, _vp, _vp, ctypes.POINTER(_SwaC), _vp, _i64, _vp, _vp,
                               _i32, _vp, _f32, _vp, _vp, _vp, _sz, _vp, _vp], _i32),
 }
+
+_SIGS.update({
+    "csa2_paged_append": ([_vp, _i64, _i32, _vp, _vp, _i32, ctypes.POINTER(_PagedC), _vp, _vp],
+                          _i32),
+    "csa2_paged_attn_workspace_size": ([_i32, _i32, _i64], _sz),
+    "csa2_paged_attn": ([_vp, _i32, _i32, _vp, _vp, ctypes.POINTER(_PagedC), _i32, _i64, _i64,
+                         _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+})
 
 _LIB = None
 
@@ -376,3 +393,110 @@ def csa2_sparse_attn_fp4(q, q_seq, q_pos, swa, plane4, plane_rows, row_base, sel
                                       _p(plane4), plane_rows, _p(row_base), _p(sel), nsel,
                                       _p(sink), float(scale), _p(out), _p(lse), _p(ws), nbytes,
                                       _p(inv_freq), _stream(stream)))
+
+
+@dataclass(frozen=True)
+class Paged:
+    """A paged latent cache: data [n_pages, page_rows, 512] bf16 or [n_pages, page_rows, 528]
+    uint8 (pages may be strided, a page is dense), table [B, columns] int32 of page ids (rows
+    may be strided).  The tensors are checked here, once; a call reads their addresses."""
+    data: torch.Tensor
+    table: torch.Tensor
+    fp8_dtype: int = SWA_FP8_S128  # the layout of uint8 rows: SWA_FP8_S128 or SWA_FP8_E8M0
+
+    def __post_init__(self):
+        d, t = self.data, self.table
+        row = {torch.bfloat16: 512, torch.uint8: 528}.get(d.dtype)
+        if row is None or d.dim() != 3 or d.shape[2] != row:
+            raise ValueError("csa2: a paged cache is [pages, rows, 512] bf16 or [.., 528] uint8")
+        if t.dtype != torch.int32 or t.dim() != 2:
+            raise ValueError("csa2: the page table is [sequences, pages] int32")
+        if not (d.is_cuda and t.is_cuda and d.device == t.device):
+            raise ValueError("csa2: tensors must live on one GPU")
+        if d.numel() == 0 or t.numel() == 0:
+            raise ValueError("csa2: the cache and its table must not be empty")
+        if d.stride(2) != 1 or d.stride(1) != row or t.stride(1) != 1:
+            raise ValueError("csa2: pages and table rows must be dense")
+        if (d.shape[0] > 1 and d.stride(0) < row * d.shape[1]) or (t.shape[0] > 1 and
+                                                                    t.stride(0) < t.shape[1]):
+            raise ValueError("csa2: pages or table rows overlap")
+        page = row * d.shape[1] if d.shape[0] == 1 else d.stride(0)
+        ld = t.shape[1] if t.shape[0] == 1 else t.stride(0)
+        c = _PagedC(SWA_BF16 if row == 512 else self.fp8_dtype, d.shape[1], None, d.shape[0],
+                    page * d.element_size(), None, t.shape[0], ld, t.shape[1])
+        object.__setattr__(self, "_c", c)
+
+    def c(self):
+        self._c.data = self.data.data_ptr()
+        self._c.table = self.table.data_ptr()
+        return self._c
+
+
+def _arg(name, t, dtype, shape, device):
+    """Address of a dense tensor of this type and shape (None entries: any size) on the device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"csa2: {name} must be a contiguous {dtype} tensor on {device}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"csa2: {name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
+    return t.data_ptr()
+
+
+def _stream_on(stream, device):
+    """The stream of a call on `device`; the caller makes that device current."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise ValueError(f"csa2: the stream belongs to {s.device}, the tensors to {device}")
+    return s.cuda_stream
+
+
+def csa2_paged_append(kv, cu_seqlens, start_row, cache: Paged, inv_freq=None, ratio=1,
+                      stream=None):
+    """Rows kv [T, 512] bf16 (row stride a multiple of 8) into the cache, rotated by their
+    position j * ratio when inv_freq is given."""
+    dev = cache.data.device
+    if kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != 512 or kv.device != dev:
+        raise ValueError(f"csa2: kv must be [T, 512] bf16 on {dev}")
+    T = kv.shape[0]
+    if T > 0 and kv.stride(1) != 1:
+        raise ValueError("csa2: the rows of kv must be dense")
+    B = cache.table.shape[0]
+    args = (kv.data_ptr(), kv.stride(0) if T > 1 else 512, T,
+            _arg("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev),
+            _arg("start_row", start_row, torch.int64, (B,), dev), ratio, ctypes.byref(cache.c()),
+            _arg("inv_freq", inv_freq, torch.float32, (32,), dev), _stream_on(stream, dev))
+    if dev.index == torch.cuda.current_device():
+        _check(lib().csa2_paged_append(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(lib().csa2_paged_append(*args))
+
+
+def csa2_paged_attn_workspace_size(Q, H, max_rows):
+    return int(lib().csa2_paged_attn_workspace_size(Q, H, max_rows))
+
+
+def csa2_paged_attn(q, q_seq, q_pos, cache: Paged, out, ws=None, max_rows=None, ratio=1, window=0,
+                    sink=None, lse=None, scale=512 ** -0.5, inv_freq=None, stream=None):
+    """Dense attention of q [Q, H, 512] over the paged rows each query sees; max_rows bounds
+    them (None: what the page table can hold)."""
+    dev = cache.data.device
+    if q.dim() != 3:
+        raise ValueError("csa2: q must be [Q, H, 512]")
+    Q, H = q.shape[0], q.shape[1]
+    if max_rows is None:
+        max_rows = cache.table.shape[1] * cache.data.shape[1]
+    args = (_arg("q", q, torch.bfloat16, (Q, H, 512), dev), Q, H,
+            _arg("q_seq", q_seq, torch.int32, (Q,), dev),
+            _arg("q_pos", q_pos, torch.int64, (Q,), dev), ctypes.byref(cache.c()), ratio, window,
+            max_rows, _arg("sink", sink, torch.float32, (H,), dev), scale,
+            _arg("out", out, torch.bfloat16, (Q, H, 512), dev),
+            _arg("lse", lse, torch.float32, (Q, H), dev),
+            _arg("inv_freq", inv_freq, torch.float32, (32,), dev), _p(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), _stream_on(stream, dev))
+    if dev.index == torch.cuda.current_device():
+        _check(lib().csa2_paged_attn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(lib().csa2_paged_attn(*args))

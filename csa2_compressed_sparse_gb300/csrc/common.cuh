@@ -141,7 +141,61 @@ struct AttnArgs {
                           //    each carrying on from query to query
 };
 
+// A paged latent cache: row j of sequence b is row j % page_rows of page
+// table[b * table_ld + j / page_rows], page_stride bytes from page to page.
+struct PagedCache {
+  int dtype;              // 0: bf16 rows of 1024 bytes; 1: FP8_S128, 2: FP8_E8M0 (528 bytes)
+  int page_rows;
+  uint8_t* data;
+  int64_t n_pages;
+  int64_t page_stride;
+  const int32_t* table;
+  int B;
+  int64_t table_ld, table_cols;
+};
+
+struct PagedAppendArgs {
+  const uint16_t* kv;
+  int64_t kv_ld;          // elements from token to token
+  int T;
+  const int32_t* cu_seqlens;
+  const int64_t* start_row;
+  int ratio;              // position of cache row j: j * ratio
+  const float* inv_freq;  // [32] or null: rows are stored as they are
+  PagedCache cache;
+};
+
+struct PagedAttnArgs {
+  const uint16_t* q;
+  int Q, H;
+  int ng;                 // head groups of up to 64
+  const int32_t* q_seq;
+  const int64_t* q_pos;
+  PagedCache cache;
+  int64_t cap_rows;       // rows a query may see: the caller's bound and the table's capacity
+  int ratio;
+  int64_t window;         // 0: all visible rows
+  const float* sink;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  const float* inv_freq;
+  int ut;                 // tiles of 64 rows per unit
+  int box_rows;           // rows per tensor copy: the largest of 64, 32, 16, 8 dividing page_rows
+  int shared;             // more items than sequences: rows are read more than once
+  int nctas;
+  // workspace: parts [2 nctas][padded heads * 512], their m, l, r, and each item's CTA range
+  float* part;
+  float* pstat;
+  int2* rec;
+};
+
 cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+int paged_head_pad(int H);    // heads of an item, padded: 16, 32 or 64
+int paged_unit_tiles();
+int paged_max_ctas();         // most CTAs of one attention call
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool join, cudaStream_t s);
 // One CTA whose bounded wait runs out after limit_ns (test of the timeout path).
 cudaError_t launch_wait_timeout(uint64_t limit_ns, cudaStream_t s);
 cudaError_t launch_index(const IndexArgs& a, int num_sms, cudaStream_t s);
@@ -187,6 +241,7 @@ int take_fault_compress();
 int take_fault_index();
 int take_fault_topk();
 int take_fault_attn();
+int take_fault_paged();
 
 // Order-preserving map of fp32 scores to uint32 keys: NaN ranks as -inf, -0 as +0,
 // and every key of a real score is >= 1 so that 0 can mark "not scored".

@@ -174,7 +174,7 @@ csa2_status csa2_device_status(csa2_stream stream) {
   if (e != cudaSuccess) return cuda_fail(e, "csa2_device_status");
   int f = 0;
   for (int v : {csa2::take_fault_compress(), csa2::take_fault_index(), csa2::take_fault_topk(),
-                csa2::take_fault_attn()})
+                csa2::take_fault_attn(), csa2::take_fault_paged()})
     if (!f) f = v;
   if (f == csa2::kFaultTimeout) return fail(CSA2_ETIMEOUT, "a kernel gave up a bounded wait");
   if (f == csa2::kFaultBounds) return fail(CSA2_EBOUNDS, "a kernel met an index outside its buffer");
@@ -587,6 +587,140 @@ csa2_status csa2_sparse_attn_fp4(const csa2_bf16* q, int Q, const int32_t* q_seq
   return attn_common("csa2_sparse_attn_fp4", q, Q, q_seq, q_pos, swa, plane, plane_rows,
                      row_base, sel, nsel, sink, scale, out, lse, ws, ws_bytes, inv_freq, 1,
                      stream);
+}
+
+namespace {
+
+// Checks of a paged cache; fills *c.
+csa2_status paged_args(const char* name, const csa2_paged* p, csa2::PagedCache* c) {
+  REQUIRE(p, "%s: cache is required", name);
+  REQUIRE(p->dtype == CSA2_SWA_BF16 || p->dtype == CSA2_SWA_FP8_S128 ||
+              p->dtype == CSA2_SWA_FP8_E8M0,
+          "%s: bad cache.dtype %d", name, p->dtype);
+  REQUIRE(p->page_rows >= 8 && p->page_rows <= 65536 && p->page_rows % 8 == 0,
+          "%s: cache.page_rows must be a multiple of 8 in [8, 65536] (got %d)", name, p->page_rows);
+  REQUIRE(p->data && aligned16(p->data), "%s: cache.data must be a 16-byte aligned pointer", name);
+  REQUIRE(p->n_pages >= 1 && p->n_pages < ((int64_t)1 << 31),
+          "%s: cache.n_pages must be in [1, 2^31) (got %lld)", name, (long long)p->n_pages);
+  const int64_t page = (int64_t)p->page_rows * (p->dtype == CSA2_SWA_BF16 ? 1024 : 528);
+  REQUIRE(p->page_stride >= page && p->page_stride % 16 == 0 &&
+              p->page_stride < ((int64_t)1 << 40),
+          "%s: cache.page_stride must be a multiple of 16 in [%lld, 2^40) (got %lld)", name,
+          (long long)page, (long long)p->page_stride);
+  REQUIRE(p->B >= 1 && p->B <= 65535, "%s: cache.B must be in [1, 65535] (got %d)", name, p->B);
+  REQUIRE(p->table, "%s: cache.table is required", name);
+  REQUIRE(p->table_cols >= 1 && p->table_ld >= p->table_cols,
+          "%s: cache.table_cols must be in [1, table_ld] (got %lld, table_ld %lld)", name,
+          (long long)p->table_cols, (long long)p->table_ld);
+  c->dtype = p->dtype; c->page_rows = p->page_rows; c->data = static_cast<uint8_t*>(p->data);
+  c->n_pages = p->n_pages; c->page_stride = p->page_stride; c->table = p->table; c->B = p->B;
+  c->table_ld = p->table_ld; c->table_cols = p->table_cols;
+  return CSA2_OK;
+}
+
+// Workspace of csa2_paged_attn: the parts of items that more than one CTA works on.
+struct PagedWs {
+  size_t part, pstat, rec, total;
+  int nctas;   // most CTAs the call uses
+  bool split;  // an item can be split
+};
+PagedWs paged_ws_layout(int Q, int H, int64_t max_rows) {
+  PagedWs w{};
+  const int ut = csa2::paged_unit_tiles();
+  const int64_t items = (int64_t)Q * (H > 64 ? 2 : 1);
+  // a window that begins inside a tile adds one tile
+  const int64_t units = ((max_rows + 63) / 64 + 1 + ut - 1) / ut;
+  const int64_t all = items * units;
+  w.nctas = (int)(all < csa2::paged_max_ctas() ? all : csa2::paged_max_ctas());
+  w.split = (max_rows + 63) / 64 > ut;
+  size_t o = 0;
+  const size_t hp = (size_t)csa2::paged_head_pad(H);
+  if (w.split) {
+    w.part = o; o = up256(o + (size_t)w.nctas * 2 * hp * 512 * 4);
+    w.pstat = o; o = up256(o + (size_t)w.nctas * 2 * hp * 3 * 4);
+    w.rec = o; o = up256(o + (size_t)items * 8);
+  }
+  w.total = o;
+  return w;
+}
+
+}  // namespace
+
+csa2_status csa2_paged_append(const csa2_bf16* kv, int64_t kv_ld, int T, const int32_t* cu_seqlens,
+                              const int64_t* start_row, int ratio, const csa2_paged* cache,
+                              const float* inv_freq, csa2_stream stream) {
+  const char* name = "csa2_paged_append";
+  REQUIRE(T >= 0, "%s: T must be >= 0 (got %d)", name, T);
+  if (T == 0) return CSA2_OK;
+  csa2::PagedAppendArgs a{};
+  csa2_status st = paged_args(name, cache, &a.cache);
+  if (st != CSA2_OK) return st;
+  REQUIRE(kv && cu_seqlens && start_row, "%s: kv, cu_seqlens and start_row are required", name);
+  REQUIRE(aligned16(kv), "%s: kv must be 16-byte aligned", name);
+  REQUIRE(kv_ld >= 512 && kv_ld % 8 == 0, "%s: kv_ld must be a multiple of 8, >= 512 (got %lld)",
+          name, (long long)kv_ld);
+  REQUIRE(ratio >= 1 && ratio <= 65536, "%s: ratio must be in [1, 65536] (got %d)", name, ratio);
+  a.kv = kv; a.kv_ld = kv_ld; a.T = T; a.cu_seqlens = cu_seqlens; a.start_row = start_row;
+  a.ratio = ratio; a.inv_freq = inv_freq;
+  cudaError_t e = csa2::launch_paged_append(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return CSA2_OK;
+}
+
+size_t csa2_paged_attn_workspace_size(int Q, int H, int64_t max_rows) {
+  if (Q < 0 || Q > 65535 || H < 1 || H > 128 || max_rows < 0 || max_rows > 0x7FFFFF00) return 0;
+  if (Q == 0) return 0;
+  return paged_ws_layout(Q, H, max_rows).total;
+}
+
+csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_seq,
+                            const int64_t* q_pos, const csa2_paged* cache, int ratio,
+                            int64_t window, int64_t max_rows, const float* sink, float scale,
+                            csa2_bf16* out, float* lse, const float* inv_freq, void* ws,
+                            size_t ws_bytes, csa2_stream stream) {
+  const char* name = "csa2_paged_attn";
+  REQUIRE(Q >= 0 && Q <= 65535, "%s: Q must be in [0, 65535] (got %d)", name, Q);
+  if (Q == 0) return CSA2_OK;
+  csa2::PagedAttnArgs a{};
+  csa2_status st = paged_args(name, cache, &a.cache);
+  if (st != CSA2_OK) return st;
+  REQUIRE(q && q_seq && q_pos && out, "%s: q, q_seq, q_pos and out are required", name);
+  REQUIRE(aligned16(q) && aligned16(out), "%s: q and out must be 16-byte aligned", name);
+  REQUIRE(H >= 1 && H <= 128, "%s: H must be in [1, 128] (got %d)", name, H);
+  REQUIRE(ratio >= 1 && ratio <= 65536, "%s: ratio must be in [1, 65536] (got %d)", name, ratio);
+  REQUIRE(window >= 0, "%s: window must be >= 0 (got %lld)", name, (long long)window);
+  REQUIRE(max_rows >= 0 && max_rows <= 0x7FFFFF00,
+          "%s: max_rows must be in [0, 2^31 - 256] (got %lld)", name, (long long)max_rows);
+  REQUIRE(std::isfinite(scale), "%s: scale must be finite", name);
+  REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255u) == 0, "%s: ws must be 256-byte aligned", name);
+  const PagedWs w = paged_ws_layout(Q, H, max_rows);
+  if (w.split && (!ws || ws_bytes < w.total))
+    return fail(CSA2_ENOSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws ? ws_bytes : 0,
+                w.total);
+  const int sms = num_sms();
+  if (sms <= 0) return fail(CSA2_ECUDA, "%s: no CUDA device", name);
+  a.q = q; a.Q = Q; a.H = H; a.ng = H > 64 ? 2 : 1; a.q_seq = q_seq; a.q_pos = q_pos;
+  const int64_t cols = a.cache.table_cols < ((int64_t)1 << 31) ? a.cache.table_cols
+                                                               : (int64_t)1 << 31;
+  a.cap_rows = cols * a.cache.page_rows < max_rows ? cols * a.cache.page_rows : max_rows;
+  a.ratio = ratio; a.window = window; a.sink = sink; a.scale = scale; a.out = out; a.lse = lse;
+  a.inv_freq = inv_freq; a.ut = csa2::paged_unit_tiles();
+  a.box_rows = a.cache.page_rows % 64 == 0 ? 64 : a.cache.page_rows % 32 == 0 ? 32
+               : a.cache.page_rows % 16 == 0 ? 16 : 8;
+  a.shared = (int64_t)Q * a.ng > a.cache.B ? 1 : 0;
+  a.nctas = w.nctas < sms ? w.nctas : sms;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  if (w.split) {
+    a.part = reinterpret_cast<float*>(base + w.part);
+    a.pstat = reinterpret_cast<float*>(base + w.pstat);
+    a.rec = reinterpret_cast<int2*>(base + w.rec);
+  }
+  // tiles an item can have: a window of w rows touches at most (w + 62) / 64 + 1
+  const int64_t most = (a.cap_rows + 63) / 64;
+  const int64_t tiles = window > 0 && (window + 62) / 64 + 1 < most ? (window + 62) / 64 + 1 : most;
+  cudaError_t e = csa2::launch_paged_attn(a, tiles > a.ut, stream);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return CSA2_OK;
 }
 
 size_t csa2_plane_fp4_bytes(int64_t rows) { return rows <= 0 ? 0 : (size_t)rows * 288; }

@@ -1,0 +1,1190 @@
+// k_paged.cu -- the paged latent cache: rows appended with their position's rotation
+// (paged_append_kernel), and dense attention of one new token per query over a sequence's
+// pages (paged_attn_kernel, paged_join_kernel).
+//
+// A cache row is one 512-d latent, key and value of every head.  Pages hold page_rows rows;
+// table[b][j / page_rows] is the page of row j of sequence b.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "compress_dev.cuh"
+
+CSA2_DEFINE_FAULT_FLAG(paged)
+
+namespace csa2 {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ================================ append ================================================
+//
+// One warp per token.  A lane holds the 16-byte chunks `lane` (dims 8 l ..) and, below lane
+// 24, 32 + lane (dims 256 + 8 l ..) of the row, and one rotation pair each: dims 448 + 2 l,
+// 449 + 2 l, so the 32 angles of a row take one sine and cosine per lane.  bf16 rows outside
+// the rotated dims are copied as they are.  Bound by the bytes moved: 1024 read, 1024 or 528
+// written per token.
+
+constexpr int kAppWarps = 8;
+
+// E4M3 codes of eight values of v over s.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = cvt_e4m3x2(v[2 * i] / s, v[2 * i + 1] / s);
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The smallest exponent byte e in [0, 254] with top <= 448 * 2^(e - 127); 127 for zero.
+__device__ __forceinline__ uint32_t e8m0_of(float top) {
+  if (!(top > 0.f)) return 127u;
+  // top = m 2^x with m in [1, 2): 448 = 1.75 * 2^8, so e - 127 = x - 8, one more when m > 1.75.
+  // Values below 2^-118 need no exact x: e is clamped to 0 there.
+  const uint32_t u = __float_as_uint(top);
+  const int x = (int)(u >> 23) - 127;
+  const int e = x - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0) + 127;
+  return (uint32_t)min(max(e, 0), 254);
+}
+__device__ __forceinline__ float e8m0_value(uint32_t e) {
+  return e == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23);
+}
+
+__device__ __forceinline__ float top8(const float (&v)[8]) {
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t = fmaxf(t, fabsf(v[i]));
+  return t;
+}
+// Maximum over aligned groups of `n` lanes.
+template <int N>
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+
+__device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kAppWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const uint16_t* src = a.kv + t * a.kv_ld;
+  const uint4 c0 = __ldcs(reinterpret_cast<const uint4*>(src) + lane);
+  uint4 c1 = make_uint4(0u, 0u, 0u, 0u);
+  if (lane < 24) c1 = __ldcs(reinterpret_cast<const uint4*>(src) + 32 + lane);
+  const uint32_t pr = __ldcs(reinterpret_cast<const uint32_t*>(src + kRopeDim0) + lane);
+  const int b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t, lane);
+  const int64_t t0 = a.cu_seqlens[b];
+  if (t < t0 || t >= a.cu_seqlens[b + 1]) return;  // behind the last sequence: padding
+  const int64_t j = a.start_row[b] + (t - t0);
+  const int64_t lp = j / a.cache.page_rows;
+  int32_t page = -1;
+  if (j >= 0 && lp < a.cache.table_cols) page = a.cache.table[(int64_t)b * a.cache.table_ld + lp];
+  if (page < 0 || page >= a.cache.n_pages) {
+    if (lane == 0) raise_fault(kFaultBounds);
+    return;
+  }
+  uint8_t* dst = a.cache.data + (int64_t)page * a.cache.page_stride +
+                 (j - lp * a.cache.page_rows) * (a.cache.dtype == 0 ? 1024 : 528);
+  float x0 = __uint_as_float(pr << 16), x1 = __uint_as_float(pr & 0xFFFF0000u);
+  if (a.inv_freq) {
+    float s, c;
+    sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)j * (uint64_t)a.ratio), &s, &c);
+    const float y0 = x0 * c - x1 * s;
+    x1 = x0 * s + x1 * c;
+    x0 = y0;
+  }
+  if (a.cache.dtype == 0) {
+    *(reinterpret_cast<uint4*>(dst) + lane) = c0;
+    if (lane < 24) *(reinterpret_cast<uint4*>(dst) + 32 + lane) = c1;
+    *(reinterpret_cast<uint32_t*>(dst + 2 * kRopeDim0) + lane) = pack_bf16x2(x0, x1);
+    return;
+  }
+  float v0[8], v1[8];
+  unpack8(c0, v0);
+  unpack8(c1, v1);
+  const float tr = fmaxf(fabsf(x0), fabsf(x1));
+  float s0, s1, sr;
+  if (a.cache.dtype == 1) {
+    // groups of 128 dims: 16 lanes of a chunk; the last one is lanes 16..23's second chunks
+    // and all 32 pairs
+    const float m0 = lanes_max<16>(top8(v0)), m1 = lanes_max<16>(top8(v1));
+    const float m3 = fmaxf(__shfl_sync(0xFFFFFFFFu, m1, 16), lanes_max<32>(tr));
+    s0 = m0 > 0.f ? m0 / 448.f : 1.f;
+    s1 = lane < 16 ? m1 : m3;
+    s1 = s1 > 0.f ? s1 / 448.f : 1.f;
+    sr = m3 > 0.f ? m3 / 448.f : 1.f;
+    float* sc = reinterpret_cast<float*>(dst + 512);
+    if ((lane & 15) == 0) {
+      sc[lane >> 4] = s0;
+      sc[2 + (lane >> 4)] = s1;
+    }
+  } else {
+    // groups of 32 dims: four lanes of a chunk, 16 lanes' pairs
+    const uint32_t e0 = e8m0_of(lanes_max<4>(top8(v0))), e1 = e8m0_of(lanes_max<4>(top8(v1)));
+    const uint32_t er = e8m0_of(lanes_max<16>(tr));
+    s0 = e8m0_value(e0);
+    s1 = e8m0_value(e1);
+    sr = e8m0_value(er);
+    uint8_t* sc = dst + 512;
+    if ((lane & 3) == 0) {
+      sc[lane >> 2] = (uint8_t)e0;
+      if (lane < 24) sc[8 + (lane >> 2)] = (uint8_t)e1;
+    }
+    if ((lane & 15) == 0) sc[14 + (lane >> 4)] = (uint8_t)er;
+  }
+  *(reinterpret_cast<uint2*>(dst) + lane) = codes8(v0, s0);
+  if (lane < 24) *(reinterpret_cast<uint2*>(dst + 256) + lane) = codes8(v1, s1);
+  *(reinterpret_cast<uint16_t*>(dst + kRopeDim0) + lane) = (uint16_t)cvt_e4m3x2(x0 / sr, x1 / sr);
+}
+
+// ================================ attention =============================================
+//
+// An item is a query and up to 64 of its heads; its visible rows lo .. hi - 1 form tiles of
+// 64 rows (tile boundaries at multiples of 64), and `ut` tiles a unit.  The units of all
+// items, in order, are dealt evenly to the CTAs (one per SM), so a CTA works on a run of
+// tiles of one item (a segment), then of the next: batches of unequal lengths and single
+// long sequences alike keep every SM busy.  An item that lies within one CTA is finished
+// there; of the others each CTA writes its part (O^T unscaled, running maximum and sums, in
+// fp32) to the workspace and paged_join_kernel joins them.
+//
+// A tile passes through a ring of 16 KiB slots, each a quarter of it (64 rows x 128 dims, as
+// two 128-byte-swizzled blocks of 64 dims):
+//   load     warp 6: one tensor copy per page piece and dim block (bf16 rows), or sixteen
+//            warps that load FP8 rows into registers a tile ahead and store them as bf16
+//   S        warp 4: Q[64 x 512] . X^T, a quarter as it lands; head h in TMEM lane
+//            32 (h / 16) + h % 16, column = row
+//   softmax  warps 0..3: P = 2^(s - m) with the running maximum m, which moves only when a
+//            score exceeds it by more than 2^64 (P <= 2^64 keeps bf16 P and fp32 sums finite)
+//   O^T     += X^T[512 x 64] . P^T: warp 5, four M = 128 tiles of dims, each releasing its
+//            slot, so the quarter of a later tile starts to load while this one is finished
+// Rows outside lo .. hi - 1 or on a bad page get P = 0 and are zeroed before the product
+// (what the page holds there may be NaN).
+//
+// The sum of P exists twice: of the bf16-rounded values, which the output is divided by (a
+// common rounding error of the largest weights cancels), and of the unrounded ones for lse.
+
+constexpr int kSlotBytes = 16384;
+constexpr int kBlock = 8192;  // 64 dims of 64 rows
+constexpr int kMaxSmem = 232448;
+constexpr float kLazy = 64.0f;
+constexpr uint32_t kColO = 256;  // O^T tiles at 256 + 64 mt
+
+struct __align__(16) PagedAux {
+  uint64_t full[12], empty[12];  // ring slots
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], s_empty[2];
+  uint64_t p_full, pv_done;
+  uint64_t fin[2];
+  uint64_t mask[4];     // valid rows of tile c at c & 3 (bf16 rows)
+  uint32_t nib[4][4];   // the same for FP8 rows: four rows' bits in each byte
+  int64_t sums[32];     // scan of the plan
+  int64_t total;
+  int64_t it0;          // first item of this CTA and the units before it within the item
+  int64_t it0_unit;
+  float fac[64];        // rescale factor or 1 / sum, per head
+  float rope_c[32], rope_s[32];
+  uint32_t tmem_slot;
+  int abort;
+};
+
+// kMode 0: bf16 rows; 1: FP8_S128 (fp32 scales stay outside the products: one accumulator
+// and one P per 128 dims); 2: FP8_E8M0 (a power of two times a code is exact in bf16).
+template <int kHp, int kMode>
+struct PagedCfg {
+  static constexpr bool kScaled = kMode == 1;
+  static constexpr int kThreads = kMode == 0 ? 256 : 768;
+  static constexpr int kQBlock = kHp * 128;
+  static constexpr int kQBytes = 8 * kQBlock;
+  static constexpr int kPBytes = kHp * 128 * (kScaled ? 4 : 1);
+  static constexpr int kScBytes = kScaled ? 4 * 4 * 64 * 4 : 0;  // [tile & 3][quarter][row]
+  static constexpr int kFree =
+      (kMaxSmem - 1024 - kQBytes - kPBytes - kScBytes - (int)sizeof(PagedAux)) / kSlotBytes;
+  static constexpr int kSlots = kFree < 12 ? kFree : 12;
+  static constexpr int kSmem =
+      1024 + kQBytes + kSlots * kSlotBytes + kPBytes + kScBytes + (int)sizeof(PagedAux);
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, 1, 128, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+// What an item sees: rows lo .. hi - 1 of sequence seq in `tiles` tiles from tile0, `units`
+// units (0: a padded query, or one whose sequence is outside the table).
+struct Item {
+  int64_t q;
+  int hg;     // head group
+  int seq;
+  int lo, hi;
+  int tile0, tiles, units;
+};
+
+__device__ __forceinline__ Item load_item(const PagedAttnArgs& a, int64_t it, bool report) {
+  Item i;
+  i.q = a.ng == 2 ? it >> 1 : it;
+  i.hg = a.ng == 2 ? (int)(it & 1) : 0;
+  i.seq = a.q_seq[i.q];
+  i.lo = i.hi = i.tile0 = 0;
+  i.tiles = i.units = 0;
+  if (i.seq < 0 || i.seq >= a.cache.B) {
+    if (report && i.seq != -1) raise_fault(kFaultBounds);
+    return i;
+  }
+  const int64_t p = a.q_pos[i.q];
+  int64_t hi = p < 0 ? 0 : p / a.ratio + (p % a.ratio == a.ratio - 1 ? 1 : 0);  // (p + 1) / ratio
+  int64_t lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+  if (hi > a.cap_rows) {
+    if (report) raise_fault(kFaultBounds);
+    hi = a.cap_rows;
+    lo = lo < hi ? lo : hi;
+  }
+  i.lo = (int)lo;
+  i.hi = (int)hi;
+  i.tile0 = i.lo >> 6;
+  // an empty item is one masked tile, which writes its zeros
+  i.tiles = i.hi > i.lo ? ((i.hi + 63) >> 6) - i.tile0 : 1;
+  i.units = (i.tiles + a.ut - 1) / a.ut;
+  return i;
+}
+
+// A CTA's walk over its segments: item it, tiles t .. t_end - 1 of it.
+struct Walk {
+  int64_t it;      // item
+  int64_t left;    // units of this CTA from this segment on
+  int64_t unit;    // unit within the item where the segment begins
+  Item i;
+  int t, t_end;    // tiles of the segment, relative to i.tile0
+  int seg_units;
+};
+__device__ __forceinline__ void walk_fit(const PagedAttnArgs& a, Walk& w) {
+  const int64_t rest = w.i.units - w.unit;
+  w.seg_units = (int)(rest < w.left ? rest : w.left);
+  w.t = (int)w.unit * a.ut;
+  const int e = ((int)w.unit + w.seg_units) * a.ut;
+  w.t_end = e < w.i.tiles ? e : w.i.tiles;
+}
+__device__ __forceinline__ void walk_start(const PagedAttnArgs& a, const PagedAux& X, int64_t left,
+                                           Walk& w) {
+  w.it = X.it0;
+  w.unit = X.it0_unit;
+  w.left = left;
+  w.i = load_item(a, w.it, false);
+  walk_fit(a, w);
+}
+// The next segment; false when the CTA is done.
+__device__ __forceinline__ bool walk_next(const PagedAttnArgs& a, Walk& w) {
+  w.left -= w.seg_units;
+  if (w.left <= 0) return false;
+  w.unit = 0;
+  do {
+    if (++w.it >= (int64_t)a.Q * a.ng) return false;
+    w.i = load_item(a, w.it, false);
+  } while (w.i.units == 0);
+  walk_fit(a, w);
+  return true;
+}
+
+// Valid rows of the 64-row tile that begins at row r0, as bits.
+__device__ __forceinline__ uint64_t tile_mask(int64_t r0, int lo, int hi) {
+  const int64_t f = lo - r0, l = hi - r0;  // first valid, end
+  uint64_t m = l >= 64 ? ~0ull : l <= 0 ? 0ull : (1ull << l) - 1;
+  if (f >= 64) m = 0;
+  else if (f > 0) m &= ~0ull << f;
+  return m;
+}
+
+// The 64-bit mask of sixteen bytes that hold four bits each.
+__device__ __forceinline__ uint64_t gather_nibbles(const uint32_t (&n)[4]) {
+  uint64_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x = n[i];
+    x = (x | (x >> 4)) & 0x00FF00FFu;
+    m |= (uint64_t)((x | (x >> 8)) & 0xFFFFu) << (16 * i);
+  }
+  return m;
+}
+
+template <int kHp, int kMode>
+__global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
+    paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap) {
+  using C = PagedCfg<kHp, kMode>;
+  constexpr int NS = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // Q first: the S products read 64 rows of each Q block, with fewer heads past the block
+  // (into what follows it; those TMEM lanes are never used)
+  const uint32_t q_s = smem_u32(smem), ring = q_s + C::kQBytes, p_s = ring + NS * kSlotBytes;
+  float* sc_s = reinterpret_cast<float*>(smem + C::kQBytes + NS * kSlotBytes + C::kPBytes);
+  PagedAux& X = *reinterpret_cast<PagedAux*>(reinterpret_cast<uint8_t*>(sc_s) + C::kScBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  griddep_launch_dependents();
+  if (tid == 0) {
+    prefetch_tensormap(&qmap);
+    if (kMode == 0) prefetch_tensormap(&kmap);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(smem_u32(&X.full[s]), kMode == 0 ? 1 : 16);
+      mbar_init(smem_u32(&X.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&X.q_full), 1);
+    mbar_init(smem_u32(&X.q_empty), 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&X.s_full[b]), 1);
+      mbar_init(smem_u32(&X.s_empty[b]), 128);
+      mbar_init(smem_u32(&X.fin[b]), 1);
+    }
+    mbar_init(smem_u32(&X.p_full), 128);
+    mbar_init(smem_u32(&X.pv_done), 1);
+    X.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(&X.tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // ---- the plan: every CTA sums the units of all items (positions only: they are this
+  // call's own inputs) and finds its share of them ----
+  int64_t u0, u1, U;
+  int64_t ncta;
+  {
+    const int64_t items = (int64_t)a.Q * a.ng;
+    const int64_t per = (items + C::kThreads - 1) / C::kThreads;
+    const int64_t i0 = tid * per, i1 = i0 + per < items ? i0 + per : items;
+    int64_t s = 0;
+    for (int64_t i = i0; i < i1; ++i) s += load_item(a, i, blockIdx.x == 0).units;
+    int64_t x = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) X.sums[warp] = x;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      if (w < warp) before += X.sums[w];
+      total += X.sums[w];
+    }
+    before += x - s;  // units of the items before this thread's
+    U = total;
+    ncta = (int64_t)gridDim.x < U ? (int64_t)gridDim.x : U;
+    const int64_t c = blockIdx.x;
+    u0 = c < ncta ? U * c / ncta : 0;
+    u1 = c < ncta ? U * (c + 1) / ncta : 0;
+    if (u1 > u0 && before <= u0 && u0 < before + s) {  // one thread
+      int64_t at = before;
+      for (int64_t i = i0; i < i1; ++i) {
+        const int n = load_item(a, i, false).units;
+        if (u0 < at + n) {
+          X.it0 = i;
+          X.it0_unit = u0 - at;
+          break;
+        }
+        at += n;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = X.tmem_slot;
+
+  if (u1 > u0) {
+    if (warp < 4) {
+      // ================= softmax, rescale, output =================
+      const int r4 = lane & 3;
+      const int hA = 16 * warp + (lane >> 2), hB = hA + 8;
+      const bool on = 16 * warp < kHp;  // this warp's 16 heads exist
+      const uint32_t lrow = (uint32_t)(warp * 32) << 16;
+      const float s_abs = fabsf(a.scale) * kLog2e;
+      const uint32_t flip = a.scale < 0.f ? 0x80000000u : 0u;
+      Walk w;
+      walk_start(a, X, u1 - u0, w);
+      int c = 0;                       // tiles of this CTA so far
+      int sl = 0;                      // ring slot of the tile's first quarter
+      uint32_t sph = 0;                // its phase
+      int64_t u = u0;                  // unit where the segment begins
+      griddep_wait();  // the output and the workspace may still be in use by what precedes
+      do {
+        const int Hg = min(64, a.H - 64 * w.i.hg);
+        float mA = -INFINITY, mB = -INFINITY;
+        float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums: unrounded, rounded
+        if (a.sink) {
+          if (hA < Hg) mA = a.sink[64 * w.i.hg + hA] * kLog2e;
+          if (hB < Hg) mB = a.sink[64 * w.i.hg + hB] * kLog2e;
+        }
+        const float sinkA = mA, sinkB = mB;
+        for (int t = w.t; t < w.t_end; ++t, ++c) {
+          const int sb = C::kScaled ? 0 : c & 1;
+          const uint32_t sphase = C::kScaled ? (uint32_t)c & 1 : (uint32_t)(c >> 1) & 1;
+          if (!X.abort && !mbar_wait(smem_u32(&X.s_full[sb]), sphase)) X.abort = 1;
+          {  // the tile's quarters have landed (S read them): the mask and scales are visible
+            int s = sl;
+            uint32_t ph = sph;
+            for (int k = 0; k < 4; ++k) {
+              if (!X.abort && !mbar_wait(smem_u32(&X.full[s]), ph)) X.abort = 1;
+              if (++s == NS) { s = 0; ph ^= 1; }
+            }
+          }
+          tc_fence_after();
+          const uint64_t mask = kMode == 0 ? X.mask[c & 3] : gather_nibbles(X.nib[c & 3]);
+          const bool all = mask == ~0ull;
+          float xA[16], xB[16];  // scores of rows 8 g + 2 r4 + {0, 1} at 2 g + {0, 1}
+          if (on) {
+            if (!C::kScaled) {
+              const uint32_t sa = tmem + lrow + 64 * sb;
+              uint32_t x[8][4];
+#pragma unroll
+              for (int g = 0; g < 8; ++g) tmem_ld_16x256b(sa + 8 * g, x[g]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int g = 0; g < 8; ++g) {
+                xA[2 * g] = __uint_as_float(x[g][0] ^ flip);
+                xA[2 * g + 1] = __uint_as_float(x[g][1] ^ flip);
+                xB[2 * g] = __uint_as_float(x[g][2] ^ flip);
+                xB[2 * g + 1] = __uint_as_float(x[g][3] ^ flip);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) xA[i] = xB[i] = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t x[8][4];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) tmem_ld_16x256b(tmem + lrow + 64 * k + 8 * g, x[g]);
+                tmem_ld_wait();
+                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 2 * r4;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                  const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
+                  xA[2 * g] = fmaf(__uint_as_float(x[g][0] ^ flip), f.x, xA[2 * g]);
+                  xA[2 * g + 1] = fmaf(__uint_as_float(x[g][1] ^ flip), f.y, xA[2 * g + 1]);
+                  xB[2 * g] = fmaf(__uint_as_float(x[g][2] ^ flip), f.x, xB[2 * g]);
+                  xB[2 * g + 1] = fmaf(__uint_as_float(x[g][3] ^ flip), f.y, xB[2 * g + 1]);
+                }
+              }
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(smem_u32(&X.s_empty[sb]));
+          float facA = 1.f, facB = 1.f;
+          bool need = false;
+          uint32_t pa[8], pb[8];
+          if (on) {
+            if (!all) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g) {
+                const uint32_t mk = (uint32_t)(mask >> (8 * g + 2 * r4)) & 3u;
+                if (!(mk & 1u)) xA[2 * g] = xB[2 * g] = -INFINITY;
+                if (!(mk & 2u)) xA[2 * g + 1] = xB[2 * g + 1] = -INFINITY;
+              }
+            }
+            float nA = -INFINITY, nB = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              nA = fmaxf(nA, xA[i]);
+              nB = fmaxf(nB, xB[i]);
+            }
+            nA = fmaxf(nA, __shfl_xor_sync(0xFFFFFFFFu, nA, 1));
+            nA = fmaxf(nA, __shfl_xor_sync(0xFFFFFFFFu, nA, 2));
+            nB = fmaxf(nB, __shfl_xor_sync(0xFFFFFFFFu, nB, 1));
+            nB = fmaxf(nB, __shfl_xor_sync(0xFFFFFFFFu, nB, 2));
+            // a scale of zero times a masked score would be NaN
+            nA = nA == -INFINITY ? nA : nA * s_abs;
+            nB = nB == -INFINITY ? nB : nB * s_abs;
+            if (hA < Hg && nA > mA + kLazy) {  // also with mA = -inf and any score
+              facA = ex2(mA - nA);
+              mA = nA;
+              need = true;
+            }
+            if (hB < Hg && nB > mB + kLazy) {
+              facB = ex2(mB - nB);
+              mB = nB;
+              need = true;
+            }
+            // no score yet: any finite maximum will do
+            const float eA = mA == -INFINITY ? 0.f : mA, eB = mB == -INFINITY ? 0.f : mB;
+            float sA = 0.f, sB = 0.f, tA = 0.f, tB = 0.f;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const float a0 = ex2(fmaf(xA[2 * g], s_abs, -eA));
+              const float a1 = ex2(fmaf(xA[2 * g + 1], s_abs, -eA));
+              const float b0 = ex2(fmaf(xB[2 * g], s_abs, -eB));
+              const float b1 = ex2(fmaf(xB[2 * g + 1], s_abs, -eB));
+              float p0 = a0, p1 = a1, p2 = b0, p3 = b1;
+              if (!all) {
+                const uint32_t mk = (uint32_t)(mask >> (8 * g + 2 * r4)) & 3u;
+                if (!(mk & 1u)) p0 = p2 = 0.f;
+                if (!(mk & 2u)) p1 = p3 = 0.f;
+              }
+              sA += p0 + p1;
+              sB += p2 + p3;
+              if (!C::kScaled) {
+                pa[g] = pack_bf16x2(p0, p1);
+                pb[g] = pack_bf16x2(p2, p3);
+                tA += __uint_as_float(pa[g] << 16) + __uint_as_float(pa[g] & 0xFFFF0000u);
+                tB += __uint_as_float(pb[g] << 16) + __uint_as_float(pb[g] & 0xFFFF0000u);
+              } else {
+                xA[2 * g] = p0;
+                xA[2 * g + 1] = p1;
+                xB[2 * g] = p2;
+                xB[2 * g + 1] = p3;
+              }
+            }
+            lA = fmaf(lA, facA, sA);
+            lB = fmaf(lB, facB, sB);
+            if (!C::kScaled) {
+              rA = fmaf(rA, facA, tA);
+              rB = fmaf(rB, facB, tB);
+            }
+          }
+          // P's buffer and O^T are free once the previous tile's products are done
+          if (c > 0 && !X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1))
+            X.abort = 1;
+          if (on && r4 == 0) {
+            X.fac[hA] = facA;
+            X.fac[hB] = facB;
+          }
+          if (soft_any(need) && t > w.t) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll 1
+              for (int hb = 0; hb < kHp; hb += 16) {
+                uint32_t v[16];
+                const uint32_t ta = tmem + lrow + kColO + 64 * mt + hb;
+                tmem_ld16(ta, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  v[j] = __float_as_uint(__uint_as_float(v[j]) * X.fac[hb + j]);
+                tmem_st16(ta, v);
+              }
+            }
+            tmem_st_wait();
+            soft_sync();  // fac is read by all before the next tile writes it
+          }
+          if (on) {
+            const int sw = hA & 7;  // hB & 7 is the same
+#pragma unroll
+            for (int k = 0; k < (C::kScaled ? 4 : 1); ++k) {
+              const uint32_t pA = p_s + k * (kHp * 128) + hA * 128 + 4 * r4, pB = pA + 8 * 128;
+              const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 2 * r4;
+#pragma unroll
+              for (int g = 0; g < 8; ++g) {
+                if (C::kScaled) {
+                  const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
+                  pa[g] = pack_bf16x2(xA[2 * g] * f.x, xA[2 * g + 1] * f.y);
+                  pb[g] = pack_bf16x2(xB[2 * g] * f.x, xB[2 * g + 1] * f.y);
+                }
+                st_shared32(pA + ((g ^ sw) << 4), pa[g]);
+                st_shared32(pB + ((g ^ sw) << 4), pb[g]);
+              }
+            }
+          }
+          if (kMode == 0 && !all) {
+            // rows outside the item: whatever the page holds there must not meet P's zeros
+            const int piece = tid & 63;
+            for (int r = tid >> 6; r < 64; r += 2) {
+              if ((mask >> r) & 1) continue;
+              int s = sl + (piece >> 4);
+              if (s >= NS) s -= NS;
+              st_shared16(ring + s * kSlotBytes + ((piece >> 3) & 1) * kBlock + r * 128 +
+                              (piece & 7) * 16,
+                          make_uint4(0u, 0u, 0u, 0u));
+            }
+          }
+          sl += 4;
+          if (sl >= NS) { sl -= NS; sph ^= 1; }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&X.p_full));
+        }
+        // ---- the segment's end ----
+        lA += __shfl_xor_sync(0xFFFFFFFFu, lA, 1);
+        lA += __shfl_xor_sync(0xFFFFFFFFu, lA, 2);
+        lB += __shfl_xor_sync(0xFFFFFFFFu, lB, 1);
+        lB += __shfl_xor_sync(0xFFFFFFFFu, lB, 2);
+        rA += __shfl_xor_sync(0xFFFFFFFFu, rA, 1);
+        rA += __shfl_xor_sync(0xFFFFFFFFu, rA, 2);
+        rB += __shfl_xor_sync(0xFFFFFFFFu, rB, 1);
+        rB += __shfl_xor_sync(0xFFFFFFFFu, rB, 2);
+        if (C::kScaled) { rA = lA; rB = lB; }
+        const bool whole = w.unit == 0 && w.seg_units == w.i.units;
+        if (!X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1)) X.abort = 1;
+        tc_fence_after();
+        const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
+        if (a.rec && w.unit == 0 && tid == 0) {
+          // CTAs of the item's first and last unit; (-1, -1): finished here
+          const int64_t ul = u + w.i.units - 1;
+          a.rec[w.it] = whole ? make_int2(-1, -1)
+                              : make_int2((int)blockIdx.x, (int)(((ul + 1) * ncta - 1) / U));
+        }
+        if (whole) {
+          if (a.sink) {
+            if (sinkA > -INFINITY) { lA += ex2(sinkA - mA); rA += ex2(sinkA - mA); }
+            if (sinkB > -INFINITY) { lB += ex2(sinkB - mB); rB += ex2(sinkB - mB); }
+          }
+          if (on && r4 == 0) {
+            X.fac[hA] = rA > 0.f || rA != rA ? 1.f / rA : 0.f;  // no row and no sink: zeros
+            X.fac[hB] = rB > 0.f || rB != rB ? 1.f / rB : 0.f;
+            if (a.lse) {
+              float* d = a.lse + w.i.q * a.H + 64 * w.i.hg;
+              if (hA < Hg) d[hA] = lA == 0.f ? -INFINITY : (mA + __log2f(lA)) * kLn2;
+              if (hB < Hg) d[hB] = lB == 0.f ? -INFINITY : (mB + __log2f(lB)) * kLn2;
+            }
+          }
+          if (a.inv_freq && warp == 0) {
+            float s, cs;
+            sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
+            X.rope_c[lane] = cs;
+            X.rope_s[lane] = s;
+          }
+          soft_sync();
+          uint16_t* out = a.out + (w.i.q * a.H + 64 * w.i.hg) * kDLat;
+#pragma unroll 1
+          for (int mt = 0; mt < 4; ++mt) {
+            const int d = mt * 128 + warp * 32 + lane;
+            const bool rot = a.inv_freq && d >= kRopeDim0;  // uniform in a warp
+            const float cs = rot ? X.rope_c[(d - kRopeDim0) >> 1] : 1.f;
+            const float sn = rot ? X.rope_s[(d - kRopeDim0) >> 1] : 0.f;
+#pragma unroll 1
+            for (int hb = 0; hb < Hg; hb += 16) {
+              uint32_t v[16];
+              tmem_ld16(tmem + lrow + kColO + 64 * mt + hb, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                v[j] = __float_as_uint(__uint_as_float(v[j]) * X.fac[hb + j]);
+              if (rot) {  // pair (2i, 2i + 1) times e^{-i p theta_i}: the partner is lane ^ 1
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float x = __uint_as_float(v[j]);
+                  const float pt = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+                  v[j] = __float_as_uint((lane & 1) ? x * cs - pt * sn : x * cs + pt * sn);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float a0 = __uint_as_float(v[j]), a1 = __uint_as_float(v[j + 1]);
+                const float rcv = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? a0 : a1, 1);
+                // the even lane writes head hb + j at dims (d, d + 1), the odd one head
+                // hb + j + 1 at (d - 1, d)
+                const int hr = hb + j + (lane & 1);
+                if (hr < Hg)
+                  __stcs(reinterpret_cast<unsigned int*>(out + hr * kDLat + (d & ~1)),
+                         (lane & 1) ? pack_bf16x2(rcv, a1) : pack_bf16x2(a0, rcv));
+              }
+            }
+          }
+          soft_sync();  // fac and the rotation are read before the next segment writes them
+        } else {
+          float* st = a.pstat + part * (3 * kHp);
+          if (on && r4 == 0) {
+            st[hA] = mA; st[hB] = mB;
+            st[kHp + hA] = lA; st[kHp + hB] = lB;
+            st[2 * kHp + hA] = rA; st[2 * kHp + hB] = rB;
+          }
+          // [dim tile][four heads][128 dims][4]: a lane writes 16 bytes, a warp 512
+          float* po = a.part + part * (int64_t)(kHp * kDLat) + (warp * 32 + lane) * 4;
+#pragma unroll 1
+          for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll 1
+            for (int hb = 0; hb < Hg; hb += 16) {
+              uint32_t v[16];
+              tmem_ld16(tmem + lrow + kColO + 64 * mt + hb, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j4 = 0; j4 < 4; ++j4)
+                *reinterpret_cast<uint4*>(po + (mt * (kHp / 4) + (hb >> 2) + j4) * 512) =
+                    make_uint4(v[4 * j4], v[4 * j4 + 1], v[4 * j4 + 2], v[4 * j4 + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        u += w.seg_units;
+      } while (walk_next(a, w));
+    } else if (warp == 4) {
+      // ================= S products =================
+      if (lane == 0) {
+        Walk w;
+        walk_start(a, X, u1 - u0, w);
+        int c = 0, sl = 0;
+        uint32_t sph = 0, qph = 0;
+        const uint32_t id = idesc_bf16(64, 64, 0, 0);
+        const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), r_d = sdesc_sw128(ring, 16, 1024);
+        bool ok = true;
+        do {
+          ok = !X.abort && mbar_wait(smem_u32(&X.q_full), qph);
+          qph ^= 1;
+          for (int t = w.t; ok && t < w.t_end; ++t, ++c) {
+            const int sb = C::kScaled ? 0 : c & 1;
+            const int lag = C::kScaled ? 1 : 2;
+            if (c >= lag)
+              ok = mbar_wait(smem_u32(&X.s_empty[sb]),
+                             C::kScaled ? (uint32_t)(c - 1) & 1 : (uint32_t)((c - 2) >> 1) & 1);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              ok = ok && mbar_wait(smem_u32(&X.full[sl]), sph);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t d = tmem + 64 * (C::kScaled ? k : sb);
+              const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                umma_bf16(d, q_d + (((2 * k + (i >> 2)) * C::kQBlock + (i & 3) * 32) >> 4),
+                          rd + (((i >> 2) * kBlock + (i & 3) * 32) >> 4), id,
+                          i > 0 || (!C::kScaled && k > 0));
+              if (++sl == NS) { sl = 0; sph ^= 1; }
+            }
+            if (!ok) break;
+            umma_commit(smem_u32(&X.s_full[sb]));
+          }
+          if (!ok) { X.abort = 1; break; }
+          umma_commit(smem_u32(&X.q_empty));
+        } while (walk_next(a, w));
+        // no MMA may still be running when the TMEM is released, whatever happened above
+        umma_commit(smem_u32(&X.fin[0]));
+        mbar_wait(smem_u32(&X.fin[0]), 0, 100000000ull);
+      }
+    } else if (warp == 5) {
+      // ================= O^T products =================
+      if (lane == 0) {
+        Walk w;
+        walk_start(a, X, u1 - u0, w);
+        int c = 0, sl = 0;
+        const uint32_t id = idesc_bf16(128, kHp, 1, 0);
+        const uint64_t r_d = sdesc_sw128(ring, kBlock, 1024), p_d = sdesc_sw128(p_s, 16, 1024);
+        bool ok = true;
+        do {
+          for (int t = w.t; t < w.t_end; ++t, ++c) {
+            ok = !X.abort && mbar_wait(smem_u32(&X.p_full), (uint32_t)c & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+              const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
+              const uint64_t pd = p_d + (C::kScaled ? (mt * kHp * 128) >> 4 : 0);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem + kColO + 64 * mt, rd + ((kk * 2048) >> 4), pd + ((kk * 32) >> 4),
+                          id, t > w.t || kk > 0);
+              umma_commit(smem_u32(&X.empty[sl]));
+              if (++sl == NS) sl = 0;
+            }
+            umma_commit(smem_u32(&X.pv_done));
+          }
+          if (!ok) { X.abort = 1; break; }
+        } while (walk_next(a, w));
+        umma_commit(smem_u32(&X.fin[1]));
+        mbar_wait(smem_u32(&X.fin[1]), 0, 100000000ull);
+      }
+    } else if (warp == 7) {
+      // ================= Q of each segment =================
+      if (lane == 0) {
+        Walk w;
+        walk_start(a, X, u1 - u0, w);
+        const uint64_t pol = policy_evict_first();
+        uint32_t n = 0;  // segments so far
+        const uint32_t qf = smem_u32(&X.q_full);
+        do {
+          if (n > 0 && (X.abort || !mbar_wait(smem_u32(&X.q_empty), (n - 1) & 1))) {
+            X.abort = 1;
+            break;
+          }
+          mbar_arrive_expect_tx(qf, C::kQBytes);
+#pragma unroll
+          for (int db = 0; db < 8; ++db)
+            tma_load_2d(q_s + db * C::kQBlock, &qmap, 64 * db, (int32_t)(w.i.q * a.H + 64 * w.i.hg),
+                        qf, pol);
+          ++n;
+        } while (walk_next(a, w));
+        mbar_wait(qf, (n - 1) & 1, 100000000ull);  // no copy may land after the CTA's exit
+      }
+    } else if (kMode == 0 && warp == 6) {
+      // ================= bf16 rows by tensor copies =================
+      griddep_wait();  // rows and table entries may come from the kernel before this one
+      Walk w;
+      walk_start(a, X, u1 - u0, w);
+      const uint64_t pol = a.shared ? policy_evict_normal() : policy_evict_first();
+      const int R = a.box_rows, nc = 64 / R;      // page pieces per tile
+      const int tb = 32 / nc;                     // tiles whose pieces the lanes look up at once
+      const int cl = lane & (nc - 1);             // this lane's piece of a tile
+      int sl = 0, c = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      uint32_t filled = 0;  // slots that were ever used
+      do {
+        for (int tbeg = w.t; ok && tbeg < w.t_end; tbeg += tb) {
+          // piece `lane` of the next tb tiles: its page and row, valid rows
+          const int64_t row = ((int64_t)w.i.tile0 + tbeg) * 64 + (int64_t)lane * R;
+          int32_t py = 0, pz = (int32_t)a.cache.n_pages;  // beyond the pool: zeros
+          uint64_t m = 0;
+          if (row < w.i.hi && row + R > w.i.lo && tbeg + lane / nc < w.t_end) {
+            const int32_t lp = (int32_t)row / a.cache.page_rows;
+            const int32_t page = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
+            if (page >= 0 && page < a.cache.n_pages) {
+              py = (int32_t)row - lp * a.cache.page_rows;
+              pz = page;
+              m = tile_mask(row, w.i.lo, w.i.hi);
+              if (R < 64) m &= (1ull << R) - 1;
+            } else {
+              raise_fault(kFaultBounds);
+            }
+          }
+          m <<= cl * R;
+          for (int o = 1; o < nc; o <<= 1) m |= __shfl_xor_sync(0xFFFFFFFFu, m, o);
+          const int te = min(tbeg + tb, w.t_end);
+          for (int t = tbeg; ok && t < te; ++t, ++c) {
+            const int src = (t - tbeg) * nc;
+            const int32_t y = __shfl_sync(0xFFFFFFFFu, py, src + cl);
+            const int32_t z = __shfl_sync(0xFFFFFFFFu, pz, src + cl);
+            const uint64_t mk = __shfl_sync(0xFFFFFFFFu, m, src);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t bar = smem_u32(&X.full[sl]);
+              if (filled >> sl & 1)
+                ok = !X.abort && mbar_wait(smem_u32(&X.empty[sl]), ph ^ 1);
+              ok = __all_sync(0xFFFFFFFFu, ok);
+              if (!ok) break;
+              filled |= 1u << sl;
+              if (lane == 0) {
+                if (k == 0) X.mask[c & 3] = mk;
+                mbar_arrive_expect_tx(bar, kSlotBytes);
+              }
+              __syncwarp();
+              if (lane < 2 * nc) {
+                const int d2 = lane / nc;
+                tma_load_3d(ring + sl * kSlotBytes + d2 * kBlock + cl * R * 128, &kmap,
+                            128 * (2 * k + d2), y, z, bar, pol);
+              }
+              if (++sl == NS) { sl = 0; ph ^= 1; }
+            }
+          }
+        }
+        if (!ok) break;
+      } while (walk_next(a, w));
+      if (!ok) X.abort = 1;
+      // no copy may still be landing when the CTA exits
+      if (lane < NS && (filled >> lane & 1))
+        mbar_wait(smem_u32(&X.full[lane]), lane < sl ? ph : ph ^ 1, 100000000ull);
+    } else if (kMode != 0 && warp >= 8) {
+      // ================= FP8 rows through registers =================
+      // Thread t of 512: row t / 8 of a tile, 16 dims of each quarter (piece t % 8).  A tile's
+      // codes are loaded while the tile before it is converted, its page looked up one
+      // tile earlier still.
+      griddep_wait();
+      const int t512 = tid - 256, r = t512 >> 3, pc = t512 & 7;
+      Walk w;
+      walk_start(a, X, u1 - u0, w);
+      int tn = w.t;            // next tile to look up
+      bool more = true;
+      auto look = [&](const uint8_t*& src) -> bool {  // false: no further tile
+        src = nullptr;
+        if (!more) return false;
+        const int64_t r0 = ((int64_t)w.i.tile0 + tn) * 64;
+        const int64_t row = r0 + r;
+        if (row >= w.i.lo && row < w.i.hi) {
+          const int32_t lp = (int32_t)row / a.cache.page_rows;
+          const int32_t page = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
+          if (page >= 0 && page < a.cache.n_pages)
+            src = a.cache.data + (int64_t)page * a.cache.page_stride +
+                  (int64_t)((int32_t)row - lp * a.cache.page_rows) * 528;
+          else if (pc == 0)
+            raise_fault(kFaultBounds);
+        }
+        if (++tn == w.t_end) {
+          more = walk_next(a, w);
+          tn = w.t;
+        }
+        return true;
+      };
+      uint4 cur[4], nxt[4], csc, nsc;
+      auto fetch = [&](const uint8_t* src, uint4 (&d)[4], uint4& sc) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[k] = make_uint4(0u, 0u, 0u, 0u);
+        sc = make_uint4(0u, 0u, 0u, 0u);
+        if (src) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            d[k] = __ldcs(reinterpret_cast<const uint4*>(src + 128 * k + 16 * pc));
+          if (kMode == 2 || pc == 0) sc = __ldcs(reinterpret_cast<const uint4*>(src + 512));
+        }
+      };
+      const uint8_t *s_cur, *s_nxt = nullptr;
+      bool have = look(s_cur);
+      bool have_nxt = look(s_nxt);
+      fetch(s_cur, cur, csc);
+      bool v_cur = s_cur != nullptr;
+      int sl = 0, c = 0;
+      uint32_t ph = 0, filled = 0;
+      const uint32_t off0 = sw128_off(r, (2 * pc) & 7) + (pc >> 2) * kBlock;
+      const uint32_t off1 = sw128_off(r, (2 * pc + 1) & 7) + (pc >> 2) * kBlock;
+      bool ok = true;
+      while (have) {
+        // the next tile's codes, and the page of the one after it
+        if (have_nxt) fetch(s_nxt, nxt, nsc);
+        const bool v_nxt = s_nxt != nullptr;
+        const bool had = have_nxt;
+        have_nxt = look(s_nxt);
+        // valid rows: a warp holds four of them, one ballot bit per row
+        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, v_cur);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (filled >> sl & 1) ok = ok && !X.abort && mbar_wait(smem_u32(&X.empty[sl]), ph ^ 1);
+          filled |= 1u << sl;
+          if (k == 0 && lane == 0)
+            reinterpret_cast<uint8_t*>(X.nib[c & 3])[warp - 8] =
+                (uint8_t)((bal & 1u) | (bal >> 7 & 2u) | (bal >> 14 & 4u) | (bal >> 21 & 8u));
+          const uint32_t w4[4] = {cur[k].x, cur[k].y, cur[k].z, cur[k].w};
+          float scale = 1.f;
+          if (kMode == 2) {
+            const uint32_t word = k == 0 ? csc.x : k == 1 ? csc.y : k == 2 ? csc.z : csc.w;
+            scale = e8m0_value((word >> (8 * (pc >> 1))) & 0xFFu);
+          }
+          uint32_t packed[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                  (__nv_fp8x2_storage_t)((w4[j] >> (16 * hh)) & 0xFFFFu), __NV_E4M3);
+              float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+              if (kMode == 2) { f.x *= scale; f.y *= scale; }
+              packed[2 * j + hh] = pack_bf16x2(f.x, f.y);
+            }
+          }
+          const uint32_t base = ring + sl * kSlotBytes;
+          st_shared16(base + off0, make_uint4(packed[0], packed[1], packed[2], packed[3]));
+          st_shared16(base + off1, make_uint4(packed[4], packed[5], packed[6], packed[7]));
+          if (kMode == 1 && pc == 0)
+            sc_s[((c & 3) * 4 + k) * 64 + r] =
+                __uint_as_float(k == 0 ? csc.x : k == 1 ? csc.y : k == 2 ? csc.z : csc.w);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&X.full[sl]));
+          if (++sl == NS) { sl = 0; ph ^= 1; }
+        }
+        ++c;
+        have = had;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cur[k] = nxt[k];
+        csc = nsc;
+        v_cur = v_nxt;
+      }
+      if (!ok) X.abort = 1;
+    }
+  }
+  // a CTA without work must not let the grid complete before what precedes it has
+  griddep_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 4) tmem_dealloc(tmem, 512);
+}
+
+// ================================ join ===================================================
+//
+// Joins the parts of the items that several CTAs worked on: with M the largest running
+// maximum (and the sink logit), weights 2^(m - M) and Z = 2^(sink - M) + sum 2^(m - M) l,
+// out = sum 2^(m - M) O / Z.  One CTA per item, four heads and 128 dims; four groups of 64
+// threads (a pair of dims and four heads each) take every fourth part.
+constexpr int kMaxCtas = 152;
+
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedAttnArgs a, int hp) {
+  __shared__ float wt[kMaxCtas][4];
+  __shared__ float inv[4];
+  __shared__ float acc_s[3][64][8];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t it = blockIdx.x;
+  const int hc = blockIdx.y >> 2, mt = blockIdx.y & 3;
+  const int64_t q = a.ng == 2 ? it >> 1 : it;
+  const int hg = a.ng == 2 ? (int)(it & 1) : 0;
+  const int h0 = 64 * hg + 4 * hc;  // first of the four heads
+  if (h0 >= a.H) return;
+  const int seq = a.q_seq[q];
+  if (seq < 0 || seq >= a.cache.B) return;
+  const int2 rec = a.rec[it];
+  if (rec.x < 0) return;
+  const int n = min(rec.y - rec.x + 1, kMaxCtas);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto part = [&](int s) -> int64_t { return 2 * (int64_t)(rec.x + s) + (s == 0 ? 1 : 0); };
+  if (warp < 4 && h0 + warp < a.H) {
+    const int h = 4 * hc + warp;
+    const float sink = a.sink ? a.sink[h0 + warp] * kLog2e : -INFINITY;
+    float M = sink;
+    for (int s = lane; s < n; s += 32) M = fmaxf(M, a.pstat[part(s) * (3 * hp) + h]);
+    M = lanes_max<32>(M);
+    const float Mf = M == -INFINITY ? 0.f : M;
+    float l = 0.f, r = 0.f;
+    for (int s = lane; s < n; s += 32) {
+      const float* st = a.pstat + part(s) * (3 * hp) + h;
+      const float w = ex2(st[0] - Mf);
+      wt[s][warp] = w;
+      l = fmaf(w, st[hp], l);
+      r = fmaf(w, st[2 * hp], r);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+      r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+    }
+    const float sk = sink == -INFINITY ? 0.f : ex2(sink - Mf);
+    l += sk;
+    r += sk;
+    if (lane == 0) {
+      inv[warp] = r > 0.f || r != r ? 1.f / r : 0.f;
+      if (a.lse && mt == 0)
+        a.lse[q * a.H + h0 + warp] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
+    }
+  } else if (warp < 4) {
+    for (int s = lane; s < n; s += 32) wt[s][warp] = 0.f;
+    if (lane == 0) inv[warp] = 0.f;
+  }
+  __syncthreads();
+  const int pair = tid & 63, grp = tid >> 6;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const float* src = a.part + (mt * (hp / 4) + hc) * 512 + pair * 8;
+#pragma unroll 4
+  for (int s = grp; s < n; s += 4) {
+    const float* p = src + part(s) * (int64_t)(hp * kDLat);
+    const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+    const float4 y = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    const float4 w = *reinterpret_cast<const float4*>(wt[s]);
+    acc[0] = fmaf(x.x, w.x, acc[0]);
+    acc[1] = fmaf(x.y, w.y, acc[1]);
+    acc[2] = fmaf(x.z, w.z, acc[2]);
+    acc[3] = fmaf(x.w, w.w, acc[3]);
+    acc[4] = fmaf(y.x, w.x, acc[4]);
+    acc[5] = fmaf(y.y, w.y, acc[5]);
+    acc[6] = fmaf(y.z, w.z, acc[6]);
+    acc[7] = fmaf(y.w, w.w, acc[7]);
+  }
+  if (grp > 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc_s[grp - 1][pair][i] = acc[i];
+  }
+  __syncthreads();
+  if (grp > 0) return;
+#pragma unroll
+  for (int g = 0; g < 3; ++g)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += acc_s[g][pair][i];
+  const int d = mt * 128 + 2 * pair;
+  float cs = 1.f, sn = 0.f;
+  if (a.inv_freq && d >= kRopeDim0)
+    sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), (uint64_t)a.q_pos[q]), &sn, &cs);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    if (h0 + h >= a.H) break;
+    const float x = acc[h] * inv[h], y = acc[4 + h] * inv[h];
+    __stcs(reinterpret_cast<unsigned int*>(a.out + (q * a.H + h0 + h) * kDLat + d),
+           pack_bf16x2(x * cs + y * sn, y * cs - x * sn));
+  }
+}
+
+template <int kHp, int kMode>
+cudaError_t launch_attn_inst(const PagedAttnArgs& a, const CUtensorMap& qm, const CUtensorMap& km,
+                             cudaStream_t s) {
+  using C = PagedCfg<kHp, kMode>;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<kHp, kMode>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_attn_kernel<kHp, kMode>, dim3((unsigned)a.nctas), dim3(C::kThreads),
+                    C::kSmem, s, a, qm, km);
+}
+
+template <int kHp>
+cudaError_t launch_attn_mode(const PagedAttnArgs& a, const CUtensorMap& qm, const CUtensorMap& km,
+                             cudaStream_t s) {
+  switch (a.cache.dtype) {
+    case 0: return launch_attn_inst<kHp, 0>(a, qm, km, s);
+    case 1: return launch_attn_inst<kHp, 1>(a, qm, km, s);
+    default: return launch_attn_inst<kHp, 2>(a, qm, km, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  return launch_pdl(paged_append_kernel, dim3((unsigned)((a.T + kAppWarps - 1) / kAppWarps)),
+                    dim3(kAppWarps * 32), 0, s, a);
+}
+
+int paged_head_pad(int H) { return H <= 16 ? 16 : H <= 32 ? 32 : 64; }
+
+// Tiles of a unit: the share of an item that is not split further.
+int paged_unit_tiles() { return 4; }
+
+int paged_max_ctas() { return kMaxCtas; }
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool join, cudaStream_t s) {
+  if (a.Q == 0) return cudaSuccess;
+  const int hp = paged_head_pad(a.H);
+  CUtensorMap qm, km;
+  if (!encode_rows_bf16(&qm, a.q, (uint64_t)a.Q * a.H, kDLat, 64, (uint32_t)hp))
+    return cudaErrorInvalidValue;
+  km = qm;
+  if (a.cache.dtype == 0) {
+    const uint64_t dims[3] = {1024, (uint64_t)a.cache.page_rows, (uint64_t)a.cache.n_pages};
+    const uint64_t strides[2] = {1024, (uint64_t)a.cache.page_stride};
+    const uint32_t box[3] = {128, (uint32_t)a.box_rows, 1};
+    if (!encode_bytes(&km, a.cache.data, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  cudaError_t e = hp == 16   ? launch_attn_mode<16>(a, qm, km, s)
+                  : hp == 32 ? launch_attn_mode<32>(a, qm, km, s)
+                             : launch_attn_mode<64>(a, qm, km, s);
+  if (e != cudaSuccess || !join) return e;
+  return launch_pdl(paged_join_kernel, dim3((unsigned)(a.Q * a.ng), (unsigned)hp), dim3(256), 0, s, a,
+                    hp);
+}
+
+}  // namespace csa2

@@ -480,6 +480,100 @@ csa2_status csa2_sparse_attn_fp4(const csa2_bf16* q, int Q, const int32_t* q_seq
                                  float* lse, void* ws, size_t ws_bytes, const float* inv_freq,
                                  csa2_stream stream);
 
+/* ---------------------------------------------------------------------------------
+ * A paged latent cache.  The library's other caches are flat per sequence; a serving
+ * engine keeps the rows of many sequences in one pool of pages ([A] pool of 8-row blocks;
+ * [E] paged offsets).  One row is the 512-d latent that is key and value of every head;
+ * row j of sequence b is row j % page_rows of page table[b * table_ld + j / page_rows].
+ * (HOST struct, device pointers inside.)
+ *   dtype        csa2_swa_dtype: BF16 rows of 1024 bytes, FP8_S128 or FP8_E8M0 rows of 528
+ *                bytes, laid out as csa2_sparse_attn's window rows
+ *   page_rows    rows per page, a multiple of 8, 8 .. 65536
+ *   data         page 0, 16-byte aligned; page i starts page_stride * i bytes on, so the
+ *                pages of several layers may be interleaved
+ *   n_pages      pages in the pool, 1 .. 2^31 - 1
+ *   page_stride  bytes, a multiple of 16, at least a page
+ *   table        device [B] rows of table_cols page ids, table_ld entries apart.  Entries of
+ *                pages that a call does not need are not read (-1 by convention); a needed
+ *                entry outside [0, n_pages) raises CSA2_EBOUNDS and its rows are skipped
+ *   B            sequences, 1 .. 65535 */
+typedef struct {
+  int32_t dtype;
+  int32_t page_rows;
+  void* data;
+  int64_t n_pages;
+  int64_t page_stride;
+  const int32_t* table;
+  int32_t B;
+  int64_t table_ld;
+  int64_t table_cols;
+} csa2_paged;
+
+/* ---------------------------------------------------------------------------------
+ * csa2_paged_append -- new rows into a paged cache, rotated on the way.  [B] §6.1 (RoPE on
+ * the last 64 dims), §4.1 and §4.4 (rows of the window and of the compressed plane);
+ * [C] §5.5 (K = V, one row per position).
+ *
+ * Tokens cu_seqlens[b] .. cu_seqlens[b+1] - 1 of kv become rows start_row[b],
+ * start_row[b] + 1, .. of sequence b.  Row j sits at position p = j * ratio (ratio 1: one
+ * row per token; m: the rows of groups of m tokens, at the group head).  With inv_freq,
+ * pair i of dims 448 + 2i, 449 + 2i is multiplied by e^{i p theta_i} in fp32 (theta_i =
+ * inv_freq[i], the phase exact as in csa2_compress); without it rows are stored as given.
+ * The row is then rounded once, to nearest even:
+ *   BF16      to bf16
+ *   FP8_S128  code = E4M3(x / s), s = max |x| / 448 in fp32 over each 128 dims (1 when all
+ *             are zero)
+ *   FP8_E8M0  code = E4M3(x / 2^(e - 127)), e the smallest byte in [0, 254] with
+ *             max |x| <= 448 * 2^(e - 127) over each 32 dims (127 when all are zero)
+ * The FP8 forms want finite values.
+ *   kv           [T] rows of 512 bf16, kv_ld elements apart (a multiple of 8, >= 512)
+ *   cu_seqlens   [cache->B + 1] int32, non-decreasing, cu_seqlens[0] == 0.  Tokens from
+ *                cu_seqlens[B] on (a padded batch) are skipped
+ *   start_row    [cache->B] int64; rows outside the table raise CSA2_EBOUNDS and are skipped
+ *   ratio        1 .. 65536
+ *   inv_freq     [32] fp32 or NULL
+ * Rows of other positions are left as they were.  Two tokens that land on one row (sequences
+ * that share a page) leave one of them, or bytes of both: give each row one token. */
+csa2_status csa2_paged_append(const csa2_bf16* kv, int64_t kv_ld, int T, const int32_t* cu_seqlens,
+                              const int64_t* start_row, int ratio, const csa2_paged* cache,
+                              const float* inv_freq, csa2_stream stream);
+
+/* ---------------------------------------------------------------------------------
+ * csa2_paged_attn -- dense attention of new tokens over their sequences' paged rows: the
+ * form that csa2_sparse_attn takes when every visible row is selected ([E]: top-k = all
+ * rows is dense attention), without its limit of 512 rows.  [B] §4.1; [C] §5.5-5.6; [E]
+ * Fig. 2d (sink in the denominator).
+ *
+ * Query q of sequence b = q_seq[q] at position p = q_pos[q] sees rows lo <= j < hi,
+ *     hi = floor((p + 1) / ratio) (0 for p < 0),  lo = window > 0 ? max(0, hi - window) : 0,
+ * and for each of its H heads
+ *     s_j   = scale * <q[q][h], x_j>
+ *     Z     = e^{sink[h]} + sum_j e^{s_j}
+ *     out_h = sum_j e^{s_j} x_j / Z,   lse_h = ln Z
+ * with fp32 sums of bf16 products (FP8 codes are exact in bf16; their scales are applied in
+ * fp32 or as powers of two); the weights e^{s_j - m} are rounded to bf16 for the second
+ * product.  A query that sees no row gets zeros and lse = sink[h] (-inf without a sink).
+ * q_seq[q] == -1 marks a padded query, whose out and lse are left as they were; other
+ * values outside [0, B) raise CSA2_EBOUNDS and are treated so too.
+ *   q, out     [Q][H][512] bf16;  Q 0 .. 65535;  H 1 .. 128
+ *   q_seq      [Q] int32 (several queries may share a sequence);  q_pos [Q] int64
+ *   ratio      1 .. 65536;  window >= 0 (0: all visible rows)
+ *   max_rows   bound on hi, 0 .. 2^31 - 256; a larger hi, or one beyond the table, raises
+ *              CSA2_EBOUNDS and is clipped
+ *   sink       [H] fp32, finite or -inf, or NULL;  scale finite
+ *   lse        [Q][H] fp32 or NULL
+ *   inv_freq   [32] fp32 or NULL: the output's dims 448.. are rotated back by p, as in
+ *              csa2_sparse_attn_rope
+ *   ws         workspace of csa2_paged_attn_workspace_size(Q, H, max_rows) bytes, 256-byte
+ *              aligned (0 for max_rows up to 256: NULL will do); contents are scratch.
+ *              Calls that can overlap need one each. */
+size_t csa2_paged_attn_workspace_size(int Q, int H, int64_t max_rows);
+csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_seq,
+                            const int64_t* q_pos, const csa2_paged* cache, int ratio,
+                            int64_t window, int64_t max_rows, const float* sink, float scale,
+                            csa2_bf16* out, float* lse, const float* inv_freq, void* ws,
+                            size_t ws_bytes, csa2_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
