@@ -160,13 +160,15 @@ __global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppen
 //
 // A tile passes through a ring of 16 KiB slots, each a quarter of it (64 rows x 128 dims, as
 // two 128-byte-swizzled blocks of 64 dims):
-//   load     warp 6: one tensor copy per page piece and dim block (bf16 rows), or sixteen
+//   load     warp 10: one tensor copy per page piece and dim block (bf16 rows), or sixteen
 //            warps that load FP8 rows into registers a tile ahead and store them as bf16
-//   S        warp 4: Q[64 x 512] . X^T, a quarter as it lands; head h in TMEM lane
+//   S        warp 8: Q[64 x 512] . X^T, a quarter as it lands; head h in TMEM lane
 //            32 (h / 16) + h % 16, column = row
-//   softmax  warps 0..3: P = 2^(s - m) with the running maximum m, which moves only when a
-//            score exceeds it by more than 2^64 (P <= 2^64 keeps bf16 P and fp32 sums finite)
-//   O^T     += X^T[512 x 64] . P^T: warp 5, four M = 128 tiles of dims, each releasing its
+//   softmax  warps 0..7, half of the rows each four: P = 2^(s - m) with the running maximum m,
+//            which moves only when a score exceeds it by more than 2^64 (P <= 2^64 keeps bf16
+//            P and fp32 sums finite), so a tile's usual pass needs no maximum across threads,
+//            one vote only
+//   O^T     += X^T[512 x 64] . P^T: warp 9, four M = 128 tiles of dims, each releasing its
 //            slot, so the quarter of a later tile starts to load while this one is finished
 // Rows outside lo .. hi - 1 or on a bad page get P = 0 and are zeroed before the product
 // (what the page holds there may be NaN).
@@ -193,6 +195,9 @@ struct __align__(16) PagedAux {
   int64_t it0;          // first item of this CTA and the units before it within the item
   int64_t it0_unit;
   float fac[64];        // rescale factor or 1 / sum, per head
+  float top[2][64];     // largest score above the running maximum, by half of the rows
+  float lsum[2][64], rsum[2][64];  // sums of P by half: unrounded, rounded
+  float m_run[64];
   float rope_c[32], rope_s[32];
   uint32_t tmem_slot;
   int abort;
@@ -203,7 +208,7 @@ struct __align__(16) PagedAux {
 template <int kHp, int kMode>
 struct PagedCfg {
   static constexpr bool kScaled = kMode == 1;
-  static constexpr int kThreads = kMode == 0 ? 256 : 768;
+  static constexpr int kThreads = kMode == 0 ? 384 : 896;
   static constexpr int kQBlock = kHp * 128;
   static constexpr int kQBytes = 8 * kQBlock;
   static constexpr int kPBytes = kHp * 128 * (kScaled ? 4 : 1);
@@ -221,16 +226,46 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
-      "bar.red.or.pred po, 1, 128, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      "bar.red.or.pred po, 1, 256, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)pred)
       : "memory");
   return r != 0;
+}
+
+// Two fp32 lanes at once: a * b + c and a + b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// 16 TMEM lanes x 32 columns: thread t receives lanes t / 4 and t / 4 + 8 of columns
+// 8 i + 2 (t % 4) + {0, 1} at r[4 i ..] (as tmem_ld_16x256b, four times).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -375,15 +410,15 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     mbar_init(smem_u32(&X.q_empty), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&X.s_full[b]), 1);
-      mbar_init(smem_u32(&X.s_empty[b]), 128);
+      mbar_init(smem_u32(&X.s_empty[b]), 8);
       mbar_init(smem_u32(&X.fin[b]), 1);
     }
-    mbar_init(smem_u32(&X.p_full), 128);
+    mbar_init(smem_u32(&X.p_full), 8);
     mbar_init(smem_u32(&X.pv_done), 1);
     X.abort = 0;
     mbar_fence_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(smem_u32(&X.tmem_slot), 512);
     tmem_relinquish();
   }
@@ -435,14 +470,16 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   const uint32_t tmem = X.tmem_slot;
 
   if (u1 > u0) {
-    if (warp < 4) {
+    if (warp < 8) {
       // ================= softmax, rescale, output =================
-      const int r4 = lane & 3;
-      const int hA = 16 * warp + (lane >> 2), hB = hA + 8;
-      const bool on = 16 * warp < kHp;  // this warp's 16 heads exist
-      const uint32_t lrow = (uint32_t)(warp * 32) << 16;
-      const float s_abs = fabsf(a.scale) * kLog2e;
-      const uint32_t flip = a.scale < 0.f ? 0x80000000u : 0u;
+      // Warp w and w + 4 hold heads 16 w .. 16 w + 15 (TMEM lanes 32 w ..), rows 0..31 and
+      // 32..63 of a tile; thread t the heads hA = 16 w + t / 4 and hB = hA + 8 and of its rows
+      // 8 g + 2 (t % 4) + {0, 1}, g = 0..3.
+      const int quad = warp & 3, half = warp >> 2, r4 = lane & 3;
+      const int hA = 16 * quad + (lane >> 2), hB = hA + 8;
+      const bool on = 16 * quad < kHp;  // this warp's 16 heads exist
+      const uint32_t lrow = (uint32_t)(quad * 32) << 16;
+      const float sc2 = a.scale * kLog2e;
       Walk w;
       walk_start(a, X, u1 - u0, w);
       int c = 0;                       // tiles of this CTA so far
@@ -453,184 +490,202 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       do {
         const int Hg = min(64, a.H - 64 * w.i.hg);
         float mA = -INFINITY, mB = -INFINITY;
-        float lA = 0.f, lB = 0.f, rA = 0.f, rB = 0.f;  // sums: unrounded, rounded
+        float2 lA = make_float2(0.f, 0.f), lB = lA, rA = lA, rB = lA;  // unrounded, rounded
         if (a.sink) {
           if (hA < Hg) mA = a.sink[64 * w.i.hg + hA] * kLog2e;
           if (hB < Hg) mB = a.sink[64 * w.i.hg + hB] * kLog2e;
         }
-        const float sinkA = mA, sinkB = mB;
         for (int t = w.t; t < w.t_end; ++t, ++c) {
           const int sb = C::kScaled ? 0 : c & 1;
           const uint32_t sphase = C::kScaled ? (uint32_t)c & 1 : (uint32_t)(c >> 1) & 1;
           if (!X.abort && !mbar_wait(smem_u32(&X.s_full[sb]), sphase)) X.abort = 1;
-          {  // the tile's quarters have landed (S read them): the mask and scales are visible
-            int s = sl;
-            uint32_t ph = sph;
-            for (int k = 0; k < 4; ++k) {
-              if (!X.abort && !mbar_wait(smem_u32(&X.full[s]), ph)) X.abort = 1;
-              if (++s == NS) { s = 0; ph ^= 1; }
-            }
-          }
+          // the tile has landed (S read it); waiting for that here too makes what its loader
+          // wrote visible: the mask (first quarter), the scales (all of them)
+          auto landed = [&](int k) {
+            const int i = sl + k;
+            const uint32_t ph = i >= NS ? sph ^ 1 : sph;
+            if (!X.abort && !mbar_wait(smem_u32(&X.full[i >= NS ? i - NS : i]), ph)) X.abort = 1;
+          };
+          landed(0);
+          if (C::kScaled) { landed(1); landed(2); landed(3); }
           tc_fence_after();
           const uint64_t mask = kMode == 0 ? X.mask[c & 3] : gather_nibbles(X.nib[c & 3]);
           const bool all = mask == ~0ull;
-          float xA[16], xB[16];  // scores of rows 8 g + 2 r4 + {0, 1} at 2 g + {0, 1}
+          // bit 8 g: row 8 g + 2 r4 of this half, bit 8 g + 1 the one after it
+          const uint32_t mk = (uint32_t)(mask >> (32 * half + 2 * r4));
+          float2 xA[4], xB[4];
           if (on) {
             if (!C::kScaled) {
-              const uint32_t sa = tmem + lrow + 64 * sb;
-              uint32_t x[8][4];
-#pragma unroll
-              for (int g = 0; g < 8; ++g) tmem_ld_16x256b(sa + 8 * g, x[g]);
+              uint32_t x[16];
+              tmem_ld_16x256b_x4(tmem + lrow + 64 * sb + 32 * half, x);
               tmem_ld_wait();
 #pragma unroll
-              for (int g = 0; g < 8; ++g) {
-                xA[2 * g] = __uint_as_float(x[g][0] ^ flip);
-                xA[2 * g + 1] = __uint_as_float(x[g][1] ^ flip);
-                xB[2 * g] = __uint_as_float(x[g][2] ^ flip);
-                xB[2 * g + 1] = __uint_as_float(x[g][3] ^ flip);
+              for (int g = 0; g < 4; ++g) {
+                xA[g] = make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1]));
+                xB[g] = make_float2(__uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3]));
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) xA[i] = xB[i] = 0.f;
+              for (int g = 0; g < 4; ++g) xA[g] = xB[g] = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                uint32_t x[8][4];
-#pragma unroll
-                for (int g = 0; g < 8; ++g) tmem_ld_16x256b(tmem + lrow + 64 * k + 8 * g, x[g]);
+                uint32_t x[16];
+                tmem_ld_16x256b_x4(tmem + lrow + 64 * k + 32 * half, x);
                 tmem_ld_wait();
-                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 2 * r4;
+                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 32 * half + 2 * r4;
 #pragma unroll
-                for (int g = 0; g < 8; ++g) {
+                for (int g = 0; g < 4; ++g) {
                   const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
-                  xA[2 * g] = fmaf(__uint_as_float(x[g][0] ^ flip), f.x, xA[2 * g]);
-                  xA[2 * g + 1] = fmaf(__uint_as_float(x[g][1] ^ flip), f.y, xA[2 * g + 1]);
-                  xB[2 * g] = fmaf(__uint_as_float(x[g][2] ^ flip), f.x, xB[2 * g]);
-                  xB[2 * g + 1] = fmaf(__uint_as_float(x[g][3] ^ flip), f.y, xB[2 * g + 1]);
+                  xA[g] = fma2(make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1])),
+                               f, xA[g]);
+                  xB[g] = fma2(
+                      make_float2(__uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3])), f,
+                      xB[g]);
                 }
               }
             }
           }
           tc_fence_before();
-          mbar_arrive(smem_u32(&X.s_empty[sb]));
-          float facA = 1.f, facB = 1.f;
-          bool need = false;
-          uint32_t pa[8], pb[8];
-          if (on) {
-            if (!all) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&X.s_empty[sb]));
+          // P = 2^(score - m), m the running maximum (no score yet: 0); the largest exponent
+          // met and the sums of P
+          uint32_t pa[4], pb[4];
+          float2 eA[4], eB[4];
+          float tA, tB;
+          float2 sA, sB, uA, uB;
+          auto weights = [&]() {
+            const float nA = mA == -INFINITY ? 0.f : -mA, nB = mB == -INFINITY ? 0.f : -mB;
+            tA = tB = -INFINITY;
+            sA = sB = uA = uB = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int g = 0; g < 8; ++g) {
-                const uint32_t mk = (uint32_t)(mask >> (8 * g + 2 * r4)) & 3u;
-                if (!(mk & 1u)) xA[2 * g] = xB[2 * g] = -INFINITY;
-                if (!(mk & 2u)) xA[2 * g + 1] = xB[2 * g + 1] = -INFINITY;
-              }
-            }
-            float nA = -INFINITY, nB = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              nA = fmaxf(nA, xA[i]);
-              nB = fmaxf(nB, xB[i]);
-            }
-            nA = fmaxf(nA, __shfl_xor_sync(0xFFFFFFFFu, nA, 1));
-            nA = fmaxf(nA, __shfl_xor_sync(0xFFFFFFFFu, nA, 2));
-            nB = fmaxf(nB, __shfl_xor_sync(0xFFFFFFFFu, nB, 1));
-            nB = fmaxf(nB, __shfl_xor_sync(0xFFFFFFFFu, nB, 2));
-            // a scale of zero times a masked score would be NaN
-            nA = nA == -INFINITY ? nA : nA * s_abs;
-            nB = nB == -INFINITY ? nB : nB * s_abs;
-            if (hA < Hg && nA > mA + kLazy) {  // also with mA = -inf and any score
-              facA = ex2(mA - nA);
-              mA = nA;
-              need = true;
-            }
-            if (hB < Hg && nB > mB + kLazy) {
-              facB = ex2(mB - nB);
-              mB = nB;
-              need = true;
-            }
-            // no score yet: any finite maximum will do
-            const float eA = mA == -INFINITY ? 0.f : mA, eB = mB == -INFINITY ? 0.f : mB;
-            float sA = 0.f, sB = 0.f, tA = 0.f, tB = 0.f;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const float a0 = ex2(fmaf(xA[2 * g], s_abs, -eA));
-              const float a1 = ex2(fmaf(xA[2 * g + 1], s_abs, -eA));
-              const float b0 = ex2(fmaf(xB[2 * g], s_abs, -eB));
-              const float b1 = ex2(fmaf(xB[2 * g + 1], s_abs, -eB));
-              float p0 = a0, p1 = a1, p2 = b0, p3 = b1;
+            for (int g = 0; g < 4; ++g) {
+              float2 y = fma2(xA[g], make_float2(sc2, sc2), make_float2(nA, nA));
+              float2 z = fma2(xB[g], make_float2(sc2, sc2), make_float2(nB, nB));
               if (!all) {
-                const uint32_t mk = (uint32_t)(mask >> (8 * g + 2 * r4)) & 3u;
-                if (!(mk & 1u)) p0 = p2 = 0.f;
-                if (!(mk & 2u)) p1 = p3 = 0.f;
+                if (!(mk >> (8 * g) & 1u)) y.x = z.x = -INFINITY;
+                if (!(mk >> (8 * g + 1) & 1u)) y.y = z.y = -INFINITY;
               }
-              sA += p0 + p1;
-              sB += p2 + p3;
-              if (!C::kScaled) {
-                pa[g] = pack_bf16x2(p0, p1);
-                pb[g] = pack_bf16x2(p2, p3);
-                tA += __uint_as_float(pa[g] << 16) + __uint_as_float(pa[g] & 0xFFFF0000u);
-                tB += __uint_as_float(pb[g] << 16) + __uint_as_float(pb[g] & 0xFFFF0000u);
+              tA = fmaxf(tA, fmaxf(y.x, y.y));
+              tB = fmaxf(tB, fmaxf(z.x, z.y));
+              y = make_float2(ex2(y.x), ex2(y.y));
+              z = make_float2(ex2(z.x), ex2(z.y));
+              sA = add2(sA, y);
+              sB = add2(sB, z);
+              if (C::kScaled) {
+                eA[g] = y;
+                eB[g] = z;
               } else {
-                xA[2 * g] = p0;
-                xA[2 * g + 1] = p1;
-                xB[2 * g] = p2;
-                xB[2 * g + 1] = p3;
+                pa[g] = pack_bf16x2(y.x, y.y);
+                pb[g] = pack_bf16x2(z.x, z.y);
+                uA = add2(uA, make_float2(__uint_as_float(pa[g] << 16),
+                                          __uint_as_float(pa[g] & 0xFFFF0000u)));
+                uB = add2(uB, make_float2(__uint_as_float(pb[g] << 16),
+                                          __uint_as_float(pb[g] & 0xFFFF0000u)));
               }
             }
-            lA = fmaf(lA, facA, sA);
-            lB = fmaf(lB, facB, sB);
+          };
+          bool need = false;
+          if (on) {
+            weights();
+            need = (hA < Hg && (tA > kLazy || (mA == -INFINITY && tA > -INFINITY))) ||
+                   (hB < Hg && (tB > kLazy || (mB == -INFINITY && tB > -INFINITY)));
+          }
+          if (soft_any(need)) {
+            // a head's maximum moves: the largest exponent of its rows in both halves
+            if (on) {
+              tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, 1));
+              tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, 2));
+              tB = fmaxf(tB, __shfl_xor_sync(0xFFFFFFFFu, tB, 1));
+              tB = fmaxf(tB, __shfl_xor_sync(0xFFFFFFFFu, tB, 2));
+              if (r4 == 0) {
+                X.top[half][hA] = tA;
+                X.top[half][hB] = tB;
+              }
+            }
+            soft_sync();
+            float fA = 1.f, fB = 1.f;
+            if (on) {
+              tA = fmaxf(X.top[0][hA], X.top[1][hA]);
+              tB = fmaxf(X.top[0][hB], X.top[1][hB]);
+              if (tA > kLazy || (mA == -INFINITY && tA > -INFINITY)) {
+                fA = mA == -INFINITY ? 0.f : ex2(-tA);
+                mA = mA == -INFINITY ? tA : mA + tA;
+              }
+              if (tB > kLazy || (mB == -INFINITY && tB > -INFINITY)) {
+                fB = mB == -INFINITY ? 0.f : ex2(-tB);
+                mB = mB == -INFINITY ? tB : mB + tB;
+              }
+              if (half == 0 && r4 == 0) {
+                X.fac[hA] = fA;
+                X.fac[hB] = fB;
+              }
+              const float2 qA = make_float2(fA, fA), qB = make_float2(fB, fB), o0 = make_float2(0.f, 0.f);
+              lA = fma2(lA, qA, o0);
+              lB = fma2(lB, qB, o0);
+              rA = fma2(rA, qA, o0);
+              rB = fma2(rB, qB, o0);
+              weights();
+            }
+            if (c > 0 && !X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1))
+              X.abort = 1;
+            soft_sync();  // fac is written
+            if (t > w.t) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
+#pragma unroll 1
+                for (int hb = 0; hb < kHp; hb += 16) {
+                  uint32_t v[16];
+                  const uint32_t ta = tmem + lrow + kColO + 64 * mt + hb;
+                  tmem_ld16(ta, v);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    v[j] = __float_as_uint(__uint_as_float(v[j]) * X.fac[hb + j]);
+                  tmem_st16(ta, v);
+                }
+              }
+              tmem_st_wait();
+            }
+            soft_sync();  // fac and top are read by all before a later tile writes them
+          }
+          if (on) {
+            lA = add2(lA, sA);
+            lB = add2(lB, sB);
             if (!C::kScaled) {
-              rA = fmaf(rA, facA, tA);
-              rB = fmaf(rB, facB, tB);
+              rA = add2(rA, uA);
+              rB = add2(rB, uB);
             }
           }
           // P's buffer and O^T are free once the previous tile's products are done
           if (c > 0 && !X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1))
             X.abort = 1;
-          if (on && r4 == 0) {
-            X.fac[hA] = facA;
-            X.fac[hB] = facB;
-          }
-          if (soft_any(need) && t > w.t) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int mt = 0; mt < 4; ++mt) {
-#pragma unroll 1
-              for (int hb = 0; hb < kHp; hb += 16) {
-                uint32_t v[16];
-                const uint32_t ta = tmem + lrow + kColO + 64 * mt + hb;
-                tmem_ld16(ta, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  v[j] = __float_as_uint(__uint_as_float(v[j]) * X.fac[hb + j]);
-                tmem_st16(ta, v);
-              }
-            }
-            tmem_st_wait();
-            soft_sync();  // fac is read by all before the next tile writes it
-          }
           if (on) {
             const int sw = hA & 7;  // hB & 7 is the same
 #pragma unroll
             for (int k = 0; k < (C::kScaled ? 4 : 1); ++k) {
               const uint32_t pA = p_s + k * (kHp * 128) + hA * 128 + 4 * r4, pB = pA + 8 * 128;
-              const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 2 * r4;
+              const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 32 * half + 2 * r4;
 #pragma unroll
-              for (int g = 0; g < 8; ++g) {
+              for (int g = 0; g < 4; ++g) {
                 if (C::kScaled) {
                   const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
-                  pa[g] = pack_bf16x2(xA[2 * g] * f.x, xA[2 * g + 1] * f.y);
-                  pb[g] = pack_bf16x2(xB[2 * g] * f.x, xB[2 * g + 1] * f.y);
+                  pa[g] = pack_bf16x2(eA[g].x * f.x, eA[g].y * f.y);
+                  pb[g] = pack_bf16x2(eB[g].x * f.x, eB[g].y * f.y);
                 }
-                st_shared32(pA + ((g ^ sw) << 4), pa[g]);
-                st_shared32(pB + ((g ^ sw) << 4), pb[g]);
+                st_shared32(pA + (((4 * half + g) ^ sw) << 4), pa[g]);
+                st_shared32(pB + (((4 * half + g) ^ sw) << 4), pb[g]);
               }
             }
           }
           if (kMode == 0 && !all) {
             // rows outside the item: whatever the page holds there must not meet P's zeros
+            landed(1);
+            landed(2);
+            landed(3);
             const int piece = tid & 63;
-            for (int r = tid >> 6; r < 64; r += 2) {
+            for (int r = tid >> 6; r < 64; r += 4) {
               if ((mask >> r) & 1) continue;
               int s = sl + (piece >> 4);
               if (s >= NS) s -= NS;
@@ -643,53 +698,73 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           if (sl >= NS) { sl -= NS; sph ^= 1; }
           fence_proxy_async_smem();
           tc_fence_before();
-          mbar_arrive(smem_u32(&X.p_full));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&X.p_full));
         }
-        // ---- the segment's end ----
-        lA += __shfl_xor_sync(0xFFFFFFFFu, lA, 1);
-        lA += __shfl_xor_sync(0xFFFFFFFFu, lA, 2);
-        lB += __shfl_xor_sync(0xFFFFFFFFu, lB, 1);
-        lB += __shfl_xor_sync(0xFFFFFFFFu, lB, 2);
-        rA += __shfl_xor_sync(0xFFFFFFFFu, rA, 1);
-        rA += __shfl_xor_sync(0xFFFFFFFFu, rA, 2);
-        rB += __shfl_xor_sync(0xFFFFFFFFu, rB, 1);
-        rB += __shfl_xor_sync(0xFFFFFFFFu, rB, 2);
-        if (C::kScaled) { rA = lA; rB = lB; }
+        // ---- the segment's end: sums of each head, then its part or its output ----
+        if (on) {
+          float v[4] = {lA.x + lA.y, lB.x + lB.y, rA.x + rA.y, rB.x + rB.y};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 1);
+            v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 2);
+          }
+          if (r4 == 0) {
+            X.lsum[half][hA] = v[0];
+            X.lsum[half][hB] = v[1];
+            // with scaled weights no rounded sum stands for the output's weights
+            X.rsum[half][hA] = C::kScaled ? v[0] : v[2];
+            X.rsum[half][hB] = C::kScaled ? v[1] : v[3];
+            if (half == 0) {
+              X.m_run[hA] = mA;
+              X.m_run[hB] = mB;
+            }
+          }
+        }
         const bool whole = w.unit == 0 && w.seg_units == w.i.units;
-        if (!X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1)) X.abort = 1;
-        tc_fence_after();
         const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
+        soft_sync();
+        if (tid < Hg) {
+          float l = X.lsum[0][tid] + X.lsum[1][tid], r = X.rsum[0][tid] + X.rsum[1][tid];
+          const float m = X.m_run[tid];
+          if (whole) {
+            if (a.sink) {
+              const float sk = a.sink[64 * w.i.hg + tid] * kLog2e;
+              if (sk > -INFINITY) {
+                l += ex2(sk - m);
+                r += ex2(sk - m);
+              }
+            }
+            X.fac[tid] = r > 0.f || r != r ? 1.f / r : 0.f;  // no row and no sink: zeros
+            if (a.lse)
+              a.lse[w.i.q * a.H + 64 * w.i.hg + tid] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
+          } else {
+            float* st = a.pstat + part * (3 * kHp) + tid;
+            st[0] = m;
+            st[kHp] = l;
+            st[2 * kHp] = r;
+          }
+        }
         if (a.rec && w.unit == 0 && tid == 0) {
           // CTAs of the item's first and last unit; (-1, -1): finished here
           const int64_t ul = u + w.i.units - 1;
           a.rec[w.it] = whole ? make_int2(-1, -1)
                               : make_int2((int)blockIdx.x, (int)(((ul + 1) * ncta - 1) / U));
         }
+        if (whole && a.inv_freq && warp == 7) {
+          float s, cs;
+          sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
+          X.rope_c[lane] = cs;
+          X.rope_s[lane] = s;
+        }
+        if (!X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1)) X.abort = 1;
+        tc_fence_after();
+        soft_sync();
         if (whole) {
-          if (a.sink) {
-            if (sinkA > -INFINITY) { lA += ex2(sinkA - mA); rA += ex2(sinkA - mA); }
-            if (sinkB > -INFINITY) { lB += ex2(sinkB - mB); rB += ex2(sinkB - mB); }
-          }
-          if (on && r4 == 0) {
-            X.fac[hA] = rA > 0.f || rA != rA ? 1.f / rA : 0.f;  // no row and no sink: zeros
-            X.fac[hB] = rB > 0.f || rB != rB ? 1.f / rB : 0.f;
-            if (a.lse) {
-              float* d = a.lse + w.i.q * a.H + 64 * w.i.hg;
-              if (hA < Hg) d[hA] = lA == 0.f ? -INFINITY : (mA + __log2f(lA)) * kLn2;
-              if (hB < Hg) d[hB] = lB == 0.f ? -INFINITY : (mB + __log2f(lB)) * kLn2;
-            }
-          }
-          if (a.inv_freq && warp == 0) {
-            float s, cs;
-            sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
-            X.rope_c[lane] = cs;
-            X.rope_s[lane] = s;
-          }
-          soft_sync();
           uint16_t* out = a.out + (w.i.q * a.H + 64 * w.i.hg) * kDLat;
 #pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
-            const int d = mt * 128 + warp * 32 + lane;
+          for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
+            const int d = mt * 128 + quad * 32 + lane;
             const bool rot = a.inv_freq && d >= kRopeDim0;  // uniform in a warp
             const float cs = rot ? X.rope_c[(d - kRopeDim0) >> 1] : 1.f;
             const float sn = rot ? X.rope_s[(d - kRopeDim0) >> 1] : 0.f;
@@ -722,18 +797,11 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               }
             }
           }
-          soft_sync();  // fac and the rotation are read before the next segment writes them
         } else {
-          float* st = a.pstat + part * (3 * kHp);
-          if (on && r4 == 0) {
-            st[hA] = mA; st[hB] = mB;
-            st[kHp + hA] = lA; st[kHp + hB] = lB;
-            st[2 * kHp + hA] = rA; st[2 * kHp + hB] = rB;
-          }
           // [dim tile][four heads][128 dims][4]: a lane writes 16 bytes, a warp 512
-          float* po = a.part + part * (int64_t)(kHp * kDLat) + (warp * 32 + lane) * 4;
+          float* po = a.part + part * (int64_t)(kHp * kDLat) + (quad * 32 + lane) * 4;
 #pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
 #pragma unroll 1
             for (int hb = 0; hb < Hg; hb += 16) {
               uint32_t v[16];
@@ -747,9 +815,10 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           }
         }
         tc_fence_before();
+        soft_sync();  // fac, the sums and the rotation are read before the next segment's
         u += w.seg_units;
       } while (walk_next(a, w));
-    } else if (warp == 4) {
+    } else if (warp == 8) {
       // ================= S products =================
       if (lane == 0) {
         Walk w;
@@ -793,7 +862,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         umma_commit(smem_u32(&X.fin[0]));
         mbar_wait(smem_u32(&X.fin[0]), 0, 100000000ull);
       }
-    } else if (warp == 5) {
+    } else if (warp == 9) {
       // ================= O^T products =================
       if (lane == 0) {
         Walk w;
@@ -825,7 +894,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         umma_commit(smem_u32(&X.fin[1]));
         mbar_wait(smem_u32(&X.fin[1]), 0, 100000000ull);
       }
-    } else if (warp == 7) {
+    } else if (warp == 11) {
       // ================= Q of each segment =================
       if (lane == 0) {
         Walk w;
@@ -847,7 +916,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         } while (walk_next(a, w));
         mbar_wait(qf, (n - 1) & 1, 100000000ull);  // no copy may land after the CTA's exit
       }
-    } else if (kMode == 0 && warp == 6) {
+    } else if (kMode == 0 && warp == 10) {
       // ================= bf16 rows by tensor copies =================
       griddep_wait();  // rows and table entries may come from the kernel before this one
       Walk w;
@@ -914,13 +983,13 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       // no copy may still be landing when the CTA exits
       if (lane < NS && (filled >> lane & 1))
         mbar_wait(smem_u32(&X.full[lane]), lane < sl ? ph : ph ^ 1, 100000000ull);
-    } else if (kMode != 0 && warp >= 8) {
+    } else if (kMode != 0 && warp >= 12) {
       // ================= FP8 rows through registers =================
       // Thread t of 512: row t / 8 of a tile, 16 dims of each quarter (piece t % 8).  A tile's
       // codes are loaded while the tile before it is converted, its page looked up one
       // tile earlier still.
       griddep_wait();
-      const int t512 = tid - 256, r = t512 >> 3, pc = t512 & 7;
+      const int t512 = tid - 384, r = t512 >> 3, pc = t512 & 7;
       Walk w;
       walk_start(a, X, u1 - u0, w);
       int tn = w.t;            // next tile to look up
@@ -980,7 +1049,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           if (filled >> sl & 1) ok = ok && !X.abort && mbar_wait(smem_u32(&X.empty[sl]), ph ^ 1);
           filled |= 1u << sl;
           if (k == 0 && lane == 0)
-            reinterpret_cast<uint8_t*>(X.nib[c & 3])[warp - 8] =
+            reinterpret_cast<uint8_t*>(X.nib[c & 3])[warp - 12] =
                 (uint8_t)((bal & 1u) | (bal >> 7 & 2u) | (bal >> 14 & 4u) | (bal >> 21 & 8u));
           const uint32_t w4[4] = {cur[k].x, cur[k].y, cur[k].z, cur[k].w};
           float scale = 1.f;
@@ -1006,9 +1075,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           if (kMode == 1 && pc == 0)
             sc_s[((c & 3) * 4 + k) * 64 + r] =
                 __uint_as_float(k == 0 ? csc.x : k == 1 ? csc.y : k == 2 ? csc.z : csc.w);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&X.full[sl]));
+          if (k & 1) {  // one fence for two quarters
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&X.full[sl == 0 ? NS - 1 : sl - 1]));
+              mbar_arrive(smem_u32(&X.full[sl]));
+            }
+          }
           if (++sl == NS) { sl = 0; ph ^= 1; }
         }
         ++c;
@@ -1026,7 +1100,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_dealloc(tmem, 512);
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 // ================================ join ===================================================
