@@ -213,7 +213,7 @@ int attn_num_splits(int Q, int nsel, int num_sms);
 
 // 2-D tensor map over `rows` bf16 rows of `cols` elements (row stride cols * 2 bytes),
 // boxes of box_cols x box_rows, 128-byte swizzle, out-of-range elements read as zero.
-// A tensor map over bytes: rank 2 or 3, dims[0] contiguous, strides[i] = byte stride of
+// A tensor map over bytes: rank 2 to 5, dims[0] contiguous, strides[i] = byte stride of
 // dims[i + 1]; 128-byte swizzle (box[0] must be 128).
 bool encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                   const uint64_t* strides, const uint32_t* box);

@@ -757,9 +757,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 bool encode_bytes(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                   const uint64_t* strides, const uint32_t* box) {
   auto fn = tensor_map_encoder();
-  if (!fn || !base || rank < 2 || rank > 3) return false;
-  cuuint64_t d[3], st[2];
-  cuuint32_t bx[3], es[3] = {1, 1, 1};
+  if (!fn || !base || rank < 2 || rank > 5) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     bx[i] = box[i];

@@ -159,17 +159,21 @@ __global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppen
 // fp32) to the workspace and paged_join_kernel joins them.
 //
 // A tile passes through a ring of 16 KiB slots, each a quarter of it (64 rows x 128 dims, as
-// two 128-byte-swizzled blocks of 64 dims):
-//   load     warp 10: one tensor copy per page piece and dim block (bf16 rows), or sixteen
-//            warps that load FP8 rows into registers a tile ahead and store them as bf16
-//   S        warp 8: Q[64 x 512] . X^T, a quarter as it lands; head h in TMEM lane
-//            32 (h / 16) + h % 16, column = row
+// eight groups of 8 rows, two 128-byte-swizzled blocks of 64 dims each):
+//   load     warps 12..15, a quarter each: one tensor copy per page piece (bf16 rows), or
+//            warps 12..27, which load FP8 rows into registers a tile ahead and store them as
+//            bf16.  A tensor copy takes its warp 50 to 100 cycles to issue, so one warp alone
+//            held the tile rate to 3200 cycles (a tile of HBM time per SM is 2800)
+//   S        warps 8 and 9: Q[64 x 512] . X^T, a quarter as it lands, a dim block each into
+//            accumulators of their own; head h in TMEM lane 32 (h / 16) + h % 16, column = row
 //   softmax  warps 0..7, half of the rows each four: P = 2^(s - m) with the running maximum m,
 //            which moves only when a score exceeds it by more than 2^64 (P <= 2^64 keeps bf16
 //            P and fp32 sums finite), so a tile's usual pass needs no maximum across threads,
 //            one vote only
-//   O^T     += X^T[512 x 64] . P^T: warp 9, four M = 128 tiles of dims, each releasing its
-//            slot, so the quarter of a later tile starts to load while this one is finished
+//   O^T     += X^T[512 x 64] . P^T: warps 10 and 11, four M = 128 tiles of dims, each releasing
+//            its slot, so the quarter of a later tile starts to load while this one is finished
+// (One thread issues an MMA of these sizes about every 47 cycles; the operands' reads from
+// shared memory, 128 bytes a cycle, allow an S product every 32.  So two issue each kind.)
 // Rows outside lo .. hi - 1 or on a bad page get P = 0 and are zeroed before the product
 // (what the page holds there may be NaN).
 //
@@ -177,7 +181,8 @@ __global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppen
 // common rounding error of the largest weights cancels), and of the unrounded ones for lse.
 
 constexpr int kSlotBytes = 16384;
-constexpr int kBlock = 8192;  // 64 dims of 64 rows
+constexpr int kBlock = 1024;  // 64 dims of 8 rows
+constexpr int kGroup = 2048;  // 128 dims of 8 rows
 constexpr int kMaxSmem = 232448;
 constexpr float kLazy = 64.0f;
 constexpr uint32_t kColO = 256;  // O^T tiles at 256 + 64 mt
@@ -187,7 +192,7 @@ struct __align__(16) PagedAux {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full, pv_done;
-  uint64_t fin[2];
+  uint64_t fin[4];
   uint64_t mask[4];     // valid rows of tile c at c & 3 (bf16 rows)
   uint32_t nib[4][4];   // the same for FP8 rows: four rows' bits in each byte
   int64_t sums[32];     // scan of the plan
@@ -208,7 +213,7 @@ struct __align__(16) PagedAux {
 template <int kHp, int kMode>
 struct PagedCfg {
   static constexpr bool kScaled = kMode == 1;
-  static constexpr int kThreads = kMode == 0 ? 384 : 896;
+  static constexpr int kThreads = kMode == 0 ? 512 : 896;
   static constexpr int kQBlock = kHp * 128;
   static constexpr int kQBytes = 8 * kQBlock;
   static constexpr int kPBytes = kHp * 128 * (kScaled ? 4 : 1);
@@ -284,6 +289,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
+      : "memory");
+}
+
+// A box of a page's rows from group y of 8 rows on, dim blocks db and db + 1 (of 64), page z.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int32_t db,
+                                            int32_t y, int32_t z, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(db), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -407,14 +422,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       mbar_init(smem_u32(&X.empty[s]), 1);
     }
     mbar_init(smem_u32(&X.q_full), 1);
-    mbar_init(smem_u32(&X.q_empty), 1);
+    mbar_init(smem_u32(&X.q_empty), 2);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&X.s_full[b]), 1);
+      mbar_init(smem_u32(&X.s_full[b]), 2);
       mbar_init(smem_u32(&X.s_empty[b]), 8);
-      mbar_init(smem_u32(&X.fin[b]), 1);
     }
+    for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&X.fin[b]), 1);
     mbar_init(smem_u32(&X.p_full), 8);
-    mbar_init(smem_u32(&X.pv_done), 1);
+    mbar_init(smem_u32(&X.pv_done), 2);
     X.abort = 0;
     mbar_fence_init();
   }
@@ -498,6 +513,10 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         for (int t = w.t; t < w.t_end; ++t, ++c) {
           const int sb = C::kScaled ? 0 : c & 1;
           const uint32_t sphase = C::kScaled ? (uint32_t)c & 1 : (uint32_t)(c >> 1) & 1;
+          // P's buffer and O^T are free once the previous tile's products are done, which they
+          // are before this tile's scores except when the tensor core is the limit
+          if (c > 0 && !X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1))
+            X.abort = 1;
           if (!X.abort && !mbar_wait(smem_u32(&X.s_full[sb]), sphase)) X.abort = 1;
           // the tile has landed (S read it); waiting for that here too makes what its loader
           // wrote visible: the mask (first quarter), the scales (all of them)
@@ -516,13 +535,17 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           float2 xA[4], xB[4];
           if (on) {
             if (!C::kScaled) {
-              uint32_t x[16];
-              tmem_ld_16x256b_x4(tmem + lrow + 64 * sb + 32 * half, x);
+              uint32_t x[16], y[16];
+              tmem_ld_16x256b_x4(tmem + lrow + 128 * sb + 32 * half, x);
+              tmem_ld_16x256b_x4(tmem + lrow + 128 * sb + 64 + 32 * half, y);
               tmem_ld_wait();
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
-                xA[g] = make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1]));
-                xB[g] = make_float2(__uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3]));
+                xA[g] = add2(make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1])),
+                             make_float2(__uint_as_float(y[4 * g]), __uint_as_float(y[4 * g + 1])));
+                xB[g] =
+                    add2(make_float2(__uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3])),
+                         make_float2(__uint_as_float(y[4 * g + 2]), __uint_as_float(y[4 * g + 3])));
               }
             } else {
 #pragma unroll
@@ -627,8 +650,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               rB = fma2(rB, qB, o0);
               weights();
             }
-            if (c > 0 && !X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1))
-              X.abort = 1;
             soft_sync();  // fac is written
             if (t > w.t) {
               tc_fence_after();
@@ -658,9 +679,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               rB = add2(rB, uB);
             }
           }
-          // P's buffer and O^T are free once the previous tile's products are done
-          if (c > 0 && !X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1))
-            X.abort = 1;
           if (on) {
             const int sw = hA & 7;  // hB & 7 is the same
 #pragma unroll
@@ -689,8 +707,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               if ((mask >> r) & 1) continue;
               int s = sl + (piece >> 4);
               if (s >= NS) s -= NS;
-              st_shared16(ring + s * kSlotBytes + ((piece >> 3) & 1) * kBlock + r * 128 +
-                              (piece & 7) * 16,
+              st_shared16(ring + s * kSlotBytes + (r >> 3) * kGroup + ((piece >> 3) & 1) * kBlock +
+                              (r & 7) * 128 + (piece & 7) * 16,
                           make_uint4(0u, 0u, 0u, 0u));
             }
           }
@@ -818,19 +836,37 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         soft_sync();  // fac, the sums and the rotation are read before the next segment's
         u += w.seg_units;
       } while (walk_next(a, w));
-    } else if (warp == 8) {
-      // ================= S products =================
+    } else if (warp < 10) {
+      // ================= S products (warp 8 also loads each segment's Q) =================
+      // Of each quarter, warp 8 + r multiplies dim block r; scaled rows keep a quarter in one
+      // accumulator, so there the warps take turns at the quarters.
+      const int r = warp - 8;
       if (lane == 0) {
         Walk w;
         walk_start(a, X, u1 - u0, w);
         int c = 0, sl = 0;
-        uint32_t sph = 0, qph = 0;
+        uint32_t sph = 0, n = 0;  // n: segments so far
         const uint32_t id = idesc_bf16(64, 64, 0, 0);
-        const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), r_d = sdesc_sw128(ring, 16, 1024);
-        bool ok = true;
+        const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), r_d = sdesc_sw128(ring, 16, kGroup);
+        const uint32_t qf = smem_u32(&X.q_full);
+        const uint64_t pol = policy_evict_first();
+        bool ok = true, asked = false;
         do {
-          ok = !X.abort && mbar_wait(smem_u32(&X.q_full), qph);
-          qph ^= 1;
+          if (r == 0) {
+            // the products of the segment before it have read Q
+            ok = n == 0 || (!X.abort && mbar_wait(smem_u32(&X.q_empty), (n - 1) & 1));
+            if (ok) {
+              mbar_arrive_expect_tx(qf, C::kQBytes);
+#pragma unroll
+              for (int db = 0; db < 8; ++db)
+                tma_load_2d(q_s + db * C::kQBlock, &qmap, 64 * db,
+                            (int32_t)(w.i.q * a.H + 64 * w.i.hg), qf, pol);
+              asked = true;
+            }
+          }
+          ok = ok && !X.abort && mbar_wait(qf, n & 1);
+          if (ok) asked = false;
+          ++n;
           for (int t = w.t; ok && t < w.t_end; ++t, ++c) {
             const int sb = C::kScaled ? 0 : c & 1;
             const int lag = C::kScaled ? 1 : 2;
@@ -840,16 +876,25 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              ok = ok && mbar_wait(smem_u32(&X.full[sl]), sph);
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t d = tmem + 64 * (C::kScaled ? k : sb);
-              const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
+              if (!C::kScaled || (k & 1) == r) {
+                ok = ok && mbar_wait(smem_u32(&X.full[sl]), sph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (C::kScaled ? 64 * k : 128 * sb + 64 * r);
+                const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
+                if (C::kScaled) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                umma_bf16(d, q_d + (((2 * k + (i >> 2)) * C::kQBlock + (i & 3) * 32) >> 4),
-                          rd + (((i >> 2) * kBlock + (i & 3) * 32) >> 4), id,
-                          i > 0 || (!C::kScaled && k > 0));
+                  for (int i = 0; i < 8; ++i)
+                    umma_bf16(d, q_d + (((2 * k + (i >> 2)) * C::kQBlock + (i & 3) * 32) >> 4),
+                              rd + (((i >> 2) * kBlock + (i & 3) * 32) >> 4), id, i > 0);
+                } else {
+                  const uint64_t qd = q_d + ((uint32_t)((2 * k + r) * C::kQBlock) >> 4);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    umma_bf16(d, qd + ((i * 32) >> 4), rd + ((uint32_t)(r * kBlock + i * 32) >> 4), id,
+                              i > 0 || k > 0);
+                }
+              }
               if (++sl == NS) { sl = 0; sph ^= 1; }
             }
             if (!ok) break;
@@ -858,18 +903,21 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           if (!ok) { X.abort = 1; break; }
           umma_commit(smem_u32(&X.q_empty));
         } while (walk_next(a, w));
-        // no MMA may still be running when the TMEM is released, whatever happened above
-        umma_commit(smem_u32(&X.fin[0]));
-        mbar_wait(smem_u32(&X.fin[0]), 0, 100000000ull);
+        // no copy may land and no MMA run when the CTA gives up its memory, whatever happened
+        // above
+        if (asked) mbar_wait(qf, (n - 1) & 1, 100000000ull);
+        umma_commit(smem_u32(&X.fin[r]));
+        mbar_wait(smem_u32(&X.fin[r]), 0, 100000000ull);
       }
-    } else if (warp == 9) {
-      // ================= O^T products =================
+    } else if (warp < 12) {
+      // ================= O^T products: warp 10 + r tiles 2 r and 2 r + 1 =================
+      const int r = warp - 10;
       if (lane == 0) {
         Walk w;
         walk_start(a, X, u1 - u0, w);
-        int c = 0, sl = 0;
+        int c = 0, sl = 2 * r;
         const uint32_t id = idesc_bf16(128, kHp, 1, 0);
-        const uint64_t r_d = sdesc_sw128(ring, kBlock, 1024), p_d = sdesc_sw128(p_s, 16, 1024);
+        const uint64_t r_d = sdesc_sw128(ring, kBlock, kGroup), p_d = sdesc_sw128(p_s, 16, 1024);
         bool ok = true;
         do {
           for (int t = w.t; t < w.t_end; ++t, ++c) {
@@ -877,47 +925,29 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-              const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
-              const uint64_t pd = p_d + (C::kScaled ? (mt * kHp * 128) >> 4 : 0);
+            for (int j = 0; j < 2; ++j) {
+              const int mt = 2 * r + j;
+              const int s = sl + j >= NS ? sl + j - NS : sl + j;
+              const uint64_t rd = r_d + ((uint32_t)(s * kSlotBytes) >> 4);
+              const uint64_t pd = p_d + (C::kScaled ? (uint32_t)(mt * kHp * 128) >> 4 : 0);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(tmem + kColO + 64 * mt, rd + ((kk * 2048) >> 4), pd + ((kk * 32) >> 4),
+                umma_bf16(tmem + kColO + 64 * mt, rd + ((kk * 2 * kGroup) >> 4), pd + ((kk * 32) >> 4),
                           id, t > w.t || kk > 0);
-              umma_commit(smem_u32(&X.empty[sl]));
-              if (++sl == NS) sl = 0;
+              umma_commit(smem_u32(&X.empty[s]));
             }
             umma_commit(smem_u32(&X.pv_done));
+            sl += 4;
+            if (sl >= NS) sl -= NS;
           }
           if (!ok) { X.abort = 1; break; }
         } while (walk_next(a, w));
-        umma_commit(smem_u32(&X.fin[1]));
-        mbar_wait(smem_u32(&X.fin[1]), 0, 100000000ull);
+        umma_commit(smem_u32(&X.fin[2 + r]));
+        mbar_wait(smem_u32(&X.fin[2 + r]), 0, 100000000ull);
       }
-    } else if (warp == 11) {
-      // ================= Q of each segment =================
-      if (lane == 0) {
-        Walk w;
-        walk_start(a, X, u1 - u0, w);
-        const uint64_t pol = policy_evict_first();
-        uint32_t n = 0;  // segments so far
-        const uint32_t qf = smem_u32(&X.q_full);
-        do {
-          if (n > 0 && (X.abort || !mbar_wait(smem_u32(&X.q_empty), (n - 1) & 1))) {
-            X.abort = 1;
-            break;
-          }
-          mbar_arrive_expect_tx(qf, C::kQBytes);
-#pragma unroll
-          for (int db = 0; db < 8; ++db)
-            tma_load_2d(q_s + db * C::kQBlock, &qmap, 64 * db, (int32_t)(w.i.q * a.H + 64 * w.i.hg),
-                        qf, pol);
-          ++n;
-        } while (walk_next(a, w));
-        mbar_wait(qf, (n - 1) & 1, 100000000ull);  // no copy may land after the CTA's exit
-      }
-    } else if (kMode == 0 && warp == 10) {
-      // ================= bf16 rows by tensor copies =================
+    } else if (kMode == 0) {
+      // ================= bf16 rows by tensor copies: warp 12 + k quarter k =================
+      const int k = warp - 12;
       griddep_wait();  // rows and table entries may come from the kernel before this one
       Walk w;
       walk_start(a, X, u1 - u0, w);
@@ -925,10 +955,9 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       const int R = a.box_rows, nc = 64 / R;      // page pieces per tile
       const int tb = 32 / nc;                     // tiles whose pieces the lanes look up at once
       const int cl = lane & (nc - 1);             // this lane's piece of a tile
-      int sl = 0, c = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      uint32_t filled = 0;  // slots that were ever used
+      int sl = k, c = 0;
+      uint32_t ph = 0;  // how often the ring has come round, modulo 2
+      bool again = false, ok = true;
       do {
         for (int tbeg = w.t; ok && tbeg < w.t_end; tbeg += tb) {
           // piece `lane` of the next tb tiles: its page and row, valid rows
@@ -939,11 +968,11 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             const int32_t lp = (int32_t)row / a.cache.page_rows;
             const int32_t page = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
             if (page >= 0 && page < a.cache.n_pages) {
-              py = (int32_t)row - lp * a.cache.page_rows;
+              py = ((int32_t)row - lp * a.cache.page_rows) >> 3;
               pz = page;
               m = tile_mask(row, w.i.lo, w.i.hi);
               if (R < 64) m &= (1ull << R) - 1;
-            } else {
+            } else if (k == 0) {
               raise_fault(kFaultBounds);
             }
           }
@@ -955,35 +984,33 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             const int32_t y = __shfl_sync(0xFFFFFFFFu, py, src + cl);
             const int32_t z = __shfl_sync(0xFFFFFFFFu, pz, src + cl);
             const uint64_t mk = __shfl_sync(0xFFFFFFFFu, m, src);
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t bar = smem_u32(&X.full[sl]);
-              if (filled >> sl & 1)
-                ok = !X.abort && mbar_wait(smem_u32(&X.empty[sl]), ph ^ 1);
-              ok = __all_sync(0xFFFFFFFFu, ok);
-              if (!ok) break;
-              filled |= 1u << sl;
-              if (lane == 0) {
-                if (k == 0) X.mask[c & 3] = mk;
-                mbar_arrive_expect_tx(bar, kSlotBytes);
-              }
-              __syncwarp();
-              if (lane < 2 * nc) {
-                const int d2 = lane / nc;
-                tma_load_3d(ring + sl * kSlotBytes + d2 * kBlock + cl * R * 128, &kmap,
-                            128 * (2 * k + d2), y, z, bar, pol);
-              }
-              if (++sl == NS) { sl = 0; ph ^= 1; }
+            const uint32_t bar = smem_u32(&X.full[sl]);
+            if (again) ok = !X.abort && mbar_wait(smem_u32(&X.empty[sl]), ph ^ 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+              if (k == 0) X.mask[c & 3] = mk;
+              mbar_arrive_expect_tx(bar, kSlotBytes);
             }
+            __syncwarp();
+            if (lane < nc) tma_load_5d(ring + sl * kSlotBytes + lane * R * 256, &kmap, 2 * k, y, z, bar, pol);
+            sl += 4;
+            if (sl >= NS) { sl -= NS; ph ^= 1; again = true; }
           }
         }
         if (!ok) break;
       } while (walk_next(a, w));
       if (!ok) X.abort = 1;
-      // no copy may still be landing when the CTA exits
-      if (lane < NS && (filled >> lane & 1))
-        mbar_wait(smem_u32(&X.full[lane]), lane < sl ? ph : ph ^ 1, 100000000ull);
-    } else if (kMode != 0 && warp >= 12) {
+      // No copy may still be landing when the CTA exits: wait for this warp's last three, but
+      // for those whose slot another quarter has taken since (they have long landed, and the
+      // barrier is in a later phase).
+      if (lane < 3 && lane < c && 4 * (c - 1 - lane) + k + NS >= 4 * c) {
+        int s = sl - 4 * (lane + 1);
+        if (s < 0) { s += NS; ph ^= 1; }
+        if (s < 0) { s += NS; ph ^= 1; }
+        mbar_wait(smem_u32(&X.full[s]), ph, 100000000ull);
+      }
+    } else {
       // ================= FP8 rows through registers =================
       // Thread t of 512: row t / 8 of a tile, 16 dims of each quarter (piece t % 8).  A tile's
       // codes are loaded while the tile before it is converted, its page looked up one
@@ -1033,8 +1060,9 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       bool v_cur = s_cur != nullptr;
       int sl = 0, c = 0;
       uint32_t ph = 0, filled = 0;
-      const uint32_t off0 = sw128_off(r, (2 * pc) & 7) + (pc >> 2) * kBlock;
-      const uint32_t off1 = sw128_off(r, (2 * pc + 1) & 7) + (pc >> 2) * kBlock;
+      const uint32_t offr = (r >> 3) * kGroup + (pc >> 2) * kBlock;
+      const uint32_t off0 = offr + sw128_off(r & 7, (2 * pc) & 7);
+      const uint32_t off1 = offr + sw128_off(r & 7, (2 * pc + 1) & 7);
       bool ok = true;
       while (have) {
         // the next tile's codes, and the page of the one after it
@@ -1107,43 +1135,75 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 //
 // Joins the parts of the items that several CTAs worked on: with M the largest running
 // maximum (and the sink logit), weights 2^(m - M) and Z = 2^(sink - M) + sum 2^(m - M) l,
-// out = sum 2^(m - M) O / Z.  One CTA per item, four heads and 128 dims; four groups of 64
-// threads (a pair of dims and four heads each) take every fourth part.
+// out = sum 2^(m - M) O / Z.  One CTA per item, four heads and 128 dims; kGroups groups of 64
+// threads (a pair of dims and four heads each) take every kGroups-th part, the first kAhead
+// of them loaded before the weights are known.  Sixteen groups for up to kFewItems items,
+// which may have 152 parts each; four for larger batches, whose items have few.
 constexpr int kMaxCtas = 152;
+constexpr int kFewItems = 16;
+constexpr int kAhead = 4;
 
-__global__ void __launch_bounds__(256) paged_join_kernel(PagedAttnArgs a, int hp) {
-  __shared__ float wt[kMaxCtas][4];
+template <int kGroups>
+__global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs a, int hp) {
+  __shared__ float4 wt[kMaxCtas];
   __shared__ float inv[4];
-  __shared__ float acc_s[3][64][8];
+  __shared__ float acc_s[kGroups > 4 ? 4 : kGroups - 1][8][64];
   griddep_launch_dependents();
-  griddep_wait();
   const int64_t it = blockIdx.x;
   const int hc = blockIdx.y >> 2, mt = blockIdx.y & 3;
   const int64_t q = a.ng == 2 ? it >> 1 : it;
   const int hg = a.ng == 2 ? (int)(it & 1) : 0;
   const int h0 = 64 * hg + 4 * hc;  // first of the four heads
-  if (h0 >= a.H) return;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int seq = a.q_seq[q];
-  if (seq < 0 || seq >= a.cache.B) return;
+  const bool live = h0 < a.H && seq >= 0 && seq < a.cache.B;
+  griddep_wait();
+  if (!live) return;
   const int2 rec = a.rec[it];
   if (rec.x < 0) return;
   const int n = min(rec.y - rec.x + 1, kMaxCtas);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto part = [&](int s) -> int64_t { return 2 * (int64_t)(rec.x + s) + (s == 0 ? 1 : 0); };
-  if (warp < 4 && h0 + warp < a.H) {
+  const int pair = tid & 63, grp = tid >> 6;
+  const float* src = a.part + (mt * (hp / 4) + hc) * 512 + pair * 8;
+  float4 x[kAhead], y[kAhead];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i * kGroups;
+      if (s < n) {
+        const float4* p = reinterpret_cast<const float4*>(src + part(s) * (int64_t)(hp * kDLat));
+        x[i] = __ldcs(p);
+        y[i] = __ldcs(p + 1);
+      }
+    }
+  };
+  load(grp);
+  if (warp < 4) {
     const int h = 4 * hc + warp;
-    const float sink = a.sink ? a.sink[h0 + warp] * kLog2e : -INFINITY;
-    float M = sink;
-    for (int s = lane; s < n; s += 32) M = fmaxf(M, a.pstat[part(s) * (3 * hp) + h]);
+    const bool there = h0 + warp < a.H;
+    const float sink = a.sink && there ? a.sink[h0 + warp] * kLog2e : -INFINITY;
+    float m[(kMaxCtas + 31) / 32], M = sink;
+#pragma unroll
+    for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) {
+      const int s = lane + 32 * i;
+      m[i] = s < n && there ? a.pstat[part(s) * (3 * hp) + h] : -INFINITY;
+      M = fmaxf(M, m[i]);
+    }
     M = lanes_max<32>(M);
     const float Mf = M == -INFINITY ? 0.f : M;
     float l = 0.f, r = 0.f;
-    for (int s = lane; s < n; s += 32) {
-      const float* st = a.pstat + part(s) * (3 * hp) + h;
-      const float w = ex2(st[0] - Mf);
-      wt[s][warp] = w;
-      l = fmaf(w, st[hp], l);
-      r = fmaf(w, st[2 * hp], r);
+#pragma unroll
+    for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) {
+      const int s = lane + 32 * i;
+      if (s < n) {
+        const float* st = a.pstat + part(s) * (3 * hp) + h;
+        const float w = there ? ex2(m[i] - Mf) : 0.f;
+        reinterpret_cast<float*>(&wt[s])[warp] = w;
+        if (there) {
+          l = fmaf(w, st[hp], l);
+          r = fmaf(w, st[2 * hp], r);
+        }
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -1155,42 +1215,49 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedAttnArgs a, int hp
     r += sk;
     if (lane == 0) {
       inv[warp] = r > 0.f || r != r ? 1.f / r : 0.f;
-      if (a.lse && mt == 0)
+      if (a.lse && mt == 0 && there)
         a.lse[q * a.H + h0 + warp] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
     }
-  } else if (warp < 4) {
-    for (int s = lane; s < n; s += 32) wt[s][warp] = 0.f;
-    if (lane == 0) inv[warp] = 0.f;
   }
   __syncthreads();
-  const int pair = tid & 63, grp = tid >> 6;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const float* src = a.part + (mt * (hp / 4) + hc) * 512 + pair * 8;
-#pragma unroll 4
-  for (int s = grp; s < n; s += 4) {
-    const float* p = src + part(s) * (int64_t)(hp * kDLat);
-    const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 y = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    const float4 w = *reinterpret_cast<const float4*>(wt[s]);
-    acc[0] = fmaf(x.x, w.x, acc[0]);
-    acc[1] = fmaf(x.y, w.y, acc[1]);
-    acc[2] = fmaf(x.z, w.z, acc[2]);
-    acc[3] = fmaf(x.w, w.w, acc[3]);
-    acc[4] = fmaf(y.x, w.x, acc[4]);
-    acc[5] = fmaf(y.y, w.y, acc[5]);
-    acc[6] = fmaf(y.z, w.z, acc[6]);
-    acc[7] = fmaf(y.w, w.w, acc[7]);
-  }
-  if (grp > 0) {
+  for (int s0 = grp; s0 < n; s0 += kAhead * kGroups) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc_s[grp - 1][pair][i] = acc[i];
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i * kGroups;
+      if (s < n) {
+        const float4 w = wt[s];
+        acc[0] = fmaf(x[i].x, w.x, acc[0]);
+        acc[1] = fmaf(x[i].y, w.y, acc[1]);
+        acc[2] = fmaf(x[i].z, w.z, acc[2]);
+        acc[3] = fmaf(x[i].w, w.w, acc[3]);
+        acc[4] = fmaf(y[i].x, w.x, acc[4]);
+        acc[5] = fmaf(y[i].y, w.y, acc[5]);
+        acc[6] = fmaf(y[i].z, w.z, acc[6]);
+        acc[7] = fmaf(y[i].w, w.w, acc[7]);
+      }
+    }
+    load(s0 + kAhead * kGroups);
   }
-  __syncthreads();
+  // the groups' sums: sixteen fold into four through shared memory, four into one
+#pragma unroll
+  for (int top = kGroups; top > 1; top >>= 2) {
+    const int low = top / 4;  // groups that remain
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      if (grp >= k * low && grp < (k + 1) * low) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc_s[grp - k * low][i][pair] = acc[i];
+      }
+      __syncthreads();
+      if (grp < low) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += acc_s[grp][i][pair];
+      }
+      __syncthreads();
+    }
+  }
   if (grp > 0) return;
-#pragma unroll
-  for (int g = 0; g < 3; ++g)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += acc_s[g][pair][i];
   const int d = mt * 128 + 2 * pair;
   float cs = 1.f, sn = 0.f;
   if (a.inv_freq && d >= kRopeDim0)
@@ -1198,9 +1265,9 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedAttnArgs a, int hp
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     if (h0 + h >= a.H) break;
-    const float x = acc[h] * inv[h], y = acc[4 + h] * inv[h];
+    const float x0 = acc[h] * inv[h], x1 = acc[4 + h] * inv[h];
     __stcs(reinterpret_cast<unsigned int*>(a.out + (q * a.H + h0 + h) * kDLat + d),
-           pack_bf16x2(x * cs + y * sn, y * cs - x * sn));
+           pack_bf16x2(x0 * cs + x1 * sn, x1 * cs - x0 * sn));
   }
 }
 
@@ -1248,17 +1315,20 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool join, cudaStream_t s)
     return cudaErrorInvalidValue;
   km = qm;
   if (a.cache.dtype == 0) {
-    const uint64_t dims[3] = {1024, (uint64_t)a.cache.page_rows, (uint64_t)a.cache.n_pages};
-    const uint64_t strides[2] = {1024, (uint64_t)a.cache.page_stride};
-    const uint32_t box[3] = {128, (uint32_t)a.box_rows, 1};
-    if (!encode_bytes(&km, a.cache.data, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    // a page as [8-row groups][8 dim blocks][8 rows][128 bytes]
+    const uint64_t dims[5] = {128, 8, 8, (uint64_t)a.cache.page_rows / 8, (uint64_t)a.cache.n_pages};
+    const uint64_t strides[4] = {1024, 128, 8192, (uint64_t)a.cache.page_stride};
+    const uint32_t box[5] = {128, 8, 2, (uint32_t)a.box_rows / 8, 1};
+    if (!encode_bytes(&km, a.cache.data, 5, dims, strides, box)) return cudaErrorInvalidValue;
   }
   cudaError_t e = hp == 16   ? launch_attn_mode<16>(a, qm, km, s)
                   : hp == 32 ? launch_attn_mode<32>(a, qm, km, s)
                              : launch_attn_mode<64>(a, qm, km, s);
   if (e != cudaSuccess || !join) return e;
-  return launch_pdl(paged_join_kernel, dim3((unsigned)(a.Q * a.ng), (unsigned)hp), dim3(256), 0, s, a,
-                    hp);
+  const dim3 grid((unsigned)(a.Q * a.ng), (unsigned)hp);
+  return a.Q * a.ng <= kFewItems
+             ? launch_pdl(paged_join_kernel<16>, grid, dim3(1024), 0, s, a, hp)
+             : launch_pdl(paged_join_kernel<4>, grid, dim3(256), 0, s, a, hp);
 }
 
 }  // namespace csa2
