@@ -202,7 +202,7 @@ struct __align__(16) PagedAux {
   float fac[64];        // rescale factor or 1 / sum, per head
   float top[2][64];     // largest score above the running maximum, by half of the rows
   float lsum[2][64], rsum[2][64];  // sums of P by half: unrounded, rounded
-  float m_run[64];
+  float m_run[64], sink2[64];
   float rope_c[32], rope_s[32];
   uint32_t tmem_slot;
   int abort;
@@ -317,14 +317,17 @@ __device__ __forceinline__ Item load_item(const PagedAttnArgs& a, int64_t it, bo
   i.q = a.ng == 2 ? it >> 1 : it;
   i.hg = a.ng == 2 ? (int)(it & 1) : 0;
   i.seq = a.q_seq[i.q];
+  const int64_t p = a.q_pos[i.q];
   i.lo = i.hi = i.tile0 = 0;
   i.tiles = i.units = 0;
   if (i.seq < 0 || i.seq >= a.cache.B) {
     if (report && i.seq != -1) raise_fault(kFaultBounds);
     return i;
   }
-  const int64_t p = a.q_pos[i.q];
-  int64_t hi = p < 0 ? 0 : p / a.ratio + (p % a.ratio == a.ratio - 1 ? 1 : 0);  // (p + 1) / ratio
+  int64_t hi;  // (p + 1) / ratio
+  if (p < 0) hi = 0;
+  else if (p < 0x7FFFFFFF) hi = (uint32_t)(p + 1) / (uint32_t)a.ratio;
+  else hi = p / a.ratio + (p % a.ratio == a.ratio - 1 ? 1 : 0);
   int64_t lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
   if (hi > a.cap_rows) {
     if (report) raise_fault(kFaultBounds);
@@ -509,6 +512,18 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         if (a.sink) {
           if (hA < Hg) mA = a.sink[64 * w.i.hg + hA] * kLog2e;
           if (hB < Hg) mB = a.sink[64 * w.i.hg + hB] * kLog2e;
+        }
+        const bool whole = w.unit == 0 && w.seg_units == w.i.units;
+        // what the output needs is fetched while the first tile loads
+        if (half == 0 && r4 == 0) {
+          X.sink2[hA] = mA;
+          X.sink2[hB] = mB;
+        }
+        if (whole && a.inv_freq && warp == 7) {
+          float s, cs;
+          sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
+          X.rope_c[lane] = cs;
+          X.rope_s[lane] = s;
         }
         for (int t = w.t; t < w.t_end; ++t, ++c) {
           const int sb = C::kScaled ? 0 : c & 1;
@@ -739,19 +754,16 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             }
           }
         }
-        const bool whole = w.unit == 0 && w.seg_units == w.i.units;
         const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
         soft_sync();
         if (tid < Hg) {
           float l = X.lsum[0][tid] + X.lsum[1][tid], r = X.rsum[0][tid] + X.rsum[1][tid];
           const float m = X.m_run[tid];
           if (whole) {
-            if (a.sink) {
-              const float sk = a.sink[64 * w.i.hg + tid] * kLog2e;
-              if (sk > -INFINITY) {
-                l += ex2(sk - m);
-                r += ex2(sk - m);
-              }
+            const float sk = X.sink2[tid];
+            if (sk > -INFINITY) {
+              l += ex2(sk - m);
+              r += ex2(sk - m);
             }
             X.fac[tid] = r > 0.f || r != r ? 1.f / r : 0.f;  // no row and no sink: zeros
             if (a.lse)
@@ -768,12 +780,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           const int64_t ul = u + w.i.units - 1;
           a.rec[w.it] = whole ? make_int2(-1, -1)
                               : make_int2((int)blockIdx.x, (int)(((ul + 1) * ncta - 1) / U));
-        }
-        if (whole && a.inv_freq && warp == 7) {
-          float s, cs;
-          sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
-          X.rope_c[lane] = cs;
-          X.rope_s[lane] = s;
         }
         if (!X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1)) X.abort = 1;
         tc_fence_after();
@@ -1135,58 +1141,80 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 //
 // Joins the parts of the items that several CTAs worked on: with M the largest running
 // maximum (and the sink logit), weights 2^(m - M) and Z = 2^(sink - M) + sum 2^(m - M) l,
-// out = sum 2^(m - M) O / Z.  One CTA per item, four heads and 128 dims; kGroups groups of 64
-// threads (a pair of dims and four heads each) take every kGroups-th part, the first kAhead
-// of them loaded before the weights are known.  Sixteen groups for up to kFewItems items,
-// which may have 152 parts each; four for larger batches, whose items have few.
+// out = sum 2^(m - M) O / Z.  A CTA takes one item, 128 dims and four heads, a thread a pair
+// of dims; its kGroups groups of 64 threads take every kGroups-th part, the first kAhead of
+// them loaded before the weights are known.  Of an item with up to kAhead parts, the usual
+// case in a batch, the CTA of every fourth four heads does sixteen heads, four per group, and
+// the CTAs beside it return: fewer, longer loads per thread (64 items: 19 -> 8 us).
+// Sixteen groups for up to kFewItems items, which may have 152 parts each; else four.
 constexpr int kMaxCtas = 152;
 constexpr int kFewItems = 16;
 constexpr int kAhead = 4;
 
+// Four heads of a pair of dims: (x, y) += w * (part's two dims).
+__device__ __forceinline__ void join_add(float (&acc)[8], const float4& x, const float4& y,
+                                         const float4& w) {
+  acc[0] = fmaf(x.x, w.x, acc[0]);
+  acc[1] = fmaf(x.y, w.y, acc[1]);
+  acc[2] = fmaf(x.z, w.z, acc[2]);
+  acc[3] = fmaf(x.w, w.w, acc[3]);
+  acc[4] = fmaf(y.x, w.x, acc[4]);
+  acc[5] = fmaf(y.y, w.y, acc[5]);
+  acc[6] = fmaf(y.z, w.z, acc[6]);
+  acc[7] = fmaf(y.w, w.w, acc[7]);
+}
+
 template <int kGroups>
 __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs a, int hp) {
-  __shared__ float4 wt[kMaxCtas];
-  __shared__ float inv[4];
+  __shared__ float4 wt[kMaxCtas];  // [part], or [part][four heads] for sixteen heads
+  __shared__ float4 inv_s[4];
   __shared__ float acc_s[kGroups > 4 ? 4 : kGroups - 1][8][64];
   griddep_launch_dependents();
   const int64_t it = blockIdx.x;
-  const int hc = blockIdx.y >> 2, mt = blockIdx.y & 3;
+  const int mt = blockIdx.y & 3;
+  int hc = blockIdx.y >> 2;
   const int64_t q = a.ng == 2 ? it >> 1 : it;
   const int hg = a.ng == 2 ? (int)(it & 1) : 0;
-  const int h0 = 64 * hg + 4 * hc;  // first of the four heads
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pair = tid & 63, grp = tid >> 6;
   const int seq = a.q_seq[q];
-  const bool live = h0 < a.H && seq >= 0 && seq < a.cache.B;
+  const bool live = 64 * hg + 4 * hc < a.H && seq >= 0 && seq < a.cache.B;
   griddep_wait();
   if (!live) return;
   const int2 rec = a.rec[it];
   if (rec.x < 0) return;
   const int n = min(rec.y - rec.x + 1, kMaxCtas);
+  const bool sixteen = kGroups == 4 && n <= kAhead;
+  if (sixteen && (hc & 3) != 0) return;
   auto part = [&](int s) -> int64_t { return 2 * (int64_t)(rec.x + s) + (s == 0 ? 1 : 0); };
-  const int pair = tid & 63, grp = tid >> 6;
+  const int hcl = sixteen ? grp : 0;            // this thread's four heads of the CTA's
+  const int s_beg = sixteen ? 0 : grp, s_step = sixteen ? 1 : kGroups;
+  hc += hcl;
+  const bool mine = 64 * hg + 4 * hc < a.H && 4 * hc < hp;
   const float* src = a.part + (mt * (hp / 4) + hc) * 512 + pair * 8;
   float4 x[kAhead], y[kAhead];
   auto load = [&](int s0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int s = s0 + i * kGroups;
-      if (s < n) {
+      const int s = s0 + i * s_step;
+      if (s < n && mine) {
         const float4* p = reinterpret_cast<const float4*>(src + part(s) * (int64_t)(hp * kDLat));
         x[i] = __ldcs(p);
         y[i] = __ldcs(p + 1);
       }
     }
   };
-  load(grp);
-  if (warp < 4) {
-    const int h = 4 * hc + warp;
-    const bool there = h0 + warp < a.H;
-    const float sink = a.sink && there ? a.sink[h0 + warp] * kLog2e : -INFINITY;
+  load(s_beg);
+  // weights and 1 / Z of a head by one warp
+  for (int hh = warp; hh < (sixteen ? 16 : 4); hh += 2 * kGroups) {
+    const int hb = 4 * (hc - hcl) + hh, hq = 64 * hg + hb;
+    const bool there = hq < a.H && hb < hp;
+    const float sink = a.sink && there ? a.sink[hq] * kLog2e : -INFINITY;
     float m[(kMaxCtas + 31) / 32], M = sink;
 #pragma unroll
     for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) {
       const int s = lane + 32 * i;
-      m[i] = s < n && there ? a.pstat[part(s) * (3 * hp) + h] : -INFINITY;
+      m[i] = s < n && there ? a.pstat[part(s) * (3 * hp) + hb] : -INFINITY;
       M = fmaxf(M, m[i]);
     }
     M = lanes_max<32>(M);
@@ -1196,10 +1224,10 @@ __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs 
     for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) {
       const int s = lane + 32 * i;
       if (s < n) {
-        const float* st = a.pstat + part(s) * (3 * hp) + h;
         const float w = there ? ex2(m[i] - Mf) : 0.f;
-        reinterpret_cast<float*>(&wt[s])[warp] = w;
+        reinterpret_cast<float*>(&wt[sixteen ? 4 * s + (hh >> 2) : s])[hh & 3] = w;
         if (there) {
+          const float* st = a.pstat + part(s) * (3 * hp) + hb;
           l = fmaf(w, st[hp], l);
           r = fmaf(w, st[2 * hp], r);
         }
@@ -1214,54 +1242,50 @@ __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs 
     l += sk;
     r += sk;
     if (lane == 0) {
-      inv[warp] = r > 0.f || r != r ? 1.f / r : 0.f;
+      reinterpret_cast<float*>(inv_s)[hh] = r > 0.f || r != r ? 1.f / r : 0.f;
       if (a.lse && mt == 0 && there)
-        a.lse[q * a.H + h0 + warp] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
+        a.lse[q * a.H + hq] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
     }
   }
   __syncthreads();
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s0 = grp; s0 < n; s0 += kAhead * kGroups) {
+  for (int s0 = s_beg; s0 < n; s0 += kAhead * s_step) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int s = s0 + i * kGroups;
-      if (s < n) {
-        const float4 w = wt[s];
-        acc[0] = fmaf(x[i].x, w.x, acc[0]);
-        acc[1] = fmaf(x[i].y, w.y, acc[1]);
-        acc[2] = fmaf(x[i].z, w.z, acc[2]);
-        acc[3] = fmaf(x[i].w, w.w, acc[3]);
-        acc[4] = fmaf(y[i].x, w.x, acc[4]);
-        acc[5] = fmaf(y[i].y, w.y, acc[5]);
-        acc[6] = fmaf(y[i].z, w.z, acc[6]);
-        acc[7] = fmaf(y[i].w, w.w, acc[7]);
+      const int s = s0 + i * s_step;
+      if (s < n && mine) join_add(acc, x[i], y[i], wt[sixteen ? 4 * s + hcl : s]);
+    }
+    load(s0 + kAhead * s_step);
+  }
+  if (!sixteen) {
+    // the groups' sums: sixteen fold into four through shared memory, four into one
+#pragma unroll
+    for (int top = kGroups; top > 1; top >>= 2) {
+      const int low = top / 4;  // groups that remain
+#pragma unroll
+      for (int k = 1; k < 4; ++k) {
+        if (grp >= k * low && grp < (k + 1) * low) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc_s[grp - k * low][i][pair] = acc[i];
+        }
+        __syncthreads();
+        if (grp < low) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] += acc_s[grp][i][pair];
+        }
+        __syncthreads();
       }
     }
-    load(s0 + kAhead * kGroups);
+    if (grp > 0) return;
   }
-  // the groups' sums: sixteen fold into four through shared memory, four into one
-#pragma unroll
-  for (int top = kGroups; top > 1; top >>= 2) {
-    const int low = top / 4;  // groups that remain
-#pragma unroll
-    for (int k = 1; k < 4; ++k) {
-      if (grp >= k * low && grp < (k + 1) * low) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc_s[grp - k * low][i][pair] = acc[i];
-      }
-      __syncthreads();
-      if (grp < low) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += acc_s[grp][i][pair];
-      }
-      __syncthreads();
-    }
-  }
-  if (grp > 0) return;
+  if (!mine) return;
   const int d = mt * 128 + 2 * pair;
   float cs = 1.f, sn = 0.f;
   if (a.inv_freq && d >= kRopeDim0)
     sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), (uint64_t)a.q_pos[q]), &sn, &cs);
+  const float4 iv = inv_s[hcl];
+  const float inv[4] = {iv.x, iv.y, iv.z, iv.w};
+  const int h0 = 64 * hg + 4 * hc;
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
     if (h0 + h >= a.H) break;
