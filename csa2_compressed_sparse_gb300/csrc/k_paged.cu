@@ -200,8 +200,8 @@ struct __align__(16) PagedAux {
   int64_t it0;          // first item of this CTA and the units before it within the item
   int64_t it0_unit;
   float fac[64];        // rescale factor or 1 / sum, per head
-  float top[2][64];     // largest score above the running maximum, by half of the rows
-  float lsum[2][64], rsum[2][64];  // sums of P by half: unrounded, rounded
+  float top[4][64];     // largest score above the running maximum, by part of the rows
+  float lsum[4][64], rsum[4][64];  // sums of P by part: unrounded, rounded
   float m_run[64], sink2[64];
   float rope_c[32], rope_s[32];
   uint32_t tmem_slot;
@@ -213,7 +213,14 @@ struct __align__(16) PagedAux {
 template <int kHp, int kMode>
 struct PagedCfg {
   static constexpr bool kScaled = kMode == 1;
-  static constexpr int kThreads = kMode == 0 ? 512 : 896;
+  // softmax warps: kParts of four, each with 64 / kParts rows of a tile
+  static constexpr int kParts = 2;
+  static constexpr int kSoft = 128 * kParts;         // softmax threads
+  static constexpr int kWarpS = 4 * kParts;          // two warps issue S,
+  static constexpr int kWarpO = kWarpS + 2;          // two O^T,
+  static constexpr int kWarpL = kWarpS + 4;          // the rest load
+  static constexpr int kLoadWarps = kMode == 0 ? 4 : 8;
+  static constexpr int kThreads = 32 * (kWarpL + kLoadWarps);
   static constexpr int kQBlock = kHp * 128;
   static constexpr int kQBytes = 8 * kQBlock;
   static constexpr int kPBytes = kHp * 128 * (kScaled ? 4 : 1);
@@ -231,14 +238,39 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Wait for a phase; false once something in the CTA has given up.  The flag is read only while
+// the phase is incomplete: a read of shared memory takes some hundred cycles while the tensor
+// core's operand reads fill it, and the waits stand on the path from scores to values.
+__device__ __forceinline__ bool wait_phase(PagedAux& X, uint64_t& bar, uint32_t parity) {
+  const uint32_t b = smem_u32(&bar);
+  if (mbar_try_wait(b, parity)) return true;
+  const volatile int* abort = &X.abort;
+  if (*abort) return false;
+  if (mbar_wait(b, parity)) return true;
+  X.abort = 1;
+  return false;
+}
+
+// Four 8 x 8 matrices of 16-bit values: thread t holds (t / 4, 2 (t % 4) + {0, 1}) of each; lane
+// 8 i + r gives the address of row r of matrix i.
+__device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+template <int kSoft>
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory");
+}
+template <int kSoft>
 __device__ __forceinline__ bool soft_any(bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
-      "bar.red.or.pred po, 1, 256, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      "bar.red.or.pred po, 1, %2, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)pred)
+      : "r"((uint32_t)pred), "n"(kSoft)
       : "memory");
   return r != 0;
 }
@@ -271,6 +303,20 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
+  tmem_ld_16x256b_x4(taddr, r);
+}
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[8]) {
+  tmem_ld_16x256b_x2(taddr, r);
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -421,22 +467,22 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     prefetch_tensormap(&qmap);
     if (kMode == 0) prefetch_tensormap(&kmap);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&X.full[s]), kMode == 0 ? 1 : 16);
+      mbar_init(smem_u32(&X.full[s]), kMode == 0 ? 1 : C::kLoadWarps);
       mbar_init(smem_u32(&X.empty[s]), 1);
     }
     mbar_init(smem_u32(&X.q_full), 1);
     mbar_init(smem_u32(&X.q_empty), 2);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&X.s_full[b]), 2);
-      mbar_init(smem_u32(&X.s_empty[b]), 8);
+      mbar_init(smem_u32(&X.s_full[b]), 4);
+      mbar_init(smem_u32(&X.s_empty[b]), C::kWarpS);
     }
     for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&X.fin[b]), 1);
-    mbar_init(smem_u32(&X.p_full), 8);
+    mbar_init(smem_u32(&X.p_full), C::kWarpS);
     mbar_init(smem_u32(&X.pv_done), 2);
     X.abort = 0;
     mbar_fence_init();
   }
-  if (warp == 8) {
+  if (warp == C::kWarpS) {
     tmem_alloc(smem_u32(&X.tmem_slot), 512);
     tmem_relinquish();
   }
@@ -488,11 +534,12 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   const uint32_t tmem = X.tmem_slot;
 
   if (u1 > u0) {
-    if (warp < 8) {
+    if (warp < C::kWarpS) {
       // ================= softmax, rescale, output =================
-      // Warp w and w + 4 hold heads 16 w .. 16 w + 15 (TMEM lanes 32 w ..), rows 0..31 and
-      // 32..63 of a tile; thread t the heads hA = 16 w + t / 4 and hB = hA + 8 and of its rows
-      // 8 g + 2 (t % 4) + {0, 1}, g = 0..3.
+      // Warp w holds heads 16 (w % 4) .. + 15 (TMEM lanes 32 (w % 4) ..) and rows kRows (w / 4) ..
+      // of a tile; thread t the heads hA = 16 (w % 4) + t / 4 and hB = hA + 8 and of its rows
+      // 8 g + 2 (t % 4) + {0, 1}, g < kG.
+      constexpr int kParts = C::kParts, kRows = 64 / kParts, kG = kRows / 8;
       const int quad = warp & 3, half = warp >> 2, r4 = lane & 3;
       const int hA = 16 * quad + (lane >> 2), hB = hA + 8;
       const bool on = 16 * quad < kHp;  // this warp's 16 heads exist
@@ -519,7 +566,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           X.sink2[hA] = mA;
           X.sink2[hB] = mB;
         }
-        if (whole && a.inv_freq && warp == 7) {
+        if (whole && a.inv_freq && warp == C::kWarpS - 1) {
           float s, cs;
           sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
           X.rope_c[lane] = cs;
@@ -530,32 +577,24 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           const uint32_t sphase = C::kScaled ? (uint32_t)c & 1 : (uint32_t)(c >> 1) & 1;
           // P's buffer and O^T are free once the previous tile's products are done, which they
           // are before this tile's scores except when the tensor core is the limit
-          if (c > 0 && !X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1))
-            X.abort = 1;
-          if (!X.abort && !mbar_wait(smem_u32(&X.s_full[sb]), sphase)) X.abort = 1;
-          // the tile has landed (S read it); waiting for that here too makes what its loader
-          // wrote visible: the mask (first quarter), the scales (all of them)
-          auto landed = [&](int k) {
-            const int i = sl + k;
-            const uint32_t ph = i >= NS ? sph ^ 1 : sph;
-            if (!X.abort && !mbar_wait(smem_u32(&X.full[i >= NS ? i - NS : i]), ph)) X.abort = 1;
-          };
-          landed(0);
-          if (C::kScaled) { landed(1); landed(2); landed(3); }
+          if (c > 0) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+          // the scores, and with them (the issuers have seen the tile land and arrive here too)
+          // the mask and the scales that its loader wrote
+          wait_phase(X, X.s_full[sb], sphase);
           tc_fence_after();
           const uint64_t mask = kMode == 0 ? X.mask[c & 3] : gather_nibbles(X.nib[c & 3]);
           const bool all = mask == ~0ull;
-          // bit 8 g: row 8 g + 2 r4 of this half, bit 8 g + 1 the one after it
-          const uint32_t mk = (uint32_t)(mask >> (32 * half + 2 * r4));
-          float2 xA[4], xB[4];
+          // bit 8 g: row 8 g + 2 r4 of this part, bit 8 g + 1 the one after it
+          const uint32_t mk = (uint32_t)(mask >> (kRows * half + 2 * r4));
+          float2 xA[kG], xB[kG];
           if (on) {
             if (!C::kScaled) {
-              uint32_t x[16], y[16];
-              tmem_ld_16x256b_x4(tmem + lrow + 128 * sb + 32 * half, x);
-              tmem_ld_16x256b_x4(tmem + lrow + 128 * sb + 64 + 32 * half, y);
+              uint32_t x[4 * kG], y[4 * kG];
+              tmem_ld_rows(tmem + lrow + 128 * sb + kRows * half, x);
+              tmem_ld_rows(tmem + lrow + 128 * sb + 64 + kRows * half, y);
               tmem_ld_wait();
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
+              for (int g = 0; g < kG; ++g) {
                 xA[g] = add2(make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1])),
                              make_float2(__uint_as_float(y[4 * g]), __uint_as_float(y[4 * g + 1])));
                 xB[g] =
@@ -563,22 +602,24 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                          make_float2(__uint_as_float(y[4 * g + 2]), __uint_as_float(y[4 * g + 3])));
               }
             } else {
+              uint32_t x[4][4 * kG];
 #pragma unroll
-              for (int g = 0; g < 4; ++g) xA[g] = xB[g] = make_float2(0.f, 0.f);
+              for (int k = 0; k < 4; ++k) tmem_ld_rows(tmem + lrow + 64 * k + kRows * half, x[k]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int g = 0; g < kG; ++g) xA[g] = xB[g] = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                uint32_t x[16];
-                tmem_ld_16x256b_x4(tmem + lrow + 64 * k + 32 * half, x);
-                tmem_ld_wait();
-                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 32 * half + 2 * r4;
+                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + kRows * half + 2 * r4;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < kG; ++g) {
                   const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
-                  xA[g] = fma2(make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1])),
-                               f, xA[g]);
+                  xA[g] = fma2(
+                      make_float2(__uint_as_float(x[k][4 * g]), __uint_as_float(x[k][4 * g + 1])), f,
+                      xA[g]);
                   xB[g] = fma2(
-                      make_float2(__uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3])), f,
-                      xB[g]);
+                      make_float2(__uint_as_float(x[k][4 * g + 2]), __uint_as_float(x[k][4 * g + 3])),
+                      f, xB[g]);
                 }
               }
             }
@@ -588,8 +629,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           if (lane == 0) mbar_arrive(smem_u32(&X.s_empty[sb]));
           // P = 2^(score - m), m the running maximum (no score yet: 0); the largest exponent
           // met and the sums of P
-          uint32_t pa[4], pb[4];
-          float2 eA[4], eB[4];
+          uint32_t pa[kG], pb[kG];
+          float2 eA[kG], eB[kG];
           float tA, tB;
           float2 sA, sB, uA, uB;
           auto weights = [&]() {
@@ -597,7 +638,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             tA = tB = -INFINITY;
             sA = sB = uA = uB = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < kG; ++g) {
               float2 y = fma2(xA[g], make_float2(sc2, sc2), make_float2(nA, nA));
               float2 z = fma2(xB[g], make_float2(sc2, sc2), make_float2(nB, nB));
               if (!all) {
@@ -629,7 +670,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             need = (hA < Hg && (tA > kLazy || (mA == -INFINITY && tA > -INFINITY))) ||
                    (hB < Hg && (tB > kLazy || (mB == -INFINITY && tB > -INFINITY)));
           }
-          if (soft_any(need)) {
+          if (soft_any<C::kSoft>(need)) {
             // a head's maximum moves: the largest exponent of its rows in both halves
             if (on) {
               tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, 1));
@@ -641,11 +682,16 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                 X.top[half][hB] = tB;
               }
             }
-            soft_sync();
+            soft_sync<C::kSoft>();
             float fA = 1.f, fB = 1.f;
             if (on) {
-              tA = fmaxf(X.top[0][hA], X.top[1][hA]);
-              tB = fmaxf(X.top[0][hB], X.top[1][hB]);
+              tA = X.top[0][hA];
+              tB = X.top[0][hB];
+#pragma unroll
+              for (int i = 1; i < kParts; ++i) {
+                tA = fmaxf(tA, X.top[i][hA]);
+                tB = fmaxf(tB, X.top[i][hB]);
+              }
               if (tA > kLazy || (mA == -INFINITY && tA > -INFINITY)) {
                 fA = mA == -INFINITY ? 0.f : ex2(-tA);
                 mA = mA == -INFINITY ? tA : mA + tA;
@@ -665,11 +711,11 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               rB = fma2(rB, qB, o0);
               weights();
             }
-            soft_sync();  // fac is written
+            soft_sync<C::kSoft>();  // fac is written
             if (t > w.t) {
               tc_fence_after();
 #pragma unroll 1
-              for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
+              for (int mt = half; mt < 4; mt += kParts) {
 #pragma unroll 1
                 for (int hb = 0; hb < kHp; hb += 16) {
                   uint32_t v[16];
@@ -684,7 +730,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               }
               tmem_st_wait();
             }
-            soft_sync();  // fac and top are read by all before a later tile writes them
+            soft_sync<C::kSoft>();  // fac and top are read by all before a later tile writes them
           }
           if (on) {
             lA = add2(lA, sA);
@@ -695,30 +741,34 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             }
           }
           if (on) {
-            const int sw = hA & 7;  // hB & 7 is the same
+            // P [head][64 rows], 128-byte swizzled: matrix i is this part's rows 8 i .. of eight
+            // heads
+            static_assert(kG == 4, "a warp's rows are four matrices");
+            const int hr = 16 * quad + (lane & 7);
+            const uint32_t pA = p_s + hr * 128 + (((kG * half + (lane >> 3)) ^ (lane & 7)) << 4);
 #pragma unroll
             for (int k = 0; k < (C::kScaled ? 4 : 1); ++k) {
-              const uint32_t pA = p_s + k * (kHp * 128) + hA * 128 + 4 * r4, pB = pA + 8 * 128;
-              const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + 32 * half + 2 * r4;
+              if (C::kScaled) {
+                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + kRows * half + 2 * r4;
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                if (C::kScaled) {
+                for (int g = 0; g < kG; ++g) {
                   const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
                   pa[g] = pack_bf16x2(eA[g].x * f.x, eA[g].y * f.y);
                   pb[g] = pack_bf16x2(eB[g].x * f.x, eB[g].y * f.y);
                 }
-                st_shared32(pA + (((4 * half + g) ^ sw) << 4), pa[g]);
-                st_shared32(pB + (((4 * half + g) ^ sw) << 4), pb[g]);
               }
+              store_matrices(pA + k * (kHp * 128), pa);
+              store_matrices(pA + k * (kHp * 128) + 8 * 128, pb);
             }
           }
           if (kMode == 0 && !all) {
             // rows outside the item: whatever the page holds there must not meet P's zeros
-            landed(1);
-            landed(2);
-            landed(3);
+            for (int k = 0; k < 4; ++k) {  // the copies themselves, too, are complete
+              const int i = sl + k;
+              wait_phase(X, X.full[i >= NS ? i - NS : i], i >= NS ? sph ^ 1 : sph);
+            }
             const int piece = tid & 63;
-            for (int r = tid >> 6; r < 64; r += 4) {
+            for (int r = tid >> 6; r < 64; r += C::kSoft / 64) {
               if ((mask >> r) & 1) continue;
               int s = sl + (piece >> 4);
               if (s >= NS) s -= NS;
@@ -755,9 +805,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           }
         }
         const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
-        soft_sync();
+        soft_sync<C::kSoft>();
         if (tid < Hg) {
-          float l = X.lsum[0][tid] + X.lsum[1][tid], r = X.rsum[0][tid] + X.rsum[1][tid];
+          float l = X.lsum[0][tid], r = X.rsum[0][tid];
+#pragma unroll
+          for (int i = 1; i < kParts; ++i) {
+            l += X.lsum[i][tid];
+            r += X.rsum[i][tid];
+          }
           const float m = X.m_run[tid];
           if (whole) {
             const float sk = X.sink2[tid];
@@ -781,13 +836,13 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           a.rec[w.it] = whole ? make_int2(-1, -1)
                               : make_int2((int)blockIdx.x, (int)(((ul + 1) * ncta - 1) / U));
         }
-        if (!X.abort && !mbar_wait(smem_u32(&X.pv_done), (uint32_t)(c - 1) & 1)) X.abort = 1;
+        wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
         tc_fence_after();
-        soft_sync();
+        soft_sync<C::kSoft>();
         if (whole) {
           uint16_t* out = a.out + (w.i.q * a.H + 64 * w.i.hg) * kDLat;
 #pragma unroll 1
-          for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
+          for (int mt = half; mt < 4; mt += kParts) {
             const int d = mt * 128 + quad * 32 + lane;
             const bool rot = a.inv_freq && d >= kRopeDim0;  // uniform in a warp
             const float cs = rot ? X.rope_c[(d - kRopeDim0) >> 1] : 1.f;
@@ -825,7 +880,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           // [dim tile][four heads][128 dims][4]: a lane writes 16 bytes, a warp 512
           float* po = a.part + part * (int64_t)(kHp * kDLat) + (quad * 32 + lane) * 4;
 #pragma unroll 1
-          for (int mt = 2 * half; mt < 2 * half + 2; ++mt) {
+          for (int mt = half; mt < 4; mt += kParts) {
 #pragma unroll 1
             for (int hb = 0; hb < Hg; hb += 16) {
               uint32_t v[16];
@@ -839,14 +894,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           }
         }
         tc_fence_before();
-        soft_sync();  // fac, the sums and the rotation are read before the next segment's
+        soft_sync<C::kSoft>();  // fac, the sums and the rotation are read before the next segment's
         u += w.seg_units;
       } while (walk_next(a, w));
-    } else if (warp < 10) {
-      // ================= S products (warp 8 also loads each segment's Q) =================
-      // Of each quarter, warp 8 + r multiplies dim block r; scaled rows keep a quarter in one
+    } else if (warp < C::kWarpO) {
+      // ================= S products (the first warp also loads each segment's Q) =============
+      // Of each quarter, warp r multiplies dim block r; scaled rows keep a quarter in one
       // accumulator, so there the warps take turns at the quarters.
-      const int r = warp - 8;
+      const int r = warp - C::kWarpS;
       if (lane == 0) {
         Walk w;
         walk_start(a, X, u1 - u0, w);
@@ -860,7 +915,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         do {
           if (r == 0) {
             // the products of the segment before it have read Q
-            ok = n == 0 || (!X.abort && mbar_wait(smem_u32(&X.q_empty), (n - 1) & 1));
+            ok = n == 0 || wait_phase(X, X.q_empty, (n - 1) & 1);
             if (ok) {
               mbar_arrive_expect_tx(qf, C::kQBytes);
 #pragma unroll
@@ -870,21 +925,23 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               asked = true;
             }
           }
-          ok = ok && !X.abort && mbar_wait(qf, n & 1);
+          ok = ok && wait_phase(X, X.q_full, n & 1);
           if (ok) asked = false;
           ++n;
           for (int t = w.t; ok && t < w.t_end; ++t, ++c) {
             const int sb = C::kScaled ? 0 : c & 1;
             const int lag = C::kScaled ? 1 : 2;
             if (c >= lag)
-              ok = mbar_wait(smem_u32(&X.s_empty[sb]),
-                             C::kScaled ? (uint32_t)(c - 1) & 1 : (uint32_t)((c - 2) >> 1) & 1);
+              ok = wait_phase(X, X.s_empty[sb],
+                              C::kScaled ? (uint32_t)(c - 1) & 1 : (uint32_t)((c - 2) >> 1) & 1);
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (!C::kScaled || (k & 1) == r) {
-                ok = ok && mbar_wait(smem_u32(&X.full[sl]), sph);
+                ok = ok && wait_phase(X, X.full[sl], sph);
                 if (!ok) break;
+                // the tile's mask came with its first quarter, the scales with each
+                if (k == (C::kScaled ? 2 + r : 0)) mbar_arrive(smem_u32(&X.s_full[sb]));
                 tc_fence_after();
                 const uint32_t d = tmem + (C::kScaled ? 64 * k : 128 * sb + 64 * r);
                 const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
@@ -915,9 +972,9 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         umma_commit(smem_u32(&X.fin[r]));
         mbar_wait(smem_u32(&X.fin[r]), 0, 100000000ull);
       }
-    } else if (warp < 12) {
-      // ================= O^T products: warp 10 + r tiles 2 r and 2 r + 1 =================
-      const int r = warp - 10;
+    } else if (warp < C::kWarpL) {
+      // ================= O^T products: warp r tiles 2 r and 2 r + 1 =================
+      const int r = warp - C::kWarpO;
       if (lane == 0) {
         Walk w;
         walk_start(a, X, u1 - u0, w);
@@ -927,7 +984,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         bool ok = true;
         do {
           for (int t = w.t; t < w.t_end; ++t, ++c) {
-            ok = !X.abort && mbar_wait(smem_u32(&X.p_full), (uint32_t)c & 1);
+            ok = wait_phase(X, X.p_full, (uint32_t)c & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -952,8 +1009,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         mbar_wait(smem_u32(&X.fin[2 + r]), 0, 100000000ull);
       }
     } else if (kMode == 0) {
-      // ================= bf16 rows by tensor copies: warp 12 + k quarter k =================
-      const int k = warp - 12;
+      // ================= bf16 rows by tensor copies: warp k quarter k =================
+      const int k = warp - C::kWarpL;
       griddep_wait();  // rows and table entries may come from the kernel before this one
       Walk w;
       walk_start(a, X, u1 - u0, w);
@@ -991,7 +1048,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             const int32_t z = __shfl_sync(0xFFFFFFFFu, pz, src + cl);
             const uint64_t mk = __shfl_sync(0xFFFFFFFFu, m, src);
             const uint32_t bar = smem_u32(&X.full[sl]);
-            if (again) ok = !X.abort && mbar_wait(smem_u32(&X.empty[sl]), ph ^ 1);
+            if (again) ok = wait_phase(X, X.empty[sl], ph ^ 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (lane == 0) {
@@ -1018,28 +1075,29 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       }
     } else {
       // ================= FP8 rows through registers =================
-      // Thread t of 512: row t / 8 of a tile, 16 dims of each quarter (piece t % 8).  A tile's
-      // codes are loaded while the tile before it is converted, its page looked up one
-      // tile earlier still.
+      // Thread t of 256: rows t / 8 and 32 + t / 8 of a tile, 16 dims of each quarter (piece
+      // t % 8).  A quarter's registers are loaded for the next tile as soon as this tile's
+      // codes are converted, so three to four quarters are always in flight; the pages are
+      // looked up one tile earlier still.
       griddep_wait();
-      const int t512 = tid - 384, r = t512 >> 3, pc = t512 & 7;
+      const int t256 = tid - 32 * C::kWarpL, r = t256 >> 3, pc = t256 & 7;
       Walk w;
       walk_start(a, X, u1 - u0, w);
-      int tn = w.t;            // next tile to look up
+      int tn = w.t;  // next tile to look up
       bool more = true;
-      auto look = [&](const uint8_t*& src) -> bool {  // false: no further tile
-        src = nullptr;
+      // The pages and rows within them of the next tile's two rows (row -1: none); false: no
+      // further tile.
+      auto look = [&](int (&page)[2], int (&row)[2]) -> bool {
+        page[0] = page[1] = row[0] = row[1] = -1;
         if (!more) return false;
-        const int64_t r0 = ((int64_t)w.i.tile0 + tn) * 64;
-        const int64_t row = r0 + r;
-        if (row >= w.i.lo && row < w.i.hi) {
-          const int32_t lp = (int32_t)row / a.cache.page_rows;
-          const int32_t page = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
-          if (page >= 0 && page < a.cache.n_pages)
-            src = a.cache.data + (int64_t)page * a.cache.page_stride +
-                  (int64_t)((int32_t)row - lp * a.cache.page_rows) * 528;
-          else if (pc == 0)
-            raise_fault(kFaultBounds);
+        const int64_t r0 = ((int64_t)w.i.tile0 + tn) * 64 + r;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (r0 + 32 * i >= w.i.lo && r0 + 32 * i < w.i.hi) {
+            const int32_t j = (int32_t)(r0 + 32 * i), lp = j / a.cache.page_rows;
+            row[i] = j - lp * a.cache.page_rows;
+            page[i] = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
+          }
         }
         if (++tn == w.t_end) {
           more = walk_next(a, w);
@@ -1047,68 +1105,90 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         }
         return true;
       };
-      uint4 cur[4], nxt[4], csc, nsc;
-      auto fetch = [&](const uint8_t* src, uint4 (&d)[4], uint4& sc) {
+      // Addresses of the two rows (null: none), and the tile's valid rows among this warp's
+      // eight, four bits each of two bytes.
+      auto place = [&](const int (&page)[2], const int (&row)[2], const uint8_t* (&src)[2]) {
+        uint32_t bits = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) d[k] = make_uint4(0u, 0u, 0u, 0u);
-        sc = make_uint4(0u, 0u, 0u, 0u);
-        if (src) {
+        for (int i = 0; i < 2; ++i) {
+          src[i] = nullptr;
+          if (row[i] >= 0) {
+            if (page[i] >= 0 && page[i] < a.cache.n_pages)
+              src[i] = a.cache.data + (int64_t)page[i] * a.cache.page_stride + (int64_t)row[i] * 528;
+            else if (pc == 0)
+              raise_fault(kFaultBounds);
+          }
+          const uint32_t bal = __ballot_sync(0xFFFFFFFFu, src[i] != nullptr);
+          bits |= ((bal & 1u) | (bal >> 7 & 2u) | (bal >> 14 & 4u) | (bal >> 21 & 8u)) << (8 * i);
+        }
+        return bits;
+      };
+      uint4 buf[2][4];
+      float scl[2][4];  // FP8_S128: the quarter's scale (piece 0 only); FP8_E8M0: the piece's
+      auto fetch = [&](const uint8_t* const (&src)[2], int k) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            d[k] = __ldcs(reinterpret_cast<const uint4*>(src + 128 * k + 16 * pc));
-          if (kMode == 2 || pc == 0) sc = __ldcs(reinterpret_cast<const uint4*>(src + 512));
+        for (int i = 0; i < 2; ++i) {
+          buf[i][k] = make_uint4(0u, 0u, 0u, 0u);
+          scl[i][k] = 0.f;
+          if (src[i]) {
+            buf[i][k] = __ldcs(reinterpret_cast<const uint4*>(src[i] + 128 * k + 16 * pc));
+            if (kMode == 1) {
+              if (pc == 0) scl[i][k] = __ldcs(reinterpret_cast<const float*>(src[i] + 512) + k);
+            } else {
+              scl[i][k] = __uint_as_float((uint32_t)__ldcs(src[i] + 512 + 4 * k + (pc >> 1)));
+            }
+          }
         }
       };
-      const uint8_t *s_cur, *s_nxt = nullptr;
-      bool have = look(s_cur);
-      bool have_nxt = look(s_nxt);
-      fetch(s_cur, cur, csc);
-      bool v_cur = s_cur != nullptr;
+      int page[2], row[2];
+      const uint8_t* src[2];
+      look(page, row);
+      uint32_t bits = place(page, row, src);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) fetch(src, k);
+      bool nxt = look(page, row);
       int sl = 0, c = 0;
-      uint32_t ph = 0, filled = 0;
+      uint32_t ph = 0;
+      bool again = false;
       const uint32_t offr = (r >> 3) * kGroup + (pc >> 2) * kBlock;
       const uint32_t off0 = offr + sw128_off(r & 7, (2 * pc) & 7);
       const uint32_t off1 = offr + sw128_off(r & 7, (2 * pc + 1) & 7);
-      bool ok = true;
-      while (have) {
-        // the next tile's codes, and the page of the one after it
-        if (have_nxt) fetch(s_nxt, nxt, nsc);
-        const bool v_nxt = s_nxt != nullptr;
-        const bool had = have_nxt;
-        have_nxt = look(s_nxt);
-        // valid rows: a warp holds four of them, one ballot bit per row
-        const uint32_t bal = __ballot_sync(0xFFFFFFFFu, v_cur);
+      for (bool have = true; have; ++c) {
+        const uint32_t bits_n = place(page, row, src);  // of the next tile
+        const bool nn = look(page, row);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (filled >> sl & 1) ok = ok && !X.abort && mbar_wait(smem_u32(&X.empty[sl]), ph ^ 1);
-          filled |= 1u << sl;
-          if (k == 0 && lane == 0)
-            reinterpret_cast<uint8_t*>(X.nib[c & 3])[warp - 12] =
-                (uint8_t)((bal & 1u) | (bal >> 7 & 2u) | (bal >> 14 & 4u) | (bal >> 21 & 8u));
-          const uint32_t w4[4] = {cur[k].x, cur[k].y, cur[k].z, cur[k].w};
-          float scale = 1.f;
-          if (kMode == 2) {
-            const uint32_t word = k == 0 ? csc.x : k == 1 ? csc.y : k == 2 ? csc.z : csc.w;
-            scale = e8m0_value((word >> (8 * (pc >> 1))) & 0xFFu);
-          }
-          uint32_t packed[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-                  (__nv_fp8x2_storage_t)((w4[j] >> (16 * hh)) & 0xFFFFu), __NV_E4M3);
-              float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-              if (kMode == 2) { f.x *= scale; f.y *= scale; }
-              packed[2 * j + hh] = pack_bf16x2(f.x, f.y);
-            }
+          if (again) wait_phase(X, X.empty[sl], ph ^ 1);
+          if (k == 0 && lane == 0) {
+            uint8_t* nb = reinterpret_cast<uint8_t*>(X.nib[c & 3]) + (warp - C::kWarpL);
+            nb[0] = (uint8_t)bits;
+            nb[8] = (uint8_t)(bits >> 8);
           }
           const uint32_t base = ring + sl * kSlotBytes;
-          st_shared16(base + off0, make_uint4(packed[0], packed[1], packed[2], packed[3]));
-          st_shared16(base + off1, make_uint4(packed[4], packed[5], packed[6], packed[7]));
-          if (kMode == 1 && pc == 0)
-            sc_s[((c & 3) * 4 + k) * 64 + r] =
-                __uint_as_float(k == 0 ? csc.x : k == 1 ? csc.y : k == 2 ? csc.z : csc.w);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w4[4] = {buf[i][k].x, buf[i][k].y, buf[i][k].z, buf[i][k].w};
+            const float scale = kMode == 2 ? e8m0_value(__float_as_uint(scl[i][k])) : 1.f;
+            uint32_t packed[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)((w4[j] >> (16 * hh)) & 0xFFFFu), __NV_E4M3);
+                float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                if (kMode == 2) { f.x *= scale; f.y *= scale; }
+                packed[2 * j + hh] = pack_bf16x2(f.x, f.y);
+              }
+            }
+            // rows 32 on: four groups of 8 rows further
+            st_shared16(base + 4 * kGroup * i + off0,
+                        make_uint4(packed[0], packed[1], packed[2], packed[3]));
+            st_shared16(base + 4 * kGroup * i + off1,
+                        make_uint4(packed[4], packed[5], packed[6], packed[7]));
+            if (kMode == 1 && pc == 0) sc_s[((c & 3) * 4 + k) * 64 + r + 32 * i] = scl[i][k];
+          }
+          if (nxt) fetch(src, k);
           if (k & 1) {  // one fence for two quarters
             fence_proxy_async_smem();
             __syncwarp();
@@ -1117,16 +1197,12 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               mbar_arrive(smem_u32(&X.full[sl]));
             }
           }
-          if (++sl == NS) { sl = 0; ph ^= 1; }
+          if (++sl == NS) { sl = 0; ph ^= 1; again = true; }
         }
-        ++c;
-        have = had;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cur[k] = nxt[k];
-        csc = nsc;
-        v_cur = v_nxt;
+        have = nxt;
+        nxt = nn;
+        bits = bits_n;
       }
-      if (!ok) X.abort = 1;
     }
   }
   // a CTA without work must not let the grid complete before what precedes it has
@@ -1134,7 +1210,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == C::kWarpS) tmem_dealloc(tmem, 512);
 }
 
 // ================================ join ===================================================
