@@ -164,16 +164,14 @@ __global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppen
 //            warps 12..27, which load FP8 rows into registers a tile ahead and store them as
 //            bf16.  A tensor copy takes its warp 50 to 100 cycles to issue, so one warp alone
 //            held the tile rate to 3200 cycles (a tile of HBM time per SM is 2800)
-//   S        warps 8 and 9: Q[64 x 512] . X^T, a quarter as it lands, a dim block each into
-//            accumulators of their own; head h in TMEM lane 32 (h / 16) + h % 16, column = row
+//   S        warp 8: Q[64 x 512] . X^T, a quarter as it lands; head h in TMEM lane
+//            32 (h / 16) + h % 16, column = row
 //   softmax  warps 0..7, half of the rows each four: P = 2^(s - m) with the running maximum m,
 //            which moves only when a score exceeds it by more than 2^64 (P <= 2^64 keeps bf16
 //            P and fp32 sums finite), so a tile's usual pass needs no maximum across threads,
 //            one vote only
-//   O^T     += X^T[512 x 64] . P^T: warps 10 and 11, four M = 128 tiles of dims, each releasing
-//            its slot, so the quarter of a later tile starts to load while this one is finished
-// (One thread issues an MMA of these sizes about every 47 cycles; the operands' reads from
-// shared memory, 128 bytes a cycle, allow an S product every 32.  So two issue each kind.)
+//   O^T     += X^T[512 x 64] . P^T: warp 9, four M = 128 tiles of dims, each releasing its
+//            slot, so the quarter of a later tile starts to load while this one is finished
 // Rows outside lo .. hi - 1 or on a bad page get P = 0 and are zeroed before the product
 // (what the page holds there may be NaN).
 //
@@ -191,8 +189,8 @@ struct __align__(16) PagedAux {
   uint64_t full[12], empty[12];  // ring slots
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_full, pv_done;
-  uint64_t fin[4];
+  uint64_t p_full[4], pv_done;  // p_full: a P per quarter of scaled rows, else [0]
+  uint64_t fin[2];
   uint64_t mask[4];     // valid rows of tile c at c & 3 (bf16 rows)
   uint32_t nib[4][4];   // the same for FP8 rows: four rows' bits in each byte
   int64_t sums[32];     // scan of the plan
@@ -216,14 +214,18 @@ struct PagedCfg {
   // softmax warps: kParts of four, each with 64 / kParts rows of a tile
   static constexpr int kParts = 2;
   static constexpr int kSoft = 128 * kParts;         // softmax threads
-  static constexpr int kWarpS = 4 * kParts;          // two warps issue S,
-  static constexpr int kWarpO = kWarpS + 2;          // two O^T,
-  static constexpr int kWarpL = kWarpS + 4;          // the rest load
-  static constexpr int kLoadWarps = kMode == 0 ? 4 : 8;
+  static constexpr int kWarpS = 4 * kParts;          // a warp issues S,
+  static constexpr int kWarpO = kWarpS + 1;          // one O^T, one loads Q,
+  static constexpr int kWarpQ = kWarpS + 2;
+  static constexpr int kWarpL = kWarpS + 4;          // the others load rows (one is spare)
+  static constexpr int kLoadWarps = kMode == 0 ? 4 : 16;
   static constexpr int kThreads = 32 * (kWarpL + kLoadWarps);
   static constexpr int kQBlock = kHp * 128;
   static constexpr int kQBytes = 8 * kQBlock;
-  static constexpr int kPBytes = kHp * 128 * (kScaled ? 4 : 1);
+  // P: one buffer; scaled rows have a P per quarter, the fourth in the first one's buffer (its
+  // products are nearly done by then), which leaves room for an eighth slot
+  static constexpr int kPBufs = kScaled ? 3 : 1;
+  static constexpr int kPBytes = kHp * 128 * kPBufs;
   static constexpr int kScBytes = kScaled ? 4 * 4 * 64 * 4 : 0;  // [tile & 3][quarter][row]
   static constexpr int kFree =
       (kMaxSmem - 1024 - kQBytes - kPBytes - kScBytes - (int)sizeof(PagedAux)) / kSlotBytes;
@@ -250,6 +252,17 @@ __device__ __forceinline__ bool wait_phase(PagedAux& X, uint64_t& bar, uint32_t 
   X.abort = 1;
   return false;
 }
+
+// One lane of the warp, and values that the compiler may take to be the same in all of it.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+__device__ __forceinline__ bool all_ok(bool x) { return __all_sync(0xFFFFFFFFu, x); }
 
 // Four 8 x 8 matrices of 16-bit values: thread t holds (t / 4, 2 (t % 4) + {0, 1}) of each; lane
 // 8 i + r gives the address of row r of matrix i.
@@ -303,20 +316,6 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
-  tmem_ld_16x256b_x4(taddr, r);
-}
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[8]) {
-  tmem_ld_16x256b_x2(taddr, r);
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -391,24 +390,24 @@ __device__ __forceinline__ Item load_item(const PagedAttnArgs& a, int64_t it, bo
 
 // A CTA's walk over its segments: item it, tiles t .. t_end - 1 of it.
 struct Walk {
-  int64_t it;      // item
+  int it;          // item
   int64_t left;    // units of this CTA from this segment on
-  int64_t unit;    // unit within the item where the segment begins
+  int unit;        // unit within the item where the segment begins
   Item i;
   int t, t_end;    // tiles of the segment, relative to i.tile0
   int seg_units;
 };
 __device__ __forceinline__ void walk_fit(const PagedAttnArgs& a, Walk& w) {
-  const int64_t rest = w.i.units - w.unit;
-  w.seg_units = (int)(rest < w.left ? rest : w.left);
-  w.t = (int)w.unit * a.ut;
-  const int e = ((int)w.unit + w.seg_units) * a.ut;
+  const int rest = w.i.units - w.unit;
+  w.seg_units = rest < w.left ? rest : (int)w.left;
+  w.t = w.unit * a.ut;
+  const int e = (w.unit + w.seg_units) * a.ut;
   w.t_end = e < w.i.tiles ? e : w.i.tiles;
 }
 __device__ __forceinline__ void walk_start(const PagedAttnArgs& a, const PagedAux& X, int64_t left,
                                            Walk& w) {
-  w.it = X.it0;
-  w.unit = X.it0_unit;
+  w.it = (int)X.it0;
+  w.unit = (int)X.it0_unit;
   w.left = left;
   w.i = load_item(a, w.it, false);
   walk_fit(a, w);
@@ -419,7 +418,7 @@ __device__ __forceinline__ bool walk_next(const PagedAttnArgs& a, Walk& w) {
   if (w.left <= 0) return false;
   w.unit = 0;
   do {
-    if (++w.it >= (int64_t)a.Q * a.ng) return false;
+    if (++w.it >= a.Q * a.ng) return false;
     w.i = load_item(a, w.it, false);
   } while (w.i.units == 0);
   walk_fit(a, w);
@@ -460,25 +459,26 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   const uint32_t q_s = smem_u32(smem), ring = q_s + C::kQBytes, p_s = ring + NS * kSlotBytes;
   float* sc_s = reinterpret_cast<float*>(smem + C::kQBytes + NS * kSlotBytes + C::kPBytes);
   PagedAux& X = *reinterpret_cast<PagedAux*>(reinterpret_cast<uint8_t*>(sc_s) + C::kScBytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the warp index as a value that the compiler knows to be the same in the whole warp
+  const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
   griddep_launch_dependents();
   if (tid == 0) {
     prefetch_tensormap(&qmap);
     if (kMode == 0) prefetch_tensormap(&kmap);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&X.full[s]), kMode == 0 ? 1 : C::kLoadWarps);
+      mbar_init(smem_u32(&X.full[s]), kMode == 0 ? 1 : C::kLoadWarps / 2);
       mbar_init(smem_u32(&X.empty[s]), 1);
     }
     mbar_init(smem_u32(&X.q_full), 1);
-    mbar_init(smem_u32(&X.q_empty), 2);
+    mbar_init(smem_u32(&X.q_empty), 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&X.s_full[b]), 4);
+      mbar_init(smem_u32(&X.s_full[b]), 2);
       mbar_init(smem_u32(&X.s_empty[b]), C::kWarpS);
     }
-    for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&X.fin[b]), 1);
-    mbar_init(smem_u32(&X.p_full), C::kWarpS);
-    mbar_init(smem_u32(&X.pv_done), 2);
+    for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&X.fin[b]), 1);
+    for (int k = 0; k < 4; ++k) mbar_init(smem_u32(&X.p_full[k]), C::kWarpS);
+    mbar_init(smem_u32(&X.pv_done), 1);
     X.abort = 0;
     mbar_fence_init();
   }
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = X.tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, X.tmem_slot, 0);
 
   if (u1 > u0) {
     if (warp < C::kWarpS) {
@@ -589,28 +589,27 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           float2 xA[kG], xB[kG];
           if (on) {
             if (!C::kScaled) {
-              uint32_t x[4 * kG], y[4 * kG];
-              tmem_ld_rows(tmem + lrow + 128 * sb + kRows * half, x);
-              tmem_ld_rows(tmem + lrow + 128 * sb + 64 + kRows * half, y);
+              uint32_t x[4 * kG];
+              tmem_ld_16x256b_x4(tmem + lrow + 64 * sb + kRows * half, x);
               tmem_ld_wait();
 #pragma unroll
               for (int g = 0; g < kG; ++g) {
-                xA[g] = add2(make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1])),
-                             make_float2(__uint_as_float(y[4 * g]), __uint_as_float(y[4 * g + 1])));
-                xB[g] =
-                    add2(make_float2(__uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3])),
-                         make_float2(__uint_as_float(y[4 * g + 2]), __uint_as_float(y[4 * g + 3])));
+                xA[g] = make_float2(__uint_as_float(x[4 * g]), __uint_as_float(x[4 * g + 1]));
+                xB[g] = make_float2(__uint_as_float(x[4 * g + 2]), __uint_as_float(x[4 * g + 3]));
               }
             } else {
-              uint32_t x[4][4 * kG];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) tmem_ld_rows(tmem + lrow + 64 * k + kRows * half, x[k]);
-              tmem_ld_wait();
 #pragma unroll
               for (int g = 0; g < kG; ++g) xA[g] = xB[g] = make_float2(0.f, 0.f);
+#pragma unroll 1
+              for (int k2 = 0; k2 < 4; k2 += 2) {
+              uint32_t x[2][4 * kG];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + kRows * half + 2 * r4;
+              for (int k = 0; k < 2; ++k)
+                tmem_ld_16x256b_x4(tmem + lrow + 64 * (k2 + k) + kRows * half, x[k]);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float* sc = sc_s + ((c & 3) * 4 + k2 + k) * 64 + kRows * half + 2 * r4;
 #pragma unroll
                 for (int g = 0; g < kG; ++g) {
                   const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
@@ -621,6 +620,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                       make_float2(__uint_as_float(x[k][4 * g + 2]), __uint_as_float(x[k][4 * g + 3])),
                       f, xB[g]);
                 }
+              }
               }
             }
           }
@@ -664,14 +664,16 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               }
             }
           };
-          bool need = false;
-          if (on) {
-            weights();
-            need = (hA < Hg && (tA > kLazy || (mA == -INFINITY && tA > -INFINITY))) ||
-                   (hB < Hg && (tB > kLazy || (mB == -INFINITY && tB > -INFINITY)));
-          }
-          if (soft_any<C::kSoft>(need)) {
-            // a head's maximum moves: the largest exponent of its rows in both halves
+          for (int pass = 0;; ++pass) {
+            bool need = false;
+            if (on) {
+              weights();
+              need = (hA < Hg && (tA > kLazy || (mA == -INFINITY && tA > -INFINITY))) ||
+                     (hB < Hg && (tB > kLazy || (mB == -INFINITY && tB > -INFINITY)));
+            }
+            if (!soft_any<C::kSoft>(need) || pass == 1) break;
+            // a head's maximum moves: the largest exponent of its rows in all parts; the weights
+            // are taken again
             if (on) {
               tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, 1));
               tA = fmaxf(tA, __shfl_xor_sync(0xFFFFFFFFu, tA, 2));
@@ -683,8 +685,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               }
             }
             soft_sync<C::kSoft>();
-            float fA = 1.f, fB = 1.f;
             if (on) {
+              float fA = 1.f, fB = 1.f;
               tA = X.top[0][hA];
               tB = X.top[0][hB];
 #pragma unroll
@@ -704,14 +706,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                 X.fac[hA] = fA;
                 X.fac[hB] = fB;
               }
-              const float2 qA = make_float2(fA, fA), qB = make_float2(fB, fB), o0 = make_float2(0.f, 0.f);
+              const float2 qA = make_float2(fA, fA), qB = make_float2(fB, fB);
+              const float2 o0 = make_float2(0.f, 0.f);
               lA = fma2(lA, qA, o0);
               lB = fma2(lB, qB, o0);
               rA = fma2(rA, qA, o0);
               rB = fma2(rB, qB, o0);
-              weights();
             }
-            soft_sync<C::kSoft>();  // fac is written
+            soft_sync<C::kSoft>();  // fac is written, and top read, by all
             if (t > w.t) {
               tc_fence_after();
 #pragma unroll 1
@@ -730,7 +732,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               }
               tmem_st_wait();
             }
-            soft_sync<C::kSoft>();  // fac and top are read by all before a later tile writes them
+            // (the next pass' vote keeps fac until all have read it)
           }
           if (on) {
             lA = add2(lA, sA);
@@ -738,27 +740,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             if (!C::kScaled) {
               rA = add2(rA, uA);
               rB = add2(rB, uB);
-            }
-          }
-          if (on) {
-            // P [head][64 rows], 128-byte swizzled: matrix i is this part's rows 8 i .. of eight
-            // heads
-            static_assert(kG == 4, "a warp's rows are four matrices");
-            const int hr = 16 * quad + (lane & 7);
-            const uint32_t pA = p_s + hr * 128 + (((kG * half + (lane >> 3)) ^ (lane & 7)) << 4);
-#pragma unroll
-            for (int k = 0; k < (C::kScaled ? 4 : 1); ++k) {
-              if (C::kScaled) {
-                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + kRows * half + 2 * r4;
-#pragma unroll
-                for (int g = 0; g < kG; ++g) {
-                  const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
-                  pa[g] = pack_bf16x2(eA[g].x * f.x, eA[g].y * f.y);
-                  pb[g] = pack_bf16x2(eB[g].x * f.x, eB[g].y * f.y);
-                }
-              }
-              store_matrices(pA + k * (kHp * 128), pa);
-              store_matrices(pA + k * (kHp * 128) + 8 * 128, pb);
             }
           }
           if (kMode == 0 && !all) {
@@ -777,12 +758,35 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                           make_uint4(0u, 0u, 0u, 0u));
             }
           }
+          // P [head][64 rows], 128-byte swizzled: matrix i is this part's rows 8 i .. of eight
+          // heads
+          static_assert(kG == 4, "a warp's rows are four matrices");
+          const uint32_t pA = p_s + (16 * quad + (lane & 7)) * 128 +
+                              (((kG * half + (lane >> 3)) ^ (lane & 7)) << 4);
+#pragma unroll
+          for (int k = 0; k < (C::kScaled ? 4 : 1); ++k) {
+            if (C::kScaled && k == C::kPBufs) wait_phase(X, X.empty[sl], sph);  // tile 0's products
+            if (on) {
+              if (C::kScaled) {
+                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + kRows * half + 2 * r4;
+#pragma unroll
+                for (int g = 0; g < kG; ++g) {
+                  const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
+                  pa[g] = pack_bf16x2(eA[g].x * f.x, eA[g].y * f.y);
+                  pb[g] = pack_bf16x2(eB[g].x * f.x, eB[g].y * f.y);
+                }
+              }
+              const uint32_t pk = pA + (k % C::kPBufs) * (kHp * 128);
+              store_matrices(pk, pa);
+              store_matrices(pk + 8 * 128, pb);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&X.p_full[k]));
+          }
           sl += 4;
           if (sl >= NS) { sl -= NS; sph ^= 1; }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&X.p_full));
         }
         // ---- the segment's end: sums of each head, then its part or its output ----
         if (on) {
@@ -897,117 +901,123 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         soft_sync<C::kSoft>();  // fac, the sums and the rotation are read before the next segment's
         u += w.seg_units;
       } while (walk_next(a, w));
-    } else if (warp < C::kWarpO) {
-      // ================= S products (the first warp also loads each segment's Q) =============
-      // Of each quarter, warp r multiplies dim block r; scaled rows keep a quarter in one
-      // accumulator, so there the warps take turns at the quarters.
-      const int r = warp - C::kWarpS;
-      if (lane == 0) {
-        Walk w;
-        walk_start(a, X, u1 - u0, w);
-        int c = 0, sl = 0;
-        uint32_t sph = 0, n = 0;  // n: segments so far
-        const uint32_t id = idesc_bf16(64, 64, 0, 0);
-        const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), r_d = sdesc_sw128(ring, 16, kGroup);
-        const uint32_t qf = smem_u32(&X.q_full);
-        const uint64_t pol = policy_evict_first();
-        bool ok = true, asked = false;
-        do {
-          if (r == 0) {
-            // the products of the segment before it have read Q
-            ok = n == 0 || wait_phase(X, X.q_empty, (n - 1) & 1);
-            if (ok) {
-              mbar_arrive_expect_tx(qf, C::kQBytes);
+    } else if (warp == C::kWarpS) {
+      // ================= S products =================
+      // The whole warp walks the loop and one elected lane issues: with operands the same in
+      // the warp an MMA takes 32 cycles (its reads of shared memory), where a lane in a branch
+      // of its own took 47 and far more beside busy warps.
+      const uint32_t lead = elect_lane();
+      Walk w;
+      walk_start(a, X, u1 - u0, w);
+      int c = 0, sl = 0;
+      uint32_t sph = 0, n = 0;  // n: segments so far
+      const uint32_t id = idesc_bf16(64, 64, 0, 0);
+      const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), r_d = sdesc_sw128(ring, 16, kGroup);
+      bool ok = true, next;
+      do {
+        ok = all_ok(wait_phase(X, X.q_full, n & 1));
+        ++n;
+        const int tiles = uniform(w.t_end - w.t);
+        for (int t = 0; ok && t < tiles; ++t, ++c) {
+          const int sb = C::kScaled ? 0 : c & 1;
+          const int lag = C::kScaled ? 1 : 2;
+          if (c >= lag)
+            ok = all_ok(wait_phase(X, X.s_empty[sb], C::kScaled ? (uint32_t)(c - 1) & 1
+                                                                : (uint32_t)((c - 2) >> 1) & 1));
+          tc_fence_after();
 #pragma unroll
-              for (int db = 0; db < 8; ++db)
-                tma_load_2d(q_s + db * C::kQBlock, &qmap, 64 * db,
-                            (int32_t)(w.i.q * a.H + 64 * w.i.hg), qf, pol);
-              asked = true;
-            }
-          }
-          ok = ok && wait_phase(X, X.q_full, n & 1);
-          if (ok) asked = false;
-          ++n;
-          for (int t = w.t; ok && t < w.t_end; ++t, ++c) {
-            const int sb = C::kScaled ? 0 : c & 1;
-            const int lag = C::kScaled ? 1 : 2;
-            if (c >= lag)
-              ok = wait_phase(X, X.s_empty[sb],
-                              C::kScaled ? (uint32_t)(c - 1) & 1 : (uint32_t)((c - 2) >> 1) & 1);
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (!C::kScaled || (k & 1) == r) {
-                ok = ok && wait_phase(X, X.full[sl], sph);
-                if (!ok) break;
-                // the tile's mask came with its first quarter, the scales with each
-                if (k == (C::kScaled ? 2 + r : 0)) mbar_arrive(smem_u32(&X.s_full[sb]));
-                tc_fence_after();
-                const uint32_t d = tmem + (C::kScaled ? 64 * k : 128 * sb + 64 * r);
-                const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
-                if (C::kScaled) {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    umma_bf16(d, q_d + (((2 * k + (i >> 2)) * C::kQBlock + (i & 3) * 32) >> 4),
-                              rd + (((i >> 2) * kBlock + (i & 3) * 32) >> 4), id, i > 0);
-                } else {
-                  const uint64_t qd = q_d + ((uint32_t)((2 * k + r) * C::kQBlock) >> 4);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    umma_bf16(d, qd + ((i * 32) >> 4), rd + ((uint32_t)(r * kBlock + i * 32) >> 4), id,
-                              i > 0 || k > 0);
-                }
-              }
-              if (++sl == NS) { sl = 0; sph ^= 1; }
-            }
+          for (int k = 0; k < 4; ++k) {
+            ok = ok && all_ok(wait_phase(X, X.full[sl], sph));
             if (!ok) break;
-            umma_commit(smem_u32(&X.s_full[sb]));
-          }
-          if (!ok) { X.abort = 1; break; }
-          umma_commit(smem_u32(&X.q_empty));
-        } while (walk_next(a, w));
-        // no copy may land and no MMA run when the CTA gives up its memory, whatever happened
-        // above
-        if (asked) mbar_wait(qf, (n - 1) & 1, 100000000ull);
-        umma_commit(smem_u32(&X.fin[r]));
-        mbar_wait(smem_u32(&X.fin[r]), 0, 100000000ull);
-      }
-    } else if (warp < C::kWarpL) {
-      // ================= O^T products: warp r tiles 2 r and 2 r + 1 =================
-      const int r = warp - C::kWarpO;
-      if (lane == 0) {
-        Walk w;
-        walk_start(a, X, u1 - u0, w);
-        int c = 0, sl = 2 * r;
-        const uint32_t id = idesc_bf16(128, kHp, 1, 0);
-        const uint64_t r_d = sdesc_sw128(ring, kBlock, kGroup), p_d = sdesc_sw128(p_s, 16, 1024);
-        bool ok = true;
-        do {
-          for (int t = w.t; t < w.t_end; ++t, ++c) {
-            ok = wait_phase(X, X.p_full, (uint32_t)c & 1);
-            if (!ok) break;
+            // FP8 rows were written by threads: the fence towards the tensor core's reads (of
+            // both kinds of products) stands here, with the thread that issues them
+            if (kMode != 0) fence_proxy_async_smem();
             tc_fence_after();
+            const uint32_t d = tmem + 64 * (C::kScaled ? k : sb);
+            const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
+            if (lead) {
+              // the tile's mask came with its first quarter, the scales with each
+              if (k == (C::kScaled ? 3 : 0)) mbar_arrive(smem_u32(&X.s_full[sb]));
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int mt = 2 * r + j;
-              const int s = sl + j >= NS ? sl + j - NS : sl + j;
-              const uint64_t rd = r_d + ((uint32_t)(s * kSlotBytes) >> 4);
-              const uint64_t pd = p_d + (C::kScaled ? (uint32_t)(mt * kHp * 128) >> 4 : 0);
+              for (int i = 0; i < 8; ++i)
+                umma_bf16(d, q_d + (((2 * k + (i >> 2)) * C::kQBlock + (i & 3) * 32) >> 4),
+                          rd + (((i >> 2) * kBlock + (i & 3) * 32) >> 4), id,
+                          i > 0 || (!C::kScaled && k > 0));
+              if (k == 3) umma_commit(smem_u32(&X.s_full[sb]));
+            }
+            __syncwarp();
+            if (++sl == NS) { sl = 0; sph ^= 1; }
+          }
+        }
+        if (!ok) break;
+        if (lead) umma_commit(smem_u32(&X.q_empty));
+        __syncwarp();
+        next = uniform(walk_next(a, w)) != 0;
+      } while (next);
+      // no MMA may still be running when the TMEM is released, whatever happened above
+      if (lead) umma_commit(smem_u32(&X.fin[0]));
+      __syncwarp();
+      mbar_wait(smem_u32(&X.fin[0]), 0, 100000000ull);
+    } else if (warp == C::kWarpO) {
+      // ================= O^T products =================
+      const uint32_t lead = elect_lane();
+      Walk w;
+      walk_start(a, X, u1 - u0, w);
+      int c = 0, sl = 0;
+      const uint32_t id = idesc_bf16(128, kHp, 1, 0);
+      const uint64_t r_d = sdesc_sw128(ring, kBlock, kGroup), p_d = sdesc_sw128(p_s, 16, 1024);
+      bool ok = true, next;
+      do {
+        const int tiles = uniform(w.t_end - w.t);
+        for (int t = 0; ok && t < tiles; ++t, ++c) {
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            if (C::kScaled || mt == 0) {
+              ok = ok && all_ok(wait_phase(X, X.p_full[C::kScaled ? mt : 0], (uint32_t)c & 1));
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
+            const uint64_t pd = p_d + ((uint32_t)((mt % C::kPBufs) * (kHp * 128)) >> 4);
+            if (lead) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(tmem + kColO + 64 * mt, rd + ((kk * 2 * kGroup) >> 4), pd + ((kk * 32) >> 4),
-                          id, t > w.t || kk > 0);
-              umma_commit(smem_u32(&X.empty[s]));
+                umma_bf16(tmem + kColO + 64 * mt, rd + ((kk * 2 * kGroup) >> 4),
+                          pd + ((kk * 32) >> 4), id, t > 0 || kk > 0);
+              umma_commit(smem_u32(&X.empty[sl]));
+              if (mt == 3) umma_commit(smem_u32(&X.pv_done));
             }
-            umma_commit(smem_u32(&X.pv_done));
-            sl += 4;
-            if (sl >= NS) sl -= NS;
+            __syncwarp();
+            if (++sl == NS) sl = 0;
           }
-          if (!ok) { X.abort = 1; break; }
+        }
+        if (!ok) break;
+        next = uniform(walk_next(a, w)) != 0;
+      } while (next);
+      if (lead) umma_commit(smem_u32(&X.fin[1]));
+      __syncwarp();
+      mbar_wait(smem_u32(&X.fin[1]), 0, 100000000ull);
+    } else if (warp == C::kWarpQ) {
+      // ================= Q of each segment =================
+      if (lane == 0) {
+        Walk w;
+        walk_start(a, X, u1 - u0, w);
+        const uint64_t pol = policy_evict_first();
+        uint32_t n = 0;  // segments so far
+        const uint32_t qf = smem_u32(&X.q_full);
+        do {
+          if (n > 0 && !wait_phase(X, X.q_empty, (n - 1) & 1)) break;
+          mbar_arrive_expect_tx(qf, C::kQBytes);
+#pragma unroll
+          for (int db = 0; db < 8; ++db)
+            tma_load_2d(q_s + db * C::kQBlock, &qmap, 64 * db, (int32_t)(w.i.q * a.H + 64 * w.i.hg),
+                        qf, pol);
+          ++n;
         } while (walk_next(a, w));
-        umma_commit(smem_u32(&X.fin[2 + r]));
-        mbar_wait(smem_u32(&X.fin[2 + r]), 0, 100000000ull);
+        mbar_wait(qf, (n - 1) & 1, 100000000ull);  // no copy may land after the CTA's exit
       }
+    } else if (warp < C::kWarpL) {
+    // spare: the loaders begin at a multiple of four warps
     } else if (kMode == 0) {
       // ================= bf16 rows by tensor copies: warp k quarter k =================
       const int k = warp - C::kWarpL;
@@ -1075,18 +1085,27 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       }
     } else {
       // ================= FP8 rows through registers =================
-      // Thread t of 256: rows t / 8 and 32 + t / 8 of a tile, 16 dims of each quarter (piece
-      // t % 8).  A quarter's registers are loaded for the next tile as soon as this tile's
-      // codes are converted, so three to four quarters are always in flight; the pages are
-      // looked up one tile earlier still.
+      // Two groups of eight warps take turns at the tiles, so a group's tile loads into its
+      // registers while the other group converts and stores (a group that loaded the next
+      // quarter after each one waited for that load before it could use the one already there:
+      // registers wait for all loads behind one counter).  Thread t of a group: rows t / 8 and
+      // 32 + t / 8 of a tile, 16 dims of each quarter (piece t % 8).  Pages are looked up a turn
+      // ahead.
       griddep_wait();
-      const int t256 = tid - 32 * C::kWarpL, r = t256 >> 3, pc = t256 & 7;
+      const int grp = (warp - C::kWarpL) >> 3, t256 = (tid - 32 * C::kWarpL) & 255;
+      const int r = t256 >> 3, pc = t256 & 7;
       Walk w;
       walk_start(a, X, u1 - u0, w);
       int tn = w.t;  // next tile to look up
       bool more = true;
-      // The pages and rows within them of the next tile's two rows (row -1: none); false: no
-      // further tile.
+      auto step = [&]() {
+        if (more && ++tn == w.t_end) {
+          more = walk_next(a, w);
+          tn = w.t;
+        }
+      };
+      // The pages and rows within them of the next tile's two rows (row -1: none), and past the
+      // other group's tile; false: no further tile.
       auto look = [&](int (&page)[2], int (&row)[2]) -> bool {
         page[0] = page[1] = row[0] = row[1] = -1;
         if (!more) return false;
@@ -1099,10 +1118,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             page[i] = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
           }
         }
-        if (++tn == w.t_end) {
-          more = walk_next(a, w);
-          tn = w.t;
-        }
+        step();
+        step();
         return true;
       };
       // Addresses of the two rows (null: none), and the tile's valid rows among this warp's
@@ -1124,84 +1141,87 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         return bits;
       };
       uint4 buf[2][4];
-      float scl[2][4];  // FP8_S128: the quarter's scale (piece 0 only); FP8_E8M0: the piece's
-      auto fetch = [&](const uint8_t* const (&src)[2], int k) {
+      // The scale word of row r + 32 (pc / 4), quarter pc % 4: an fp32 scale (FP8_S128) or four
+      // bytes (FP8_E8M0).  Every thread holds one, the eight of a row all of both rows'.
+      uint32_t scl;
+      auto fetch = [&](const uint8_t* const (&src)[2]) {
+        const uint8_t* sw = pc < 4 ? src[0] : src[1];
+        scl = sw ? __ldcs(reinterpret_cast<const uint32_t*>(sw + 512) + (pc & 3)) : 0u;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          buf[i][k] = make_uint4(0u, 0u, 0u, 0u);
-          scl[i][k] = 0.f;
-          if (src[i]) {
-            buf[i][k] = __ldcs(reinterpret_cast<const uint4*>(src[i] + 128 * k + 16 * pc));
-            if (kMode == 1) {
-              if (pc == 0) scl[i][k] = __ldcs(reinterpret_cast<const float*>(src[i] + 512) + k);
-            } else {
-              scl[i][k] = __uint_as_float((uint32_t)__ldcs(src[i] + 512 + 4 * k + (pc >> 1)));
-            }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            buf[i][k] = make_uint4(0u, 0u, 0u, 0u);
+            if (src[i]) buf[i][k] = __ldcs(reinterpret_cast<const uint4*>(src[i] + 128 * k + 16 * pc));
           }
         }
       };
       int page[2], row[2];
       const uint8_t* src[2];
-      look(page, row);
+      if (grp == 1) step();
+      bool have = look(page, row);
       uint32_t bits = place(page, row, src);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) fetch(src, k);
+      fetch(src);
       bool nxt = look(page, row);
-      int sl = 0, c = 0;
+      int c = grp, sl = 4 * grp;
       uint32_t ph = 0;
-      bool again = false;
       const uint32_t offr = (r >> 3) * kGroup + (pc >> 2) * kBlock;
-      const uint32_t off0 = offr + sw128_off(r & 7, (2 * pc) & 7);
-      const uint32_t off1 = offr + sw128_off(r & 7, (2 * pc + 1) & 7);
-      for (bool have = true; have; ++c) {
-        const uint32_t bits_n = place(page, row, src);  // of the next tile
-        const bool nn = look(page, row);
+      const bool swap = pc >= 4;
+      const uint32_t off0 = offr + sw128_off(r & 7, (2 * pc + (swap ? 1 : 0)) & 7);
+      const uint32_t off1 = offr + sw128_off(r & 7, (2 * pc + (swap ? 0 : 1)) & 7);
+      for (; have; c += 2) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (again) wait_phase(X, X.empty[sl], ph ^ 1);
+          if (4 * c + k >= NS) wait_phase(X, X.empty[sl], ph ^ 1);
           if (k == 0 && lane == 0) {
-            uint8_t* nb = reinterpret_cast<uint8_t*>(X.nib[c & 3]) + (warp - C::kWarpL);
+            uint8_t* nb = reinterpret_cast<uint8_t*>(X.nib[c & 3]) + ((warp - C::kWarpL) & 7);
             nb[0] = (uint8_t)bits;
             nb[8] = (uint8_t)(bits >> 8);
           }
+          if (kMode == 1 && k == 0)
+            sc_s[((c & 3) * 4 + (pc & 3)) * 64 + r + 32 * (pc >> 2)] = __uint_as_float(scl);
           const uint32_t base = ring + sl * kSlotBytes;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w4[4] = {buf[i][k].x, buf[i][k].y, buf[i][k].z, buf[i][k].w};
-            const float scale = kMode == 2 ? e8m0_value(__float_as_uint(scl[i][k])) : 1.f;
-            uint32_t packed[8];
+            float scale = 1.f;
+            if (kMode == 2) {
+              const uint32_t word = __shfl_sync(0xFFFFFFFFu, scl, (lane & 24) + 4 * i + k);
+              scale = e8m0_value((word >> (8 * (pc >> 1))) & 0xFFu);
+            }
+            // pieces 4..7 store their upper eight dims first, so that the eight threads of a row
+            // write eight different 16-byte columns (no bank conflicts)
+            const uint4 v = buf[i][k];
+            const uint32_t w4[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z,
+                                    swap ? v.y : v.w};
+            // rows 32 on: four groups of 8 rows further
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int h = 0; h < 2; ++h) {
+              uint32_t packed[4];
 #pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
+              for (int j = 0; j < 4; ++j) {
                 const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-                    (__nv_fp8x2_storage_t)((w4[j] >> (16 * hh)) & 0xFFFFu), __NV_E4M3);
+                    (__nv_fp8x2_storage_t)((w4[2 * h + (j >> 1)] >> (16 * (j & 1))) & 0xFFFFu),
+                    __NV_E4M3);
                 float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
                 if (kMode == 2) { f.x *= scale; f.y *= scale; }
-                packed[2 * j + hh] = pack_bf16x2(f.x, f.y);
+                packed[j] = pack_bf16x2(f.x, f.y);
               }
-            }
-            // rows 32 on: four groups of 8 rows further
-            st_shared16(base + 4 * kGroup * i + off0,
-                        make_uint4(packed[0], packed[1], packed[2], packed[3]));
-            st_shared16(base + 4 * kGroup * i + off1,
-                        make_uint4(packed[4], packed[5], packed[6], packed[7]));
-            if (kMode == 1 && pc == 0) sc_s[((c & 3) * 4 + k) * 64 + r + 32 * i] = scl[i][k];
-          }
-          if (nxt) fetch(src, k);
-          if (k & 1) {  // one fence for two quarters
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_u32(&X.full[sl == 0 ? NS - 1 : sl - 1]));
-              mbar_arrive(smem_u32(&X.full[sl]));
+              st_shared16(base + 4 * kGroup * i + (h ? off1 : off0),
+                          make_uint4(packed[0], packed[1], packed[2], packed[3]));
             }
           }
-          if (++sl == NS) { sl = 0; ph ^= 1; again = true; }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&X.full[sl]));
+          if (++sl == NS) { sl = 0; ph ^= 1; }
         }
+        sl += 4;  // the other group's tile
+        if (sl >= NS) { sl -= NS; ph ^= 1; }
         have = nxt;
-        nxt = nn;
-        bits = bits_n;
+        if (have) {
+          bits = place(page, row, src);
+          fetch(src);
+          nxt = look(page, row);
+        }
       }
     }
   }
