@@ -185,22 +185,26 @@ constexpr int kMaxSmem = 232448;
 constexpr float kLazy = 64.0f;
 constexpr uint32_t kColO = 256;  // O^T tiles at 256 + 64 mt
 
+// What lives in P's buffers while they hold no P: from the end of a tile's products to the next
+// tile's weights, and in a segment's end.
+struct __align__(16) PagedSpare {
+  float top[2][64];     // largest score above the running maximum, by part of the rows
+  float lsum[2][64], rsum[2][64];  // sums of P by part: unrounded, rounded
+  float m_run[64], sink2[64];
+};
+static_assert(sizeof(PagedSpare) <= 16 * 128, "P's buffer of 16 heads holds it");
+
 struct __align__(16) PagedAux {
   uint64_t full[12], empty[12];  // ring slots
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_full[4], pv_done;  // p_full: a P per quarter of scaled rows, else [0]
+  uint64_t p_full[2], pv_done;  // p_full: two quarters' P of scaled rows, else [0]
   uint64_t fin[2];
   uint64_t mask[4];     // valid rows of tile c at c & 3 (bf16 rows)
   uint32_t nib[4][4];   // the same for FP8 rows: four rows' bits in each byte
-  int64_t sums[32];     // scan of the plan
-  int64_t total;
   int64_t it0;          // first item of this CTA and the units before it within the item
   int64_t it0_unit;
   float fac[64];        // rescale factor or 1 / sum, per head
-  float top[4][64];     // largest score above the running maximum, by part of the rows
-  float lsum[4][64], rsum[4][64];  // sums of P by part: unrounded, rounded
-  float m_run[64], sink2[64];
   float rope_c[32], rope_s[32];
   uint32_t tmem_slot;
   int abort;
@@ -222,16 +226,18 @@ struct PagedCfg {
   static constexpr int kThreads = 32 * (kWarpL + kLoadWarps);
   static constexpr int kQBlock = kHp * 128;
   static constexpr int kQBytes = 8 * kQBlock;
-  // P: one buffer; scaled rows have a P per quarter, the fourth in the first one's buffer (its
-  // products are nearly done by then), which leaves room for an eighth slot
-  static constexpr int kPBufs = kScaled ? 3 : 1;
+  static constexpr int kPBufs = kScaled ? 4 : 1;  // scaled rows have a P per quarter
   static constexpr int kPBytes = kHp * 128 * kPBufs;
-  static constexpr int kScBytes = kScaled ? 4 * 4 * 64 * 4 : 0;  // [tile & 3][quarter][row]
+  // scales [tile][quarter][row] of the last kScTiles tiles: a tile's are written with its last
+  // quarter, whose slot with eight slots was the last quarter's two tiles before
+  static constexpr int kScTiles = kHp == 64 ? 2 : 4;
+  static constexpr int kScBytes = kScaled ? kScTiles * 4 * 64 * 4 : 0;
   static constexpr int kFree =
-      (kMaxSmem - 1024 - kQBytes - kPBytes - kScBytes - (int)sizeof(PagedAux)) / kSlotBytes;
+      (kMaxSmem - kQBytes - kPBytes - kScBytes - (int)sizeof(PagedAux)) / kSlotBytes;
   static constexpr int kSlots = kFree < 12 ? kFree : 12;
+  static_assert(!kScaled || kScTiles == 4 || kSlots <= 8, "scales are overwritten too early");
   static constexpr int kSmem =
-      1024 + kQBytes + kSlots * kSlotBytes + kPBytes + kScBytes + (int)sizeof(PagedAux);
+      kQBytes + kSlots * kSlotBytes + kPBytes + kScBytes + (int)sizeof(PagedAux);
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -452,17 +458,24 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                       const __grid_constant__ CUtensorMap kmap) {
   using C = PagedCfg<kHp, kMode>;
   constexpr int NS = C::kSlots;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  // no static shared memory in this kernel: the dynamic part begins at a 1024-byte boundary,
+  // as the swizzled tiles need (checked below)
+  extern __shared__ __align__(1024) uint8_t smem[];
   // Q first: the S products read 64 rows of each Q block, with fewer heads past the block
   // (into what follows it; those TMEM lanes are never used)
   const uint32_t q_s = smem_u32(smem), ring = q_s + C::kQBytes, p_s = ring + NS * kSlotBytes;
   float* sc_s = reinterpret_cast<float*>(smem + C::kQBytes + NS * kSlotBytes + C::kPBytes);
   PagedAux& X = *reinterpret_cast<PagedAux*>(reinterpret_cast<uint8_t*>(sc_s) + C::kScBytes);
+  PagedSpare& Y = *reinterpret_cast<PagedSpare*>(smem + C::kQBytes + NS * kSlotBytes);
   // the warp index as a value that the compiler knows to be the same in the whole warp
   const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
   griddep_launch_dependents();
+  if ((smem_u32(smem) & 1023u) != 0) {  // the same in every thread
+    griddep_wait();
+    if (tid == 0) raise_fault(kFaultBounds);
+    return;
+  }
   if (tid == 0) {
     prefetch_tensormap(&qmap);
     if (kMode == 0) prefetch_tensormap(&kmap);
@@ -477,7 +490,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       mbar_init(smem_u32(&X.s_empty[b]), C::kWarpS);
     }
     for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&X.fin[b]), 1);
-    for (int k = 0; k < 4; ++k) mbar_init(smem_u32(&X.p_full[k]), C::kWarpS);
+    for (int k = 0; k < 2; ++k) mbar_init(smem_u32(&X.p_full[k]), C::kWarpS);
     mbar_init(smem_u32(&X.pv_done), 1);
     X.abort = 0;
     mbar_fence_init();
@@ -502,12 +515,13 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) X.sums[warp] = x;
+    int64_t* sums = reinterpret_cast<int64_t*>(smem + C::kQBytes);  // the ring is not in use yet
+    if (lane == 31) sums[warp] = x;
     __syncthreads();
     int64_t before = 0, total = 0;
     for (int w = 0; w < C::kThreads / 32; ++w) {
-      if (w < warp) before += X.sums[w];
-      total += X.sums[w];
+      if (w < warp) before += sums[w];
+      total += sums[w];
     }
     before += x - s;  // units of the items before this thread's
     U = total;
@@ -561,11 +575,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           if (hB < Hg) mB = a.sink[64 * w.i.hg + hB] * kLog2e;
         }
         const bool whole = w.unit == 0 && w.seg_units == w.i.units;
-        // what the output needs is fetched while the first tile loads
-        if (half == 0 && r4 == 0) {
-          X.sink2[hA] = mA;
-          X.sink2[hB] = mB;
-        }
+        const float sinkA = mA, sinkB = mB;
+        // what the output needs is computed while the first tile loads
         if (whole && a.inv_freq && warp == C::kWarpS - 1) {
           float s, cs;
           sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
@@ -609,7 +620,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const float* sc = sc_s + ((c & 3) * 4 + k2 + k) * 64 + kRows * half + 2 * r4;
+                const float* sc = sc_s + ((c & (C::kScTiles - 1)) * 4 + k2 + k) * 64 + kRows * half + 2 * r4;
 #pragma unroll
                 for (int g = 0; g < kG; ++g) {
                   const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
@@ -680,19 +691,19 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               tB = fmaxf(tB, __shfl_xor_sync(0xFFFFFFFFu, tB, 1));
               tB = fmaxf(tB, __shfl_xor_sync(0xFFFFFFFFu, tB, 2));
               if (r4 == 0) {
-                X.top[half][hA] = tA;
-                X.top[half][hB] = tB;
+                Y.top[half][hA] = tA;
+                Y.top[half][hB] = tB;
               }
             }
             soft_sync<C::kSoft>();
             if (on) {
               float fA = 1.f, fB = 1.f;
-              tA = X.top[0][hA];
-              tB = X.top[0][hB];
+              tA = Y.top[0][hA];
+              tB = Y.top[0][hB];
 #pragma unroll
               for (int i = 1; i < kParts; ++i) {
-                tA = fmaxf(tA, X.top[i][hA]);
-                tB = fmaxf(tB, X.top[i][hB]);
+                tA = fmaxf(tA, Y.top[i][hA]);
+                tB = fmaxf(tB, Y.top[i][hB]);
               }
               if (tA > kLazy || (mA == -INFINITY && tA > -INFINITY)) {
                 fA = mA == -INFINITY ? 0.f : ex2(-tA);
@@ -732,7 +743,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               }
               tmem_st_wait();
             }
-            // (the next pass' vote keeps fac until all have read it)
+            // (the next pass' vote comes after all have read fac: P may then be written over it)
           }
           if (on) {
             lA = add2(lA, sA);
@@ -764,11 +775,10 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           const uint32_t pA = p_s + (16 * quad + (lane & 7)) * 128 +
                               (((kG * half + (lane >> 3)) ^ (lane & 7)) << 4);
 #pragma unroll
-          for (int k = 0; k < (C::kScaled ? 4 : 1); ++k) {
-            if (C::kScaled && k == C::kPBufs) wait_phase(X, X.empty[sl], sph);  // tile 0's products
+          for (int k = 0; k < C::kPBufs; ++k) {
             if (on) {
               if (C::kScaled) {
-                const float* sc = sc_s + ((c & 3) * 4 + k) * 64 + kRows * half + 2 * r4;
+                const float* sc = sc_s + ((c & (C::kScTiles - 1)) * 4 + k) * 64 + kRows * half + 2 * r4;
 #pragma unroll
                 for (int g = 0; g < kG; ++g) {
                   const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
@@ -776,19 +786,23 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                   pb[g] = pack_bf16x2(eB[g].x * f.x, eB[g].y * f.y);
                 }
               }
-              const uint32_t pk = pA + (k % C::kPBufs) * (kHp * 128);
+              const uint32_t pk = pA + k * (kHp * 128);
               store_matrices(pk, pa);
               store_matrices(pk + 8 * 128, pb);
             }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&X.p_full[k]));
+            if (!C::kScaled || (k & 1)) {  // a fence for two quarters' P
+              fence_proxy_async_smem();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&X.p_full[k >> 1]));
+            }
           }
           sl += 4;
           if (sl >= NS) { sl -= NS; sph ^= 1; }
         }
         // ---- the segment's end: sums of each head, then its part or its output ----
+        wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+        tc_fence_after();
         if (on) {
           float v[4] = {lA.x + lA.y, lB.x + lB.y, rA.x + rA.y, rB.x + rB.y};
 #pragma unroll
@@ -797,29 +811,31 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 2);
           }
           if (r4 == 0) {
-            X.lsum[half][hA] = v[0];
-            X.lsum[half][hB] = v[1];
+            Y.lsum[half][hA] = v[0];
+            Y.lsum[half][hB] = v[1];
             // with scaled weights no rounded sum stands for the output's weights
-            X.rsum[half][hA] = C::kScaled ? v[0] : v[2];
-            X.rsum[half][hB] = C::kScaled ? v[1] : v[3];
+            Y.rsum[half][hA] = C::kScaled ? v[0] : v[2];
+            Y.rsum[half][hB] = C::kScaled ? v[1] : v[3];
             if (half == 0) {
-              X.m_run[hA] = mA;
-              X.m_run[hB] = mB;
+              Y.m_run[hA] = mA;
+              Y.m_run[hB] = mB;
+              Y.sink2[hA] = sinkA;
+              Y.sink2[hB] = sinkB;
             }
           }
         }
         const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
         soft_sync<C::kSoft>();
         if (tid < Hg) {
-          float l = X.lsum[0][tid], r = X.rsum[0][tid];
+          float l = Y.lsum[0][tid], r = Y.rsum[0][tid];
 #pragma unroll
           for (int i = 1; i < kParts; ++i) {
-            l += X.lsum[i][tid];
-            r += X.rsum[i][tid];
+            l += Y.lsum[i][tid];
+            r += Y.rsum[i][tid];
           }
-          const float m = X.m_run[tid];
+          const float m = Y.m_run[tid];
           if (whole) {
-            const float sk = X.sink2[tid];
+            const float sk = Y.sink2[tid];
             if (sk > -INFINITY) {
               l += ex2(sk - m);
               r += ex2(sk - m);
@@ -840,8 +856,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           a.rec[w.it] = whole ? make_int2(-1, -1)
                               : make_int2((int)blockIdx.x, (int)(((ul + 1) * ncta - 1) / U));
         }
-        wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
-        tc_fence_after();
         soft_sync<C::kSoft>();
         if (whole) {
           uint16_t* out = a.out + (w.i.q * a.H + 64 * w.i.hg) * kDLat;
@@ -929,9 +943,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           for (int k = 0; k < 4; ++k) {
             ok = ok && all_ok(wait_phase(X, X.full[sl], sph));
             if (!ok) break;
-            // FP8 rows were written by threads: the fence towards the tensor core's reads (of
-            // both kinds of products) stands here, with the thread that issues them
-            if (kMode != 0) fence_proxy_async_smem();
             tc_fence_after();
             const uint32_t d = tmem + 64 * (C::kScaled ? k : sb);
             const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
@@ -972,13 +983,13 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         for (int t = 0; ok && t < tiles; ++t, ++c) {
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            if (C::kScaled || mt == 0) {
-              ok = ok && all_ok(wait_phase(X, X.p_full[C::kScaled ? mt : 0], (uint32_t)c & 1));
+            if (mt == 0 || (C::kScaled && mt == 2)) {
+              ok = ok && all_ok(wait_phase(X, X.p_full[mt >> 1], (uint32_t)c & 1));
               if (!ok) break;
               tc_fence_after();
             }
             const uint64_t rd = r_d + ((uint32_t)(sl * kSlotBytes) >> 4);
-            const uint64_t pd = p_d + ((uint32_t)((mt % C::kPBufs) * (kHp * 128)) >> 4);
+            const uint64_t pd = p_d + ((uint32_t)((C::kScaled ? mt : 0) * (kHp * 128)) >> 4);
             if (lead) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -1172,14 +1183,19 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       for (; have; c += 2) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (4 * c + k >= NS) wait_phase(X, X.empty[sl], ph ^ 1);
+          if (4 * c + k >= NS) {  // one warp polls, the group waits for it at a barrier
+            if (((warp - C::kWarpL) & 7) == 0) wait_phase(X, X.empty[sl], ph ^ 1);
+            asm volatile("bar.sync %0, 256;" ::"r"(2 + grp) : "memory");
+          }
           if (k == 0 && lane == 0) {
             uint8_t* nb = reinterpret_cast<uint8_t*>(X.nib[c & 3]) + ((warp - C::kWarpL) & 7);
             nb[0] = (uint8_t)bits;
             nb[8] = (uint8_t)(bits >> 8);
           }
-          if (kMode == 1 && k == 0)
-            sc_s[((c & 3) * 4 + (pc & 3)) * 64 + r + 32 * (pc >> 2)] = __uint_as_float(scl);
+          // (with the last quarter: its slot is free once the tile before the last one has read
+          // its scales)
+          if (kMode == 1 && k == 3)
+            sc_s[((c & (C::kScTiles - 1)) * 4 + (pc & 3)) * 64 + r + 32 * (pc >> 2)] = __uint_as_float(scl);
           const uint32_t base = ring + sl * kSlotBytes;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -1210,6 +1226,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                           make_uint4(packed[0], packed[1], packed[2], packed[3]));
             }
           }
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&X.full[sl]));
           if (++sl == NS) { sl = 0; ph ^= 1; }
