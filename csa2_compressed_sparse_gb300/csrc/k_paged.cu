@@ -586,9 +586,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         for (int t = w.t; t < w.t_end; ++t, ++c) {
           const int sb = C::kScaled ? 0 : c & 1;
           const uint32_t sphase = C::kScaled ? (uint32_t)c & 1 : (uint32_t)(c >> 1) & 1;
-          // P's buffer and O^T are free once the previous tile's products are done, which they
-          // are before this tile's scores except when the tensor core is the limit
-          if (c > 0) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+          // P's memory and O^T are free once the previous tile's products are done.  With bf16
+          // rows they are before this tile's scores (the loads are the limit), and waiting for
+          // them here keeps that wait off the path from scores to values; with FP8 rows the
+          // scores come earlier, so the wait stands before the first use.
+          auto products_done = [&]() {
+            if (c > 0) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+          };
+          if (kMode == 0) products_done();
           // the scores, and with them (the issuers have seen the tile land and arrive here too)
           // the mask and the scales that its loader wrote
           wait_phase(X, X.s_full[sb], sphase);
@@ -683,6 +688,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                      (hB < Hg && (tB > kLazy || (mB == -INFINITY && tB > -INFINITY)));
             }
             if (!soft_any<C::kSoft>(need) || pass == 1) break;
+            if (kMode != 0) products_done();
             // a head's maximum moves: the largest exponent of its rows in all parts; the weights
             // are taken again
             if (on) {
@@ -753,6 +759,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               rB = add2(rB, uB);
             }
           }
+          if (kMode != 0) products_done();
           if (kMode == 0 && !all) {
             // rows outside the item: whatever the page holds there must not meet P's zeros
             for (int k = 0; k < 4; ++k) {  // the copies themselves, too, are complete
