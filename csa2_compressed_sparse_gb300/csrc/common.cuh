@@ -181,6 +181,8 @@ struct PagedAttnArgs {
   float* lse;
   const float* inv_freq;
   int ut;                 // tiles of 64 rows per unit
+  uint32_t page_mul;      // j / page_rows = (j * page_mul >> 32) >> page_shift
+  int page_shift;
   int box_rows;           // rows per tensor copy: the largest of 64, 32, 16, 8 dividing page_rows
   int shared;             // more items than sequences: rows are read more than once
   int nctas;

@@ -707,6 +707,10 @@ csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_s
   a.inv_freq = inv_freq; a.ut = csa2::paged_unit_tiles();
   a.box_rows = a.cache.page_rows % 64 == 0 ? 64 : a.cache.page_rows % 32 == 0 ? 32
                : a.cache.page_rows % 16 == 0 ? 16 : 8;
+  int lg = 3;  // page_rows >= 8
+  while ((1 << lg) < a.cache.page_rows) ++lg;
+  a.page_mul = (uint32_t)((((uint64_t)1 << (31 + lg)) + a.cache.page_rows - 1) / a.cache.page_rows);
+  a.page_shift = lg - 1;
   a.shared = (int64_t)Q * a.ng > a.cache.B ? 1 : 0;
   a.nctas = w.nctas < sms ? w.nctas : sms;
   uint8_t* base = static_cast<uint8_t*>(ws);

@@ -196,12 +196,12 @@ static_assert(sizeof(PagedSpare) <= 16 * 128, "P's buffer of 16 heads holds it")
 
 struct __align__(16) PagedAux {
   uint64_t full[12], empty[12];  // ring slots
+  uint64_t landed[12];           // FP8 rows: written by the loaders, not yet fenced
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done;  // p_full: two quarters' P of scaled rows, else [0]
   uint64_t fin[2];
-  uint64_t mask[4];     // valid rows of tile c at c & 3 (bf16 rows)
-  uint32_t nib[4][4];   // the same for FP8 rows: four rows' bits in each byte
+  uint64_t mask[4];     // valid rows of tile c at c & 3
   int64_t it0;          // first item of this CTA and the units before it within the item
   int64_t it0_unit;
   float fac[64];        // rescale factor or 1 / sum, per head
@@ -221,7 +221,8 @@ struct PagedCfg {
   static constexpr int kWarpS = 4 * kParts;          // a warp issues S,
   static constexpr int kWarpO = kWarpS + 1;          // one O^T, one loads Q,
   static constexpr int kWarpQ = kWarpS + 2;
-  static constexpr int kWarpL = kWarpS + 4;          // the others load rows (one is spare)
+  static constexpr int kWarpF = kWarpS + 3;          // one fences FP8 rows (spare with bf16),
+  static constexpr int kWarpL = kWarpS + 4;          // the others load rows
   static constexpr int kLoadWarps = kMode == 0 ? 4 : 16;
   static constexpr int kThreads = 32 * (kWarpL + kLoadWarps);
   static constexpr int kQBlock = kHp * 128;
@@ -394,6 +395,13 @@ __device__ __forceinline__ Item load_item(const PagedAttnArgs& a, int64_t it, bo
   return i;
 }
 
+// j / page_rows for j < 2^31: with s = ceil(log2 d) and page_mul = ceil(2^(31 + s) / d), the
+// product is off by less than j 2^s / 2^(31 + s) < 1 / d of the quotient's unit, so its floor
+// is exact.
+__device__ __forceinline__ int32_t page_of(const PagedAttnArgs& a, uint32_t j) {
+  return (int32_t)(__umulhi(j, a.page_mul) >> a.page_shift);
+}
+
 // A CTA's walk over its segments: item it, tiles t .. t_end - 1 of it.
 struct Walk {
   int it;          // item
@@ -440,18 +448,6 @@ __device__ __forceinline__ uint64_t tile_mask(int64_t r0, int lo, int hi) {
   return m;
 }
 
-// The 64-bit mask of sixteen bytes that hold four bits each.
-__device__ __forceinline__ uint64_t gather_nibbles(const uint32_t (&n)[4]) {
-  uint64_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t x = n[i];
-    x = (x | (x >> 4)) & 0x00FF00FFu;
-    m |= (uint64_t)((x | (x >> 8)) & 0xFFFFu) << (16 * i);
-  }
-  return m;
-}
-
 template <int kHp, int kMode>
 __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap qmap,
@@ -480,7 +476,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     prefetch_tensormap(&qmap);
     if (kMode == 0) prefetch_tensormap(&kmap);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(smem_u32(&X.full[s]), kMode == 0 ? 1 : C::kLoadWarps / 2);
+      mbar_init(smem_u32(&X.full[s]), 1);
+      mbar_init(smem_u32(&X.landed[s]), 8);
       mbar_init(smem_u32(&X.empty[s]), 1);
     }
     mbar_init(smem_u32(&X.q_full), 1);
@@ -598,7 +595,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           // the mask and the scales that its loader wrote
           wait_phase(X, X.s_full[sb], sphase);
           tc_fence_after();
-          const uint64_t mask = kMode == 0 ? X.mask[c & 3] : gather_nibbles(X.nib[c & 3]);
+          const uint64_t mask = X.mask[c & 3];
           const bool all = mask == ~0ull;
           // bit 8 g: row 8 g + 2 r4 of this part, bit 8 g + 1 the one after it
           const uint32_t mk = (uint32_t)(mask >> (kRows * half + 2 * r4));
@@ -1034,8 +1031,26 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         } while (walk_next(a, w));
         mbar_wait(qf, (n - 1) & 1, 100000000ull);  // no copy may land after the CTA's exit
       }
-    } else if (warp < C::kWarpL) {
-    // spare: the loaders begin at a multiple of four warps
+    } else if (warp == C::kWarpF) {
+      // ================= FP8 rows: from the threads' writes to the tensor core's reads ========
+      // The fence between the two takes hundreds of cycles while the MMAs' reads fill shared
+      // memory; a warp of its own takes it off the loaders' and the issuer's way.
+      if (kMode != 0) {
+        Walk w;
+        walk_start(a, X, u1 - u0, w);
+        int sl = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        do {
+          for (int i = 4 * (w.t_end - w.t); ok && i > 0; --i) {
+            ok = wait_phase(X, X.landed[sl], ph);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&X.full[sl]));
+            if (++sl == NS) { sl = 0; ph ^= 1; }
+          }
+        } while (ok && walk_next(a, w));
+      }
     } else if (kMode == 0) {
       // ================= bf16 rows by tensor copies: warp k quarter k =================
       const int k = warp - C::kWarpL;
@@ -1056,7 +1071,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           int32_t py = 0, pz = (int32_t)a.cache.n_pages;  // beyond the pool: zeros
           uint64_t m = 0;
           if (row < w.i.hi && row + R > w.i.lo && tbeg + lane / nc < w.t_end) {
-            const int32_t lp = (int32_t)row / a.cache.page_rows;
+            const int32_t lp = page_of(a, (uint32_t)row);
             const int32_t page = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
             if (page >= 0 && page < a.cache.n_pages) {
               py = ((int32_t)row - lp * a.cache.page_rows) >> 3;
@@ -1106,12 +1121,13 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       // Two groups of eight warps take turns at the tiles, so a group's tile loads into its
       // registers while the other group converts and stores (a group that loaded the next
       // quarter after each one waited for that load before it could use the one already there:
-      // registers wait for all loads behind one counter).  Thread t of a group: rows t / 8 and
-      // 32 + t / 8 of a tile, 16 dims of each quarter (piece t % 8).  Pages are looked up a turn
-      // ahead.
+      // registers wait for all loads behind one counter).  Thread t of a group: row t / 4 of a
+      // tile and of each quarter dims 16 (t % 4) .. and 64 + 16 (t % 4) .., two loads of 64 whole
+      // bytes a row and stores free of bank conflicts.  The instructions issued are the limit, so
+      // a thread has one row, whose page is looked up a turn ahead.
       griddep_wait();
       const int grp = (warp - C::kWarpL) >> 3, t256 = (tid - 32 * C::kWarpL) & 255;
-      const int r = t256 >> 3, pc = t256 & 7;
+      const int r = t256 >> 2, pc = t256 & 3;
       Walk w;
       walk_start(a, X, u1 - u0, w);
       int tn = w.t;  // next tile to look up
@@ -1122,60 +1138,52 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           tn = w.t;
         }
       };
-      // The pages and rows within them of the next tile's two rows (row -1: none), and past the
-      // other group's tile; false: no further tile.
-      auto look = [&](int (&page)[2], int (&row)[2]) -> bool {
-        page[0] = page[1] = row[0] = row[1] = -1;
+      // The page and the row within it of the next tile's row (row -1: none), and past the other
+      // group's tile; false: no further tile.
+      auto look = [&](int& page, int& row) -> bool {
+        page = row = -1;
         if (!more) return false;
-        const int64_t r0 = ((int64_t)w.i.tile0 + tn) * 64 + r;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (r0 + 32 * i >= w.i.lo && r0 + 32 * i < w.i.hi) {
-            const int32_t j = (int32_t)(r0 + 32 * i), lp = j / a.cache.page_rows;
-            row[i] = j - lp * a.cache.page_rows;
-            page[i] = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
-          }
+        const int64_t j = ((int64_t)w.i.tile0 + tn) * 64 + r;
+        if (j >= w.i.lo && j < w.i.hi) {
+          const int32_t lp = page_of(a, (uint32_t)j);
+          row = (int32_t)j - lp * a.cache.page_rows;
+          page = a.cache.table[(int64_t)w.i.seq * a.cache.table_ld + lp];
         }
         step();
         step();
         return true;
       };
-      // Addresses of the two rows (null: none), and the tile's valid rows among this warp's
-      // eight, four bits each of two bytes.
-      auto place = [&](const int (&page)[2], const int (&row)[2], const uint8_t* (&src)[2]) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          src[i] = nullptr;
-          if (row[i] >= 0) {
-            if (page[i] >= 0 && page[i] < a.cache.n_pages)
-              src[i] = a.cache.data + (int64_t)page[i] * a.cache.page_stride + (int64_t)row[i] * 528;
-            else if (pc == 0)
-              raise_fault(kFaultBounds);
-          }
-          const uint32_t bal = __ballot_sync(0xFFFFFFFFu, src[i] != nullptr);
-          bits |= ((bal & 1u) | (bal >> 7 & 2u) | (bal >> 14 & 4u) | (bal >> 21 & 8u)) << (8 * i);
+      // Address of the row (null: none), and the tile's valid rows among this warp's eight.
+      auto place = [&](int page, int row, const uint8_t*& src) -> uint32_t {
+        src = nullptr;
+        if (row >= 0) {
+          if (page >= 0 && page < a.cache.n_pages)
+            src = a.cache.data + (int64_t)page * a.cache.page_stride + (int64_t)row * 528;
+          else if (pc == 0)
+            raise_fault(kFaultBounds);
         }
-        return bits;
+        uint32_t m = __ballot_sync(0xFFFFFFFFu, src != nullptr) & 0x11111111u;
+        m = (m | (m >> 3)) & 0x03030303u;
+        m = (m | (m >> 6)) & 0x000F000Fu;
+        return (m | (m >> 12)) & 0xFFu;
       };
       uint4 buf[2][4];
-      // The scale word of row r + 32 (pc / 4), quarter pc % 4: an fp32 scale (FP8_S128) or four
-      // bytes (FP8_E8M0).  Every thread holds one, the eight of a row all of both rows'.
-      uint32_t scl;
-      auto fetch = [&](const uint8_t* const (&src)[2]) {
-        const uint8_t* sw = pc < 4 ? src[0] : src[1];
-        scl = sw ? __ldcs(reinterpret_cast<const uint32_t*>(sw + 512) + (pc & 3)) : 0u;
+      uint32_t scl;  // scale word pc of the row: an fp32 scale (FP8_S128) or four bytes
+      auto fetch = [&](const uint8_t* src) {
+        scl = 0u;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int k = 0; k < 4; ++k) buf[0][k] = buf[1][k] = make_uint4(0u, 0u, 0u, 0u);
+        if (src) {
+          scl = __ldcs(reinterpret_cast<const uint32_t*>(src + 512) + pc);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            buf[i][k] = make_uint4(0u, 0u, 0u, 0u);
-            if (src[i]) buf[i][k] = __ldcs(reinterpret_cast<const uint4*>(src[i] + 128 * k + 16 * pc));
+            buf[0][k] = __ldcs(reinterpret_cast<const uint4*>(src + 16 * pc + 128 * k));
+            buf[1][k] = __ldcs(reinterpret_cast<const uint4*>(src + 16 * pc + 128 * k + 64));
           }
         }
       };
-      int page[2], row[2];
-      const uint8_t* src[2];
+      int page, row;
+      const uint8_t* src;
       if (grp == 1) step();
       bool have = look(page, row);
       uint32_t bits = place(page, row, src);
@@ -1183,40 +1191,33 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       bool nxt = look(page, row);
       int c = grp, sl = 4 * grp;
       uint32_t ph = 0;
-      const uint32_t offr = (r >> 3) * kGroup + (pc >> 2) * kBlock;
-      const bool swap = pc >= 4;
-      const uint32_t off0 = offr + sw128_off(r & 7, (2 * pc + (swap ? 1 : 0)) & 7);
-      const uint32_t off1 = offr + sw128_off(r & 7, (2 * pc + (swap ? 0 : 1)) & 7);
+      const uint32_t off0 = ring + (r >> 3) * kGroup + sw128_off(r & 7, 2 * pc);
+      const uint32_t off1 = ring + (r >> 3) * kGroup + sw128_off(r & 7, 2 * pc + 1);
       for (; have; c += 2) {
+        // the slots become free in order: one look at the last one's often stands for all four
+        bool free;
+        {
+          const int i = sl + 3;
+          free = 4 * c + 3 < NS ||
+                 all_ok(mbar_test_wait(smem_u32(&X.empty[i >= NS ? i - NS : i]),
+                                       i >= NS ? ph : ph ^ 1));
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          if (4 * c + k >= NS) {  // one warp polls, the group waits for it at a barrier
-            if (((warp - C::kWarpL) & 7) == 0) wait_phase(X, X.empty[sl], ph ^ 1);
-            asm volatile("bar.sync %0, 256;" ::"r"(2 + grp) : "memory");
-          }
-          if (k == 0 && lane == 0) {
-            uint8_t* nb = reinterpret_cast<uint8_t*>(X.nib[c & 3]) + ((warp - C::kWarpL) & 7);
-            nb[0] = (uint8_t)bits;
-            nb[8] = (uint8_t)(bits >> 8);
-          }
+          if (!free && 4 * c + k >= NS) wait_phase(X, X.empty[sl], ph ^ 1);
+          if (k == 0 && lane == 0)
+            reinterpret_cast<uint8_t*>(&X.mask[c & 3])[(warp - C::kWarpL) & 7] = (uint8_t)bits;
           // (with the last quarter: its slot is free once the tile before the last one has read
           // its scales)
           if (kMode == 1 && k == 3)
-            sc_s[((c & (C::kScTiles - 1)) * 4 + (pc & 3)) * 64 + r + 32 * (pc >> 2)] = __uint_as_float(scl);
-          const uint32_t base = ring + sl * kSlotBytes;
+            sc_s[((c & (C::kScTiles - 1)) * 4 + pc) * 64 + r] = __uint_as_float(scl);
+          uint32_t word = 0;
+          if (kMode == 2) word = __shfl_sync(0xFFFFFFFFu, scl, (lane & 28) + k) >> (8 * (pc >> 1));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float scale = 1.f;
-            if (kMode == 2) {
-              const uint32_t word = __shfl_sync(0xFFFFFFFFu, scl, (lane & 24) + 4 * i + k);
-              scale = e8m0_value((word >> (8 * (pc >> 1))) & 0xFFu);
-            }
-            // pieces 4..7 store their upper eight dims first, so that the eight threads of a row
-            // write eight different 16-byte columns (no bank conflicts)
-            const uint4 v = buf[i][k];
-            const uint32_t w4[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z,
-                                    swap ? v.y : v.w};
-            // rows 32 on: four groups of 8 rows further
+          for (int i = 0; i < 2; ++i) {  // dim block i of the quarter
+            // 2^(e - 127) twice in bf16: exponent field e, the subnormal 0x0040 for e = 0
+            const uint32_t sc2 = max(((word >> (16 * i)) & 0xFFu) * 0x00800080u, 0x00400040u);
+            const uint32_t w4[4] = {buf[i][k].x, buf[i][k].y, buf[i][k].z, buf[i][k].w};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t packed[4];
@@ -1225,17 +1226,20 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                 const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
                     (__nv_fp8x2_storage_t)((w4[2 * h + (j >> 1)] >> (16 * (j & 1))) & 0xFFFFu),
                     __NV_E4M3);
-                float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-                if (kMode == 2) { f.x *= scale; f.y *= scale; }
-                packed[j] = pack_bf16x2(f.x, f.y);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                packed[j] = pack_bf16x2(f.x, f.y);  // exact: four significant bits
+                if (kMode == 2) {
+                  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&packed[j]),
+                                                   *reinterpret_cast<const __nv_bfloat162*>(&sc2));
+                  packed[j] = *reinterpret_cast<const uint32_t*>(&v);
+                }
               }
-              st_shared16(base + 4 * kGroup * i + (h ? off1 : off0),
+              st_shared16((h ? off1 : off0) + sl * kSlotBytes + i * kBlock,
                           make_uint4(packed[0], packed[1], packed[2], packed[3]));
             }
           }
-          fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&X.full[sl]));
+          if (lane == 0) mbar_arrive(smem_u32(&X.landed[sl]));
           if (++sl == NS) { sl = 0; ph ^= 1; }
         }
         sl += 4;  // the other group's tile
