@@ -163,6 +163,9 @@ struct PagedAppendArgs {
   int ratio;              // position of cache row j: j * ratio
   const float* inv_freq;  // [32] or null: rows are stored as they are
   PagedCache cache;
+  int64_t cap_rows;       // rows that the table holds per sequence (below 2^31)
+  uint32_t page_mul;      // j / page_rows = (j * page_mul >> 32) >> page_shift
+  int page_shift;
 };
 
 struct PagedAttnArgs {
@@ -181,7 +184,7 @@ struct PagedAttnArgs {
   float* lse;
   const float* inv_freq;
   int ut;                 // tiles of 64 rows per unit
-  uint32_t page_mul;      // j / page_rows = (j * page_mul >> 32) >> page_shift
+  uint32_t page_mul;      // as in PagedAppendArgs
   int page_shift;
   int box_rows;           // rows per tensor copy: the largest of 64, 32, 16, 8 dividing page_rows
   int shared;             // more items than sequences: rows are read more than once
@@ -193,7 +196,7 @@ struct PagedAttnArgs {
 };
 
 cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s);
-cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendArgs& a, int sms, cudaStream_t s);
 int paged_head_pad(int H);    // heads of an item, padded: 16, 32 or 64
 int paged_unit_tiles();
 int paged_max_ctas();         // most CTAs of one attention call

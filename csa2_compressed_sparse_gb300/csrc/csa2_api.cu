@@ -618,6 +618,22 @@ csa2_status paged_args(const char* name, const csa2_paged* p, csa2::PagedCache* 
   return CSA2_OK;
 }
 
+// Factor and shift of a division by page_rows: with s = ceil(log2 d) and mul = ceil(2^(31 + s) /
+// d), j mul exceeds j 2^(31 + s) / d by less than j <= 2^31 times 1, so the floor of
+// j mul / 2^(31 + s) is exact for j < 2^31.
+void page_division(const csa2::PagedCache& c, uint32_t* mul, int* shift) {
+  int lg = 3;  // page_rows >= 8
+  while ((1 << lg) < c.page_rows) ++lg;
+  *mul = (uint32_t)((((uint64_t)1 << (31 + lg)) + c.page_rows - 1) / c.page_rows);
+  *shift = lg - 1;
+}
+
+// Rows that the table holds per sequence, at most 2^31 - 256.
+int64_t table_rows(const csa2::PagedCache& c) {
+  const int64_t most = 0x7FFFFF00;
+  return c.table_cols >= most / c.page_rows ? most : c.table_cols * c.page_rows;
+}
+
 // Workspace of csa2_paged_attn: the parts of items that more than one CTA works on.
 struct PagedWs {
   size_t part, pstat, rec, total;
@@ -662,7 +678,11 @@ csa2_status csa2_paged_append(const csa2_bf16* kv, int64_t kv_ld, int T, const i
   REQUIRE(ratio >= 1 && ratio <= 65536, "%s: ratio must be in [1, 65536] (got %d)", name, ratio);
   a.kv = kv; a.kv_ld = kv_ld; a.T = T; a.cu_seqlens = cu_seqlens; a.start_row = start_row;
   a.ratio = ratio; a.inv_freq = inv_freq;
-  cudaError_t e = csa2::launch_paged_append(a, stream);
+  a.cap_rows = table_rows(a.cache);
+  page_division(a.cache, &a.page_mul, &a.page_shift);
+  const int sms = num_sms();
+  if (sms <= 0) return fail(CSA2_ECUDA, "%s: no CUDA device", name);
+  cudaError_t e = csa2::launch_paged_append(a, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, name);
   return CSA2_OK;
 }
@@ -700,17 +720,12 @@ csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_s
   const int sms = num_sms();
   if (sms <= 0) return fail(CSA2_ECUDA, "%s: no CUDA device", name);
   a.q = q; a.Q = Q; a.H = H; a.ng = H > 64 ? 2 : 1; a.q_seq = q_seq; a.q_pos = q_pos;
-  const int64_t cols = a.cache.table_cols < ((int64_t)1 << 31) ? a.cache.table_cols
-                                                               : (int64_t)1 << 31;
-  a.cap_rows = cols * a.cache.page_rows < max_rows ? cols * a.cache.page_rows : max_rows;
+  a.cap_rows = table_rows(a.cache) < max_rows ? table_rows(a.cache) : max_rows;
   a.ratio = ratio; a.window = window; a.sink = sink; a.scale = scale; a.out = out; a.lse = lse;
   a.inv_freq = inv_freq; a.ut = csa2::paged_unit_tiles();
   a.box_rows = a.cache.page_rows % 64 == 0 ? 64 : a.cache.page_rows % 32 == 0 ? 32
                : a.cache.page_rows % 16 == 0 ? 16 : 8;
-  int lg = 3;  // page_rows >= 8
-  while ((1 << lg) < a.cache.page_rows) ++lg;
-  a.page_mul = (uint32_t)((((uint64_t)1 << (31 + lg)) + a.cache.page_rows - 1) / a.cache.page_rows);
-  a.page_shift = lg - 1;
+  page_division(a.cache, &a.page_mul, &a.page_shift);
   a.shared = (int64_t)Q * a.ng > a.cache.B ? 1 : 0;
   a.nctas = w.nctas < sms ? w.nctas : sms;
   uint8_t* base = static_cast<uint8_t*>(ws);
