@@ -425,52 +425,57 @@ class Paged:
         c = _PagedC(SWA_BF16 if row == 512 else self.fp8_dtype, d.shape[1], None, d.shape[0],
                     page * d.element_size(), None, t.shape[0], ld, t.shape[1])
         object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+        object.__setattr__(self, "_dev", d.get_device())
 
     def c(self):
         self._c.data = self.data.data_ptr()
         self._c.table = self.table.data_ptr()
-        return self._c
+        return self._ref
 
 
-def _arg(name, t, dtype, shape, device):
-    """Address of a dense tensor of this type and shape (None entries: any size) on the device."""
+def _arg(name, t, dtype, shape, dev):
+    """Address of a dense tensor of this type and shape on GPU dev (None: none)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"csa2: {name} must be a contiguous {dtype} tensor on {device}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"csa2: {name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
+    if (t.dtype is not dtype or t.get_device() != dev or t.shape != shape or
+            not t.is_contiguous()):
+        raise ValueError(f"csa2: {name} must be a contiguous {dtype} tensor of shape "
+                         f"{tuple(shape)} on cuda:{dev} (got {t.dtype}, {tuple(t.shape)} on "
+                         f"{t.device})")
     return t.data_ptr()
 
 
-def _stream_on(stream, device):
-    """The stream of a call on `device`; the caller makes that device current."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"csa2: the stream belongs to {s.device}, the tensors to {device}")
-    return s.cuda_stream
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with GPU dev current; the stream is one of that GPU's."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index == dev:
+        s = stream.cuda_stream
+    else:
+        raise ValueError(f"csa2: the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    if dev == torch.cuda.current_device():
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        _check(st)
 
 
 def csa2_paged_append(kv, cu_seqlens, start_row, cache: Paged, inv_freq=None, ratio=1,
                       stream=None):
     """Rows kv [T, 512] bf16 (row stride a multiple of 8) into the cache, rotated by their
     position j * ratio when inv_freq is given."""
-    dev = cache.data.device
-    if kv.dtype != torch.bfloat16 or kv.dim() != 2 or kv.shape[1] != 512 or kv.device != dev:
-        raise ValueError(f"csa2: kv must be [T, 512] bf16 on {dev}")
+    dev, B = cache._dev, cache._c.B
     T = kv.shape[0]
-    if T > 0 and kv.stride(1) != 1:
-        raise ValueError("csa2: the rows of kv must be dense")
-    B = cache.table.shape[0]
-    args = (kv.data_ptr(), kv.stride(0) if T > 1 else 512, T,
-            _arg("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev),
-            _arg("start_row", start_row, torch.int64, (B,), dev), ratio, ctypes.byref(cache.c()),
-            _arg("inv_freq", inv_freq, torch.float32, (32,), dev), _stream_on(stream, dev))
-    if dev.index == torch.cuda.current_device():
-        _check(lib().csa2_paged_append(*args))
-    else:
-        with torch.cuda.device(dev):
-            _check(lib().csa2_paged_append(*args))
+    if (kv.dtype is not torch.bfloat16 or kv.get_device() != dev or kv.shape != (T, 512) or
+            (T > 0 and kv.stride(1) != 1)):
+        raise ValueError(f"csa2: kv must be [T, 512] bf16 with dense rows on cuda:{dev}")
+    _call(lib().csa2_paged_append, dev, stream, kv.data_ptr(), kv.stride(0) if T > 1 else 512, T,
+          _arg("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev),
+          _arg("start_row", start_row, torch.int64, (B,), dev), ratio, cache.c(),
+          _arg("inv_freq", inv_freq, torch.float32, (32,), dev))
 
 
 def csa2_paged_attn_workspace_size(Q, H, max_rows):
@@ -481,22 +486,17 @@ def csa2_paged_attn(q, q_seq, q_pos, cache: Paged, out, ws=None, max_rows=None, 
                     sink=None, lse=None, scale=512 ** -0.5, inv_freq=None, stream=None):
     """Dense attention of q [Q, H, 512] over the paged rows each query sees; max_rows bounds
     them (None: what the page table can hold)."""
-    dev = cache.data.device
+    dev = cache._dev
     if q.dim() != 3:
         raise ValueError("csa2: q must be [Q, H, 512]")
-    Q, H = q.shape[0], q.shape[1]
+    Q, H, _ = q.shape
     if max_rows is None:
         max_rows = cache.table.shape[1] * cache.data.shape[1]
-    args = (_arg("q", q, torch.bfloat16, (Q, H, 512), dev), Q, H,
-            _arg("q_seq", q_seq, torch.int32, (Q,), dev),
-            _arg("q_pos", q_pos, torch.int64, (Q,), dev), ctypes.byref(cache.c()), ratio, window,
-            max_rows, _arg("sink", sink, torch.float32, (H,), dev), scale,
-            _arg("out", out, torch.bfloat16, (Q, H, 512), dev),
-            _arg("lse", lse, torch.float32, (Q, H), dev),
-            _arg("inv_freq", inv_freq, torch.float32, (32,), dev), _p(ws),
-            0 if ws is None else ws.numel() * ws.element_size(), _stream_on(stream, dev))
-    if dev.index == torch.cuda.current_device():
-        _check(lib().csa2_paged_attn(*args))
-    else:
-        with torch.cuda.device(dev):
-            _check(lib().csa2_paged_attn(*args))
+    _call(lib().csa2_paged_attn, dev, stream, _arg("q", q, torch.bfloat16, (Q, H, 512), dev), Q, H,
+          _arg("q_seq", q_seq, torch.int32, (Q,), dev),
+          _arg("q_pos", q_pos, torch.int64, (Q,), dev), cache.c(), ratio, window, max_rows,
+          _arg("sink", sink, torch.float32, (H,), dev), scale,
+          _arg("out", out, torch.bfloat16, (Q, H, 512), dev),
+          _arg("lse", lse, torch.float32, (Q, H), dev),
+          _arg("inv_freq", inv_freq, torch.float32, (32,), dev), _p(ws),
+          0 if ws is None else ws.numel() * ws.element_size())

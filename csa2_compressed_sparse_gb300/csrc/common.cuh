@@ -189,6 +189,7 @@ struct PagedAttnArgs {
   int box_rows;           // rows per tensor copy: the largest of 64, 32, 16, 8 dividing page_rows
   int shared;             // more items than sequences: rows are read more than once
   int nctas;
+  int cluster;            // CTAs per item of a small call (a cluster if more than one), else 0
   // workspace: parts [2 nctas][padded heads * 512], their m, l, r, and each item's CTA range
   float* part;
   float* pstat;
@@ -200,7 +201,9 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, int sms, cudaStream_t 
 int paged_head_pad(int H);    // heads of an item, padded: 16, 32 or 64
 int paged_unit_tiles();
 int paged_max_ctas();         // most CTAs of one attention call
-cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool join, cudaStream_t s);
+int paged_cluster(int64_t items, int64_t tiles, int sms);  // PagedAttnArgs::cluster
+// units: the most units an item can have that are joined through the workspace (1: none is)
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int units, cudaStream_t s);
 // One CTA whose bounded wait runs out after limit_ns (test of the timeout path).
 cudaError_t launch_wait_timeout(uint64_t limit_ns, cudaStream_t s);
 cudaError_t launch_index(const IndexArgs& a, int num_sms, cudaStream_t s);

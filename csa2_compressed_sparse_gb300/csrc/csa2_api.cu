@@ -737,7 +737,14 @@ csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_s
   // tiles an item can have: a window of w rows touches at most (w + 62) / 64 + 1
   const int64_t most = (a.cap_rows + 63) / 64;
   const int64_t tiles = window > 0 && (window + 62) / 64 + 1 < most ? (window + 62) / 64 + 1 : most;
-  cudaError_t e = csa2::launch_paged_attn(a, tiles > a.ut, stream);
+  const int64_t items = (int64_t)Q * a.ng;
+  a.cluster = csa2::paged_cluster(items, tiles, sms);
+  if (a.cluster > 0) {
+    a.ut = 1;
+    a.nctas = (int)items * a.cluster;
+  }
+  const int units = a.cluster > 0 ? 1 : (int)((tiles + a.ut - 1) / a.ut);
+  cudaError_t e = csa2::launch_paged_attn(a, units, stream);
   if (e != cudaSuccess) return cuda_fail(e, name);
   return CSA2_OK;
 }

@@ -205,6 +205,10 @@ __global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppen
 // there; of the others each CTA writes its part (O^T unscaled, running maximum and sums, in
 // fp32) to the workspace and paged_join_kernel joins them.
 //
+// A small call (kDirect, see paged_cluster) deals a.cluster CTAs to each item instead, one or a
+// cluster that shares the item's tiles and joins in distributed shared memory: no plan over
+// all items, one launch, no workspace.
+//
 // A tile passes through a ring of 16 KiB slots, each a quarter of it (64 rows x 128 dims, as
 // eight groups of 8 rows, two 128-byte-swizzled blocks of 64 dims each):
 //   load     warps 12..15, a quarter each: one tensor copy per page piece (bf16 rows), or
@@ -249,8 +253,7 @@ struct __align__(16) PagedAux {
   uint64_t p_full[2], pv_done;  // p_full: two quarters' P of scaled rows, else [0]
   uint64_t fin[2];
   uint64_t mask[4];     // valid rows of tile c at c & 3
-  int64_t it0;          // first item of this CTA and the units before it within the item
-  int64_t it0_unit;
+  int it0, it0_unit;    // first item of this CTA and the units before it within the item
   float fac[64];        // rescale factor or 1 / sum, per head
   float rope_c[32], rope_s[32];
   uint32_t tmem_slot;
@@ -465,8 +468,8 @@ __device__ __forceinline__ void walk_fit(const PagedAttnArgs& a, Walk& w) {
 }
 __device__ __forceinline__ void walk_start(const PagedAttnArgs& a, const PagedAux& X, int64_t left,
                                            Walk& w) {
-  w.it = (int)X.it0;
-  w.unit = (int)X.it0_unit;
+  w.it = X.it0;
+  w.unit = X.it0_unit;
   w.left = left;
   w.i = load_item(a, w.it, false);
   walk_fit(a, w);
@@ -484,6 +487,24 @@ __device__ __forceinline__ bool walk_next(const PagedAttnArgs& a, Walk& w) {
   return true;
 }
 
+// Four heads of a pair of dims: (x, y) += w * (part's two dims).
+__device__ __forceinline__ void join_add(float (&acc)[8], const float4& x, const float4& y,
+                                         const float4& w) {
+  acc[0] = fmaf(x.x, w.x, acc[0]);
+  acc[1] = fmaf(x.y, w.y, acc[1]);
+  acc[2] = fmaf(x.z, w.z, acc[2]);
+  acc[3] = fmaf(x.w, w.w, acc[3]);
+  acc[4] = fmaf(y.x, w.x, acc[4]);
+  acc[5] = fmaf(y.y, w.y, acc[5]);
+  acc[6] = fmaf(y.z, w.z, acc[6]);
+  acc[7] = fmaf(y.w, w.w, acc[7]);
+}
+
+// A 32-bit store into shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
+
 // Valid rows of the 64-row tile that begins at row r0, as bits.
 __device__ __forceinline__ uint64_t tile_mask(int64_t r0, int lo, int hi) {
   const int64_t f = lo - r0, l = hi - r0;  // first valid, end
@@ -493,7 +514,7 @@ __device__ __forceinline__ uint64_t tile_mask(int64_t r0, int lo, int hi) {
   return m;
 }
 
-template <int kHp, int kMode>
+template <int kHp, int kMode, bool kDirect>
 __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     paged_attn_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap) {
@@ -543,9 +564,19 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   }
   // ---- the plan: every CTA sums the units of all items (positions only: they are this
   // call's own inputs) and finds its share of them ----
-  int64_t u0, u1, U;
-  int64_t ncta;
-  {
+  int64_t u0, u1, U = 0;
+  int64_t ncta = 1;
+  const int cl = kDirect ? a.cluster : 1, crank = kDirect && cl > 1 ? (int)cluster_ctarank() : 0;
+  if (kDirect) {
+    const int it = blockIdx.x / cl;
+    const int tiles = load_item(a, it, crank == 0 && tid == 0).units;
+    u0 = (int64_t)tiles * crank / cl;
+    u1 = (int64_t)tiles * (crank + 1) / cl;
+    if (tid == 0) {
+      X.it0 = it;
+      X.it0_unit = (int)u0;
+    }
+  } else {
     const int64_t items = (int64_t)a.Q * a.ng;
     const int64_t per = (items + C::kThreads - 1) / C::kThreads;
     const int64_t i0 = tid * per, i1 = i0 + per < items ? i0 + per : items;
@@ -576,8 +607,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       for (int64_t i = i0; i < i1; ++i) {
         const int n = load_item(a, i, false).units;
         if (u0 < at + n) {
-          X.it0 = i;
-          X.it0_unit = u0 - at;
+          X.it0 = (int)i;
+          X.it0_unit = (int)(u0 - at);
           break;
         }
         at += n;
@@ -616,7 +647,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           if (hA < Hg) mA = a.sink[64 * w.i.hg + hA] * kLog2e;
           if (hB < Hg) mB = a.sink[64 * w.i.hg + hB] * kLog2e;
         }
-        const bool whole = w.unit == 0 && w.seg_units == w.i.units;
+        const bool whole = kDirect ? cl == 1 : w.unit == 0 && w.seg_units == w.i.units;
         const float sinkA = mA, sinkB = mB;
         // what the output needs is computed while the first tile loads
         if (whole && a.inv_freq && warp == C::kWarpS - 1) {
@@ -875,6 +906,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         }
         const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
         soft_sync<C::kSoft>();
+        if (kDirect && cl > 1) break;  // the cluster joins below
         if (tid < Hg) {
           float l = Y.lsum[0][tid], r = Y.rsum[0][tid];
 #pragma unroll
@@ -892,14 +924,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             X.fac[tid] = r > 0.f || r != r ? 1.f / r : 0.f;  // no row and no sink: zeros
             if (a.lse)
               a.lse[w.i.q * a.H + 64 * w.i.hg + tid] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
-          } else {
+          } else if (!kDirect) {
             float* st = a.pstat + part * (3 * kHp) + tid;
             st[0] = m;
             st[kHp] = l;
             st[2 * kHp] = r;
           }
         }
-        if (a.rec && w.unit == 0 && tid == 0) {
+        if (!kDirect && a.rec && w.unit == 0 && tid == 0) {
           // CTAs of the item's first and last unit; (-1, -1): finished here
           const int64_t ul = u + w.i.units - 1;
           a.rec[w.it] = whole ? make_int2(-1, -1)
@@ -920,8 +952,13 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               tmem_ld16(tmem + lrow + kColO + 64 * mt + hb, v);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                v[j] = __float_as_uint(__uint_as_float(v[j]) * X.fac[hb + j]);
+              for (int j = 0; j < 16; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&X.fac[hb + j]);
+                v[j] = __float_as_uint(__uint_as_float(v[j]) * f.x);
+                v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f.y);
+                v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f.z);
+                v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f.w);
+              }
               if (rot) {  // pair (2i, 2i + 1) times e^{-i p theta_i}: the partner is lane ^ 1
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
@@ -943,7 +980,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               }
             }
           }
-        } else {
+        } else if (!kDirect) {
           // [dim tile][four heads][128 dims][4]: a lane writes 16 bytes, a warp 512
           float* po = a.part + part * (int64_t)(kHp * kDLat) + (quad * 32 + lane) * 4;
 #pragma unroll 1
@@ -1303,6 +1340,111 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (kDirect && cl > 1) {
+    // Each CTA owns 512 / cluster dims.  Once all are done with their rings, every CTA writes its
+    // O^T (unscaled) into the rings of the dims' owners and its m, l, r to all; then the owners
+    // weigh, sum and store.
+    const int lg = cl == 8 ? 3 : cl == 4 ? 2 : 1;
+    const int slice = kDLat >> lg;
+    constexpr bool kTail = NS * kSlotBytes >= kHp * 2048 + 8 * 3 * kHp * 4;
+    // [rank][m, l, r][head], in every CTA
+    const uint32_t st_off = kTail ? (uint32_t)(C::kQBytes + kHp * 2048)
+                                  : (uint32_t)(C::kQBytes + NS * kSlotBytes + sizeof(PagedSpare));
+    static_assert(kTail || C::kPBytes >= (int)sizeof(PagedSpare) + 8 * 3 * kHp * 4, "room for m, l, r");
+    float* st = reinterpret_cast<float*>(smem + st_off);
+    const Item I = load_item(a, blockIdx.x / cl, false);
+    const bool live = I.units > 0;  // the same in the whole cluster
+    const int Hg = min(64, a.H - 64 * I.hg);
+    float own[3] = {-INFINITY, 0.f, 0.f};
+    if (live && tid < kHp && u1 > u0) {
+      own[0] = Y.m_run[tid];
+#pragma unroll
+      for (int i = 0; i < C::kParts; ++i) {
+        own[1] += Y.lsum[i][tid];
+        own[2] += Y.rsum[i][tid];
+      }
+    }
+    cluster_sync();
+    if (live && tid < kHp)
+      for (int o = 0; o < cl; ++o)
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          st_cluster32(dsmem_addr(smem_u32(st + (crank * 3 + i) * kHp + tid), o),
+                       __float_as_uint(own[i]));
+    if (live && u1 > u0 && warp < C::kWarpS) {
+#pragma unroll 1
+      for (int mt = warp >> 2; mt < 4; mt += C::kParts) {
+        const int d = mt * 128 + (warp & 3) * 32 + lane;
+        const uint32_t to = dsmem_addr(
+            ring + (uint32_t)((crank * (kHp / 4)) * slice + (d & (slice - 1))) * 16, d >> (9 - lg));
+#pragma unroll 1
+        for (int hb = 0; hb < Hg; hb += 16) {
+          uint32_t v[16];
+          tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColO + 64 * mt + hb, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st_cluster16(to + (uint32_t)((hb >> 2) + j) * slice * 16,
+                         make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+        }
+      }
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (live && tid >= Hg && tid < kHp)  // heads that are padding weigh nothing
+      for (int o = 0; o < cl; ++o) st[o * 3 * kHp + tid] = 0.f;
+    if (live && tid < Hg) {
+      const float sink = a.sink ? a.sink[64 * I.hg + tid] * kLog2e : -INFINITY;
+      float M = sink, l = 0.f, r = 0.f;
+      for (int o = 0; o < cl; ++o) M = fmaxf(M, st[o * 3 * kHp + tid]);
+      const float Mf = M == -INFINITY ? 0.f : M;
+      for (int o = 0; o < cl; ++o) {
+        float* so = st + o * 3 * kHp + tid;
+        const float w = ex2(so[0] - Mf);
+        so[0] = w;
+        l = fmaf(w, so[kHp], l);
+        r = fmaf(w, so[2 * kHp], r);
+      }
+      if (sink > -INFINITY) {
+        l += ex2(sink - Mf);
+        r += ex2(sink - Mf);
+      }
+      X.fac[tid] = r > 0.f || r != r ? 1.f / r : 0.f;
+      if (a.lse && crank == 0)
+        a.lse[I.q * a.H + 64 * I.hg + tid] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
+    }
+    __syncthreads();
+    if (live) {
+      const int half = slice >> 1;  // pairs of dims
+      for (int i = tid; i < (kHp / 4) * half; i += C::kThreads) {
+        const int hc = i >> (8 - lg), pair = i & (half - 1);
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int o = 0; o < cl; ++o) {
+          const float4 w = *reinterpret_cast<const float4*>(st + o * 3 * kHp + 4 * hc);
+          // a CTA without tiles wrote nothing, and its weights are zero
+          if (!(w.x != 0.f || w.y != 0.f || w.z != 0.f || w.w != 0.f)) continue;
+          const float4* b = reinterpret_cast<const float4*>(smem + C::kQBytes) +
+                            (o * (kHp / 4) + hc) * slice + 2 * pair;
+          join_add(acc, b[0], b[1], w);
+        }
+        const int d = crank * slice + 2 * pair;
+        float cs = 1.f, sn = 0.f;
+        if (a.inv_freq && d >= kRopeDim0)
+          sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), (uint64_t)a.q_pos[I.q]),
+                  &sn, &cs);
+        uint16_t* out = a.out + (I.q * a.H + 64 * I.hg) * kDLat + d;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (4 * hc + h >= Hg) break;
+          const float x0 = acc[h] * X.fac[4 * hc + h], x1 = acc[4 + h] * X.fac[4 * hc + h];
+          __stcs(reinterpret_cast<unsigned int*>(out + (4 * hc + h) * kDLat),
+                 pack_bf16x2(x0 * cs + x1 * sn, x1 * cs - x0 * sn));
+        }
+      }
+    }
+    __syncthreads();
+  }
   if (warp == C::kWarpS) tmem_dealloc(tmem, 512);
 }
 
@@ -1319,19 +1461,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 constexpr int kMaxCtas = 152;
 constexpr int kFewItems = 16;
 constexpr int kAhead = 4;
-
-// Four heads of a pair of dims: (x, y) += w * (part's two dims).
-__device__ __forceinline__ void join_add(float (&acc)[8], const float4& x, const float4& y,
-                                         const float4& w) {
-  acc[0] = fmaf(x.x, w.x, acc[0]);
-  acc[1] = fmaf(x.y, w.y, acc[1]);
-  acc[2] = fmaf(x.z, w.z, acc[2]);
-  acc[3] = fmaf(x.w, w.w, acc[3]);
-  acc[4] = fmaf(y.x, w.x, acc[4]);
-  acc[5] = fmaf(y.y, w.y, acc[5]);
-  acc[6] = fmaf(y.z, w.z, acc[6]);
-  acc[7] = fmaf(y.w, w.w, acc[7]);
-}
 
 template <int kGroups>
 __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs a, int hp) {
@@ -1464,24 +1593,34 @@ __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs 
   }
 }
 
-template <int kHp, int kMode>
+template <int kHp, int kMode, bool kDirect>
 cudaError_t launch_attn_inst(const PagedAttnArgs& a, const CUtensorMap& qm, const CUtensorMap& km,
                              cudaStream_t s) {
   using C = PagedCfg<kHp, kMode>;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<kHp, kMode>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  auto kern = paged_attn_kernel<kHp, kMode, kDirect>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_attn_kernel<kHp, kMode>, dim3((unsigned)a.nctas), dim3(C::kThreads),
-                    C::kSmem, s, a, qm, km);
+  const dim3 grid((unsigned)a.nctas), block(C::kThreads);
+  return kDirect && a.cluster > 1
+             ? launch_pdl_cluster(kern, grid, block, C::kSmem, s, (unsigned)a.cluster, a, qm, km)
+             : launch_pdl(kern, grid, block, C::kSmem, s, a, qm, km);
+}
+
+template <int kHp, int kMode>
+cudaError_t launch_attn_kind(const PagedAttnArgs& a, const CUtensorMap& qm, const CUtensorMap& km,
+                             cudaStream_t s) {
+  return a.cluster > 0 ? launch_attn_inst<kHp, kMode, true>(a, qm, km, s)
+                       : launch_attn_inst<kHp, kMode, false>(a, qm, km, s);
 }
 
 template <int kHp>
 cudaError_t launch_attn_mode(const PagedAttnArgs& a, const CUtensorMap& qm, const CUtensorMap& km,
                              cudaStream_t s) {
   switch (a.cache.dtype) {
-    case 0: return launch_attn_inst<kHp, 0>(a, qm, km, s);
-    case 1: return launch_attn_inst<kHp, 1>(a, qm, km, s);
-    default: return launch_attn_inst<kHp, 2>(a, qm, km, s);
+    case 0: return launch_attn_kind<kHp, 0>(a, qm, km, s);
+    case 1: return launch_attn_kind<kHp, 1>(a, qm, km, s);
+    default: return launch_attn_kind<kHp, 2>(a, qm, km, s);
   }
 }
 
@@ -1507,7 +1646,20 @@ int paged_unit_tiles() { return 4; }
 
 int paged_max_ctas() { return kMaxCtas; }
 
-cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool join, cudaStream_t s) {
+// CTAs per item of a small call, 0 for one whose tiles are dealt evenly to all CTAs and joined
+// through the workspace.  An item of up to four tiles takes one CTA.  The tiles of a
+// longer one are shared by 8, 4 or 2, as many as all items leave room for (clusters of eight do
+// not fill every SM): up to 32 tiles an item, where lengths below the caller's bound cost
+// little.  Measured, us, equal lengths, clusters against even dealing: 8 sequences of 16 tiles
+// 17.1 / 18.0, 33 of 32 tiles 27.9 / 41.7, 66 of 16 tiles 29.1 / 41.6; up to seven sequences of
+// more than 16 tiles go the other way (one of 32: 18.9 / 16.4).
+int paged_cluster(int64_t items, int64_t tiles, int sms) {
+  if (tiles <= paged_unit_tiles()) return items <= sms ? 1 : 0;
+  if (tiles > 32 || (tiles > 16 && items < 8)) return 0;
+  return items <= sms / 10 ? 8 : items <= (sms - 16) / 4 ? 4 : items <= (sms - 16) / 2 ? 2 : 0;
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, int units, cudaStream_t s) {
   if (a.Q == 0) return cudaSuccess;
   const int hp = paged_head_pad(a.H);
   CUtensorMap qm, km;
@@ -1524,9 +1676,9 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, bool join, cudaStream_t s)
   cudaError_t e = hp == 16   ? launch_attn_mode<16>(a, qm, km, s)
                   : hp == 32 ? launch_attn_mode<32>(a, qm, km, s)
                              : launch_attn_mode<64>(a, qm, km, s);
-  if (e != cudaSuccess || !join) return e;
+  if (e != cudaSuccess || units <= 1) return e;
   const dim3 grid((unsigned)(a.Q * a.ng), (unsigned)hp);
-  return a.Q * a.ng <= kFewItems
+  return a.Q * a.ng <= kFewItems && units > 4 * kFewItems
              ? launch_pdl(paged_join_kernel<16>, grid, dim3(1024), 0, s, a, hp)
              : launch_pdl(paged_join_kernel<4>, grid, dim3(256), 0, s, a, hp);
 }
