@@ -243,7 +243,7 @@ struct __align__(16) PagedSpare {
   float lsum[2][64], rsum[2][64];  // sums of P by part: unrounded, rounded
   float m_run[64], sink2[64];
 };
-static_assert(sizeof(PagedSpare) <= 16 * 128, "P's buffer of 16 heads holds it");
+static_assert(sizeof(PagedSpare) <= 8192, "it shares P's memory");
 
 struct __align__(16) PagedAux {
   uint64_t full[12], empty[12];  // ring slots
@@ -278,7 +278,9 @@ struct PagedCfg {
   static constexpr int kQBlock = kHp * 128;
   static constexpr int kQBytes = 8 * kQBlock;
   static constexpr int kPBufs = kScaled ? 4 : 1;  // scaled rows have a P per quarter
-  static constexpr int kPBytes = kHp * 128 * kPBufs;
+  // P's memory also stages the output: a KiB for each softmax warp
+  static constexpr int kPUsed = kHp * 128 * kPBufs;
+  static constexpr int kPBytes = kPUsed > 8192 ? kPUsed : 8192;
   // scales [tile][quarter][row] of the last kScTiles tiles: a tile's are written with its last
   // quarter, whose slot with eight slots was the last quarter's two tiles before
   static constexpr int kScTiles = kHp == 64 ? 2 : 4;
@@ -503,6 +505,88 @@ __device__ __forceinline__ void join_add(float (&acc)[8], const float4& x, const
 // A 32-bit store into shared memory of a CTA of the cluster.
 __device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
+
+// The low 16 bits of v into shared memory.
+__device__ __forceinline__ void st_shared16b(uint32_t addr, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 h, l;\n\tmov.b32 {l, h}, %1;\n\tst.shared.b16 [%0], l;\n\t}" ::"r"(addr),
+               "r"(v)
+               : "memory");
+}
+
+// A head's running maximum and sums over the parts of the softmax warps.
+struct HeadSums {
+  float m, l, r;  // maximum; sums of P, unrounded and rounded
+};
+template <int kParts>
+__device__ __forceinline__ HeadSums head_sums(const PagedSpare& Y, int h) {
+  HeadSums s = {Y.m_run[h], Y.lsum[0][h], Y.rsum[0][h]};
+#pragma unroll
+  for (int i = 1; i < kParts; ++i) {
+    s.l += Y.lsum[i][h];
+    s.r += Y.rsum[i][h];
+  }
+  return s;
+}
+// Adds the sink's mass, stores lse and leaves 1 / Z in X.fac.
+__device__ __forceinline__ void finish_head(const PagedAttnArgs& a, PagedAux& X, HeadSums s,
+                                            float sink, int h, const Item& i) {
+  if (sink > -INFINITY) {
+    s.l += ex2(sink - s.m);
+    s.r += ex2(sink - s.m);
+  }
+  X.fac[h] = s.r > 0.f || s.r != s.r ? 1.f / s.r : 0.f;  // no row and no sink: zeros
+  if (a.lse)
+    a.lse[i.q * a.H + 64 * i.hg + h] = s.l == 0.f ? -INFINITY : (s.m + __log2f(s.l)) * kLn2;
+}
+
+// Dims 128 mt + 32 quad .. + 31 of all heads by one warp: O^T from TMEM (lane = dim) times 1 / Z
+// and rotated back, in bf16 through a KiB of shared memory at `stage` (16 heads x 32 dims: a lane
+// writes its dim of each head and reads 16 bytes of two heads).
+__device__ __forceinline__ void store_tile(const PagedAttnArgs& a, const PagedAux& X, uint32_t tq,
+                                           int mt, int quad, int lane, int Hg, uint32_t stage,
+                                           uint16_t* out) {
+  const int d = mt * 128 + quad * 32 + lane;
+  const bool rot = a.inv_freq && d >= kRopeDim0;  // the same in a warp
+  const float cs = rot ? X.rope_c[(d - kRopeDim0) >> 1] : 1.f;
+  const float sn = rot ? X.rope_s[(d - kRopeDim0) >> 1] : 0.f;
+#pragma unroll 1
+  for (int hb = 0; hb < Hg; hb += 16) {
+    uint32_t v[16];
+    tmem_ld16(tq + kColO + 64 * mt + hb, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&X.fac[hb + j]);
+      v[j] = __float_as_uint(__uint_as_float(v[j]) * f.x);
+      v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f.y);
+      v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f.z);
+      v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f.w);
+    }
+    if (rot) {  // pair (2i, 2i + 1) times e^{-i p theta_i}: the partner is lane ^ 1
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float x = __uint_as_float(v[j]);
+        const float pt = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+        v[j] = __float_as_uint((lane & 1) ? x * cs - pt * sn : x * cs + pt * sn);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+      const uint32_t two = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+      st_shared16b(stage + j * 64 + lane * 2, two);
+      st_shared16b(stage + (j + 1) * 64 + lane * 2, two >> 16);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = hb + 8 * i + (lane >> 2);
+      const uint4 x = ld_shared16(stage + (8 * i + (lane >> 2)) * 64 + (lane & 3) * 16);
+      if (h < Hg)
+        __stcs(reinterpret_cast<uint4*>(out + h * kDLat + mt * 128 + quad * 32) + (lane & 3), x);
+    }
+    __syncwarp();
+  }
 }
 
 // Valid rows of the 64-row tile that begins at row r0, as bits.
@@ -906,32 +990,19 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         }
         const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
         soft_sync<C::kSoft>();
-        if (kDirect && cl > 1) break;  // the cluster joins below
+        if (kDirect) break;  // the output, by more warps, or the cluster's join follows below
         if (tid < Hg) {
-          float l = Y.lsum[0][tid], r = Y.rsum[0][tid];
-#pragma unroll
-          for (int i = 1; i < kParts; ++i) {
-            l += Y.lsum[i][tid];
-            r += Y.rsum[i][tid];
-          }
-          const float m = Y.m_run[tid];
+          const HeadSums h = head_sums<kParts>(Y, tid);
           if (whole) {
-            const float sk = Y.sink2[tid];
-            if (sk > -INFINITY) {
-              l += ex2(sk - m);
-              r += ex2(sk - m);
-            }
-            X.fac[tid] = r > 0.f || r != r ? 1.f / r : 0.f;  // no row and no sink: zeros
-            if (a.lse)
-              a.lse[w.i.q * a.H + 64 * w.i.hg + tid] = l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;
-          } else if (!kDirect) {
+            finish_head(a, X, h, Y.sink2[tid], tid, w.i);
+          } else {
             float* st = a.pstat + part * (3 * kHp) + tid;
-            st[0] = m;
-            st[kHp] = l;
-            st[2 * kHp] = r;
+            st[0] = h.m;
+            st[kHp] = h.l;
+            st[2 * kHp] = h.r;
           }
         }
-        if (!kDirect && a.rec && w.unit == 0 && tid == 0) {
+        if (a.rec && w.unit == 0 && tid == 0) {
           // CTAs of the item's first and last unit; (-1, -1): finished here
           const int64_t ul = u + w.i.units - 1;
           a.rec[w.it] = whole ? make_int2(-1, -1)
@@ -940,47 +1011,9 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         soft_sync<C::kSoft>();
         if (whole) {
           uint16_t* out = a.out + (w.i.q * a.H + 64 * w.i.hg) * kDLat;
-#pragma unroll 1
-          for (int mt = half; mt < 4; mt += kParts) {
-            const int d = mt * 128 + quad * 32 + lane;
-            const bool rot = a.inv_freq && d >= kRopeDim0;  // uniform in a warp
-            const float cs = rot ? X.rope_c[(d - kRopeDim0) >> 1] : 1.f;
-            const float sn = rot ? X.rope_s[(d - kRopeDim0) >> 1] : 0.f;
-#pragma unroll 1
-            for (int hb = 0; hb < Hg; hb += 16) {
-              uint32_t v[16];
-              tmem_ld16(tmem + lrow + kColO + 64 * mt + hb, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&X.fac[hb + j]);
-                v[j] = __float_as_uint(__uint_as_float(v[j]) * f.x);
-                v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f.y);
-                v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f.z);
-                v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f.w);
-              }
-              if (rot) {  // pair (2i, 2i + 1) times e^{-i p theta_i}: the partner is lane ^ 1
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float x = __uint_as_float(v[j]);
-                  const float pt = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-                  v[j] = __float_as_uint((lane & 1) ? x * cs - pt * sn : x * cs + pt * sn);
-                }
-              }
-#pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float a0 = __uint_as_float(v[j]), a1 = __uint_as_float(v[j + 1]);
-                const float rcv = __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? a0 : a1, 1);
-                // the even lane writes head hb + j at dims (d, d + 1), the odd one head
-                // hb + j + 1 at (d - 1, d)
-                const int hr = hb + j + (lane & 1);
-                if (hr < Hg)
-                  __stcs(reinterpret_cast<unsigned int*>(out + hr * kDLat + (d & ~1)),
-                         (lane & 1) ? pack_bf16x2(rcv, a1) : pack_bf16x2(a0, rcv));
-              }
-            }
-          }
-        } else if (!kDirect) {
+          for (int mt = half; mt < 4; mt += kParts)
+            store_tile(a, X, tmem + lrow, mt, quad, lane, Hg, p_s + warp * 1024, out);
+        } else {
           // [dim tile][four heads][128 dims][4]: a lane writes 16 bytes, a warp 512
           float* po = a.part + part * (int64_t)(kHp * kDLat) + (quad * 32 + lane) * 4;
 #pragma unroll 1
@@ -1136,7 +1169,9 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     } else if (kMode == 0) {
       // ================= bf16 rows by tensor copies: warp k quarter k =================
       const int k = warp - C::kWarpL;
-      griddep_wait();  // rows and table entries may come from the kernel before this one
+      // rows may come from the kernel before this one (an append); the table is this call's own
+      // input, so the first pages are looked up before the wait
+      bool waited = false;
       Walk w;
       walk_start(a, X, u1 - u0, w);
       const uint64_t pol = a.shared ? policy_evict_normal() : policy_evict_first();
@@ -1166,6 +1201,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           }
           m <<= cl * R;
           for (int o = 1; o < nc; o <<= 1) m |= __shfl_xor_sync(0xFFFFFFFFu, m, o);
+          if (!waited) griddep_wait();
+          waited = true;
           const int te = min(tbeg + tb, w.t_end);
           for (int t = tbeg; ok && t < te; ++t, ++c) {
             const int src = (t - tbeg) * nc;
@@ -1207,7 +1244,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       // tile and of each quarter dims 16 (t % 4) .. and 64 + 16 (t % 4) .., two loads of 64 whole
       // bytes a row and stores free of bank conflicts.  The instructions issued are the limit, so
       // a thread has one row, whose page is looked up a turn ahead.
-      griddep_wait();
       const int grp = (warp - C::kWarpL) >> 3, t256 = (tid - 32 * C::kWarpL) & 255;
       const int r = t256 >> 2, pc = t256 & 3;
       Walk w;
@@ -1269,6 +1305,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       if (grp == 1) step();
       bool have = look(page, row);
       uint32_t bits = place(page, row, src);
+      griddep_wait();  // rows may come from the kernel before this one; the table does not
       fetch(src);
       bool nxt = look(page, row);
       int c = grp, sl = 4 * grp;
@@ -1340,6 +1377,18 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (kDirect && cl == 1 && u1 > u0) {
+    // the item's output by sixteen warps (the ring is empty: it stages them)
+    const Item I = load_item(a, X.it0, false);
+    const int Hg = min(64, a.H - 64 * I.hg);
+    if (tid < Hg) finish_head(a, X, head_sums<C::kParts>(Y, tid), Y.sink2[tid], tid, I);
+    __syncthreads();
+    if (warp < 16)
+      store_tile(a, X, tmem + ((uint32_t)((warp & 3) * 32) << 16), warp >> 2, warp & 3, lane, Hg,
+                 ring + warp * 1024, a.out + (I.q * a.H + 64 * I.hg) * kDLat);
+    tc_fence_before();
+    __syncthreads();
+  }
   if (kDirect && cl > 1) {
     // Each CTA owns 512 / cluster dims.  Once all are done with their rings, every CTA writes its
     // O^T (unscaled) into the rings of the dims' owners and its m, l, r to all; then the owners
@@ -1371,22 +1420,19 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         for (int i = 0; i < 3; ++i)
           st_cluster32(dsmem_addr(smem_u32(st + (crank * 3 + i) * kHp + tid), o),
                        __float_as_uint(own[i]));
-    if (live && u1 > u0 && warp < C::kWarpS) {
+    if (live && u1 > u0 && warp < 16) {
+      const int mt = warp >> 2, d = mt * 128 + (warp & 3) * 32 + lane;
+      const uint32_t to = dsmem_addr(
+          ring + (uint32_t)((crank * (kHp / 4)) * slice + (d & (slice - 1))) * 16, d >> (9 - lg));
 #pragma unroll 1
-      for (int mt = warp >> 2; mt < 4; mt += C::kParts) {
-        const int d = mt * 128 + (warp & 3) * 32 + lane;
-        const uint32_t to = dsmem_addr(
-            ring + (uint32_t)((crank * (kHp / 4)) * slice + (d & (slice - 1))) * 16, d >> (9 - lg));
-#pragma unroll 1
-        for (int hb = 0; hb < Hg; hb += 16) {
-          uint32_t v[16];
-          tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColO + 64 * mt + hb, v);
-          tmem_ld_wait();
+      for (int hb = 0; hb < Hg; hb += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kColO + 64 * mt + hb, v);
+        tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st_cluster16(to + (uint32_t)((hb >> 2) + j) * slice * 16,
-                         make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-        }
+        for (int j = 0; j < 4; ++j)
+          st_cluster16(to + (uint32_t)((hb >> 2) + j) * slice * 16,
+                       make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
       }
     }
     tc_fence_before();
