@@ -1498,29 +1498,31 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 //
 // Joins the parts of the items that several CTAs worked on: with M the largest running
 // maximum (and the sink logit), weights 2^(m - M) and Z = 2^(sink - M) + sum 2^(m - M) l,
-// out = sum 2^(m - M) O / Z.  A CTA takes one item, 128 dims and four heads, a thread a pair
-// of dims; its kGroups groups of 64 threads take every kGroups-th part, the first kAhead of
+// out = sum 2^(m - M) O / Z.  A CTA takes one item, 2 kPairs dims and four heads, a thread a pair
+// of dims; its kGroups groups of kPairs threads take every kGroups-th part, the first kAhead of
 // them loaded before the weights are known.  Of an item with up to kAhead parts, the usual
 // case in a batch, the CTA of every fourth four heads does sixteen heads, four per group, and
 // the CTAs beside it return: fewer, longer loads per thread (64 items: 19 -> 8 us).
-// Sixteen groups for up to kFewItems items, which may have 152 parts each; else four.
+// A single long item, which may have 152 parts, takes 32 groups and CTAs of 64 dims, else four of
+// 128 (whole calls, us: one sequence of 1024 tiles 31.7 with 32 groups / 40.2 with four, two of
+// them 45.9 / 45.4, sixteen of 512 tiles 140 / 104).
 constexpr int kMaxCtas = 152;
-constexpr int kFewItems = 16;
 constexpr int kAhead = 4;
 
-template <int kGroups>
-__global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs a, int hp) {
+template <int kGroups, int kPairs>
+__global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnArgs a, int hp) {
   __shared__ float4 wt[kMaxCtas];  // [part], or [part][four heads] for sixteen heads
   __shared__ float4 inv_s[4];
-  __shared__ float acc_s[kGroups > 4 ? 4 : kGroups - 1][8][64];
+  __shared__ float acc_s[kGroups / 2][8][kPairs];
   griddep_launch_dependents();
   const int64_t it = blockIdx.x;
-  const int mt = blockIdx.y & 3;
-  int hc = blockIdx.y >> 2;
+  constexpr int kCuts = 256 / kPairs;  // CTAs of four heads
+  const int cut = blockIdx.y % kCuts;
+  int hc = blockIdx.y / kCuts;
   const int64_t q = a.ng == 2 ? it >> 1 : it;
   const int hg = a.ng == 2 ? (int)(it & 1) : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int pair = tid & 63, grp = tid >> 6;
+  const int pair = tid % kPairs, grp = tid / kPairs;
   const int seq = a.q_seq[q];
   const bool live = 64 * hg + 4 * hc < a.H && seq >= 0 && seq < a.cache.B;
   griddep_wait();
@@ -1535,7 +1537,8 @@ __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs 
   const int s_beg = sixteen ? 0 : grp, s_step = sixteen ? 1 : kGroups;
   hc += hcl;
   const bool mine = 64 * hg + 4 * hc < a.H && 4 * hc < hp;
-  const float* src = a.part + (mt * (hp / 4) + hc) * 512 + pair * 8;
+  const int d = 2 * (cut * kPairs + pair);  // this thread's dims d, d + 1
+  const float* src = a.part + ((d >> 7) * (hp / 4) + hc) * 512 + (d & 127) * 4;
   float4 x[kAhead], y[kAhead];
   auto load = [&](int s0) {
 #pragma unroll
@@ -1550,7 +1553,7 @@ __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs 
   };
   load(s_beg);
   // weights and 1 / Z of a head by one warp
-  for (int hh = warp; hh < (sixteen ? 16 : 4); hh += 2 * kGroups) {
+  for (int hh = warp; hh < (sixteen ? 16 : 4); hh += kPairs * kGroups / 32) {
     const int hb = 4 * (hc - hcl) + hh, hq = 64 * hg + hb;
     const bool there = hq < a.H && hb < hp;
     const float sink = a.sink && there ? a.sink[hq] * kLog2e : -INFINITY;
@@ -1587,7 +1590,7 @@ __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs 
     r += sk;
     if (lane == 0) {
       reinterpret_cast<float*>(inv_s)[hh] = r > 0.f || r != r ? 1.f / r : 0.f;
-      if (a.lse && mt == 0 && there)
+      if (a.lse && cut == 0 && there)
         a.lse[q * a.H + hq] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
     }
   }
@@ -1602,28 +1605,22 @@ __global__ void __launch_bounds__(64 * kGroups) paged_join_kernel(PagedAttnArgs 
     load(s0 + kAhead * s_step);
   }
   if (!sixteen) {
-    // the groups' sums: sixteen fold into four through shared memory, four into one
 #pragma unroll
-    for (int top = kGroups; top > 1; top >>= 2) {
-      const int low = top / 4;  // groups that remain
+    for (int low = kGroups / 2; low > 0; low >>= 1) {  // the groups' sums fold in halves
+      if (grp >= low && grp < 2 * low) {
 #pragma unroll
-      for (int k = 1; k < 4; ++k) {
-        if (grp >= k * low && grp < (k + 1) * low) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc_s[grp - k * low][i][pair] = acc[i];
-        }
-        __syncthreads();
-        if (grp < low) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] += acc_s[grp][i][pair];
-        }
-        __syncthreads();
+        for (int i = 0; i < 8; ++i) acc_s[grp - low][i][pair] = acc[i];
       }
+      __syncthreads();
+      if (grp < low) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += acc_s[grp][i][pair];
+      }
+      __syncthreads();
     }
     if (grp > 0) return;
   }
   if (!mine) return;
-  const int d = mt * 128 + 2 * pair;
   float cs = 1.f, sn = 0.f;
   if (a.inv_freq && d >= kRopeDim0)
     sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), (uint64_t)a.q_pos[q]), &sn, &cs);
@@ -1723,10 +1720,10 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int units, cudaStream_t s)
                   : hp == 32 ? launch_attn_mode<32>(a, qm, km, s)
                              : launch_attn_mode<64>(a, qm, km, s);
   if (e != cudaSuccess || units <= 1) return e;
-  const dim3 grid((unsigned)(a.Q * a.ng), (unsigned)hp);
-  return a.Q * a.ng <= kFewItems && units > 4 * kFewItems
-             ? launch_pdl(paged_join_kernel<16>, grid, dim3(1024), 0, s, a, hp)
-             : launch_pdl(paged_join_kernel<4>, grid, dim3(256), 0, s, a, hp);
+  const unsigned items = (unsigned)(a.Q * a.ng);
+  return items == 1 && units > 64
+             ? launch_pdl(paged_join_kernel<32, 32>, dim3(items, 2u * hp), dim3(1024), 0, s, a, hp)
+             : launch_pdl(paged_join_kernel<4, 64>, dim3(items, (unsigned)hp), dim3(256), 0, s, a, hp);
 }
 
 }  // namespace csa2
