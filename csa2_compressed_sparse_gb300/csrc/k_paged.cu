@@ -431,7 +431,7 @@ __device__ __forceinline__ Item load_item(const PagedAttnArgs& a, int64_t it, bo
   int64_t hi;  // (p + 1) / ratio
   if (p < 0) hi = 0;
   else if (p < 0x7FFFFFFF) hi = (uint32_t)(p + 1) / (uint32_t)a.ratio;
-  else hi = p / a.ratio + (p % a.ratio == a.ratio - 1 ? 1 : 0);
+  else hi = (int64_t)min(((uint64_t)p + 1) / (uint64_t)a.ratio, (uint64_t)1 << 62);
   int64_t lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
   if (hi > a.cap_rows) {
     if (report) raise_fault(kFaultBounds);
@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         at += n;
       }
     }
+    fence_proxy_async_smem();  // the scan's sums lie where copies will land
   }
   tc_fence_before();
   __syncthreads();

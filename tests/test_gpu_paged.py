@@ -295,6 +295,104 @@ def test_more_queries_than_sms(dtype):
     run_case(32, dtype, 64, 64, [1] * 700)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,most", [(1, 2048), (7, 1000), (10, 2000), (15, 700), (20, 2048), (33, 900),
+                                    (50, 300), (66, 2000), (120, 256), (152, 200)])
+def test_small_batches_one_cluster_per_item(dtype, B, most):
+    """One CTA per item up to four tiles, else clusters of 8, 4 and 2 by the batch; lengths from
+    zero to the bound, so some CTAs of a cluster have no tile; padded queries among them."""
+    rng = np.random.default_rng(B)
+    lens = [most] + [int(n) for n in rng.integers(0, most + 1, B - 1)]
+    run_case(100 + B, dtype, 64, 64, lens, pad=1 if B < 100 else 0)
+    run_case(200 + B, dtype, 7, 24, lens[:B // 2 + 1], sink="none", rope=False, tail=5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("page", [8, 24, 48, 192])
+def test_long_sequences_in_small_pages(dtype, page):
+    run_case(300 + page, dtype, 64, page, [9001, 200, 4097])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_two_head_groups_in_clusters_and_windows(dtype):
+    run_case(41, dtype, 128, 64, [700, 3, 1200])
+    run_case(42, dtype, 100, 16, [2000, 1500], window=333)
+    run_case(43, dtype, 64, 64, [90000], window=20000)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_pages_beyond_four_gigabytes(dtype):
+    """Offsets of pages and rows that pass 32 bits, written by the append, read by the attention."""
+    import csa2_compressed_sparse_gb300 as csa2
+    width = 512 if dtype == BF16 else 528
+    size = 64 * width * (2 if dtype == BF16 else 1)
+    n_pages = (5 << 30) // size
+    data = torch.empty((n_pages, 64, width), dtype=torch.bfloat16 if dtype == BF16 else torch.uint8,
+                       device="cuda")
+    n = 700
+    pages = [n_pages - 1 - i for i in range(0, 11)]
+    table = torch.tensor([pages], dtype=torch.int32, device="cuda")
+    kv = torch.randn((n, 512), device="cuda").bfloat16()
+    csa2.csa2_paged_append(kv, torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                           torch.zeros(1, dtype=torch.int64, device="cuda"),
+                           paged(data, table, dtype))
+    got = get(data, table, 0, 0, n)
+    check_rows(got, kv, None, dtype, False)
+    q = torch.randn((1, 64, 512), device="cuda").bfloat16()
+    out, lse = torch.empty_like(q), torch.empty((1, 64), device="cuda")
+    csa2.csa2_paged_attn(q, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                         torch.tensor([n - 1], device="cuda"), paged(data, table, dtype), out,
+                         workspace(1, 64, n), max_rows=n, lse=lse)
+    csa2.csa2_device_status()
+    check_query(out[0], lse[0], q[0], decode(got, dtype), None, 512 ** -0.5, n - 1, False)
+
+
+def test_positions_far_beyond_the_cache_and_below_zero():
+    """Positions at the ends of int64: clipped and reported, or empty; nothing else is touched."""
+    import csa2_compressed_sparse_gb300 as csa2
+    data, table, _ = pool(np.random.default_rng(3), BF16, 64, [100])
+    x = torch.randn((100, 512), device="cuda").bfloat16()
+    put(data, table, 0, x)
+    q = torch.randn((2, 64, 512), device="cuda").bfloat16()
+    out, lse = torch.empty_like(q), torch.empty((2, 64), device="cuda")
+    seq = torch.zeros(2, dtype=torch.int32, device="cuda")
+    pos = torch.tensor([2 ** 63 - 1, -2 ** 63], device="cuda")
+    for ratio in (1, 3):
+        with pytest.raises(csa2.Csa2Error) as e:
+            csa2.csa2_paged_attn(q, seq, pos, paged(data, table, BF16), out, workspace(2, 64, 100),
+                                 max_rows=100, lse=lse, ratio=ratio)
+            csa2.csa2_device_status()
+        assert e.value.status == 4
+        check_query(out[0], lse[0], q[0], x.double(), None, 512 ** -0.5, 0, False)
+        assert bool((out[1] == 0).all()) and bool((lse[1] == -float("inf")).all())
+
+
+def test_a_step_on_another_stream_and_a_shared_workspace_in_order():
+    """Calls that follow one another on one stream may share a workspace."""
+    import csa2_compressed_sparse_gb300 as csa2
+    lens = [6000, 31]
+    g = torch.Generator(device="cuda").manual_seed(2)
+    data, table, _ = pool(np.random.default_rng(2), BF16, 64, lens)
+    for b, n in enumerate(lens):
+        put(data, table, b, torch.randn((n, 512), generator=g, device="cuda").bfloat16())
+    ws = workspace(2, 64, 6000)
+    seq = torch.arange(2, dtype=torch.int32, device="cuda")
+    pos = torch.tensor(lens, device="cuda") - 1
+    qs = [torch.randn((2, 64, 512), generator=g, device="cuda").bfloat16() for _ in range(6)]
+    outs = [torch.empty_like(q) for q in qs]
+    lses = [torch.empty((2, 64), device="cuda") for _ in qs]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for q, out, lse in zip(qs, outs, lses):
+        csa2.csa2_paged_attn(q, seq, pos, paged(data, table, BF16), out, ws, max_rows=6000, lse=lse,
+                             stream=st)
+    csa2.csa2_device_status(st)
+    for q, out, lse in zip(qs, outs, lses):
+        for b, n in enumerate(lens):
+            x = decode(get(data, table, b, 0, n), BF16)
+            check_query(out[b], lse[b], q[b], x, None, 512 ** -0.5, n - 1, False)
+
+
 def test_matches_the_sparse_attention():
     """Window-free csa2_sparse_attn with every row selected is the same computation: both are
     within their tolerances of it (this one's is checked by run_case), so they differ by at most
