@@ -331,6 +331,13 @@ __device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&r
                : "memory");
 }
 
+// The same, each matrix transposed: lane 8 i + r gives the address of column r of matrix i.
+__device__ __forceinline__ void store_matrices_t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
 template <int kSoft>
 __device__ __forceinline__ void soft_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory");
@@ -374,6 +381,15 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// The same, two times 8 columns.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
       : "r"(taddr));
 }
 
@@ -507,13 +523,6 @@ __device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
 
-// The low 16 bits of v into shared memory.
-__device__ __forceinline__ void st_shared16b(uint32_t addr, uint32_t v) {
-  asm volatile("{\n\t.reg .b16 h, l;\n\tmov.b32 {l, h}, %1;\n\tst.shared.b16 [%0], l;\n\t}" ::"r"(addr),
-               "r"(v)
-               : "memory");
-}
-
 // A head's running maximum and sums over the parts of the softmax warps.
 struct HeadSums {
   float m, l, r;  // maximum; sums of P, unrounded and rounded
@@ -541,47 +550,55 @@ __device__ __forceinline__ void finish_head(const PagedAttnArgs& a, PagedAux& X,
 }
 
 // Dims 128 mt + 32 quad .. + 31 of all heads by one warp: O^T from TMEM (lane = dim) times 1 / Z
-// and rotated back, in bf16 through a KiB of shared memory at `stage` (16 heads x 32 dims: a lane
-// writes its dim of each head and reads 16 bytes of two heads).
+// and rotated back, in bf16 through a KiB of shared memory at `stage` ([16 heads][32 dims],
+// written as transposed 8 x 8 matrices; 16-byte chunk i of head h at i ^ (h / 2 % 4), free of bank
+// conflicts).  Stores of single values from a lane per dim took twice as long.
 __device__ __forceinline__ void store_tile(const PagedAttnArgs& a, const PagedAux& X, uint32_t tq,
                                            int mt, int quad, int lane, int Hg, uint32_t stage,
                                            uint16_t* out) {
-  const int d = mt * 128 + quad * 32 + lane;
-  const bool rot = a.inv_freq && d >= kRopeDim0;  // the same in a warp
-  const float cs = rot ? X.rope_c[(d - kRopeDim0) >> 1] : 1.f;
-  const float sn = rot ? X.rope_s[(d - kRopeDim0) >> 1] : 0.f;
+  const int d0 = mt * 128 + quad * 32, r4 = lane & 3;
+  const bool rot = a.inv_freq && d0 >= kRopeDim0;  // the same in a warp
+  // this thread's dims: d0 + 8 i + lane / 4, i < 4; of a pair (2 k, 2 k + 1) the other is lane ^ 4
+  float cs[4], sn[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (rot) {
+      const int k = ((d0 - kRopeDim0) >> 1) + 4 * i + (lane >> 3);
+      cs[i] = X.rope_c[k];
+      sn[i] = (lane & 4) ? -X.rope_s[k] : X.rope_s[k];
+    }
+  }
+  const uint32_t swz = (uint32_t)(lane & 7) * 64 + ((uint32_t)((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+  const uint32_t rd = stage + (uint32_t)(lane >> 2) * 64 + ((uint32_t)(r4 ^ (lane >> 3)) << 4);
 #pragma unroll 1
   for (int hb = 0; hb < Hg; hb += 16) {
-    uint32_t v[16];
-    tmem_ld16(tq + kColO + 64 * mt + hb, v);
+    uint32_t v[2][8];
+    tmem_ld_16x256b_x2(tq + kColO + 64 * mt + hb, v[0]);
+    tmem_ld_16x256b_x2(tq + (16u << 16) + kColO + 64 * mt + hb, v[1]);
     tmem_ld_wait();
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(&X.fac[hb + j]);
-      v[j] = __float_as_uint(__uint_as_float(v[j]) * f.x);
-      v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f.y);
-      v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f.z);
-      v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f.w);
-    }
-    if (rot) {  // pair (2i, 2i + 1) times e^{-i p theta_i}: the partner is lane ^ 1
+    for (int g = 0; g < 2; ++g) {
+      const float2 f = *reinterpret_cast<const float2*>(&X.fac[hb + 8 * g + 2 * r4]);
+      uint32_t m[4];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float x = __uint_as_float(v[j]);
-        const float pt = __shfl_xor_sync(0xFFFFFFFFu, x, 1);
-        v[j] = __float_as_uint((lane & 1) ? x * cs - pt * sn : x * cs + pt * sn);
+      for (int i = 0; i < 4; ++i) {
+        float x = __uint_as_float(v[i >> 1][4 * g + 2 * (i & 1)]) * f.x;
+        float y = __uint_as_float(v[i >> 1][4 * g + 2 * (i & 1) + 1]) * f.y;
+        if (rot) {  // pair (2k, 2k + 1) times e^{-i p theta_k}
+          x = x * cs[i] + __shfl_xor_sync(0xFFFFFFFFu, x, 4) * sn[i];
+          y = y * cs[i] + __shfl_xor_sync(0xFFFFFFFFu, y, 4) * sn[i];
+        }
+        m[i] = pack_bf16x2(x, y);
       }
-    }
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-      const uint32_t two = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-      st_shared16b(stage + j * 64 + lane * 2, two);
-      st_shared16b(stage + (j + 1) * 64 + lane * 2, two >> 16);
+      store_matrices_t(stage + g * 512 + swz, m);
     }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int h = hb + 8 * i + (lane >> 2);
-      const uint4 x = ld_shared16(stage + (8 * i + (lane >> 2)) * 64 + (lane & 3) * 16);
+      const uint4 x = ld_shared16(rd + i * 512);
       if (h < Hg)
         __stcs(reinterpret_cast<uint4*>(out + h * kDLat + mt * 128 + quad * 32) + (lane & 3), x);
     }
@@ -705,6 +722,15 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, X.tmem_slot, 0);
 
+  // the rotation of a small call's output, by a warp that has time, where the CTA stores
+  // rotated dims
+  if (kDirect && a.inv_freq && warp == C::kWarpF && (crank + 1) * (kDLat / cl) > kRopeDim0) {
+    const int64_t it = blockIdx.x / cl, q = a.ng == 2 ? it >> 1 : it;
+    float s, c;
+    sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[q]), &s, &c);
+    X.rope_c[lane] = c;
+    X.rope_s[lane] = s;
+  }
   if (u1 > u0) {
     if (warp < C::kWarpS) {
       // ================= softmax, rescale, output =================
@@ -735,7 +761,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         const bool whole = kDirect ? cl == 1 : w.unit == 0 && w.seg_units == w.i.units;
         const float sinkA = mA, sinkB = mB;
         // what the output needs is computed while the first tile loads
-        if (whole && a.inv_freq && warp == C::kWarpS - 1) {
+        if (!kDirect && whole && a.inv_freq && warp == C::kWarpS - 1) {
           float s, cs;
           sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[w.i.q]), &s, &cs);
           X.rope_c[lane] = cs;
@@ -1395,7 +1421,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     // O^T (unscaled) into the rings of the dims' owners and its m, l, r to all; then the owners
     // weigh, sum and store.
     const int lg = cl == 8 ? 3 : cl == 4 ? 2 : 1;
-    const int slice = kDLat >> lg;
+    const int slice = kDLat >> lg, half = slice >> 1;  // dims, pairs of them
     constexpr bool kTail = NS * kSlotBytes >= kHp * 2048 + 8 * 3 * kHp * 4;
     // [rank][m, l, r][head], in every CTA
     const uint32_t st_off = kTail ? (uint32_t)(C::kQBytes + kHp * 2048)
@@ -1423,8 +1449,11 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
                        __float_as_uint(own[i]));
     if (live && u1 > u0 && warp < 16) {
       const int mt = warp >> 2, d = mt * 128 + (warp & 3) * 32 + lane;
-      const uint32_t to = dsmem_addr(
-          ring + (uint32_t)((crank * (kHp / 4)) * slice + (d & (slice - 1))) * 16, d >> (9 - lg));
+      // [rank][four heads][even dims, odd dims][4]: the owner reads a pair's dims by neighbouring
+      // lanes without bank conflicts
+      const int at = ((d & (slice - 1)) >> 1) + (d & 1) * half;
+      const uint32_t to =
+          dsmem_addr(ring + (uint32_t)((crank * (kHp / 4)) * slice + at) * 16, d >> (9 - lg));
 #pragma unroll 1
       for (int hb = 0; hb < Hg; hb += 16) {
         uint32_t v[16];
@@ -1439,31 +1468,35 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    if (live && tid >= Hg && tid < kHp)  // heads that are padding weigh nothing
-      for (int o = 0; o < cl; ++o) st[o * 3 * kHp + tid] = 0.f;
-    if (live && tid < Hg) {
-      const float sink = a.sink ? a.sink[64 * I.hg + tid] * kLog2e : -INFINITY;
-      float M = sink, l = 0.f, r = 0.f;
-      for (int o = 0; o < cl; ++o) M = fmaxf(M, st[o * 3 * kHp + tid]);
-      const float Mf = M == -INFINITY ? 0.f : M;
-      for (int o = 0; o < cl; ++o) {
-        float* so = st + o * 3 * kHp + tid;
-        const float w = ex2(so[0] - Mf);
-        so[0] = w;
-        l = fmaf(w, so[kHp], l);
-        r = fmaf(w, so[2 * kHp], r);
+    // weights and 1 / Z: eight lanes a head, one for each rank
+    for (int i = tid; live && i < 8 * kHp; i += C::kThreads) {
+      const int h = i >> 3, o = i & 7;
+      const bool in = o < cl && h < Hg;  // heads that are padding weigh nothing
+      const float sink = a.sink && h < Hg ? a.sink[64 * I.hg + h] * kLog2e : -INFINITY;
+      float* so = st + o * 3 * kHp + h;
+      const float m = in ? so[0] : -INFINITY;
+      float M = fmaxf(m, sink);
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, x));
+      const float Mf = M == -INFINITY ? 0.f : M, w = ex2(m - Mf);
+      float l = in ? w * so[kHp] : 0.f, r = in ? w * so[2 * kHp] : 0.f;
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) {
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+        r += __shfl_xor_sync(0xFFFFFFFFu, r, x);
       }
+      if (o < cl) so[0] = in ? w : 0.f;
+      if (o > 0 || h >= Hg) continue;
       if (sink > -INFINITY) {
         l += ex2(sink - Mf);
         r += ex2(sink - Mf);
       }
-      X.fac[tid] = r > 0.f || r != r ? 1.f / r : 0.f;
+      X.fac[h] = r > 0.f || r != r ? 1.f / r : 0.f;
       if (a.lse && crank == 0)
-        a.lse[I.q * a.H + 64 * I.hg + tid] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
+        a.lse[I.q * a.H + 64 * I.hg + h] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
     }
     __syncthreads();
     if (live) {
-      const int half = slice >> 1;  // pairs of dims
       for (int i = tid; i < (kHp / 4) * half; i += C::kThreads) {
         const int hc = i >> (8 - lg), pair = i & (half - 1);
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -1472,14 +1505,15 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           // a CTA without tiles wrote nothing, and its weights are zero
           if (!(w.x != 0.f || w.y != 0.f || w.z != 0.f || w.w != 0.f)) continue;
           const float4* b = reinterpret_cast<const float4*>(smem + C::kQBytes) +
-                            (o * (kHp / 4) + hc) * slice + 2 * pair;
-          join_add(acc, b[0], b[1], w);
+                            (o * (kHp / 4) + hc) * slice + pair;
+          join_add(acc, b[0], b[half], w);
         }
         const int d = crank * slice + 2 * pair;
         float cs = 1.f, sn = 0.f;
-        if (a.inv_freq && d >= kRopeDim0)
-          sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), (uint64_t)a.q_pos[I.q]),
-                  &sn, &cs);
+        if (a.inv_freq && d >= kRopeDim0) {
+          cs = X.rope_c[(d - kRopeDim0) >> 1];
+          sn = X.rope_s[(d - kRopeDim0) >> 1];
+        }
         uint16_t* out = a.out + (I.q * a.H + 64 * I.hg) * kDLat + d;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -1514,6 +1548,7 @@ template <int kGroups, int kPairs>
 __global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnArgs a, int hp) {
   __shared__ float4 wt[kMaxCtas];  // [part], or [part][four heads] for sixteen heads
   __shared__ float4 inv_s[4];
+  __shared__ float rope_c[32], rope_s[32];
   __shared__ float acc_s[kGroups / 2][8][kPairs];
   griddep_launch_dependents();
   const int64_t it = blockIdx.x;
@@ -1526,6 +1561,11 @@ __global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnA
   const int pair = tid % kPairs, grp = tid / kPairs;
   const int seq = a.q_seq[q];
   const bool live = 64 * hg + 4 * hc < a.H && seq >= 0 && seq < a.cache.B;
+  // the rotation by one warp, where this CTA has rotated dims
+  if (a.inv_freq && live && warp == kPairs * kGroups / 32 - 1 && 2 * kPairs * (cut + 1) > kRopeDim0) {
+    sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[q]), &rope_s[lane],
+            &rope_c[lane]);
+  }
   griddep_wait();
   if (!live) return;
   const int2 rec = a.rec[it];
@@ -1623,8 +1663,10 @@ __global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnA
   }
   if (!mine) return;
   float cs = 1.f, sn = 0.f;
-  if (a.inv_freq && d >= kRopeDim0)
-    sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), (uint64_t)a.q_pos[q]), &sn, &cs);
+  if (a.inv_freq && d >= kRopeDim0) {
+    cs = rope_c[(d - kRopeDim0) >> 1];
+    sn = rope_s[(d - kRopeDim0) >> 1];
+  }
   const float4 iv = inv_s[hcl];
   const float inv[4] = {iv.x, iv.y, iv.z, iv.w};
   const int h0 = 64 * hg + 4 * hc;
@@ -1694,12 +1736,12 @@ int paged_max_ctas() { return kMaxCtas; }
 // through the workspace.  An item of up to four tiles takes one CTA.  The tiles of a
 // longer one are shared by 8, 4 or 2, as many as all items leave room for (clusters of eight do
 // not fill every SM): up to 32 tiles an item, where lengths below the caller's bound cost
-// little.  Measured, us, equal lengths, clusters against even dealing: 8 sequences of 16 tiles
-// 17.1 / 18.0, 33 of 32 tiles 27.9 / 41.7, 66 of 16 tiles 29.1 / 41.6; up to seven sequences of
-// more than 16 tiles go the other way (one of 32: 18.9 / 16.4).
+// little.  Measured, us, bf16, equal lengths, clusters against even dealing: 8 sequences of
+// 16 tiles 14.5 / 16.0, 33 of 32 tiles 24.7 / 40.2, 66 of 16 tiles 24.3 / 41.8; of more than 16
+// tiles six sequences 16.5 / 18.1, but five 16.4 / 15.0 (FP8 20.8 / 24.3 and 20.6 / 20.3).
 int paged_cluster(int64_t items, int64_t tiles, int sms) {
   if (tiles <= paged_unit_tiles()) return items <= sms ? 1 : 0;
-  if (tiles > 32 || (tiles > 16 && items < 8)) return 0;
+  if (tiles > 32 || (tiles > 16 && items < 6)) return 0;
   return items <= sms / 10 ? 8 : items <= (sms - 16) / 4 ? 4 : items <= (sms - 16) / 2 ? 2 : 0;
 }
 
