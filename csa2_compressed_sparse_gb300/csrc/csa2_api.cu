@@ -736,7 +736,8 @@ csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_s
   }
   // tiles an item can have: a window of w rows touches at most (w + 62) / 64 + 1
   const int64_t most = (a.cap_rows + 63) / 64;
-  const int64_t tiles = window > 0 && (window + 62) / 64 + 1 < most ? (window + 62) / 64 + 1 : most;
+  const bool narrow = window > 0 && window < a.cap_rows && (window + 62) / 64 + 1 < most;
+  const int64_t tiles = narrow ? (window + 62) / 64 + 1 : most;
   const int64_t items = (int64_t)Q * a.ng;
   a.cluster = csa2::paged_cluster(items, tiles, sms);
   if (a.cluster > 0) {

@@ -488,6 +488,26 @@ def test_the_same_call_twice_gives_the_same_bits():
         assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
 
 
+def test_a_window_of_any_size_beyond_the_rows_is_no_window():
+    import csa2_compressed_sparse_gb300 as csa2
+    g = torch.Generator(device="cuda").manual_seed(12)
+    n = 5000
+    data, table, _ = pool(np.random.default_rng(2), BF16, 64, [n])
+    put(data, table, 0, torch.randn((n, 512), generator=g, device="cuda").bfloat16())
+    q = torch.randn((1, 64, 512), generator=g, device="cuda").bfloat16()
+    seq = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pos = torch.tensor([n - 1], device="cuda")
+    outs = []
+    for window in (0, n, n + 1, 1 << 31, (1 << 63) - 62, (1 << 63) - 1):
+        out = torch.empty_like(q)
+        csa2.csa2_paged_attn(q, seq, pos, paged(data, table, BF16), out, workspace(1, 64, n),
+                             max_rows=n, window=window)
+        outs.append(out)
+    csa2.csa2_device_status()
+    for out in outs[1:]:  # the rows are shared out in the same way, too
+        assert torch.equal(out, outs[0])
+
+
 # ---- append ---------------------------------------------------------------------------------
 
 def check_rows(got, x, pos, dtype, rope):
