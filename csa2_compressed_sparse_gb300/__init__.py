@@ -485,13 +485,13 @@ def csa2_paged_attn_workspace_size(Q, H, max_rows):
 def csa2_paged_attn(q, q_seq, q_pos, cache: Paged, out, ws=None, max_rows=None, ratio=1, window=0,
                     sink=None, lse=None, scale=512 ** -0.5, inv_freq=None, stream=None):
     """Dense attention of q [Q, H, 512] over the paged rows each query sees; max_rows bounds
-    them (None: what the page table can hold)."""
+    them (None: what the page table can hold, at most 2^31 - 256)."""
     dev = cache._dev
     if q.dim() != 3:
         raise ValueError("csa2: q must be [Q, H, 512]")
     Q, H, _ = q.shape
     if max_rows is None:
-        max_rows = cache.table.shape[1] * cache.data.shape[1]
+        max_rows = min(cache.table.shape[1] * cache.data.shape[1], 0x7FFFFF00)
     _call(lib().csa2_paged_attn, dev, stream, _arg("q", q, torch.bfloat16, (Q, H, 512), dev), Q, H,
           _arg("q_seq", q_seq, torch.int32, (Q,), dev),
           _arg("q_pos", q_pos, torch.int64, (Q,), dev), cache.c(), ratio, window, max_rows,

@@ -508,6 +508,23 @@ def test_a_window_of_any_size_beyond_the_rows_is_no_window():
         assert torch.equal(out, outs[0])
 
 
+def test_a_page_table_beyond_two_to_the_31_rows():
+    import csa2_compressed_sparse_gb300 as csa2
+    g = torch.Generator(device="cuda").manual_seed(13)
+    data, small, _ = pool(np.random.default_rng(2), BF16, 1024, [3000])
+    x = torch.randn((3000, 512), generator=g, device="cuda").bfloat16()
+    put(data, small, 0, x)
+    table = torch.full((1, (1 << 21) + 1), -1, dtype=torch.int32, device="cuda")
+    table[:, :small.shape[1]] = small
+    q = torch.randn((1, 64, 512), generator=g, device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    csa2.csa2_paged_attn(q, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                         torch.tensor([2999], device="cuda"), paged(data, table, BF16), out,
+                         workspace(1, 64, 0x7FFFFF00))
+    csa2.csa2_device_status()
+    check_query(out[0], None, q[0], x.double(), None, 512 ** -0.5, 2999, False)
+
+
 # ---- append ---------------------------------------------------------------------------------
 
 def check_rows(got, x, pos, dtype, rope):
