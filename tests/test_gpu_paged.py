@@ -308,6 +308,16 @@ def test_small_batches_one_cluster_per_item(dtype, B, most):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,B,sink", [(64, 1, "inf"), (33, 2, "large"), (20, 16, "none"), (3, 25, "normal"),
+                                      (100, 3, "inf"), (128, 12, "normal"), (64, 60, "none")])
+def test_clusters_weigh_their_parts(dtype, H, B, sink):
+    rng = np.random.default_rng(B)
+    lens = [0, 2048] + [int(x) for x in rng.integers(0, 2049, B)]  # some parts have no rows
+    run_case(50 + B, dtype, H, 64, lens[:B] if B > 2 else lens[1:1 + B], sink=sink, spread=4.0)
+    run_case(51 + B, dtype, H, 16, [min(n, 600) for n in lens[1:1 + B]], sink=sink, rope=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("page", [8, 24, 48, 192])
 def test_long_sequences_in_small_pages(dtype, page):
     run_case(300 + page, dtype, 64, page, [9001, 200, 4097])
