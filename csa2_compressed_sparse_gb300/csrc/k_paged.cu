@@ -1041,8 +1041,10 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           for (int mt = half; mt < 4; mt += kParts)
             store_tile(a, X, tmem + lrow, mt, quad, lane, Hg, p_s + warp * 1024, out);
         } else {
-          // [dim tile][four heads][128 dims][4]: a lane writes 16 bytes, a warp 512
-          float* po = a.part + part * (int64_t)(kHp * kDLat) + (quad * 32 + lane) * 4;
+          // [dim tile][four heads][even dims, odd dims][4]: a lane writes 16 bytes, and the
+          // join's threads, which have a pair of dims each, read them side by side
+          float* po = a.part + part * (int64_t)(kHp * kDLat) +
+                      (((quad * 32 + lane) >> 1) + (lane & 1) * 64) * 4;
 #pragma unroll 1
           for (int mt = half; mt < 4; mt += kParts) {
 #pragma unroll 1
@@ -1533,36 +1535,38 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 //
 // Joins the parts of the items that several CTAs worked on: with M the largest running
 // maximum (and the sink logit), weights 2^(m - M) and Z = 2^(sink - M) + sum 2^(m - M) l,
-// out = sum 2^(m - M) O / Z.  A CTA takes one item, 2 kPairs dims and four heads, a thread a pair
-// of dims; its kGroups groups of kPairs threads take every kGroups-th part, the first kAhead of
-// them loaded before the weights are known.  Of an item with up to kAhead parts, the usual
-// case in a batch, the CTA of every fourth four heads does sixteen heads, four per group, and
-// the CTAs beside it return: fewer, longer loads per thread (64 items: 19 -> 8 us).
-// A single long item, which may have 152 parts, takes 32 groups and CTAs of 64 dims, else four of
-// 128 (whole calls, us: one sequence of 1024 tiles 31.7 with 32 groups / 40.2 with four, two of
-// them 45.9 / 45.4, sixteen of 512 tiles 140 / 104).
+// out = sum 2^(m - M) O / Z.  A CTA takes one item, 2 kPairs dims and kSets times four heads, a
+// thread a pair of dims of four heads; its kGroups groups take every kGroups-th part, the first
+// kAhead of them loaded before the weights are known.  Bound by latency: the parts come from L2.
+// Many items, of few parts each, take four sets and no groups: few CTAs with long loads.  Fewer
+// items take four groups and a set; a single long one, which may have 152 parts, 32 groups and
+// CTAs of 64 dims (whole calls, us: 64 items of 128 to 512 tiles 231 with sets / 240 with groups,
+// 16 of 256 to 512 tiles 84 / 86, 8 of them 58 / 53; one item of 1024 tiles 31.7 with 32 groups
+// / 40.2 with four, two 45.9 / 45.4).
 constexpr int kMaxCtas = 152;
 constexpr int kAhead = 4;
 
-template <int kGroups, int kPairs>
-__global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnArgs a, int hp) {
-  __shared__ float4 wt[kMaxCtas];  // [part], or [part][four heads] for sixteen heads
-  __shared__ float4 inv_s[4];
+template <int kGroups, int kSets, int kPairs>
+__global__ void __launch_bounds__(kPairs * kGroups * kSets)
+    paged_join_kernel(PagedAttnArgs a, int hp) {
+  static_assert(kGroups == 1 || kSets == 1, "the groups' sums fold over one set");
+  constexpr int kWarps = kPairs * kGroups * kSets / 32;
+  __shared__ float4 wt[kMaxCtas][kSets];
+  __shared__ float4 inv_s[kSets];
+  __shared__ float acc_s[kGroups > 1 ? kGroups / 2 : 1][8][kPairs];
   __shared__ float rope_c[32], rope_s[32];
-  __shared__ float acc_s[kGroups / 2][8][kPairs];
   griddep_launch_dependents();
   const int64_t it = blockIdx.x;
-  constexpr int kCuts = 256 / kPairs;  // CTAs of four heads
-  const int cut = blockIdx.y % kCuts;
-  int hc = blockIdx.y / kCuts;
+  constexpr int kCuts = 256 / kPairs;  // CTAs of the same heads
+  const int cut = blockIdx.y % kCuts, hc0 = kSets * (blockIdx.y / kCuts);
   const int64_t q = a.ng == 2 ? it >> 1 : it;
   const int hg = a.ng == 2 ? (int)(it & 1) : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int pair = tid % kPairs, grp = tid / kPairs;
+  const int pair = tid % kPairs, set = tid / kPairs % kSets, grp = tid / (kPairs * kSets);
   const int seq = a.q_seq[q];
-  const bool live = 64 * hg + 4 * hc < a.H && seq >= 0 && seq < a.cache.B;
+  const bool live = 64 * hg + 4 * hc0 < a.H && seq >= 0 && seq < a.cache.B;
   // the rotation by one warp, where this CTA has rotated dims
-  if (a.inv_freq && live && warp == kPairs * kGroups / 32 - 1 && 2 * kPairs * (cut + 1) > kRopeDim0) {
+  if (a.inv_freq && live && warp == kWarps - 1 && 2 * kPairs * (cut + 1) > kRopeDim0) {
     sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[q]), &rope_s[lane],
             &rope_c[lane]);
   }
@@ -1571,31 +1575,28 @@ __global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnA
   const int2 rec = a.rec[it];
   if (rec.x < 0) return;
   const int n = min(rec.y - rec.x + 1, kMaxCtas);
-  const bool sixteen = kGroups == 4 && n <= kAhead;
-  if (sixteen && (hc & 3) != 0) return;
   auto part = [&](int s) -> int64_t { return 2 * (int64_t)(rec.x + s) + (s == 0 ? 1 : 0); };
-  const int hcl = sixteen ? grp : 0;            // this thread's four heads of the CTA's
-  const int s_beg = sixteen ? 0 : grp, s_step = sixteen ? 1 : kGroups;
-  hc += hcl;
+  const int hc = hc0 + set;
   const bool mine = 64 * hg + 4 * hc < a.H && 4 * hc < hp;
   const int d = 2 * (cut * kPairs + pair);  // this thread's dims d, d + 1
-  const float* src = a.part + ((d >> 7) * (hp / 4) + hc) * 512 + (d & 127) * 4;
+  const float4* src = reinterpret_cast<const float4*>(a.part) + ((d >> 7) * (hp / 4) + hc) * 128 +
+                      ((d & 127) >> 1);
   float4 x[kAhead], y[kAhead];
   auto load = [&](int s0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int s = s0 + i * s_step;
+      const int s = s0 + i * kGroups;
       if (s < n && mine) {
-        const float4* p = reinterpret_cast<const float4*>(src + part(s) * (int64_t)(hp * kDLat));
+        const float4* p = src + part(s) * (int64_t)(hp * kDLat / 4);
         x[i] = __ldcs(p);
-        y[i] = __ldcs(p + 1);
+        y[i] = __ldcs(p + 64);
       }
     }
   };
-  load(s_beg);
+  load(grp);
   // weights and 1 / Z of a head by one warp
-  for (int hh = warp; hh < (sixteen ? 16 : 4); hh += kPairs * kGroups / 32) {
-    const int hb = 4 * (hc - hcl) + hh, hq = 64 * hg + hb;
+  for (int hh = warp; hh < 4 * kSets; hh += kWarps) {
+    const int hb = 4 * hc0 + hh, hq = 64 * hg + hb;
     const bool there = hq < a.H && hb < hp;
     const float sink = a.sink && there ? a.sink[hq] * kLog2e : -INFINITY;
     float m[(kMaxCtas + 31) / 32], M = sink;
@@ -1613,7 +1614,7 @@ __global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnA
       const int s = lane + 32 * i;
       if (s < n) {
         const float w = there ? ex2(m[i] - Mf) : 0.f;
-        reinterpret_cast<float*>(&wt[sixteen ? 4 * s + (hh >> 2) : s])[hh & 3] = w;
+        reinterpret_cast<float*>(&wt[s][0])[hh] = w;
         if (there) {
           const float* st = a.pstat + part(s) * (3 * hp) + hb;
           l = fmaf(w, st[hp], l);
@@ -1637,15 +1638,15 @@ __global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnA
   }
   __syncthreads();
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int s0 = s_beg; s0 < n; s0 += kAhead * s_step) {
+  for (int s0 = grp; s0 < n; s0 += kAhead * kGroups) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int s = s0 + i * s_step;
-      if (s < n && mine) join_add(acc, x[i], y[i], wt[sixteen ? 4 * s + hcl : s]);
+      const int s = s0 + i * kGroups;
+      if (s < n && mine) join_add(acc, x[i], y[i], wt[s][set]);
     }
-    load(s0 + kAhead * s_step);
+    load(s0 + kAhead * kGroups);
   }
-  if (!sixteen) {
+  if (kGroups > 1) {
 #pragma unroll
     for (int low = kGroups / 2; low > 0; low >>= 1) {  // the groups' sums fold in halves
       if (grp >= low && grp < 2 * low) {
@@ -1667,7 +1668,7 @@ __global__ void __launch_bounds__(kPairs * kGroups) paged_join_kernel(PagedAttnA
     cs = rope_c[(d - kRopeDim0) >> 1];
     sn = rope_s[(d - kRopeDim0) >> 1];
   }
-  const float4 iv = inv_s[hcl];
+  const float4 iv = inv_s[set];
   const float inv[4] = {iv.x, iv.y, iv.z, iv.w};
   const int h0 = 64 * hg + 4 * hc;
 #pragma unroll
@@ -1764,9 +1765,11 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, int units, cudaStream_t s)
                              : launch_attn_mode<64>(a, qm, km, s);
   if (e != cudaSuccess || units <= 1) return e;
   const unsigned items = (unsigned)(a.Q * a.ng);
-  return items == 1 && units > 64
-             ? launch_pdl(paged_join_kernel<32, 32>, dim3(items, 2u * hp), dim3(1024), 0, s, a, hp)
-             : launch_pdl(paged_join_kernel<4, 64>, dim3(items, (unsigned)hp), dim3(256), 0, s, a, hp);
+  if (items == 1 && units > 64)
+    return launch_pdl(paged_join_kernel<32, 1, 32>, dim3(items, 2u * hp), dim3(1024), 0, s, a, hp);
+  return items >= 16
+             ? launch_pdl(paged_join_kernel<1, 4, 64>, dim3(items, hp / 4u), dim3(256), 0, s, a, hp)
+             : launch_pdl(paged_join_kernel<4, 1, 64>, dim3(items, (unsigned)hp), dim3(256), 0, s, a, hp);
 }
 
 }  // namespace csa2
