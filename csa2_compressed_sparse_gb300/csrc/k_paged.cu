@@ -250,7 +250,7 @@ struct __align__(16) PagedAux {
   uint64_t landed[12];           // FP8 rows: written by the loaders, not yet fenced
   uint64_t q_full, q_empty;
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_full[2], pv_done;  // p_full: two quarters' P of scaled rows, else [0]
+  uint64_t p_full[2], pv_done;  // p_full: [1] with FP8_S128 rows only
   uint64_t fin[2];
   uint64_t mask[4];     // valid rows of tile c at c & 3
   int it0, it0_unit;    // first item of this CTA and the units before it within the item
@@ -281,8 +281,9 @@ struct PagedCfg {
   // P's memory also stages the output: a KiB for each softmax warp
   static constexpr int kPUsed = kHp * 128 * kPBufs;
   static constexpr int kPBytes = kPUsed > 8192 ? kPUsed : 8192;
-  // scales [tile][quarter][row] of the last kScTiles tiles: a tile's are written with its last
-  // quarter, whose slot with eight slots was the last quarter's two tiles before
+  // scales [tile][quarter][row] of the last kScTiles tiles, the eight rows of a softmax thread
+  // side by side (row bits 5, 2..1, 4..3, 0): a tile's are written with its last quarter, whose
+  // slot with eight slots was the last quarter's two tiles before
   static constexpr int kScTiles = kHp == 64 ? 2 : 4;
   static constexpr int kScBytes = kScaled ? kScTiles * 4 * 64 * 4 : 0;
   static constexpr int kFree =
@@ -324,11 +325,11 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, 
 __device__ __forceinline__ bool all_ok(bool x) { return __all_sync(0xFFFFFFFFu, x); }
 
 // Four 8 x 8 matrices of 16-bit values: thread t holds (t / 4, 2 (t % 4) + {0, 1}) of each; lane
-// 8 i + r gives the address of row r of matrix i.
+// 8 i + r gives the address of row r of matrix i.  (No memory clobber: what it writes is read
+// after a fence and a barrier, which have one, and loads of scales may move past it.)
 __device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&r)[4]) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
 }
 
 // The same, each matrix transposed: lane 8 i + r gives the address of column r of matrix i.
@@ -800,27 +801,30 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
             } else {
 #pragma unroll
               for (int g = 0; g < kG; ++g) xA[g] = xB[g] = make_float2(0.f, 0.f);
-#pragma unroll 1
+#pragma unroll
               for (int k2 = 0; k2 < 4; k2 += 2) {
-              uint32_t x[2][4 * kG];
+                uint32_t x[2][4 * kG];
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                tmem_ld_16x256b_x4(tmem + lrow + 64 * (k2 + k) + kRows * half, x[k]);
-              tmem_ld_wait();
+                for (int k = 0; k < 2; ++k)
+                  tmem_ld_16x256b_x4(tmem + lrow + 64 * (k2 + k) + kRows * half, x[k]);
+                tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float* sc = sc_s + ((c & (C::kScTiles - 1)) * 4 + k2 + k) * 64 + kRows * half + 2 * r4;
+                for (int k = 0; k < 2; ++k) {
+                  const float4* sc = reinterpret_cast<const float4*>(
+                      sc_s + ((c & (C::kScTiles - 1)) * 4 + k2 + k) * 64 + kRows * half + 8 * r4);
+                  const float4 f4[2] = {sc[0], sc[1]};
 #pragma unroll
-                for (int g = 0; g < kG; ++g) {
-                  const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
-                  xA[g] = fma2(
-                      make_float2(__uint_as_float(x[k][4 * g]), __uint_as_float(x[k][4 * g + 1])), f,
-                      xA[g]);
-                  xB[g] = fma2(
-                      make_float2(__uint_as_float(x[k][4 * g + 2]), __uint_as_float(x[k][4 * g + 3])),
-                      f, xB[g]);
+                  for (int g = 0; g < kG; ++g) {
+                    const float2 f = g & 1 ? make_float2(f4[g >> 1].z, f4[g >> 1].w)
+                                           : make_float2(f4[g >> 1].x, f4[g >> 1].y);
+                    xA[g] = fma2(
+                        make_float2(__uint_as_float(x[k][4 * g]), __uint_as_float(x[k][4 * g + 1])), f,
+                        xA[g]);
+                    xB[g] = fma2(
+                        make_float2(__uint_as_float(x[k][4 * g + 2]), __uint_as_float(x[k][4 * g + 3])),
+                        f, xB[g]);
+                  }
                 }
-              }
               }
             }
           }
@@ -969,24 +973,32 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           for (int k = 0; k < C::kPBufs; ++k) {
             if (on) {
               if (C::kScaled) {
-                const float* sc = sc_s + ((c & (C::kScTiles - 1)) * 4 + k) * 64 + kRows * half + 2 * r4;
+                const float4* sc = reinterpret_cast<const float4*>(
+                    sc_s + ((c & (C::kScTiles - 1)) * 4 + k) * 64 + kRows * half + 8 * r4);
+                const float4 f4[2] = {sc[0], sc[1]};
 #pragma unroll
                 for (int g = 0; g < kG; ++g) {
-                  const float2 f = *reinterpret_cast<const float2*>(sc + 8 * g);
-                  pa[g] = pack_bf16x2(eA[g].x * f.x, eA[g].y * f.y);
-                  pb[g] = pack_bf16x2(eB[g].x * f.x, eB[g].y * f.y);
+                  const float2 f = g & 1 ? make_float2(f4[g >> 1].z, f4[g >> 1].w)
+                                         : make_float2(f4[g >> 1].x, f4[g >> 1].y);
+                  const float2 o0 = make_float2(0.f, 0.f);
+                  const float2 x = fma2(eA[g], f, o0), y = fma2(eB[g], f, o0);
+                  pa[g] = pack_bf16x2(x.x, x.y);
+                  pb[g] = pack_bf16x2(y.x, y.y);
                 }
               }
               const uint32_t pk = pA + k * (kHp * 128);
               store_matrices(pk, pa);
               store_matrices(pk + 8 * 128, pb);
             }
-            if (!C::kScaled || (k & 1)) {  // a fence for two quarters' P
-              fence_proxy_async_smem();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&X.p_full[k >> 1]));
-            }
+          }
+          // one fence for all: with FP8_S128 rows two, each for two quarters' P, took longer
+          // (346 against 339 us for 64 sequences of 8192 to 32768 rows)
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&X.p_full[0]));
+            if (C::kScaled) mbar_arrive(smem_u32(&X.p_full[1]));
           }
           sl += 4;
           if (sl >= NS) { sl -= NS; sph ^= 1; }
@@ -1131,6 +1143,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         for (int t = 0; ok && t < tiles; ++t, ++c) {
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
+            // (with FP8_S128 rows a second wait, for what is then there, lets the other issuer's
+            // products in between: 341 against 350 us for 64 sequences of 8192 to 32768 rows)
             if (mt == 0 || (C::kScaled && mt == 2)) {
               ok = ok && all_ok(wait_phase(X, X.p_full[mt >> 1], (uint32_t)c & 1));
               if (!ok) break;
@@ -1358,7 +1372,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           // (with the last quarter: its slot is free once the tile before the last one has read
           // its scales)
           if (kMode == 1 && k == 3)
-            sc_s[((c & (C::kScTiles - 1)) * 4 + pc) * 64 + r] = __uint_as_float(scl);
+            sc_s[((c & (C::kScTiles - 1)) * 4 + pc) * 64 + (r & 33) + ((r & 6) << 2) +
+                 ((r & 24) >> 2)] = __uint_as_float(scl);
           uint32_t word = 0;
           if (kMode == 2) word = __shfl_sync(0xFFFFFFFFu, scl, (lane & 28) + k) >> (8 * (pc >> 1));
 #pragma unroll
