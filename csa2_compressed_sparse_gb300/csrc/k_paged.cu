@@ -303,12 +303,13 @@ __device__ __forceinline__ float ex2(float x) {
 // Wait for a phase; false once something in the CTA has given up.  The flag is read only while
 // the phase is incomplete: a read of shared memory takes some hundred cycles while the tensor
 // core's operand reads fill it, and the waits stand on the path from scores to values.
-__device__ __forceinline__ bool wait_phase(PagedAux& X, uint64_t& bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_phase(PagedAux& X, uint64_t& bar, uint32_t parity,
+                                           uint64_t limit_ns = 2000000000ull) {
   const uint32_t b = smem_u32(&bar);
   if (mbar_try_wait(b, parity)) return true;
   const volatile int* abort = &X.abort;
   if (*abort) return false;
-  if (mbar_wait(b, parity)) return true;
+  if (mbar_wait(b, parity, limit_ns)) return true;
   X.abort = 1;
   return false;
 }
@@ -1177,9 +1178,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         walk_start(a, X, u1 - u0, w);
         const uint64_t pol = policy_evict_first();
         uint32_t n = 0;  // segments so far
+        int tiles = 0;   // of the last one
         const uint32_t qf = smem_u32(&X.q_full);
         do {
-          if (n > 0 && !wait_phase(X, X.q_empty, (n - 1) & 1)) break;
+          // this wait lasts as long as a segment, which may be millions of tiles of some 2 us
+          if (n > 0 &&
+              !wait_phase(X, X.q_empty, (n - 1) & 1, 2000000000ull + 50000ull * (uint32_t)tiles))
+            break;
+          tiles = w.t_end - w.t;
           mbar_arrive_expect_tx(qf, C::kQBytes);
 #pragma unroll
           for (int db = 0; db < 8; ++db)
