@@ -25,7 +25,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // outside the rotated dims are copied as they are.  Bound by the bytes moved: 1024 read, 1024
 // or 528 written per token.  The lanes' angular steps (64-bit floating point, of which an SM does
 // two a cycle) are computed once per warp, so many tokens run on a grid that stays (kTok = 4,
-// whose rows load together); few tokens take a warp each (kTok = 1).
+// whose rows load together); few tokens take a warp each (kTok = 1).  Measured: 57.7 us for
+// four bf16 prompts of 16384 to 65535 tokens (86 % of the copy rate), 5 us for 4096 FP8_E8M0
+// tokens, 3 us for 64 tokens.
 
 constexpr int kAppWarps = 8;
 constexpr int kAppCtas = 6;  // CTAs of an SM with many tokens
@@ -225,6 +227,12 @@ __global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppen
 //            slot, so the quarter of a later tile starts to load while this one is finished
 // Rows outside lo .. hi - 1 or on a bad page get P = 0 and are zeroed before the product
 // (what the page holds there may be NaN).
+//
+// Measured, 64 heads: 16 sequences of 262144 rows 662 us in bf16 (96 % of the copy rate), 977 us
+// as FP8_S128, 900 us as FP8_E8M0; 64 sequences of 8192 to 32768 rows 231 us in bf16, 339 us as
+// FP8_S128.  bf16 rows are bound by HBM.  FP8 rows are bound by the data pipe of L1 and shared
+// memory (77 % busy: a tile takes 1780 cycles of operand reads, 1010 of row loads, 890 of
+// stores, 650 of loads and waits) and by what waits for it: a slot's way round the ring.
 //
 // The sum of P exists twice: of the bf16-rounded values, which the output is divided by (a
 // common rounding error of the largest weights cancels), and of the unrounded ones for lse.
@@ -1291,8 +1299,9 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       // quarter after each one waited for that load before it could use the one already there:
       // registers wait for all loads behind one counter).  Thread t of a group: row t / 4 of a
       // tile and of each quarter dims 16 (t % 4) .. and 64 + 16 (t % 4) .., two loads of 64 whole
-      // bytes a row and stores free of bank conflicts.  The instructions issued are the limit, so
-      // a thread has one row, whose page is looked up a turn ahead.
+      // bytes a row and stores free of bank conflicts; a thread has one row, whose page is looked
+      // up a turn ahead.  (Eight lanes a row, whole lines: 2 % less time for FP8_S128 rows, 3 %
+      // more for FP8_E8M0.)
       const int grp = (warp - C::kWarpL) >> 3, t256 = (tid - 32 * C::kWarpL) & 255;
       const int r = t256 >> 2, pc = t256 & 3;
       Walk w;
