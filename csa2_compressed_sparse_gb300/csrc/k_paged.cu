@@ -673,8 +673,11 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     tmem_alloc(smem_u32(&X.tmem_slot), 512);
     tmem_relinquish();
   }
-  // ---- the plan: every CTA sums the units of all items (positions only: they are this
-  // call's own inputs) and finds its share of them ----
+  // Every thread waits here: queries, positions, page ids and rows may come from the kernel
+  // before this one, and the output and the workspace may still be in use by it.  The waits
+  // below, which are bounded, then time this kernel's work alone.
+  griddep_wait();
+  // ---- the plan: every CTA sums the units of all items and finds its share of them ----
   int64_t u0, u1, U = 0;
   int64_t ncta = 1;
   const int cl = kDirect ? a.cluster : 1, crank = kDirect && cl > 1 ? (int)cluster_ctarank() : 0;
@@ -759,7 +762,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       int sl = 0;                      // ring slot of the tile's first quarter
       uint32_t sph = 0;                // its phase
       int64_t u = u0;                  // unit where the segment begins
-      griddep_wait();  // the output and the workspace may still be in use by what precedes
       do {
         const int Hg = min(64, a.H - 64 * w.i.hg);
         float mA = -INFINITY, mB = -INFINITY;
@@ -1226,9 +1228,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     } else if (kMode == 0) {
       // ================= bf16 rows by tensor copies: warp k quarter k =================
       const int k = warp - C::kWarpL;
-      // rows may come from the kernel before this one (an append); the table is this call's own
-      // input, so the first pages are looked up before the wait
-      bool waited = false;
       Walk w;
       walk_start(a, X, u1 - u0, w);
       const uint64_t pol = a.shared ? policy_evict_normal() : policy_evict_first();
@@ -1258,8 +1257,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           }
           m <<= cl * R;
           for (int o = 1; o < nc; o <<= 1) m |= __shfl_xor_sync(0xFFFFFFFFu, m, o);
-          if (!waited) griddep_wait();
-          waited = true;
           const int te = min(tbeg + tb, w.t_end);
           for (int t = tbeg; ok && t < te; ++t, ++c) {
             const int src = (t - tbeg) * nc;
@@ -1363,7 +1360,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       if (grp == 1) step();
       bool have = look(page, row);
       uint32_t bits = place(page, row, src);
-      griddep_wait();  // rows may come from the kernel before this one; the table does not
       fetch(src);
       bool nxt = look(page, row);
       int c = grp, sl = 4 * grp;
@@ -1431,8 +1427,6 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       }
     }
   }
-  // a CTA without work must not let the grid complete before what precedes it has
-  griddep_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1586,6 +1580,7 @@ __global__ void __launch_bounds__(kPairs * kGroups * kSets)
   __shared__ float acc_s[kGroups > 1 ? kGroups / 2 : 1][8][kPairs];
   __shared__ float rope_c[32], rope_s[32];
   griddep_launch_dependents();
+  griddep_wait();  // for the parts, and for what the attention's call was given
   const int64_t it = blockIdx.x;
   constexpr int kCuts = 256 / kPairs;  // CTAs of the same heads
   const int cut = blockIdx.y % kCuts, hc0 = kSets * (blockIdx.y / kCuts);
@@ -1593,6 +1588,7 @@ __global__ void __launch_bounds__(kPairs * kGroups * kSets)
   const int hg = a.ng == 2 ? (int)(it & 1) : 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int pair = tid % kPairs, set = tid / kPairs % kSets, grp = tid / (kPairs * kSets);
+  const int2 rec = a.rec[it];  // (of an item that is not live: not written, and not used)
   const int seq = a.q_seq[q];
   const bool live = 64 * hg + 4 * hc0 < a.H && seq >= 0 && seq < a.cache.B;
   // the rotation by one warp, where this CTA has rotated dims
@@ -1600,10 +1596,7 @@ __global__ void __launch_bounds__(kPairs * kGroups * kSets)
     sincosf(rope_angle(rope_turn(a.inv_freq[lane]), (uint64_t)a.q_pos[q]), &rope_s[lane],
             &rope_c[lane]);
   }
-  griddep_wait();
-  if (!live) return;
-  const int2 rec = a.rec[it];
-  if (rec.x < 0) return;
+  if (!live || rec.x < 0) return;
   const int n = min(rec.y - rec.x + 1, kMaxCtas);
   auto part = [&](int s) -> int64_t { return 2 * (int64_t)(rec.x + s) + (s == 0 ? 1 : 0); };
   const int hc = hc0 + set;

@@ -406,10 +406,12 @@ __device__ __forceinline__ void cp_async_wait_group() {
 
 // ---- programmatic dependent launch --------------------------------------------------------
 // Kernels of this library are launched with programmatic stream serialisation: the next
-// kernel may be scheduled while this one drains.  Every kernel calls griddep_wait()
-// before its first global-memory access, which waits for the previous kernel in the
-// stream to complete with all its writes visible, so the stream order of reads and
-// writes is unchanged; only launch latency and local set-up overlap.
+// kernel may be scheduled while this one drains.  griddep_wait() waits for the previous
+// kernel in the stream to complete with all its writes visible.  Every kernel calls it
+// before its first write to global memory and before it reads what a kernel of the same
+// call, or a selection, key or plane before it, may still be writing.  The paged kernels
+// read nothing at all before it.  The kernels of the sparse step read the call inputs
+// that csa2.h lists before it, so that these loads overlap with the previous kernel too.
 __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -15,11 +15,22 @@
  *     memory is caller-provided through the *_workspace_size queries.
  *   - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  No call synchronises except csa2_device_status().  Kernels are
- *     launched as programmatic dependents: a call may start while the preceding kernel
- *     of this library on the stream drains, and reads only its own inputs (queries,
- *     positions, window rows) before that kernel has finished; whatever that kernel
- *     produces (a selection, keys) is read after it, and workspace is written after it.
- *     Inputs written by other kernels must be complete in stream order, as usual.
+ *     launched as programmatic dependents and let their own dependents start early: a
+ *     call may begin while the kernel before it on the stream drains.  Outputs and
+ *     workspace are written, and selections, candidates, keys, scores and planes read,
+ *     only once that kernel has finished.
+ *   - csa2_paged_append and csa2_paged_attn read everything else after it too, so stream
+ *     order is all that their inputs need.
+ *   - The calls of the sparse step (index, top-k, attention, and the compressor's tokens
+ *     in csa2_compress_index_topk) read some inputs before the kernel in front of them has
+ *     finished: queries, sequence ids, positions and row bases, window rows, new tokens
+ *     with cu_seqlens, and inv_freq.  They must not be written by a kernel that itself lets
+ *     its dependents start early and that no other launch separates from the call.  That
+ *     is any kernel of this library (an attention output taken as queries, a window filled
+ *     by csa2_paged_append) and any other that triggers programmatic launches.  Between the
+ *     two, a kernel launched without the programmatic attribute, a copy, or a wait for an
+ *     event of another stream makes them complete; kernels that trigger nothing and
+ *     copies are so by themselves.
  *   - Argument errors are detected on the host before anything is launched and
  *     return CSA2_EINVAL.  CUDA launch failures return CSA2_ECUDA.  The text of the
  *     last failure on the calling thread is available from csa2_last_error().
