@@ -242,6 +242,7 @@ constexpr int kBlock = 1024;  // 64 dims of 8 rows
 constexpr int kGroup = 2048;  // 128 dims of 8 rows
 constexpr int kMaxSmem = 232448;
 constexpr float kLazy = 64.0f;
+constexpr float kLowSink = -1048576.0f;  // from here on fp32's steps are 1/8 and less
 constexpr uint32_t kColO = 256;  // O^T tiles at 256 + 64 mt
 
 // What lives in P's buffers while they hold no P: from the end of a tile's products to the next
@@ -547,16 +548,20 @@ __device__ __forceinline__ HeadSums head_sums(const PagedSpare& Y, int h) {
   }
   return s;
 }
-// Adds the sink's mass, stores lse and leaves 1 / Z in X.fac.
+// Adds the sink's mass, stores lse and leaves 2^(m - M) / Z in X.fac, M the larger of m and sink.
 __device__ __forceinline__ void finish_head(const PagedAttnArgs& a, PagedAux& X, HeadSums s,
                                             float sink, int h, const Item& i) {
+  // (the sink is above the rows' maximum only where that did not start at it)
+  const float M = fmaxf(s.m, sink), Mf = M == -INFINITY ? 0.f : M, w = ex2(s.m - Mf);
+  s.l *= w;
+  s.r *= w;
   if (sink > -INFINITY) {
-    s.l += ex2(sink - s.m);
-    s.r += ex2(sink - s.m);
+    s.l += ex2(sink - Mf);
+    s.r += ex2(sink - Mf);
   }
-  X.fac[h] = s.r > 0.f || s.r != s.r ? 1.f / s.r : 0.f;  // no row and no sink: zeros
+  X.fac[h] = s.r > 0.f || s.r != s.r ? w / s.r : 0.f;  // no row and no sink: zeros
   if (a.lse)
-    a.lse[i.q * a.H + 64 * i.hg + h] = s.l == 0.f ? -INFINITY : (s.m + __log2f(s.l)) * kLn2;
+    a.lse[i.q * a.H + 64 * i.hg + h] = s.l == 0.f ? -INFINITY : (Mf + __log2f(s.l)) * kLn2;
 }
 
 // Dims 128 mt + 32 quad .. + 31 of all heads by one warp: O^T from TMEM (lane = dim) times 1 / Z
@@ -772,6 +777,10 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         }
         const bool whole = kDirect ? cl == 1 : w.unit == 0 && w.seg_units == w.i.units;
         const float sinkA = mA, sinkB = mB;
+        // A maximum is moved by adding a score's distance to it, which loses the score where the
+        // two are far apart: from a sink far below all scores no maximum starts.
+        if (mA < kLowSink) mA = -INFINITY;
+        if (mB < kLowSink) mB = -INFINITY;
         // what the output needs is computed while the first tile loads
         if (!kDirect && whole && a.inv_freq && warp == C::kWarpS - 1) {
           float s, cs;
