@@ -4,6 +4,8 @@
 //
 // A cache row is one 512-d latent, key and value of every head.  Pages hold page_rows rows;
 // table[b][j / page_rows] is the page of row j of sequence b.
+#include <cfloat>
+
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -534,6 +536,16 @@ __device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
 
+// A sink's logit in log2.  A finite one stays finite: the largest and lowest of fp32 overflow.
+__device__ __forceinline__ float sink_log2(float sink) {
+  const float y = sink * kLog2e;
+  return fabsf(y) == INFINITY && fabsf(sink) < INFINITY ? copysignf(FLT_MAX, sink) : y;
+}
+// ln Z of sums l (of rows and sink) under the maximum M; the sink itself where the rows' sum is 0.
+__device__ __forceinline__ float head_lse(float M, float l, float rows, float sink) {
+  return rows == 0.f ? sink : (M + __log2f(l)) * kLn2;
+}
+
 // A head's running maximum and sums over the parts of the softmax warps.
 struct HeadSums {
   float m, l, r;  // maximum; sums of P, unrounded and rounded
@@ -548,20 +560,23 @@ __device__ __forceinline__ HeadSums head_sums(const PagedSpare& Y, int h) {
   }
   return s;
 }
-// Adds the sink's mass, stores lse and leaves 2^(m - M) / Z in X.fac, M the larger of m and sink.
+// Adds the sink's mass, stores lse and leaves 2^(m - M) / Z in X.fac, M the larger of m and sink
+// (log2).
 __device__ __forceinline__ void finish_head(const PagedAttnArgs& a, PagedAux& X, HeadSums s,
                                             float sink, int h, const Item& i) {
   // (the sink is above the rows' maximum only where that did not start at it)
   const float M = fmaxf(s.m, sink), Mf = M == -INFINITY ? 0.f : M, w = ex2(s.m - Mf);
-  s.l *= w;
+  const float rows = s.l *= w;
   s.r *= w;
   if (sink > -INFINITY) {
     s.l += ex2(sink - Mf);
     s.r += ex2(sink - Mf);
   }
   X.fac[h] = s.r > 0.f || s.r != s.r ? w / s.r : 0.f;  // no row and no sink: zeros
-  if (a.lse)
-    a.lse[i.q * a.H + 64 * i.hg + h] = s.l == 0.f ? -INFINITY : (Mf + __log2f(s.l)) * kLn2;
+  if (a.lse) {
+    const int hq = 64 * i.hg + h;
+    a.lse[i.q * a.H + hq] = head_lse(Mf, s.l, rows, a.sink ? a.sink[hq] : -INFINITY);
+  }
 }
 
 // Dims 128 mt + 32 quad .. + 31 of all heads by one warp: O^T from TMEM (lane = dim) times 1 / Z
@@ -772,8 +787,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         float mA = -INFINITY, mB = -INFINITY;
         float2 lA = make_float2(0.f, 0.f), lB = lA, rA = lA, rB = lA;  // unrounded, rounded
         if (a.sink) {
-          if (hA < Hg) mA = a.sink[64 * w.i.hg + hA] * kLog2e;
-          if (hB < Hg) mB = a.sink[64 * w.i.hg + hB] * kLog2e;
+          if (hA < Hg) mA = sink_log2(a.sink[64 * w.i.hg + hA]);
+          if (hB < Hg) mB = sink_log2(a.sink[64 * w.i.hg + hB]);
         }
         const bool whole = kDirect ? cl == 1 : w.unit == 0 && w.seg_units == w.i.units;
         const float sinkA = mA, sinkB = mB;
@@ -1507,7 +1522,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     for (int i = tid; live && i < 8 * kHp; i += C::kThreads) {
       const int h = i >> 3, o = i & 7;
       const bool in = o < cl && h < Hg;  // heads that are padding weigh nothing
-      const float sink = a.sink && h < Hg ? a.sink[64 * I.hg + h] * kLog2e : -INFINITY;
+      const float logit = a.sink && h < Hg ? a.sink[64 * I.hg + h] : -INFINITY;
+      const float sink = sink_log2(logit);
       float* so = st + o * 3 * kHp + h;
       const float m = in ? so[0] : -INFINITY;
       float M = fmaxf(m, sink);
@@ -1522,13 +1538,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       }
       if (o < cl) so[0] = in ? w : 0.f;
       if (o > 0 || h >= Hg) continue;
+      const float rows = l;
       if (sink > -INFINITY) {
         l += ex2(sink - Mf);
         r += ex2(sink - Mf);
       }
       X.fac[h] = r > 0.f || r != r ? 1.f / r : 0.f;
       if (a.lse && crank == 0)
-        a.lse[I.q * a.H + 64 * I.hg + h] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
+        a.lse[I.q * a.H + 64 * I.hg + h] = head_lse(Mf, l, rows, logit);
     }
     __syncthreads();
     if (live) {
@@ -1630,7 +1647,7 @@ __global__ void __launch_bounds__(kPairs * kGroups * kSets)
   for (int hh = warp; hh < 4 * kSets; hh += kWarps) {
     const int hb = 4 * hc0 + hh, hq = 64 * hg + hb;
     const bool there = hq < a.H && hb < hp;
-    const float sink = a.sink && there ? a.sink[hq] * kLog2e : -INFINITY;
+    const float logit = a.sink && there ? a.sink[hq] : -INFINITY, sink = sink_log2(logit);
     float m[(kMaxCtas + 31) / 32], M = sink;
 #pragma unroll
     for (int i = 0; i < (kMaxCtas + 31) / 32; ++i) {
@@ -1659,13 +1676,13 @@ __global__ void __launch_bounds__(kPairs * kGroups * kSets)
       l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
       r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
     }
-    const float sk = sink == -INFINITY ? 0.f : ex2(sink - Mf);
+    const float sk = sink == -INFINITY ? 0.f : ex2(sink - Mf), rows = l;
     l += sk;
     r += sk;
     if (lane == 0) {
       reinterpret_cast<float*>(inv_s)[hh] = r > 0.f || r != r ? 1.f / r : 0.f;
       if (a.lse && cut == 0 && there)
-        a.lse[q * a.H + hq] = l == 0.f ? -INFINITY : (Mf + __log2f(l)) * kLn2;
+        a.lse[q * a.H + hq] = head_lse(Mf, l, rows, logit);
     }
   }
   __syncthreads();

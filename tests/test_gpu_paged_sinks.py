@@ -72,3 +72,12 @@ def test_a_sink_far_below_zero_and_above_the_scores(dtype, n, copies):
     csa2.csa2_device_status()
     for i in range(0, copies, 53):
         check_query(out[i], lse[i], q[i], rows, sink, -3e4, n - 1, False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("path", PATHS)
+def test_sinks_at_the_ends_of_fp32(dtype, path):
+    """Finite sinks whose base-2 logit is not: no mass below, all of it above, and lse of a query
+    without rows is the sink."""
+    big = float(np.finfo(np.float32).max)
+    run(dtype, PATHS[path], 64, [big, -big, 3e38, -3e38, 0.25, 2e38, -2e38], 512 ** -0.5, 5)
