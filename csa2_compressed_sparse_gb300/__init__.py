@@ -446,6 +446,16 @@ def _arg(name, t, dtype, shape, dev):
     return t.data_ptr()
 
 
+def _workspace(ws, dev):
+    """Address and bytes of a dense workspace of any type on GPU dev (None: none)."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"csa2: ws must be a contiguous tensor on cuda:{dev} (got one on "
+                         f"{ws.device})")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with GPU dev current; the stream is one of that GPU's."""
     if stream is None:
@@ -498,5 +508,4 @@ def csa2_paged_attn(q, q_seq, q_pos, cache: Paged, out, ws=None, max_rows=None, 
           _arg("sink", sink, torch.float32, (H,), dev), scale,
           _arg("out", out, torch.bfloat16, (Q, H, 512), dev),
           _arg("lse", lse, torch.float32, (Q, H), dev),
-          _arg("inv_freq", inv_freq, torch.float32, (32,), dev), _p(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+          _arg("inv_freq", inv_freq, torch.float32, (32,), dev), *_workspace(ws, dev))
