@@ -2,6 +2,8 @@
 // per-translation-unit fault flag helpers.
 #pragma once
 
+#include <cfloat>
+
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
@@ -16,6 +18,7 @@ constexpr int kHeads = 64;   // attention query heads
 constexpr int kRing = 128;   // sliding-window slots
 constexpr int kRopeDim0 = 448;
 constexpr int kMaxK = 512;   // largest top-k
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct CompressArgs {
   const uint16_t* kv;
@@ -264,6 +267,12 @@ __device__ __forceinline__ uint64_t rope_turn(float theta) {
 }
 __device__ __forceinline__ float rope_angle(uint64_t turn, uint64_t p) {
   return (float)(int64_t)(p * turn) * 3.4061215800865545e-19f;  // 2 pi / 2^64
+}
+
+// A sink's logit in log2.  A finite one stays finite: the largest and lowest of fp32 overflow.
+__device__ __forceinline__ float sink_log2(float sink) {
+  const float y = sink * kLog2e;
+  return isinf(y) && !isinf(sink) ? copysignf(FLT_MAX, sink) : y;
 }
 
 __host__ __device__ __forceinline__ uint32_t score_key(float f) {

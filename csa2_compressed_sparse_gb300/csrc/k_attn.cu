@@ -64,8 +64,13 @@ constexpr int kPBytes = 64 * 128;         // P [64 heads][64 rows] bf16
 constexpr uint32_t kColSa = 0;            // TMEM columns of S buffer b, dims 0..255: 64 b
 constexpr uint32_t kColSb = 128;          // the same for dims 256..511: 128 + 64 b
 constexpr uint32_t kColO = 256;           // O^T tiles at 256 + 64 * mt
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 64.0f;
+// Where a running max starts for a sink below it (or of -inf), and for a head whose first scores
+// are all -inf or NaN.  A max is moved by adding a score's distance to it, which would lose the
+// score where the two are far apart (fp32's steps are 1/8 here); and the heads of a warp, which
+// loads TMEM as a whole, all have a max or none.  The price: such a head gets no weights where all
+// its scores are below this, too (-726817 as natural logarithms).
+constexpr float kLowMax = -1048576.0f;
 constexpr int kRopeDim0 = 448;            // dims 448..511 carry the RoPE phase
 
 struct __align__(16) Aux {
@@ -615,13 +620,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the running max starts at the sink logit, so no chunk needs a separate max pass;
       // the sink's own mass enters the sum here with one CTA per query, else once in the
       // merge
-      mA = a.sink[hA] * kLog2e;
-      mB = a.sink[hB] * kLog2e;
-      if (nsplit == 1 && r4 == 0) { lA = 1.f; lB = 1.f; }
+      mA = sink_log2(a.sink[hA]);
+      mB = sink_log2(a.sink[hB]);
     }
     if (r4 == 0) {
       X.sink2[hA] = mA;
       X.sink2[hB] = mB;
+    }
+    if (a.sink) {
+      mA = fmaxf(mA, kLowMax);
+      mB = fmaxf(mB, kLowMax);
+      if (nsplit == 1 && r4 == 0) { lA = mA > kLowMax ? 1.f : 0.f; lB = mB > kLowMax ? 1.f : 0.f; }
     }
     for (int it = 0; it < n; ++it) {
       const int bsel = it & 1;
@@ -669,8 +678,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         smA = fmaxf(smA, __shfl_xor_sync(0xFFFFFFFFu, smA, 2));
         smB = fmaxf(smB, __shfl_xor_sync(0xFFFFFFFFu, smB, 1));
         smB = fmaxf(smB, __shfl_xor_sync(0xFFFFFFFFu, smB, 2));
-        mA = smA;
-        mB = smB;
+        const float low = (mlo | mhi) != 0u ? kLowMax : -INFINITY;
+        mA = smA == -INFINITY ? low : smA;
+        mB = smB == -INFINITY ? low : smB;
         facA = 0.f;
         facB = 0.f;
         need = true;
@@ -1127,14 +1137,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r4 = lane & 3;
     const int hA = 16 * warp + (lane >> 2), hB = hA + 8;
     const uint32_t lrow = (uint32_t)(warp * 32) << 16;
-    const float skA = a.sink ? a.sink[hA] * kLog2e : -INFINITY;
-    const float skB = a.sink ? a.sink[hB] * kLog2e : -INFINITY;
+    const float skA = a.sink ? fmaxf(sink_log2(a.sink[hA]), kLowMax) : -INFINITY;
+    const float skB = a.sink ? fmaxf(sink_log2(a.sink[hB]), kLowMax) : -INFINITY;
     auto group_sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
     for (int j = 0; j < nq; ++j) {
       const int q = q0 + j * G, par = j & 1;
       // the running max starts at the sink logit and the sum at the sink's mass
       float mA = skA, mB = skB, lA = 0.f, lB = 0.f;
-      if (a.sink && r4 == 0) { lA = 1.f; lB = 1.f; }
+      if (a.sink && r4 == 0) { lA = skA > kLowMax ? 1.f : 0.f; lB = skB > kLowMax ? 1.f : 0.f; }
       for (int c = 0; c < n; ++c) {
         const int cg = j * n + c;
         const int bsel = cg & 1;
@@ -1187,8 +1197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           smA = fmaxf(smA, __shfl_xor_sync(0xFFFFFFFFu, smA, 2));
           smB = fmaxf(smB, __shfl_xor_sync(0xFFFFFFFFu, smB, 1));
           smB = fmaxf(smB, __shfl_xor_sync(0xFFFFFFFFu, smB, 2));
-          mA = smA;
-          mB = smB;
+          const float low = (mlo | mhi) != 0u ? kLowMax : -INFINITY;
+          mA = smA == -INFINITY ? low : smA;
+          mB = smB == -INFINITY ? low : smB;
           facA = 0.f;
           facB = 0.f;
           need = true;

@@ -4,8 +4,6 @@
 //
 // A cache row is one 512-d latent, key and value of every head.  Pages hold page_rows rows;
 // table[b][j / page_rows] is the page of row j of sequence b.
-#include <cfloat>
-
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -16,7 +14,6 @@ CSA2_DEFINE_FAULT_FLAG(paged)
 namespace csa2 {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ================================ append ================================================
@@ -536,11 +533,6 @@ __device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
 
-// A sink's logit in log2.  A finite one stays finite: the largest and lowest of fp32 overflow.
-__device__ __forceinline__ float sink_log2(float sink) {
-  const float y = sink * kLog2e;
-  return fabsf(y) == INFINITY && fabsf(sink) < INFINITY ? copysignf(FLT_MAX, sink) : y;
-}
 // ln Z of sums l (of rows and sink) under the maximum M; the sink itself where the rows' sum is 0.
 __device__ __forceinline__ float head_lse(float M, float l, float rows, float sink) {
   return rows == 0.f ? sink : (M + __log2f(l)) * kLn2;

@@ -399,7 +399,9 @@ csa2_status csa2_topk_scores(const float* scores, const int32_t* n, int Q, int64
  *   plane  [plane_rows][512] bf16, plane_rows < 2^31;  row_base int64;
  *          sel [Q][nsel] int32, nsel <= 512
  *          (sel may be NULL with nsel == 0: window only)
- *   sink   [64] fp32 or NULL (no sink term);  scale: softmax temperature (1/sqrt(512))
+ *   sink   [64] fp32, finite or -inf, or NULL (no sink term).  Beyond +-2.36e38 (fp32's
+ *          largest value in base 2) a sink is taken as that.  A head whose sink and scores are
+ *          all below -7.2e5 gets zeros.  scale: softmax temperature (1/sqrt(512))
  *   out    [Q][64][512] bf16;  lse [Q][64] fp32 or NULL
  *   ws     optional workspace (256-byte aligned, NULL allowed) of
  *          csa2_attn_workspace_size(Q, nsel) bytes, which is 0: a query's entries run on
