@@ -241,6 +241,11 @@ constexpr int kBlock = 1024;  // 64 dims of 8 rows
 constexpr int kGroup = 2048;  // 128 dims of 8 rows
 constexpr int kMaxSmem = 232448;
 constexpr float kLazy = 64.0f;
+// Most tiles that O^T sums up, a power of two.  The tensor core cuts the low bits of its running
+// sums instead of rounding them, so sums of one sign come out short by some 2^-24 of themselves per
+// product of 16 rows: 0.04 % after 65536 rows, a tenth of the output's own rounding, but 0.6 % after
+// a million.  A longer segment is done in runs, whose parts are added up in fp32.
+constexpr int kRunTiles = 1024;
 constexpr float kLowSink = -1048576.0f;  // from here on fp32's steps are 1/8 and less
 constexpr uint32_t kColO = 256;  // O^T tiles at 256 + 64 mt
 
@@ -262,7 +267,7 @@ struct __align__(16) PagedAux {
   uint64_t fin[2];
   uint64_t mask[4];     // valid rows of tile c at c & 3
   int it0, it0_unit;    // first item of this CTA and the units before it within the item
-  float fac[64];        // rescale factor or 1 / sum, per head
+  __align__(16) float fac[64];  // rescale factor or 1 / sum, per head
   float rope_c[32], rope_s[32];
   uint32_t tmem_slot;
   int abort;
@@ -571,6 +576,60 @@ __device__ __forceinline__ void finish_head(const PagedAttnArgs& a, PagedAux& X,
   }
 }
 
+// Adds the part of an item's earlier runs (po: this lane's place in it, st: this thread's head's m,
+// l, r) to the run in TMEM and Y, both under the larger maximum; the sum goes to both places.
+template <int kHp, int kSoft, int kParts>
+__device__ __forceinline__ void fold_run(float* po, float* st, PagedAux& X, PagedSpare& Y, uint32_t tq,
+                                      int half, int Hg, int tid) {
+  if (tid < Hg) {
+    const HeadSums h = head_sums<kParts>(Y, tid);
+    const float M = fmaxf(st[0], h.m), Mf = M == -INFINITY ? 0.f : M;
+    const float f0 = ex2(st[0] - Mf), f1 = ex2(h.m - Mf);
+    Y.top[0][tid] = f0;
+    X.fac[tid] = f1;
+    st[0] = M;
+    st[kHp] = h.l * f1 + st[kHp] * f0;
+    st[2 * kHp] = h.r * f1 + st[2 * kHp] * f0;
+  }
+  soft_sync<kSoft>();
+#pragma unroll 1
+  for (int mt = half; mt < 4; mt += kParts) {
+#pragma unroll 1
+    for (int hb = 0; hb < Hg; hb += 16) {
+      uint32_t v[16];
+      tmem_ld16(tq + kColO + 64 * mt + hb, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        float4* to = reinterpret_cast<float4*>(po + (mt * (kHp / 4) + ((hb + j) >> 2)) * 512);
+        const float4 f0 = *reinterpret_cast<const float4*>(&Y.top[0][hb + j]);
+        const float4 f1 = *reinterpret_cast<const float4*>(&X.fac[hb + j]);
+        float4 x = *to;
+        x.x = x.x * f0.x + __uint_as_float(v[j]) * f1.x;
+        x.y = x.y * f0.y + __uint_as_float(v[j + 1]) * f1.y;
+        x.z = x.z * f0.z + __uint_as_float(v[j + 2]) * f1.z;
+        x.w = x.w * f0.w + __uint_as_float(v[j + 3]) * f1.w;
+        *to = x;
+        v[j] = __float_as_uint(x.x);
+        v[j + 1] = __float_as_uint(x.y);
+        v[j + 2] = __float_as_uint(x.z);
+        v[j + 3] = __float_as_uint(x.w);
+      }
+      tmem_st16(tq + kColO + 64 * mt + hb, v);
+    }
+  }
+  tmem_st_wait();
+  soft_sync<kSoft>();  // the factors are read
+}
+
+// The same as a call.  Rare as it is, it costs the loop over the tiles registers: as a call 1 to 2 us
+// less with bf16 rows (231 and 152 us in all), but 14 us more with FP8_S128 rows (344).
+template <int kHp, int kSoft, int kParts>
+__device__ __noinline__ void call_fold_run(float* po, float* st, PagedAux& X, PagedSpare& Y,
+                                           uint32_t tq, int half, int Hg, int tid) {
+  fold_run<kHp, kSoft, kParts>(po, st, X, Y, tq, half, Hg, tid);
+}
+
 // Dims 128 mt + 32 quad .. + 31 of all heads by one warp: O^T from TMEM (lane = dim) times 1 / Z
 // and rotated back, in bf16 through a KiB of shared memory at `stage` ([16 heads][32 dims],
 // written as transposed 8 x 8 matrices; 16-byte chunk i of head h at i ^ (h / 2 % 4), free of bank
@@ -774,7 +833,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
       int sl = 0;                      // ring slot of the tile's first quarter
       uint32_t sph = 0;                // its phase
       int64_t u = u0;                  // unit where the segment begins
-      do {
+      int t0 = w.t;                    // tile where the run begins
+      for (;;) {
         const int Hg = min(64, a.H - 64 * w.i.hg);
         float mA = -INFINITY, mB = -INFINITY;
         float2 lA = make_float2(0.f, 0.f), lB = lA, rA = lA, rB = lA;  // unrounded, rounded
@@ -795,7 +855,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
           X.rope_c[lane] = cs;
           X.rope_s[lane] = s;
         }
-        for (int t = w.t; t < w.t_end; ++t, ++c) {
+        const int t_run = kDirect ? w.t_end : min(t0 + kRunTiles, w.t_end);
+        for (int t = t0; t < t_run; ++t, ++c) {
           const int sb = C::kScaled ? 0 : c & 1;
           const uint32_t sphase = C::kScaled ? (uint32_t)c & 1 : (uint32_t)(c >> 1) & 1;
           // P's memory and O^T are free once the previous tile's products are done.  With bf16
@@ -946,7 +1007,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               rB = fma2(rB, qB, o0);
             }
             soft_sync<C::kSoft>();  // fac is written, and top read, by all
-            if (t > w.t) {
+            if (t > t0) {
               tc_fence_after();
 #pragma unroll 1
               for (int mt = half; mt < 4; mt += kParts) {
@@ -1057,33 +1118,42 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         const int64_t part = 2 * (int64_t)blockIdx.x + (w.unit == 0 ? 1 : 0);
         soft_sync<C::kSoft>();
         if (kDirect) break;  // the output, by more warps, or the cluster's join follows below
+        float* st = a.pstat + part * (3 * kHp) + tid;
+        // [dim tile][four heads][even dims, odd dims][4]: a lane writes 16 bytes, and the
+        // join's threads, which have a pair of dims each, read them side by side
+        float* po = a.part + part * (int64_t)(kHp * kDLat) +
+                    (((quad * 32 + lane) >> 1) + (lane & 1) * 64) * 4;
+        const bool onto = t0 > w.t, last = t_run == w.t_end;  // of the segment's runs
+        if (onto) {
+          if (C::kScaled)
+            fold_run<kHp, C::kSoft, kParts>(po, st, X, Y, tmem + lrow, half, Hg, tid);
+          else
+            call_fold_run<kHp, C::kSoft, kParts>(po, st, X, Y, tmem + lrow, half, Hg, tid);
+        }
         if (tid < Hg) {
-          const HeadSums h = head_sums<kParts>(Y, tid);
-          if (whole) {
+          if (whole && last) {
+            const HeadSums h =
+                onto ? HeadSums{st[0], st[kHp], st[2 * kHp]} : head_sums<kParts>(Y, tid);
             finish_head(a, X, h, Y.sink2[tid], tid, w.i);
-          } else {
-            float* st = a.pstat + part * (3 * kHp) + tid;
+          } else if (!onto) {
+            const HeadSums h = head_sums<kParts>(Y, tid);
             st[0] = h.m;
             st[kHp] = h.l;
             st[2 * kHp] = h.r;
           }
         }
-        if (a.rec && w.unit == 0 && tid == 0) {
+        if (a.rec && last && w.unit == 0 && tid == 0) {
           // CTAs of the item's first and last unit; (-1, -1): finished here
           const int64_t ul = u + w.i.units - 1;
           a.rec[w.it] = whole ? make_int2(-1, -1)
-                              : make_int2((int)blockIdx.x, (int)(((ul + 1) * ncta - 1) / U));
+                             : make_int2((int)blockIdx.x, (int)(((ul + 1) * ncta - 1) / U));
         }
         soft_sync<C::kSoft>();
-        if (whole) {
+        if (whole && last) {
           uint16_t* out = a.out + (w.i.q * a.H + 64 * w.i.hg) * kDLat;
           for (int mt = half; mt < 4; mt += kParts)
             store_tile(a, X, tmem + lrow, mt, quad, lane, Hg, p_s + warp * 1024, out);
-        } else {
-          // [dim tile][four heads][even dims, odd dims][4]: a lane writes 16 bytes, and the
-          // join's threads, which have a pair of dims each, read them side by side
-          float* po = a.part + part * (int64_t)(kHp * kDLat) +
-                      (((quad * 32 + lane) >> 1) + (lane & 1) * 64) * 4;
+        } else if (!onto) {
 #pragma unroll 1
           for (int mt = half; mt < 4; mt += kParts) {
 #pragma unroll 1
@@ -1100,8 +1170,14 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
         }
         tc_fence_before();
         soft_sync<C::kSoft>();  // fac, the sums and the rotation are read before the next segment's
+        if (!last) {
+          t0 = t_run;
+          continue;
+        }
         u += w.seg_units;
-      } while (walk_next(a, w));
+        if (!walk_next(a, w)) break;
+        t0 = w.t;
+      }
     } else if (warp == C::kWarpS) {
       // ================= S products =================
       // The whole warp walks the loop and one elected lane issues: with operands the same in
@@ -1183,7 +1259,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma_bf16(tmem + kColO + 64 * mt, rd + ((kk * 2 * kGroup) >> 4),
-                          pd + ((kk * 32) >> 4), id, t > 0 || kk > 0);
+                          pd + ((kk * 32) >> 4), id, (t & (kRunTiles - 1)) > 0 || kk > 0);
               umma_commit(smem_u32(&X.empty[sl]));
               if (mt == 3) umma_commit(smem_u32(&X.pv_done));
             }
