@@ -29,7 +29,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 // tokens, 3 us for 64 tokens.
 
 constexpr int kAppWarps = 8;
-constexpr int kAppCtas = 6;  // CTAs of an SM with many tokens
+constexpr int kAppCtas = 6;  // CTAs of an SM with many tokens (three at a time, by registers)
 
 // E4M3 codes of v over scale s, as products with r = 1 / s: within 2^-23 of the quotients, against
 // the 2^-4 of a code, and equal to them when s is a power of two.  (Eighteen divisions a lane
@@ -227,10 +227,10 @@ __global__ void __launch_bounds__(kAppWarps * 32) paged_append_kernel(PagedAppen
 // Rows outside lo .. hi - 1 or on a bad page get P = 0 and are zeroed before the product
 // (what the page holds there may be NaN).
 //
-// Measured, 64 heads: 16 sequences of 262144 rows 662 us in bf16 (96 % of the copy rate), 977 us
-// as FP8_S128, 900 us as FP8_E8M0; 64 sequences of 8192 to 32768 rows 231 us in bf16, 339 us as
+// Measured, 64 heads: 16 sequences of 262144 rows 664 us in bf16 (95 % of the copy rate), 964 us
+// as FP8_S128, 853 us as FP8_E8M0; 64 sequences of 8192 to 32768 rows 234 us in bf16, 343 us as
 // FP8_S128.  bf16 rows are bound by HBM.  FP8 rows are bound by the data pipe of L1 and shared
-// memory (77 % busy: a tile takes 1780 cycles of operand reads, 1010 of row loads, 890 of
+// memory (78 % busy: a tile takes 1780 cycles of operand reads, 1010 of row loads, 890 of
 // stores, 650 of loads and waits) and by what waits for it: a slot's way round the ring.
 //
 // The sum of P exists twice: of the bf16-rounded values, which the output is divided by (a
@@ -274,7 +274,8 @@ struct __align__(16) PagedAux {
 };
 
 // kMode 0: bf16 rows; 1: FP8_S128 (fp32 scales stay outside the products: one accumulator
-// and one P per 128 dims); 2: FP8_E8M0 (a power of two times a code is exact in bf16).
+// and one P per 128 dims); 2: FP8_E8M0 (a power of two times a code is exact in bf16 for scale
+// bytes from 3 on; below, values under 2^-127 may lose their last bits).
 template <int kHp, int kMode>
 struct PagedCfg {
   static constexpr bool kScaled = kMode == 1;
@@ -622,8 +623,10 @@ __device__ __forceinline__ void fold_run(float* po, float* st, PagedAux& X, Page
   soft_sync<kSoft>();  // the factors are read
 }
 
-// The same as a call.  Rare as it is, it costs the loop over the tiles registers: as a call 1 to 2 us
-// less with bf16 rows (231 and 152 us in all), but 14 us more with FP8_S128 rows (344).
+// The same as a call: rare as it is, inline it costs the loop over the tiles registers.  Inline / as
+// a call, us: 64 bf16 sequences of 8192 to 32768 rows 234.6 / 233.8, 200 short ones with 16 heads
+// 152.6 / 151.8, FP8_E8M0 rows of eight sequences with four tokens each 105.8 / 102.6; but FP8_S128
+// rows of the 64 sequences 343 / 358.
 template <int kHp, int kSoft, int kParts>
 __device__ __noinline__ void call_fold_run(float* po, float* st, PagedAux& X, PagedSpare& Y,
                                            uint32_t tq, int half, int Hg, int tid) {
@@ -1079,8 +1082,8 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
               store_matrices(pk + 8 * 128, pb);
             }
           }
-          // one fence for all: with FP8_S128 rows two, each for two quarters' P, took longer
-          // (346 against 339 us for 64 sequences of 8192 to 32768 rows)
+          // one fence for all: with FP8_S128 rows two, each for two quarters' P, took 2 % longer
+          // (64 sequences of 8192 to 32768 rows)
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
@@ -1247,7 +1250,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
             // (with FP8_S128 rows a second wait, for what is then there, lets the other issuer's
-            // products in between: 341 against 350 us for 64 sequences of 8192 to 32768 rows)
+            // products in between: 3 % less for 64 sequences of 8192 to 32768 rows)
             if (mt == 0 || (C::kScaled && mt == 2)) {
               ok = ok && all_ok(wait_phase(X, X.p_full[mt >> 1], (uint32_t)c & 1));
               if (!ok) break;
@@ -1658,9 +1661,9 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
 // kAhead of them loaded before the weights are known.  Bound by latency: the parts come from L2.
 // Many items, of few parts each, take four sets and no groups: few CTAs with long loads.  Fewer
 // items take four groups and a set; a single long one, which may have 152 parts, 32 groups and
-// CTAs of 64 dims (whole calls, us: 64 items of 128 to 512 tiles 231 with sets / 240 with groups,
-// 16 of 256 to 512 tiles 84 / 86, 8 of them 58 / 53; one item of 1024 tiles 31.7 with 32 groups
-// / 40.2 with four, two 45.9 / 45.4).
+// CTAs of 64 dims (whole calls, us: 64 items of 128 to 512 tiles 234 with sets / 240 with groups,
+// 16 of 256 to 512 tiles 88 / 87, 8 of them 62 / 54; one item of 1024 tiles 31.8 with 32 groups
+// / 45.4 with four, two 46.7 / 49.9).
 constexpr int kMaxCtas = 152;
 constexpr int kAhead = 4;
 
@@ -1855,8 +1858,8 @@ int paged_max_ctas() { return kMaxCtas; }
 // longer one are shared by 8, 4 or 2, as many as all items leave room for (clusters of eight do
 // not fill every SM): up to 32 tiles an item, where lengths below the caller's bound cost
 // little.  Measured, us, bf16, equal lengths, clusters against even dealing: 8 sequences of
-// 16 tiles 14.5 / 16.0, 33 of 32 tiles 24.7 / 40.2, 66 of 16 tiles 24.3 / 41.8; of more than 16
-// tiles six sequences 16.5 / 18.1, but five 16.4 / 15.0 (FP8 20.8 / 24.3 and 20.6 / 20.3).
+// 16 tiles 16.0 / 17.7, 33 of 32 tiles 26.6 / 36.8, 66 of 16 tiles 26.3 / 38.6; of 32 tiles six
+// sequences 18.4 / 17.8 and five 17.9 / 17.6 (FP8_S128 23.3 / 23.7 and 22.8 / 23.5).
 int paged_cluster(int64_t items, int64_t tiles, int sms) {
   if (tiles <= paged_unit_tiles()) return items <= sms ? 1 : 0;
   if (tiles > 32 || (tiles > 16 && items < 6)) return 0;

@@ -538,7 +538,8 @@ typedef struct {
  *             are zero)
  *   FP8_E8M0  code = E4M3(x / 2^(e - 127)), e the smallest byte in [0, 254] with
  *             max |x| <= 448 * 2^(e - 127) over each 32 dims (127 when all are zero)
- * The FP8 forms want finite values.
+ * The quotient x / s is the product with the rounded 1 / s, within 2^-23 of itself: at a tie
+ * between two codes (FP8_S128) either may come out.  The FP8 forms want finite values.
  *   kv           [T] rows of 512 bf16, kv_ld elements apart (a multiple of 8, >= 512)
  *   cu_seqlens   [cache->B + 1] int32, non-decreasing, cu_seqlens[0] == 0.  Tokens from
  *                cu_seqlens[B] on (a padded batch) are skipped
@@ -563,9 +564,10 @@ csa2_status csa2_paged_append(const csa2_bf16* kv, int64_t kv_ld, int T, const i
  *     s_j   = scale * <q[q][h], x_j>
  *     Z     = e^{sink[h]} + sum_j e^{s_j}
  *     out_h = sum_j e^{s_j} x_j / Z,   lse_h = ln Z
- * with fp32 sums of bf16 products (FP8 codes are exact in bf16; their scales are applied in
- * fp32 or as powers of two); the weights e^{s_j - m} are rounded to bf16 for the second
- * product.  A query that sees no row gets zeros and lse = sink[h] (-inf without a sink).
+ * with fp32 sums of bf16 products (FP8 codes are exact in bf16; their scales are applied to
+ * the scores in fp32, or as powers of two to the codes); the weights e^{s_j - m}, with
+ * FP8_S128 rows times the row's scale of each 128 dims, are rounded to bf16 for the second
+ * product.  Over many rows of one sign the tensor core's sums come out up to 0.04 % short.  A query that sees no row gets zeros and lse = sink[h] (-inf without a sink).
  * q_seq[q] == -1 marks a padded query, whose out and lse are left as they were; other
  * values outside [0, B) raise CSA2_EBOUNDS and are treated so too.
  *   q, out     [Q][H][512] bf16;  Q 0 .. 65535;  H 1 .. 128
