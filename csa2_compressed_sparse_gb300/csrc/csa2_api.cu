@@ -28,7 +28,8 @@ csa2_status cuda_fail(cudaError_t e, const char* where) {
   return fail(CSA2_ECUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(size_t n, const void* p) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool aligned16(const void* p) { return aligned_to(16, p); }
 
 #define REQUIRE(cond, ...)                         \
   do {                                             \
@@ -609,6 +610,7 @@ csa2_status paged_args(const char* name, const csa2_paged* p, csa2::PagedCache* 
           (long long)page, (long long)p->page_stride);
   REQUIRE(p->B >= 1 && p->B <= 65535, "%s: cache.B must be in [1, 65535] (got %d)", name, p->B);
   REQUIRE(p->table, "%s: cache.table is required", name);
+  REQUIRE(aligned_to(4, p->table), "%s: cache.table must be 4-byte aligned", name);
   REQUIRE(p->table_cols >= 1 && p->table_ld >= p->table_cols,
           "%s: cache.table_cols must be in [1, table_ld] (got %lld, table_ld %lld)", name,
           (long long)p->table_cols, (long long)p->table_ld);
@@ -673,6 +675,8 @@ csa2_status csa2_paged_append(const csa2_bf16* kv, int64_t kv_ld, int T, const i
   if (st != CSA2_OK) return st;
   REQUIRE(kv && cu_seqlens && start_row, "%s: kv, cu_seqlens and start_row are required", name);
   REQUIRE(aligned16(kv), "%s: kv must be 16-byte aligned", name);
+  REQUIRE(aligned_to(4, cu_seqlens) && aligned_to(8, start_row) && aligned_to(4, inv_freq),
+          "%s: cu_seqlens, start_row and inv_freq must be aligned to their elements", name);
   REQUIRE(kv_ld >= 512 && kv_ld % 8 == 0, "%s: kv_ld must be a multiple of 8, >= 512 (got %lld)",
           name, (long long)kv_ld);
   REQUIRE(ratio >= 1 && ratio <= 65536, "%s: ratio must be in [1, 65536] (got %d)", name, ratio);
@@ -706,6 +710,9 @@ csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_s
   if (st != CSA2_OK) return st;
   REQUIRE(q && q_seq && q_pos && out, "%s: q, q_seq, q_pos and out are required", name);
   REQUIRE(aligned16(q) && aligned16(out), "%s: q and out must be 16-byte aligned", name);
+  REQUIRE(aligned_to(4, q_seq) && aligned_to(8, q_pos) && aligned_to(4, sink) &&
+              aligned_to(4, lse) && aligned_to(4, inv_freq),
+          "%s: q_seq, q_pos, sink, lse and inv_freq must be aligned to their elements", name);
   REQUIRE(H >= 1 && H <= 128, "%s: H must be in [1, 128] (got %d)", name, H);
   REQUIRE(ratio >= 1 && ratio <= 65536, "%s: ratio must be in [1, 65536] (got %d)", name, ratio);
   REQUIRE(window >= 0, "%s: window must be >= 0 (got %lld)", name, (long long)window);

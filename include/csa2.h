@@ -39,7 +39,9 @@
  *     device-side flag; csa2_device_status() reports and clears it.
  *   - Row ids in `sel`/`cand` are sequence-local; -1 marks an empty entry.  bf16
  *     tensors are raw 16-bit patterns (csa2_bf16).  Layouts are row-major, dense.
- *   - Base addresses must be 16-byte aligned; the library checks this.
+ *   - Rows, planes, states and outputs of rows must be 16-byte aligned, which the library
+ *     checks; indices, positions, sinks, lse and the like to their elements, which the calls
+ *     on the paged cache check too.
  *
  * Page references ("section" names are the pages' own headings):
  *   [A] "DeepSeek-V4.1-Flash 架构解剖" (perryzhang01.github.io, v41_flash_anatomy)
