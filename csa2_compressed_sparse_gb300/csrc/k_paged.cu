@@ -1543,6 +1543,7 @@ __global__ void __launch_bounds__(PagedCfg<kHp, kMode>::kThreads, 1)
     // weigh, sum and store.
     const int lg = cl == 8 ? 3 : cl == 4 ? 2 : 1;
     const int slice = kDLat >> lg, half = slice >> 1;  // dims, pairs of them
+    static_assert(NS * kSlotBytes >= kHp * 2048, "room for the parts, [ranks][heads][a rank's dims]");
     constexpr bool kTail = NS * kSlotBytes >= kHp * 2048 + 8 * 3 * kHp * 4;
     // [rank][m, l, r][head], in every CTA
     const uint32_t st_off = kTail ? (uint32_t)(C::kQBytes + kHp * 2048)
