@@ -28,13 +28,15 @@ __all__ = [
     "csa2_topk_scores", "csa2_attn_workspace_size", "csa2_sparse_attn", "csa2_reuse_attn",
     "csa2_sparse_attn_rope", "csa2_reuse_attn_rope", "csa2_plane_fp4_bytes", "csa2_plane_fp4",
     "csa2_sparse_attn_fp4", "csa2_selftest_wait_timeout", "Paged", "csa2_paged_append",
-    "csa2_paged_attn_workspace_size", "csa2_paged_attn",
+    "csa2_paged_attn_workspace_size", "csa2_paged_attn", "csa2_paged_read",
+    "csa2_paged_chunk_attn_workspace_size", "csa2_paged_chunk_attn", "csa2_qk_norm_rope",
 ]
 
 STATUS = {0: "CSA2_OK", 1: "CSA2_EINVAL", 2: "CSA2_ECUDA", 3: "CSA2_ETIMEOUT", 4: "CSA2_EBOUNDS",
           5: "CSA2_ENOSPACE"}
 SWA_RING, SWA_LINEAR = 0, 1
 SWA_BF16, SWA_FP8_S128, SWA_FP8_E8M0 = 0, 1, 2
+ROPE_PAIRS, ROPE_HALVES = 0, 1
 
 
 class Csa2Error(RuntimeError):
@@ -55,6 +57,13 @@ class _PagedC(ctypes.Structure):
                 ("page_stride", ctypes.c_int64), ("table", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("table_ld", ctypes.c_int64),
                 ("table_cols", ctypes.c_int64)]
+
+
+class _HeadsC(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_token", ctypes.c_int64),
+                ("x_head", ctypes.c_int64), ("out_token", ctypes.c_int64),
+                ("out_head", ctypes.c_int64), ("H", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("norm_w", ctypes.c_void_p)]
 
 
 _vp, _i32, _i64, _f32, _sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float,
@@ -113,6 +122,15 @@ _SIGS.update({
     "csa2_paged_attn_workspace_size": ([_i32, _i32, _i64], _sz),
     "csa2_paged_attn": ([_vp, _i32, _i32, _vp, _vp, ctypes.POINTER(_PagedC), _i32, _i64, _i64,
                          _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+})
+
+_SIGS.update({
+    "csa2_paged_read": ([_vp, _i64, _i32, _vp, _vp, _i32, ctypes.POINTER(_PagedC), _vp, _vp], _i32),
+    "csa2_paged_chunk_attn_workspace_size": ([_i32, _i32, ctypes.POINTER(_PagedC), _i64, _i64], _sz),
+    "csa2_paged_chunk_attn": ([_vp, _i32, _i32, _vp, _vp, ctypes.POINTER(_PagedC), _i32, _i64, _i64,
+                               _i64, _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "csa2_qk_norm_rope": ([ctypes.POINTER(_HeadsC), ctypes.POINTER(_HeadsC), _i32, _i32, _f32, _vp,
+                           _vp, _i32, _i32, _i32, _f32, _vp], _i32),
 })
 
 _LIB = None
@@ -509,3 +527,90 @@ def csa2_paged_attn(q, q_seq, q_pos, cache: Paged, out, ws=None, max_rows=None, 
           _arg("out", out, torch.bfloat16, (Q, H, 512), dev),
           _arg("lse", lse, torch.float32, (Q, H), dev),
           _arg("inv_freq", inv_freq, torch.float32, (32,), dev), *_workspace(ws, dev))
+
+
+def csa2_paged_read(out, cu_seqlens, start_row, cache: Paged, inv_freq=None, ratio=1, stream=None):
+    """Rows start_row[b].. of the cache's sequences as bf16 rows out [T, 512] (row stride a multiple
+    of 8), cu_seqlens[b].. each; rotated back by their position j * ratio when inv_freq is given."""
+    dev, B = cache._dev, cache._c.B
+    T = out.shape[0]
+    if (out.dtype is not torch.bfloat16 or out.get_device() != dev or out.shape != (T, 512) or
+            (T > 0 and out.stride(1) != 1) or (T > 1 and out.stride(0) < 512)):
+        raise ValueError(f"csa2: out must be [T, 512] bf16 with dense rows on cuda:{dev}")
+    _call(lib().csa2_paged_read, dev, stream, out.data_ptr(), out.stride(0) if T > 1 else 512, T,
+          _arg("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev),
+          _arg("start_row", start_row, torch.int64, (B,), dev), ratio, cache.c(),
+          _arg("inv_freq", inv_freq, torch.float32, (32,), dev))
+
+
+def _chunk_rows(cache, max_rows, total_rows):
+    """The bounds of a chunk's attention: what the page table can hold where none is given."""
+    if max_rows is None:
+        max_rows = min(cache.table.shape[1] * cache.data.shape[1], 0x7FFFFF00)
+    if total_rows is None:
+        total_rows = min(cache._c.B * max_rows, 0x7FFFFF00)
+    return max_rows, total_rows
+
+
+def csa2_paged_chunk_attn_workspace_size(T, H, cache: Paged, max_rows=None, total_rows=None):
+    max_rows, total_rows = _chunk_rows(cache, max_rows, total_rows)
+    return int(lib().csa2_paged_chunk_attn_workspace_size(T, H, cache.c(), max_rows, total_rows))
+
+
+def csa2_paged_chunk_attn(q, cu_seqlens, start_pos, cache: Paged, out, ws=None, max_rows=None,
+                          total_rows=None, ratio=1, window=0, sink=None, lse=None,
+                          scale=512 ** -0.5, inv_freq=None, stream=None):
+    """Attention of chunks q [T, H, 512], tokens cu_seqlens[b].. of sequence b from position
+    start_pos[b] on, over the paged rows each token sees; max_rows bounds a sequence's rows and
+    total_rows those of all sequences together (None: what the page table can hold)."""
+    dev, B = cache._dev, cache._c.B
+    if q.dim() != 3:
+        raise ValueError("csa2: q must be [T, H, 512]")
+    T, H, _ = q.shape
+    max_rows, total_rows = _chunk_rows(cache, max_rows, total_rows)
+    _call(lib().csa2_paged_chunk_attn, dev, stream, _arg("q", q, torch.bfloat16, (T, H, 512), dev), T,
+          H, _arg("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev),
+          _arg("start_pos", start_pos, torch.int64, (B,), dev), cache.c(), ratio, window, max_rows,
+          total_rows, _arg("sink", sink, torch.float32, (H,), dev), scale,
+          _arg("out", out, torch.bfloat16, (T, H, 512), dev),
+          _arg("lse", lse, torch.float32, (T, H), dev),
+          _arg("inv_freq", inv_freq, torch.float32, (32,), dev), *_workspace(ws, dev))
+
+
+def _heads(name, x, out, norm, norm_w, T, D, dev):
+    """One set of heads x [T, H, D] and its output, any strides of tokens and heads."""
+    if x is None:
+        if out is not None or norm_w is not None:
+            raise ValueError(f"csa2: {name} is missing")
+        return None
+    H = x.shape[1] if x.dim() == 3 else 0
+    for what, t in ((name, x), (f"{name}_out", out)):
+        if (t is None or t.dtype is not torch.bfloat16 or t.get_device() != dev or
+                t.shape != (T, H, D) or (t.numel() > 0 and t.stride(2) != 1)):
+            raise ValueError(f"csa2: {what} must be [{T}, H, {D}] bf16 with dense heads on cuda:{dev}")
+    head = [t.stride(1) if H > 1 else 0 for t in (x, out)]
+    token = [t.stride(0) if T > 1 else 0 for t in (x, out)]
+    return ctypes.byref(_HeadsC(x.data_ptr(), out.data_ptr(), token[0], head[0], token[1], head[1], H,
+                                1 if norm else 0,
+                                _arg(f"{name}_norm_w", norm_w, torch.float32, (D,), dev)))
+
+
+def csa2_qk_norm_rope(q, q_out, pos, inv_freq, k=None, k_out=None, q_norm=True, k_norm=True,
+                      q_norm_w=None, k_norm_w=None, eps=1e-6, rope_dim0=None, layout=ROPE_PAIRS,
+                      factor=1.0, stream=None):
+    """RMSNorm of each head of q [T, H, D] and k [T, K, D] (k: optional), then the rotation of their
+    positions pos [T] by inv_freq [n] in 2 n dims from rope_dim0 on (None: the last ones); inv_freq
+    None is the norm alone.  Outputs may be the inputs."""
+    if q.dim() != 3:
+        raise ValueError("csa2: q must be [T, H, D]")
+    T, _, D = q.shape
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("csa2: tensors must live on the GPU")
+    n = 0 if inv_freq is None else inv_freq.numel()
+    if rope_dim0 is None:
+        rope_dim0 = max(0, D - 2 * n)
+    _call(lib().csa2_qk_norm_rope, dev, stream, _heads("q", q, q_out, q_norm, q_norm_w, T, D, dev),
+          _heads("k", k, k_out, k_norm, k_norm_w, T, D, dev), T, D, eps,
+          _arg("pos", pos, torch.int64, (T,), dev), _arg("inv_freq", inv_freq, torch.float32, (n,), dev),
+          rope_dim0, 2 * n, layout, factor)

@@ -199,7 +199,65 @@ struct PagedAttnArgs {
   int2* rec;
 };
 
+// Rows start_row[b] + i of the cache to row cu_seqlens[b] + i of out, as bf16.
+struct PagedReadArgs {
+  uint16_t* out;
+  int64_t out_ld;         // elements from row to row
+  int T;
+  const int32_t* cu_seqlens;
+  const int64_t* start_row;
+  int ratio;
+  const float* inv_freq;  // [32] or null: the rotation by j * ratio is undone
+  PagedCache cache;
+  int64_t cap_rows;       // these three as in PagedAppendArgs
+  uint32_t page_mul;
+  int page_shift;
+};
+
+// Attention of a chunk of new tokens: token cu_seqlens[b] + i of q sits at start_pos[b] + i.
+struct ChunkArgs {
+  const uint16_t* q;      // [T][H][512]
+  int T, H;
+  const int32_t* cu_seqlens;
+  const int64_t* start_pos;
+  PagedCache cache;
+  int64_t cap_rows;
+  int ratio;
+  int64_t window;
+  const float* sink;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  const float* inv_freq;
+  uint32_t page_mul;
+  int page_shift;
+};
+
+// Heads of queries or of keys: token t's head h at x + t x_token + h x_head (elements).
+struct HeadSet {
+  const uint16_t* x;
+  uint16_t* out;
+  int64_t x_token, x_head, out_token, out_head;
+  int H;                  // 0: none
+  int norm;
+  const float* norm_w;    // [D] or null: ones
+};
+struct HeadsArgs {
+  HeadSet q, k;
+  int T, D;
+  float eps;
+  const int64_t* pos;     // [T]
+  const float* inv_freq;  // [rope_dims / 2]
+  int rope_dim0, rope_dims, halves;
+  float factor;
+  int rows;               // heads of an item
+};
+
 cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s);
+cudaError_t launch_heads(const HeadsArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_paged_read(const PagedReadArgs& a, int sms, cudaStream_t s);
+// q_seq [T] and q_pos [T] of a chunk's tokens (-1: behind the last sequence).
+cudaError_t launch_chunk_tokens(const ChunkArgs& a, int32_t* q_seq, int64_t* q_pos, cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int sms, cudaStream_t s);
 int paged_head_pad(int H);    // heads of an item, padded: 16, 32 or 64
 int paged_unit_tiles();
@@ -253,6 +311,7 @@ int take_fault_index();
 int take_fault_topk();
 int take_fault_attn();
 int take_fault_paged();
+int take_fault_chunk();
 
 // Order-preserving map of fp32 scores to uint32 keys: NaN ranks as -inf, -0 as +0,
 // and every key of a real score is >= 1 so that 0 can mark "not scored".
@@ -267,6 +326,15 @@ __device__ __forceinline__ uint64_t rope_turn(float theta) {
 }
 __device__ __forceinline__ float rope_angle(uint64_t turn, uint64_t p) {
   return (float)(int64_t)(p * turn) * 3.4061215800865545e-19f;  // 2 pi / 2^64
+}
+
+__device__ __forceinline__ void unpack_bf16x8(uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
 }
 
 // A sink's logit in log2.  A finite one stays finite: the largest and lowest of fp32 overflow.

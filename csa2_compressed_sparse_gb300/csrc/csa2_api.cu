@@ -175,7 +175,7 @@ csa2_status csa2_device_status(csa2_stream stream) {
   if (e != cudaSuccess) return cuda_fail(e, "csa2_device_status");
   int f = 0;
   for (int v : {csa2::take_fault_compress(), csa2::take_fault_index(), csa2::take_fault_topk(),
-                csa2::take_fault_attn(), csa2::take_fault_paged()})
+                csa2::take_fault_attn(), csa2::take_fault_paged(), csa2::take_fault_chunk()})
     if (!f) f = v;
   if (f == csa2::kFaultTimeout) return fail(CSA2_ETIMEOUT, "a kernel gave up a bounded wait");
   if (f == csa2::kFaultBounds) return fail(CSA2_EBOUNDS, "a kernel met an index outside its buffer");
@@ -754,6 +754,172 @@ csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_s
   const int units = a.cluster > 0 ? 1 : (int)((tiles + a.ut - 1) / a.ut);
   cudaError_t e = csa2::launch_paged_attn(a, units, stream);
   if (e != cudaSuccess) return cuda_fail(e, name);
+  return CSA2_OK;
+}
+
+csa2_status csa2_paged_read(csa2_bf16* out, int64_t out_ld, int T, const int32_t* cu_seqlens,
+                            const int64_t* start_row, int ratio, const csa2_paged* cache,
+                            const float* inv_freq, csa2_stream stream) {
+  const char* name = "csa2_paged_read";
+  REQUIRE(T >= 0, "%s: T must be >= 0 (got %d)", name, T);
+  if (T == 0) return CSA2_OK;
+  csa2::PagedReadArgs a{};
+  csa2_status st = paged_args(name, cache, &a.cache);
+  if (st != CSA2_OK) return st;
+  REQUIRE(out && cu_seqlens && start_row, "%s: out, cu_seqlens and start_row are required", name);
+  REQUIRE(aligned16(out), "%s: out must be 16-byte aligned", name);
+  REQUIRE(aligned_to(4, cu_seqlens) && aligned_to(8, start_row) && aligned_to(4, inv_freq),
+          "%s: cu_seqlens, start_row and inv_freq must be aligned to their elements", name);
+  REQUIRE(out_ld >= 512 && out_ld % 8 == 0, "%s: out_ld must be a multiple of 8, >= 512 (got %lld)",
+          name, (long long)out_ld);
+  REQUIRE(ratio >= 1 && ratio <= 65536, "%s: ratio must be in [1, 65536] (got %d)", name, ratio);
+  a.out = out; a.out_ld = out_ld; a.T = T; a.cu_seqlens = cu_seqlens; a.start_row = start_row;
+  a.ratio = ratio; a.inv_freq = inv_freq;
+  a.cap_rows = table_rows(a.cache);
+  page_division(a.cache, &a.page_mul, &a.page_shift);
+  const int sms = num_sms();
+  if (sms <= 0) return fail(CSA2_ECUDA, "%s: no CUDA device", name);
+  cudaError_t e = csa2::launch_paged_read(a, sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return CSA2_OK;
+}
+
+namespace {
+
+// Checks of one set of heads; fills *s.
+csa2_status head_args(const char* name, const char* which, const csa2_heads* h, int T, int D,
+                      csa2::HeadSet* s) {
+  REQUIRE(h->H >= 1 && h->H <= 1024, "%s: %s.H must be in [1, 1024] (got %d)", name, which, h->H);
+  REQUIRE(h->x && h->out, "%s: %s.x and %s.out are required", name, which, which);
+  REQUIRE(aligned16(h->x) && aligned16(h->out), "%s: %s.x and %s.out must be 16-byte aligned", name,
+          which, which);
+  REQUIRE(h->x_token >= 0 && h->x_head >= 0 && h->out_token >= 0 && h->out_head >= 0 &&
+              ((h->x_token | h->x_head | h->out_token | h->out_head) & 7) == 0,
+          "%s: %s's strides must be multiples of 8, >= 0", name, which);
+  REQUIRE((h->H == 1 || h->out_head >= D) && (T == 1 || h->out_token >= D),
+          "%s: %s.out's heads or tokens overlap", name, which);
+  REQUIRE(aligned16(h->norm_w), "%s: %s.norm_w must be 16-byte aligned", name, which);
+  s->x = h->x; s->out = h->out; s->x_token = h->x_token; s->x_head = h->x_head;
+  s->out_token = h->out_token; s->out_head = h->out_head; s->H = h->H; s->norm = h->norm ? 1 : 0;
+  s->norm_w = h->norm ? h->norm_w : nullptr;
+  return CSA2_OK;
+}
+
+}  // namespace
+
+csa2_status csa2_qk_norm_rope(const csa2_heads* q, const csa2_heads* k, int T, int D, float eps,
+                              const int64_t* pos, const float* inv_freq, int rope_dim0,
+                              int rope_dims, int layout, float factor, csa2_stream stream) {
+  const char* name = "csa2_qk_norm_rope";
+  REQUIRE(T >= 0, "%s: T must be >= 0 (got %d)", name, T);
+  if (T == 0) return CSA2_OK;
+  REQUIRE(q || k, "%s: q or k is required", name);
+  REQUIRE(D >= 8 && D <= 512 && D % 8 == 0, "%s: D must be a multiple of 8 in [8, 512] (got %d)", name,
+          D);
+  REQUIRE(layout == CSA2_ROPE_PAIRS || layout == CSA2_ROPE_HALVES, "%s: bad layout %d", name, layout);
+  REQUIRE(rope_dim0 >= 0 && rope_dims >= 0 && rope_dim0 % 8 == 0 && rope_dims % 8 == 0 &&
+              rope_dims <= D && rope_dim0 <= D - rope_dims,
+          "%s: rope_dim0 and rope_dims must be multiples of 8 within D (got %d, %d)", name, rope_dim0,
+          rope_dims);
+  REQUIRE(layout == CSA2_ROPE_PAIRS || rope_dims % 16 == 0,
+          "%s: rope_dims must be a multiple of 16 with halves (got %d)", name, rope_dims);
+  REQUIRE(rope_dims == 0 || (pos && inv_freq), "%s: pos and inv_freq are required", name);
+  REQUIRE(aligned_to(8, pos) && aligned_to(4, inv_freq),
+          "%s: pos and inv_freq must be aligned to their elements", name);
+  REQUIRE(std::isfinite(eps) && eps >= 0.f, "%s: eps must be finite and >= 0", name);
+  REQUIRE(std::isfinite(factor), "%s: factor must be finite", name);
+  csa2::HeadsArgs a{};
+  if (q) {
+    csa2_status st = head_args(name, "q", q, T, D, &a.q);
+    if (st != CSA2_OK) return st;
+  }
+  if (k) {
+    csa2_status st = head_args(name, "k", k, T, D, &a.k);
+    if (st != CSA2_OK) return st;
+  }
+  a.T = T; a.D = D; a.eps = eps; a.pos = pos; a.inv_freq = inv_freq; a.rope_dim0 = rope_dim0;
+  a.rope_dims = rope_dims; a.halves = layout == CSA2_ROPE_HALVES; a.factor = factor;
+  const int sms = num_sms();
+  if (sms <= 0) return fail(CSA2_ECUDA, "%s: no CUDA device", name);
+  cudaError_t e = csa2::launch_heads(a, sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return CSA2_OK;
+}
+
+namespace {
+
+// Workspace of csa2_paged_chunk_attn.
+struct ChunkWs {
+  size_t seq, pos, attn, total;
+  size_t attn_bytes;
+};
+ChunkWs chunk_ws_layout(int T, int H, int64_t max_rows) {
+  ChunkWs w{};
+  size_t o = 0;
+  w.seq = o; o = up256(o + (size_t)T * 4);
+  w.pos = o; o = up256(o + (size_t)T * 8);
+  w.attn = o;
+  w.attn_bytes = csa2_paged_attn_workspace_size(T < 65535 ? T : 65535, H, max_rows);
+  w.total = o + w.attn_bytes;
+  return w;
+}
+
+}  // namespace
+
+size_t csa2_paged_chunk_attn_workspace_size(int T, int H, const csa2_paged* cache, int64_t max_rows,
+                                            int64_t total_rows) {
+  if (T < 0 || T > 1048576 || H < 1 || H > 128 || max_rows < 0 || max_rows > 0x7FFFFF00 ||
+      total_rows < 0 || !cache)
+    return 0;
+  if (T == 0) return 0;
+  return chunk_ws_layout(T, H, max_rows).total;
+}
+
+csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_t* cu_seqlens,
+                                  const int64_t* start_pos, const csa2_paged* cache, int ratio,
+                                  int64_t window, int64_t max_rows, int64_t total_rows,
+                                  const float* sink, float scale, csa2_bf16* out, float* lse,
+                                  const float* inv_freq, void* ws, size_t ws_bytes,
+                                  csa2_stream stream) {
+  const char* name = "csa2_paged_chunk_attn";
+  REQUIRE(T >= 0 && T <= 1048576, "%s: T must be in [0, 1048576] (got %d)", name, T);
+  if (T == 0) return CSA2_OK;
+  csa2::ChunkArgs a{};
+  csa2_status st = paged_args(name, cache, &a.cache);
+  if (st != CSA2_OK) return st;
+  REQUIRE(q && cu_seqlens && start_pos && out, "%s: q, cu_seqlens, start_pos and out are required",
+          name);
+  REQUIRE(aligned16(q) && aligned16(out), "%s: q and out must be 16-byte aligned", name);
+  REQUIRE(aligned_to(4, cu_seqlens) && aligned_to(8, start_pos) && aligned_to(4, sink) &&
+              aligned_to(4, lse) && aligned_to(4, inv_freq),
+          "%s: cu_seqlens, start_pos, sink, lse and inv_freq must be aligned to their elements", name);
+  REQUIRE(H >= 1 && H <= 128, "%s: H must be in [1, 128] (got %d)", name, H);
+  REQUIRE(ratio >= 1 && ratio <= 65536, "%s: ratio must be in [1, 65536] (got %d)", name, ratio);
+  REQUIRE(window >= 0, "%s: window must be >= 0 (got %lld)", name, (long long)window);
+  REQUIRE(max_rows >= 0 && max_rows <= 0x7FFFFF00,
+          "%s: max_rows must be in [0, 2^31 - 256] (got %lld)", name, (long long)max_rows);
+  REQUIRE(total_rows >= 0 && total_rows <= 0x7FFFFF00,
+          "%s: total_rows must be in [0, 2^31 - 256] (got %lld)", name, (long long)total_rows);
+  REQUIRE(std::isfinite(scale), "%s: scale must be finite", name);
+  REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255u) == 0, "%s: ws must be 256-byte aligned", name);
+  const ChunkWs w = chunk_ws_layout(T, H, max_rows);
+  if (!ws || ws_bytes < w.total)
+    return fail(CSA2_ENOSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws ? ws_bytes : 0,
+                w.total);
+  a.q = q; a.T = T; a.H = H; a.cu_seqlens = cu_seqlens; a.start_pos = start_pos;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  int32_t* q_seq = reinterpret_cast<int32_t*>(base + w.seq);
+  int64_t* q_pos = reinterpret_cast<int64_t*>(base + w.pos);
+  cudaError_t e = csa2::launch_chunk_tokens(a, q_seq, q_pos, stream);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  for (int t = 0; t < T; t += 65535) {
+    const int n = T - t < 65535 ? T - t : 65535;
+    const int64_t at = (int64_t)t * H;
+    st = csa2_paged_attn(q + at * 512, n, H, q_seq + t, q_pos + t, cache, ratio, window, max_rows,
+                         sink, scale, out + at * 512, lse ? lse + at : nullptr, inv_freq,
+                         base + w.attn, w.attn_bytes, stream);
+    if (st != CSA2_OK) return st;
+  }
   return CSA2_OK;
 }
 

@@ -19,8 +19,8 @@
  *     call may begin while the kernel before it on the stream drains.  Outputs and
  *     workspace are written, and selections, candidates, keys, scores and planes read,
  *     only once that kernel has finished.
- *   - csa2_paged_append and csa2_paged_attn read everything else after it too, so stream
- *     order is all that their inputs need.
+ *   - The calls on the paged cache (csa2_paged_*) and csa2_qk_norm_rope read everything else
+ *     after it too, so stream order is all that their inputs need.
  *   - The calls of the sparse step (index, top-k, attention, and the compressor's tokens
  *     in csa2_compress_index_topk) read some inputs before the kernel in front of them has
  *     finished: queries, sequence ids, positions and row bases, window rows, new tokens
@@ -590,6 +590,94 @@ csa2_status csa2_paged_attn(const csa2_bf16* q, int Q, int H, const int32_t* q_s
                             int64_t window, int64_t max_rows, const float* sink, float scale,
                             csa2_bf16* out, float* lse, const float* inv_freq, void* ws,
                             size_t ws_bytes, csa2_stream stream);
+
+/* ---------------------------------------------------------------------------------
+ * csa2_paged_read -- rows of a paged cache back as bf16, the inverse of csa2_paged_append: for
+ * a handoff to another engine, a cache of another type, or a library that wants dense rows.
+ *
+ * Rows start_row[b], start_row[b] + 1, .. of sequence b go to rows cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1 of out.  FP8 rows are decoded, x = code * scale in fp32.  With inv_freq,
+ * pair i of dims 448 + 2i, 449 + 2i of row j is multiplied by e^{-i p theta_i}, p = j * ratio,
+ * in fp32, which undoes the rotation of csa2_paged_append; without it rows keep their rotation.
+ * Rounded once to bf16 (rows of bf16 that are not rotated are copied).
+ *   out          [T] rows of 512 bf16, out_ld elements apart (a multiple of 8, >= 512)
+ *   cu_seqlens   [cache->B + 1] int32, non-decreasing, cu_seqlens[0] == 0.  Rows of out from
+ *                cu_seqlens[B] on are left as they were
+ *   start_row    [cache->B] int64; rows outside the table, or on a page outside the pool, raise
+ *                CSA2_EBOUNDS, and their rows of out are left as they were
+ *   ratio        1 .. 65536
+ *   inv_freq     [32] fp32 or NULL */
+csa2_status csa2_paged_read(csa2_bf16* out, int64_t out_ld, int T, const int32_t* cu_seqlens,
+                            const int64_t* start_row, int ratio, const csa2_paged* cache,
+                            const float* inv_freq, csa2_stream stream);
+
+/* ---------------------------------------------------------------------------------
+ * csa2_paged_chunk_attn -- csa2_paged_attn for chunks: attention of many new tokens of each
+ * sequence over its paged rows, each row read once for many tokens.  A prefill chunk, the
+ * tokens of a draft, or (with start_pos 0) whole prompts, causal and packed.  [B] §4.1; [C]
+ * §5.5-5.6; [E] Fig. 2d (sink in the denominator), "prefix + extend".
+ *
+ * Token cu_seqlens[b] + i of q is sequence b's token at position p = start_pos[b] + i; its own row
+ * is in the cache already (csa2_paged_append).  What it sees and its result are those of
+ * csa2_paged_attn:
+ *     hi = floor((p + 1) / ratio) (0 for p < 0),  lo = window > 0 ? max(0, hi - window) : 0
+ *     s_j = scale * <q[t][h], x_j>, lo <= j < hi;   Z = e^{sink[h]} + sum_j e^{s_j}
+ *     out_h = sum_j e^{s_j} x_j / Z,   lse_h = ln Z
+ *   q, out       [T][H][512] bf16;  T 0 .. 1048576;  H 1 .. 128
+ *   cu_seqlens   [cache->B + 1] int32, non-decreasing, cu_seqlens[0] == 0; empty sequences are
+ *                fine.  Tokens from cu_seqlens[B] on (a padded batch) keep their out and lse
+ *   start_pos    [cache->B] int64
+ *   max_rows     bound on hi, 0 .. 2^31 - 256; a larger hi, or one beyond the table, raises
+ *                CSA2_EBOUNDS and is clipped
+ *   total_rows   bound on the rows seen by all sequences together (each sequence's from its first
+ *                token's lo to its last token's hi), 0 .. 2^31 - 256
+ *   ratio, window, sink, scale, lse, inv_freq   as csa2_paged_attn
+ *   ws           workspace of csa2_paged_chunk_attn_workspace_size(T, H, cache, max_rows,
+ *                total_rows) bytes, 256-byte aligned; contents are scratch.  Calls that can overlap
+ *                need one each. */
+size_t csa2_paged_chunk_attn_workspace_size(int T, int H, const csa2_paged* cache, int64_t max_rows,
+                                            int64_t total_rows);
+csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_t* cu_seqlens,
+                                  const int64_t* start_pos, const csa2_paged* cache, int ratio,
+                                  int64_t window, int64_t max_rows, int64_t total_rows,
+                                  const float* sink, float scale, csa2_bf16* out, float* lse,
+                                  const float* inv_freq, void* ws, size_t ws_bytes,
+                                  csa2_stream stream);
+
+/* ---------------------------------------------------------------------------------
+ * csa2_qk_norm_rope -- the norm of queries and keys for each head and the rotation of their
+ * positions in one pass: what the step's q, iq, window rows and new latents have behind them.
+ * [A] "四种层合并出来的是什么形状" (norms of the projections' outputs); [B] §6.1 (partial RoPE).
+ *
+ * For token t and each head x of D values:
+ *     y = x * rsqrt(mean(x^2) + eps) * norm_w      (norm != 0; else y = x)
+ *     the rope_dims dims from rope_dim0 on: pair i is multiplied by factor * e^{i p theta_i},
+ *     p = pos[t], theta_i = inv_freq[i], i < rope_dims / 2
+ * in fp32 (the phase exact as in csa2_compress), rounded once to bf16.  PAIRS: pair i is dims
+ * rope_dim0 + 2i and + 2i + 1; HALVES: rope_dim0 + i and rope_dim0 + rope_dims / 2 + i.  A table
+ * for long contexts (YaRN) comes as inv_freq, its magnitude as factor.
+ *   q, k         HOST structs (device pointers inside), either may be NULL; head h of token t is at
+ *                x + t * x_token + h * x_head (elements, multiples of 8), D values side by side;
+ *                out likewise.  out may be x with x's strides, and may not overlap it otherwise
+ *   H            1 .. 1024;  norm_w [D] fp32, 16-byte aligned, or NULL (ones)
+ *   D            a multiple of 8, 8 .. 512
+ *   pos          [T] int64 (of any sign);  inv_freq [rope_dims / 2] fp32; neither is read with
+ *                rope_dims 0 (a norm alone)
+ *   rope_dim0, rope_dims   multiples of 8 (rope_dims of 16 with HALVES)
+ *   factor       finite; it scales the rotated dims only */
+typedef enum { CSA2_ROPE_PAIRS = 0, CSA2_ROPE_HALVES = 1 } csa2_rope_layout;
+typedef struct {
+  const csa2_bf16* x;
+  csa2_bf16* out;
+  int64_t x_token, x_head, out_token, out_head;
+  int32_t H;
+  int32_t norm;
+  const float* norm_w;
+} csa2_heads;
+
+csa2_status csa2_qk_norm_rope(const csa2_heads* q, const csa2_heads* k, int T, int D, float eps,
+                              const int64_t* pos, const float* inv_freq, int rope_dim0,
+                              int rope_dims, int layout, float factor, csa2_stream stream);
 
 #ifdef __cplusplus
 }
