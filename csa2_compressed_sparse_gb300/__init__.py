@@ -548,7 +548,7 @@ def _chunk_rows(cache, max_rows, total_rows):
     if max_rows is None:
         max_rows = min(cache.table.shape[1] * cache.data.shape[1], 0x7FFFFF00)
     if total_rows is None:
-        total_rows = min(cache._c.B * max_rows, 0x7FFFFF00)
+        total_rows = min(cache._c.B * max_rows, 1 << 30)
     return max_rows, total_rows
 
 

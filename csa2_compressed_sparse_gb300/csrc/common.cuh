@@ -19,6 +19,7 @@ constexpr int kRing = 128;   // sliding-window slots
 constexpr int kRopeDim0 = 448;
 constexpr int kMaxK = 512;   // largest top-k
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct CompressArgs {
   const uint16_t* kv;
@@ -202,6 +203,7 @@ struct PagedAttnArgs {
 // Rows start_row[b] + i of the cache to row cu_seqlens[b] + i of out, as bf16.
 struct PagedReadArgs {
   uint16_t* out;
+  const int64_t* row_end; // or null; rows from row_end[b] on, and those on bad pages, become zeros
   int64_t out_ld;         // elements from row to row
   int T;
   const int32_t* cu_seqlens;
@@ -214,6 +216,23 @@ struct PagedReadArgs {
   int page_shift;
 };
 
+// A tile of a chunk's attention: 128 rows (token, head) of one sequence, and its key tiles.
+struct __align__(16) ChunkTile {
+  int32_t seq, row0, rows;  // rows row0 .. row0 + rows - 1 of [T * H]
+  int32_t k0, kn;           // key tiles of 256 cache rows: k0 .. k0 + kn - 1
+  int32_t c0, c1;           // the first and last CTA pair that works on it
+  int32_t tok0;             // the sequence's first token,
+  int64_t start;            // and its position
+  int64_t off;              // staged rows: cache row j is row j + off
+  int32_t clip;             // rows the sequence may see
+  int32_t pad[3];
+};
+// A pair's share: `count` units (key tiles) from key tile `unit` of tile `tile` on.
+struct __align__(16) ChunkShare {
+  int32_t tile, unit;
+  int64_t count;
+};
+
 // Attention of a chunk of new tokens: token cu_seqlens[b] + i of q sits at start_pos[b] + i.
 struct ChunkArgs {
   const uint16_t* q;      // [T][H][512]
@@ -221,7 +240,7 @@ struct ChunkArgs {
   const int32_t* cu_seqlens;
   const int64_t* start_pos;
   PagedCache cache;
-  int64_t cap_rows;
+  int64_t cap_rows;       // rows a token may see: the caller's bound and the table's capacity
   int ratio;
   int64_t window;
   const float* sink;
@@ -229,8 +248,23 @@ struct ChunkArgs {
   uint16_t* out;
   float* lse;
   const float* inv_freq;
-  uint32_t page_mul;
+  uint32_t page_mul;      // as in PagedAppendArgs
   int page_shift;
+  int box_rows;           // rows per tensor copy
+  int pairs;              // CTA pairs of the launch
+  // workspace
+  ChunkTile* tile;        // [max_tiles]
+  int64_t* prefix;        // [max_tiles] units before each tile
+  int max_tiles;
+  ChunkShare* share;      // [pairs]
+  float* part;            // [2 pairs][2 CTAs][64 float4 columns][128 lanes][4]
+  float* pstat;           // [2 pairs][2 CTAs][m, l, r][64]
+  // rows that are not read from their pages: staged as dense bf16 rows (stage null: none are)
+  uint16_t* stage;        // [stage_rows][512]
+  int64_t stage_rows;
+  int32_t* stage_cu;      // [B + 1]
+  int64_t* stage_first;   // [B]
+  int64_t* stage_end;     // [B]
 };
 
 // Heads of queries or of keys: token t's head h at x + t x_token + h x_head (elements).
@@ -256,8 +290,9 @@ struct HeadsArgs {
 cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s);
 cudaError_t launch_heads(const HeadsArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_paged_read(const PagedReadArgs& a, int sms, cudaStream_t s);
-// q_seq [T] and q_pos [T] of a chunk's tokens (-1: behind the last sequence).
-cudaError_t launch_chunk_tokens(const ChunkArgs& a, int32_t* q_seq, int64_t* q_pos, cudaStream_t s);
+cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s);
+int chunk_max_pairs();        // most CTA pairs of a chunk's attention
+int chunk_whole_keys();       // key tiles up to which few tiles go to a pair each
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int sms, cudaStream_t s);
 int paged_head_pad(int H);    // heads of an item, padded: 16, 32 or 64
 int paged_unit_tiles();
@@ -341,6 +376,20 @@ __device__ __forceinline__ void unpack_bf16x8(uint4 u, float (&v)[8]) {
 __device__ __forceinline__ float sink_log2(float sink) {
   const float y = sink * kLog2e;
   return isinf(y) && !isinf(sink) ? copysignf(FLT_MAX, sink) : y;
+}
+
+// ln Z of sums l (of rows and sink) under the maximum M; the sink itself where the rows' sum is 0.
+__device__ __forceinline__ float head_lse(float M, float l, float rows, float sink) {
+  return rows == 0.f ? sink : (M + __log2f(l)) * kLn2;
+}
+
+// Valid rows of the 64-row tile that begins at row r0, as bits.
+__device__ __forceinline__ uint64_t tile_mask(int64_t r0, int lo, int hi) {
+  const int64_t f = lo - r0, l = hi - r0;  // first valid, end
+  uint64_t m = l >= 64 ? ~0ull : l <= 0 ? 0ull : (1ull << l) - 1;
+  if (f >= 64) m = 0;
+  else if (f > 0) m &= ~0ull << f;
+  return m;
 }
 
 __host__ __device__ __forceinline__ uint32_t score_key(float f) {

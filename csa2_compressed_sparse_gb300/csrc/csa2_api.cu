@@ -850,17 +850,39 @@ namespace {
 
 // Workspace of csa2_paged_chunk_attn.
 struct ChunkWs {
-  size_t seq, pos, attn, total;
-  size_t attn_bytes;
+  size_t tile, prefix, share, part, pstat, stage, stage_cu, stage_first, stage_end, total;
+  int max_tiles, pairs;
+  bool split;      // a tile may need parts
+  int64_t rows;    // staged
 };
-ChunkWs chunk_ws_layout(int T, int H, int64_t max_rows) {
+ChunkWs chunk_ws_layout(int T, int H, const csa2_paged& c, int64_t max_rows, int64_t total_rows) {
   ChunkWs w{};
+  // sequences with tokens; each may have an incomplete tile
+  const int64_t seqs = c.B < T ? c.B : T;
+  const int64_t tiles = ((int64_t)T * H + 127) / 128 + seqs;
+  // key tiles of a tile: a window that begins inside one adds one
+  const int64_t keys = (max_rows + 255) / 256 + 1;
+  w.max_tiles = (int)tiles;
+  w.split = tiles > csa2::chunk_max_pairs() || keys > csa2::chunk_whole_keys();
+  const int64_t most = w.split ? tiles * keys : tiles;
+  w.pairs = (int)(most < csa2::chunk_max_pairs() ? most : csa2::chunk_max_pairs());
   size_t o = 0;
-  w.seq = o; o = up256(o + (size_t)T * 4);
-  w.pos = o; o = up256(o + (size_t)T * 8);
-  w.attn = o;
-  w.attn_bytes = csa2_paged_attn_workspace_size(T < 65535 ? T : 65535, H, max_rows);
-  w.total = o + w.attn_bytes;
+  w.tile = o; o = up256(o + (size_t)tiles * sizeof(csa2::ChunkTile));
+  w.prefix = o; o = up256(o + (size_t)tiles * 8);
+  w.share = o; o = up256(o + (size_t)w.pairs * sizeof(csa2::ChunkShare));
+  if (w.split) {
+    w.part = o; o = up256(o + (size_t)w.pairs * 2 * 128 * 512 * 4);
+    w.pstat = o; o = up256(o + (size_t)w.pairs * 2 * 128 * 3 * 4);
+  }
+  if (c.dtype != CSA2_SWA_BF16) {
+    // whole groups of eight rows of each sequence
+    w.rows = ((total_rows + 7) & ~(int64_t)7) + 16 * seqs;
+    w.stage = o; o = up256(o + (size_t)w.rows * 1024);
+    w.stage_cu = o; o = up256(o + (size_t)(c.B + 1) * 4);
+    w.stage_first = o; o = up256(o + (size_t)c.B * 8);
+    w.stage_end = o; o = up256(o + (size_t)c.B * 8);
+  }
+  w.total = o;
   return w;
 }
 
@@ -869,10 +891,10 @@ ChunkWs chunk_ws_layout(int T, int H, int64_t max_rows) {
 size_t csa2_paged_chunk_attn_workspace_size(int T, int H, const csa2_paged* cache, int64_t max_rows,
                                             int64_t total_rows) {
   if (T < 0 || T > 1048576 || H < 1 || H > 128 || max_rows < 0 || max_rows > 0x7FFFFF00 ||
-      total_rows < 0 || !cache)
+      total_rows < 0 || total_rows > (1 << 30) || !cache || cache->B < 1 || cache->B > 65535)
     return 0;
   if (T == 0) return 0;
-  return chunk_ws_layout(T, H, max_rows).total;
+  return chunk_ws_layout(T, H, *cache, max_rows, total_rows).total;
 }
 
 csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_t* cu_seqlens,
@@ -898,28 +920,43 @@ csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_
   REQUIRE(window >= 0, "%s: window must be >= 0 (got %lld)", name, (long long)window);
   REQUIRE(max_rows >= 0 && max_rows <= 0x7FFFFF00,
           "%s: max_rows must be in [0, 2^31 - 256] (got %lld)", name, (long long)max_rows);
-  REQUIRE(total_rows >= 0 && total_rows <= 0x7FFFFF00,
-          "%s: total_rows must be in [0, 2^31 - 256] (got %lld)", name, (long long)total_rows);
+  REQUIRE(total_rows >= 0 && total_rows <= (1 << 30),
+          "%s: total_rows must be in [0, 2^30] (got %lld)", name, (long long)total_rows);
   REQUIRE(std::isfinite(scale), "%s: scale must be finite", name);
   REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255u) == 0, "%s: ws must be 256-byte aligned", name);
-  const ChunkWs w = chunk_ws_layout(T, H, max_rows);
+  const ChunkWs w = chunk_ws_layout(T, H, *cache, max_rows, total_rows);
   if (!ws || ws_bytes < w.total)
     return fail(CSA2_ENOSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws ? ws_bytes : 0,
                 w.total);
+  const int sms = num_sms();
+  if (sms <= 0) return fail(CSA2_ECUDA, "%s: no CUDA device", name);
   a.q = q; a.T = T; a.H = H; a.cu_seqlens = cu_seqlens; a.start_pos = start_pos;
+  a.cap_rows = table_rows(a.cache) < max_rows ? table_rows(a.cache) : max_rows;
+  a.ratio = ratio; a.window = window; a.sink = sink; a.scale = scale; a.out = out; a.lse = lse;
+  a.inv_freq = inv_freq;
+  page_division(a.cache, &a.page_mul, &a.page_shift);
+  a.pairs = w.pairs;
   uint8_t* base = static_cast<uint8_t*>(ws);
-  int32_t* q_seq = reinterpret_cast<int32_t*>(base + w.seq);
-  int64_t* q_pos = reinterpret_cast<int64_t*>(base + w.pos);
-  cudaError_t e = csa2::launch_chunk_tokens(a, q_seq, q_pos, stream);
-  if (e != cudaSuccess) return cuda_fail(e, name);
-  for (int t = 0; t < T; t += 65535) {
-    const int n = T - t < 65535 ? T - t : 65535;
-    const int64_t at = (int64_t)t * H;
-    st = csa2_paged_attn(q + at * 512, n, H, q_seq + t, q_pos + t, cache, ratio, window, max_rows,
-                         sink, scale, out + at * 512, lse ? lse + at : nullptr, inv_freq,
-                         base + w.attn, w.attn_bytes, stream);
-    if (st != CSA2_OK) return st;
+  a.tile = reinterpret_cast<csa2::ChunkTile*>(base + w.tile);
+  a.prefix = reinterpret_cast<int64_t*>(base + w.prefix);
+  a.max_tiles = w.max_tiles;
+  a.share = reinterpret_cast<csa2::ChunkShare*>(base + w.share);
+  if (w.split) {
+    a.part = reinterpret_cast<float*>(base + w.part);
+    a.pstat = reinterpret_cast<float*>(base + w.pstat);
   }
+  a.box_rows = a.cache.page_rows % 64 == 0 ? 64 : a.cache.page_rows % 32 == 0 ? 32
+               : a.cache.page_rows % 16 == 0 ? 16 : 8;
+  if (w.rows > 0) {
+    a.box_rows = 64;
+    a.stage = reinterpret_cast<uint16_t*>(base + w.stage);
+    a.stage_rows = w.rows;
+    a.stage_cu = reinterpret_cast<int32_t*>(base + w.stage_cu);
+    a.stage_first = reinterpret_cast<int64_t*>(base + w.stage_first);
+    a.stage_end = reinterpret_cast<int64_t*>(base + w.stage_end);
+  }
+  cudaError_t e = csa2::launch_chunk_attn(a, sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, name);
   return CSA2_OK;
 }
 

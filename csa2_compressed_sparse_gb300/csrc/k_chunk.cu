@@ -52,11 +52,13 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
     // where the rows are
     const uint8_t* src[kTok];
     int64_t j[kTok];
+    bool zero[kTok];
     int b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t, lane);
     int64_t t0 = a.cu_seqlens[b], t1 = a.cu_seqlens[b + 1], first = a.start_row[b];
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       src[i] = nullptr;
+      zero[i] = false;
       if (t + i >= total) continue;
       if (i > 0 && t + i >= t1) {  // on to the row's sequence
         b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t + i, lane);
@@ -65,6 +67,8 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
         first = a.start_row[b];
       }
       j[i] = first + (t + i - t0);
+      zero[i] = a.row_end != nullptr;
+      if (a.row_end && j[i] >= a.row_end[b]) continue;
       int32_t page = -1, row = 0;
       if (j[i] >= 0 && j[i] < a.cap_rows) {
         const int32_t lp = (int32_t)(__umulhi((uint32_t)j[i], a.page_mul) >> a.page_shift);
@@ -128,7 +132,11 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
     }
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
-      if (!src[i]) continue;
+      if (!src[i]) {
+        if (!zero[i]) continue;
+        c0[i] = c1[i] = make_uint4(0u, 0u, 0u, 0u);
+        x0[i] = x1[i] = 0.f;
+      }
       if (a.inv_freq) {  // times e^{-i p theta}
         float s, c;
         sincosf(rope_angle(turn, (uint64_t)j[i] * (uint64_t)a.ratio), &s, &c);
@@ -144,24 +152,936 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
   }
 }
 
-// ================================ chunk =================================================
+// ================================ chunk attention =======================================
+//
+// Rows (token, head) of a sequence's new tokens form tiles of 128, in the order of q; all of them
+// share the keys, so the scores of a tile are one product of 128 x 512 by 512 x 256 cache rows (a
+// key tile), and the output another of 128 x 256 by 256 x 512.
+//
+// A pair of CTAs works on a tile (tcgen05 with cta_group::2, M = 128: 64 rows in each CTA), because
+// the output's 512 fp32 columns for 128 rows are all of an SM's tensor memory: here each CTA holds
+// them for its 64 rows in 256 columns, folded over 128 lanes (lane r and 64 + r are row r: the first
+// and second half of a product's columns), beside two buffers of scores of 128 columns.  For S a CTA
+// brings 128 of the key tile's rows, for O 256 of the 512 dims of all its rows, so a cache row is
+// loaded once as key and once as value by a pair, in slots of 16 KiB that one ring of 8 holds:
+//   K slot k        this CTA's 128 rows x dims 64 k .. 64 k + 63
+//   V slot (c, h)   rows 64 c .. 64 c + 63 x this CTA's dims 256 h + 128 rank .. + 127
+// A key tile is eight slots of each, a revolution of the ring: K(0) K(1) V(0) K(2) V(1) ..
+//   warps 0..7   softmax: thread (lane r or 64 + r, half of its columns) has 64 scores of a row, all in
+//                one 64-row block of P.  The running maximum m moves only when a score exceeds it by
+//                2^64, so a tile's usual pass is one vote
+//   warp 8       issues all products (even CTA)
+//   warp 9       loads each tile's Q and all slots
+// The plan deals the key tiles of all tiles evenly to the pairs; a tile that several pairs work on is
+// joined from their parts by chunk_join_kernel.
+//
+// A row that some tokens of a tile see and others do not may hold NaN or infinities, which must not
+// reach those others through 0 * NaN.  Such a row makes its scores non-finite for every query, so
+// where a key tile is masked for some row, a masked score that is not finite flags the cache row in
+// both CTAs, and its values lose their non-finite elements before the product (the tokens that see
+// the row have NaN weights).  Rows behind the last visible one are garbage and are treated so too.
 
-// The sequence and position of each token, for attention token by token.
-__global__ void __launch_bounds__(256) chunk_tokens_kernel(ChunkArgs a, int32_t* q_seq, int64_t* q_pos) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  const int b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t, lane);
-  const int64_t t0 = a.cu_seqlens[b];
-  const bool live = t >= t0 && t < a.cu_seqlens[b + 1];
-  if (lane == 0) {
-    q_seq[t] = live ? b : -1;
-    q_pos[t] = live ? a.start_pos[b] + (t - t0) : 0;
+constexpr int kQRows = 128, kKeys = 256;
+constexpr int kSlotBytes = 16384, kSlots = 8;
+constexpr int kQBytes = 65536, kPBytes = 32768;
+constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 32 * 10;
+constexpr uint32_t kColS = 256;
+constexpr float kLazy = 64.0f;
+// Key tiles that O sums up in tensor memory (65536 rows; the tensor core cuts the low bits of its
+// running sums).  A longer segment is done in runs, which add up in fp32 in the pair's part.
+constexpr int kRun = 256;
+
+struct __align__(16) ChunkAux {
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2];
+  uint64_t p_full, pv_done;
+  uint64_t mask_full[4];
+  uint64_t masked;        // both CTAs' softmax warps have flagged a masked tile's rows
+  uint64_t landed;        // a flagged tile's values are in both CTAs
+  uint64_t fin;
+  uint32_t groups[4];     // key tile c & 3: groups of eight rows that are on a page
+  uint32_t flags[2][8];   // rows of a masked tile to be cleaned
+  uint64_t turn[32];
+  float fac[64];
+  float top[4][64];
+  uint32_t tmem_slot;
+  int abort;
+};
+constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kPBytes + (int)sizeof(ChunkAux);
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+// In P's memory at a segment's end.
+struct ChunkEnd {
+  float l[4][64], r[4][64];
+  float2 rope[66][32];  // of the tokens of this CTA's rows
+};
+static_assert(sizeof(ChunkEnd) <= kPBytes, "it shares P's memory");
+
+__device__ __forceinline__ bool wait_phase(ChunkAux& X, uint64_t& bar, uint32_t parity,
+                                           uint64_t limit_ns = 2000000000ull) {
+  const uint32_t b = smem_u32(&bar);
+  if (mbar_try_wait_cluster(b, parity)) return true;
+  const volatile int* abort = &X.abort;
+  if (*abort) return false;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_cluster(b, parity)) return true;
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      raise_fault(kFaultTimeout);
+      X.abort = 1;
+      return false;
+    }
   }
 }
 
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+__device__ __forceinline__ bool soft_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\t"
+      "bar.red.or.pred po, 1, %2, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "n"(kSoft)
+      : "memory");
+  return r != 0;
+}
+
+// Rows lo .. hi - 1 that the token at position p sees, of at most clip; true if there were more.
+__device__ __forceinline__ bool token_rows(const ChunkArgs& a, int64_t p, int64_t clip, int& lo, int& hi) {
+  int64_t h;
+  if (p < 0) h = 0;
+  else if (p < 0x7FFFFFFF) h = (uint32_t)(p + 1) / (uint32_t)a.ratio;
+  else h = (int64_t)min(((uint64_t)p + 1) / (uint64_t)a.ratio, (uint64_t)1 << 62);
+  int64_t l = a.window > 0 && h > a.window ? h - a.window : 0;
+  const bool over = h > clip;
+  if (over) {
+    h = clip;
+    l = l < h ? l : h;
+  }
+  lo = (int)l;
+  hi = (int)h;
+  return over;
+}
+
+// ---- plan ------------------------------------------------------------------------------
+//
+// One CTA: the tiles of all sequences with their key tiles, the staged rows' places, and each pair's
+// share of the W units (key tiles).  Up to as many tiles as pairs, none longer than kWhole, go to a
+// pair each.  Otherwise pair c gets units W c / C .. W (c + 1) / C - 1, C as many pairs as leave each
+// kShare units or a tile.
+constexpr int kPlanThreads = 1024;
+constexpr int kWhole = 6, kShare = 4;
+
+// Exclusive prefix of x over the CTA's threads; *total gets the sum.
+__device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* sums, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t y = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t z = __shfl_up_sync(0xFFFFFFFFu, y, o);
+    if (lane >= o) y += z;
+  }
+  if (lane == 31) sums[warp] = y;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t v = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += z;
+    }
+    sums[lane] = v;
+  }
+  __syncthreads();
+  *total = sums[31];
+  const int64_t before = (warp ? sums[warp - 1] : 0) + y - x;
+  __syncthreads();
+  return before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
+  __shared__ int64_t sums[32];
+  __shared__ int tile0[kPlanThreads + 1], tok0[kPlanThreads], count[kPlanThreads], clip[kPlanThreads];
+  __shared__ int64_t off[kPlanThreads], start[kPlanThreads];
+  __shared__ int longest;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x;
+  if (tid == 0) longest = 0;
+  int64_t tiles = 0, units = 0, staged = 0;
+  const int B = a.cache.B;
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int t0 = 0, n = 0, c = (int)a.cap_rows;
+    int64_t s = 0, first = 0, len = 0, end = 0;
+    if (b < B) {
+      t0 = min(max(a.cu_seqlens[b], 0), a.T);
+      n = max(0, min(a.cu_seqlens[b + 1], a.T) - t0);
+      s = a.start_pos[b];
+    }
+    if (a.stage && n > 0) {
+      int lo, hi, x;
+      token_rows(a, s, a.cap_rows, lo, x);
+      token_rows(a, s + n - 1, a.cap_rows, x, hi);
+      first = lo & ~7;
+      end = hi > lo ? hi : first;
+      len = (end - first + 7) & ~(int64_t)7;
+    }
+    int64_t total = 0;
+    if (a.stage) {
+      const int64_t at = staged + plan_scan(len, sums, &total);
+      if (at + len > a.stage_rows) {  // more rows than announced
+        raise_fault(kFaultBounds);
+        len = max((int64_t)0, a.stage_rows - at) & ~(int64_t)7;
+        end = min(end, first + len);
+        c = (int)end;
+      }
+      if (b < B) {
+        a.stage_cu[b] = (int32_t)min(at, a.stage_rows);
+        a.stage_first[b] = first;
+        a.stage_end[b] = end;
+      }
+      off[tid] = at - first;
+      staged += total;
+    } else {
+      off[tid] = 0;
+    }
+    const int64_t nt = ((int64_t)n * a.H + kQRows - 1) / kQRows;
+    const int64_t mine = plan_scan(nt, sums, &total);
+    tile0[tid] = (int)mine;
+    tok0[tid] = t0;
+    count[tid] = n;
+    clip[tid] = c;
+    start[tid] = s;
+    if (tid == 0) tile0[kPlanThreads] = (int)total;
+    __syncthreads();
+    const int here = (int)total;
+    for (int x0 = 0; x0 < here; x0 += kPlanThreads) {
+      const int x = x0 + tid;
+      ChunkTile t{};
+      if (x < here) {
+        int i = 0, e = kPlanThreads;  // the last sequence with tile0 <= x
+        while (e - i > 1) {
+          const int m = (i + e) >> 1;
+          if (tile0[m] <= x) i = m;
+          else e = m;
+        }
+        const int k = x - tile0[i];
+        const int64_t rows = (int64_t)count[i] * a.H - (int64_t)k * kQRows;
+        t.seq = b0 + i;
+        t.rows = (int)min(rows, (int64_t)kQRows);
+        t.row0 = tok0[i] * a.H + k * kQRows;
+        t.tok0 = tok0[i];
+        t.start = start[i];
+        t.off = off[i];
+        t.clip = clip[i];
+        int lo, hi, y;
+        bool over = token_rows(a, t.start + (t.row0 / a.H - t.tok0), t.clip, lo, y);
+        over |= token_rows(a, t.start + ((t.row0 + t.rows - 1) / a.H - t.tok0), t.clip, y, hi);
+        if (over && t.clip == a.cap_rows) raise_fault(kFaultBounds);
+        t.k0 = hi > lo ? lo / kKeys : 0;
+        t.kn = hi > lo ? (hi + kKeys - 1) / kKeys - t.k0 : 1;
+        atomicMax(&longest, t.kn);
+      }
+      const int64_t before = units + plan_scan(t.kn, sums, &total);
+      if (x < here && tiles + x < a.max_tiles) {
+        a.tile[tiles + x] = t;
+        a.prefix[tiles + x] = before;
+      }
+      units += total;
+    }
+    tiles += here;
+    __syncthreads();
+  }
+  if (a.stage && tid == 0) a.stage_cu[B] = (int32_t)min(staged, a.stage_rows);
+  __syncthreads();
+  const int64_t n = min(tiles, (int64_t)a.max_tiles);
+  const bool whole = n <= a.pairs && longest <= kWhole;
+  int64_t C = max(n, (units + kShare - 1) / kShare);
+  C = C < a.pairs ? C : a.pairs;
+  for (int64_t c = tid; c < a.pairs; c += kPlanThreads)
+    if (c >= (whole ? n : C)) a.share[c] = ChunkShare{0, 0, 0};
+  for (int64_t x = tid; x < n; x += kPlanThreads) {
+    ChunkTile& t = a.tile[x];
+    const int64_t p = a.prefix[x], e = p + t.kn;
+    if (whole) {
+      t.c0 = t.c1 = (int)x;
+      a.share[x] = ChunkShare{(int32_t)x, 0, t.kn};
+      continue;
+    }
+    t.c0 = (int)(((p + 1) * C - 1) / units);
+    t.c1 = (int)((e * C - 1) / units);
+    for (int64_t c = (p * C + units - 1) / units; c < C; ++c) {  // pairs that begin in this tile
+      const int64_t u = units * c / C;
+      if (u >= e) break;
+      if (u >= p) a.share[c] = ChunkShare{(int32_t)x, (int32_t)(u - p), units * (c + 1) / C - u};
+    }
+  }
+}
+
+// ---- attention -------------------------------------------------------------------------
+
+// A pair's walk over its segments: key tiles k .. k_end - 1 (of all) of a tile.
+struct ChunkWalk {
+  int64_t left;  // units from this segment on
+  int tile, unit, n;
+  ChunkTile t;
+};
+__device__ __forceinline__ void walk_fit(ChunkWalk& w) {
+  const int rest = w.t.kn - w.unit;
+  w.n = rest < w.left ? rest : (int)w.left;
+}
+__device__ __forceinline__ bool walk_start(const ChunkArgs& a, int pair, ChunkWalk& w) {
+  const ChunkShare s = a.share[pair];
+  w.left = s.count;
+  if (w.left <= 0) return false;
+  w.tile = s.tile;
+  w.unit = s.unit;
+  w.t = a.tile[w.tile];
+  walk_fit(w);
+  return true;
+}
+__device__ __forceinline__ bool walk_next(const ChunkArgs& a, ChunkWalk& w) {
+  w.left -= w.n;
+  if (w.left <= 0) return false;
+  w.unit = 0;
+  w.t = a.tile[++w.tile];
+  walk_fit(w);
+  return true;
+}
+// What the tokens of a tile see: the first's lo, the last's hi.
+__device__ __forceinline__ void tile_rows(const ChunkArgs& a, const ChunkTile& t, int& lo0, int& hi0,
+                                          int& lo1, int& hi1) {
+  token_rows(a, t.start + (t.row0 / a.H - t.tok0), t.clip, lo0, hi0);
+  token_rows(a, t.start + ((t.row0 + t.rows - 1) / a.H - t.tok0), t.clip, lo1, hi1);
+}
+
+// Groups of eight rows of a key tile, one a lane: where each lies.
+struct Places {
+  int32_t y, z;  // group within the page, page
+  bool good;     // on a page, or not needed
+};
+__device__ __forceinline__ Places place_groups(const ChunkArgs& a, const ChunkTile& t, int64_t base, int lo,
+                                               int hi, int lane, bool report) {
+  Places p;
+  const int64_t j = base + 8 * lane;
+  const bool needed = j < hi && j + 8 > lo;
+  p.y = a.cache.page_rows >> 3;  // outside every page: reads as zeros
+  p.z = 0;
+  p.good = true;
+  if (j < t.clip) {
+    const int32_t lp = (int32_t)(__umulhi((uint32_t)j, a.page_mul) >> a.page_shift);
+    const int32_t page = a.cache.table[(int64_t)t.seq * a.cache.table_ld + lp];
+    if (page >= 0 && page < a.cache.n_pages) {
+      if (!a.stage) {
+        p.y = (int32_t)(j - (int64_t)lp * a.cache.page_rows) >> 3;
+        p.z = page;
+      }
+    } else if (needed) {
+      p.good = false;
+      if (report) raise_fault(kFaultBounds);
+    }
+  }
+  if (a.stage) p.y = (int32_t)((j + t.off) >> 3);
+  return p;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t q_s = smem_u32(smem), ring = q_s + kQBytes, p_s = ring + kSlots * kSlotBytes;
+  ChunkAux& X = *reinterpret_cast<ChunkAux*>(smem + kQBytes + kSlots * kSlotBytes + kPBytes);
+  ChunkEnd& Y = *reinterpret_cast<ChunkEnd*>(smem + kQBytes + kSlots * kSlotBytes);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1;
+  griddep_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&X.full[i]), 1);
+      mbar_init(smem_u32(&X.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&X.q_full), 1);
+    mbar_init(smem_u32(&X.q_empty), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&X.s_full[i]), 1);
+    mbar_init(smem_u32(&X.p_full), 2 * kSoftWarps);
+    mbar_init(smem_u32(&X.pv_done), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&X.mask_full[i]), 1);
+    mbar_init(smem_u32(&X.masked), 2 * kSoftWarps);
+    mbar_init(smem_u32(&X.landed), 1);
+    mbar_init(smem_u32(&X.fin), 1);
+    X.abort = 0;
+    mbar_fence_init();
+    prefetch_tensormap(&qmap);
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
+  if (tid < 16) X.flags[tid >> 3][tid & 7] = 0;
+  if (warp == kWarpMma) {
+    tmem_alloc_pair(smem_u32(&X.tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  griddep_wait();
+  if (a.inv_freq && tid < 32) X.turn[tid] = rope_turn(a.inv_freq[tid]);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, X.tmem_slot, 0);
+  ChunkWalk w;
+  const bool work = walk_start(a, pair, w);
+
+  if (work && warp < kSoftWarps) {
+    // ================= softmax, rescale, output =================
+    const int quad = warp & 3, half = warp >> 2;
+    const int L = 32 * quad + lane, row = L & 63, kh = L >> 6, blk = 2 * kh + half;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * quad) << 16);
+    const float sc2 = a.scale * kLog2e;
+    const uint32_t p_full = dsmem_addr(smem_u32(&X.p_full), 0);
+    const uint32_t peer_masked = dsmem_addr(smem_u32(&X.masked), rank ^ 1);
+    int c = 0;          // key tiles so far
+    int nmask = 0;      // masked ones
+    int nland = 0;      // flagged ones
+    int rev0 = 0;       // the ring's revolution where the segment begins
+    // (a wait that gave up is not acted on here: the loop's barriers need every thread)
+    do {
+      const ChunkTile& t = w.t;
+      int lo0, hi0, lo1, hi1, lo, hi;
+      tile_rows(a, t, lo0, hi0, lo1, hi1);
+      const int grow = t.row0 + min((int)rank * 64 + row, t.rows - 1);  // rows behind the last follow it
+      const int64_t pos = t.start + (grow / a.H - t.tok0);
+      token_rows(a, pos, t.clip, lo, hi);
+      const bool whole = t.c0 == t.c1;
+      float m = -INFINITY, mslot = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f), r2 = l2;  // unrounded, rounded
+      const int64_t slot = 2 * (int64_t)pair + (w.unit == 0 ? 1 : 0);
+      float4* part = reinterpret_cast<float4*>(a.part) + ((slot * 2 + rank) * 64 + 16 * half) * 128 + L;
+      for (int i = 0; i < w.n; ++i, ++c) {
+        const int64_t base = (int64_t)(t.k0 + w.unit + i) * kKeys;
+        wait_phase(X, X.s_full[c & 1], (uint32_t)(c >> 1) & 1);
+        wait_phase(X, X.mask_full[c & 3], (uint32_t)(c >> 2) & 1);
+        tc_fence_after();
+        float2 x[32];
+        {
+          uint32_t v[32];
+          tmem_ld32(tlane + kColS + 128 * (c & 1) + 64 * half, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          tmem_ld32(tlane + kColS + 128 * (c & 1) + 64 * half + 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            x[16 + j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        }
+        const uint32_t groups = X.groups[c & 3];
+        const bool masked = base < lo1 || base + kKeys > hi0 || groups != 0xFFFFFFFFu;  // the same in the pair
+        uint64_t seen = ~0ull;
+        if (masked) {
+          seen = tile_mask(base + 64 * blk, lo, hi);
+          const uint32_t g8 = (groups >> (8 * blk)) & 0xFFu;
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            if (!(g8 >> g & 1u)) seen &= ~(0xFFull << (8 * g));
+          // rows that must not be seen and whose scores are not finite
+          uint32_t bad[2] = {0u, 0u};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (!(seen >> (2 * j) & 1u) && !(fabsf(x[j].x) <= FLT_MAX)) bad[j >> 4] |= 1u << (2 * (j & 15));
+            if (!(seen >> (2 * j + 1) & 1u) && !(fabsf(x[j].y) <= FLT_MAX)) bad[j >> 4] |= 2u << (2 * (j & 15));
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            bad[k] = __reduce_or_sync(0xFFFFFFFFu, bad[k]);
+            if (lane == 0 && bad[k]) {
+              const uint32_t at = smem_u32(&X.flags[nmask & 1][2 * blk + k]);
+              red_or_cluster(dsmem_addr(at, rank), bad[k]);
+              red_or_cluster(dsmem_addr(at, rank ^ 1), bad[k]);
+            }
+          }
+        }
+        // P = 2^(score - m), m the running maximum (none yet: 0)
+        uint32_t pk[32];
+        float top;
+        float2 ls, rs;
+        auto weights = [&]() {
+          const float nm = m == -INFINITY ? 0.f : -m;
+          top = -INFINITY;
+          ls = rs = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float2 y = fma2(x[j], make_float2(sc2, sc2), make_float2(nm, nm));
+            if (masked) {
+              if (!(seen >> (2 * j) & 1u)) y.x = -INFINITY;
+              if (!(seen >> (2 * j + 1) & 1u)) y.y = -INFINITY;
+            }
+            top = fmaxf(top, fmaxf(y.x, y.y));
+            y = make_float2(ex2(y.x), ex2(y.y));
+            ls = add2(ls, y);
+            pk[j] = pack_bf16x2(y.x, y.y);
+            rs = add2(rs, make_float2(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xFFFF0000u)));
+          }
+        };
+        weights();
+        if (soft_any(top > kLazy || (m == -INFINITY && top > -INFINITY))) {
+          // a row's maximum moves: the largest exponent of its four threads; the weights are taken again
+          X.top[blk][row] = top;
+          soft_sync();
+          float mx = X.top[0][row];
+#pragma unroll
+          for (int k = 1; k < 4; ++k) mx = fmaxf(mx, X.top[k][row]);
+          float f = 1.f;
+          if (mx > kLazy || (m == -INFINITY && mx > -INFINITY)) {
+            f = m == -INFINITY ? 0.f : ex2(-mx);
+            m = m == -INFINITY ? mx : m + mx;
+            const float2 ff = make_float2(f, f), o = make_float2(0.f, 0.f);
+            l2 = fma2(l2, ff, o);
+            r2 = fma2(r2, ff, o);
+          }
+          if (c > 0) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+          tc_fence_after();
+          if ((i & (kRun - 1)) != 0 && __any_sync(0xFFFFFFFFu, f != 1.f)) {
+#pragma unroll 1
+            for (int k = 0; k < 128; k += 16) {
+              uint32_t v[16];
+              tmem_ld16(tlane + 128 * half + k, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+              tmem_st16(tlane + 128 * half + k, v);
+            }
+            tmem_st_wait();
+          }
+          weights();
+          soft_sync();  // top is read by all
+        }
+        l2 = add2(l2, ls);
+        r2 = add2(r2, rs);
+        if (c > 0) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          st_shared16(p_s + blk * 8192 + sw128_off(row, k),
+                      make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]));
+        if (masked) {
+          // the flags of both CTAs; the other buffer's were read before this tile's votes
+          if (tid < 8) X.flags[(nmask & 1) ^ 1][tid] = 0;
+          soft_sync();
+          if (lane == 0) {
+            mbar_arrive_cluster(dsmem_addr(smem_u32(&X.masked), rank));
+            mbar_arrive_cluster(peer_masked);
+          }
+          wait_phase(X, X.masked, (uint32_t)nmask & 1);
+          uint32_t any = 0;
+          for (int k = 0; k < 8; ++k) any |= X.flags[nmask & 1][k];
+          if (any) {
+            // V(i) is revolution 2 i + 2 of the segment (the last one comes one earlier)
+            const uint32_t rev = (uint32_t)(rev0 + min(2 * i + 2, 2 * w.n - 1));
+            if (rank == 0) {
+              // (the next tile's scores are complete once its keys, one revolution earlier, are)
+              if (i + 1 < w.n) wait_phase(X, X.s_full[(c + 1) & 1], (uint32_t)((c + 1) >> 1) & 1);
+              for (int k = 0; k < kSlots; ++k) wait_phase(X, X.full[k], rev & 1);
+              if (tid == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&X.landed), 1));
+            } else {
+              wait_phase(X, X.landed, (uint32_t)nland & 1);
+            }
+            ++nland;
+            // row r's values: slots (r / 64, 0) and (r / 64, 1), group r % 64 / 8, two blocks of 64 dims
+            for (int r = warp; r < kKeys; r += kSoftWarps) {
+              if (!(X.flags[nmask & 1][r >> 5] >> (r & 31) & 1u)) continue;
+              const uint32_t at = ring + (uint32_t)((r >> 6) * 2 + (lane >> 4)) * kSlotBytes + ((r & 63) >> 3) * 2048 +
+                                  ((lane >> 3) & 1) * 1024 + (r & 7) * 128 + (lane & 7) * 16;
+              uint4 v = ld_shared16(at);
+              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+                if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
+              }
+              st_shared16(at, v);
+            }
+          }
+          ++nmask;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_full);
+        const bool last = i + 1 == w.n;
+        if (!last && ((i + 1) & (kRun - 1)) == 0) {
+          // a run's end: O joins what the part holds
+          wait_phase(X, X.pv_done, (uint32_t)c & 1);
+          tc_fence_after();
+          const float f = mslot == -INFINITY ? 0.f : ex2(mslot - m);
+          const bool first = i + 1 == kRun;
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll 1
+            for (int k = 0; k < 64; k += 16) {
+              uint32_t v[16];
+              tmem_ld16(tlane + 128 * hh + 64 * half + k, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float4* to = part + (hh * 32 + (k >> 2) + j) * 128;
+                float4 o = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *to;
+                o.x = o.x * f + __uint_as_float(v[4 * j]);
+                o.y = o.y * f + __uint_as_float(v[4 * j + 1]);
+                o.z = o.z * f + __uint_as_float(v[4 * j + 2]);
+                o.w = o.w * f + __uint_as_float(v[4 * j + 3]);
+                *to = o;
+              }
+            }
+          }
+          mslot = m;
+          tc_fence_before();
+        }
+      }
+      rev0 += 2 * w.n;
+      // ---- the segment's end ----
+      wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+      tc_fence_after();
+      Y.l[blk][row] = l2.x + l2.y;
+      Y.r[blk][row] = r2.x + r2.y;
+      const bool folded = w.n > kRun;
+      const int crow0 = t.row0 + (int)rank * 64;
+      if (whole && a.inv_freq) {
+        const int64_t tok = crow0 / a.H;
+        const int n = (int)((crow0 + 63) / a.H - tok) + 1;
+        for (int k = tid; k < n * 32; k += kSoft) {
+          float s, cs;
+          sincosf(rope_angle(X.turn[k & 31], (uint64_t)(t.start + (tok + (k >> 5) - t.tok0))), &s, &cs);
+          Y.rope[k >> 5][k & 31] = make_float2(cs, s);
+        }
+      }
+      soft_sync();
+      float l = 0.f, r = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l += Y.l[k][row];
+        r += Y.r[k][row];
+      }
+      const bool live = (int)rank * 64 + row < t.rows;
+      const int h = grow - grow / a.H * a.H;
+      float fac = 0.f;
+      if (whole) {
+        const float logit = a.sink ? a.sink[h] : -INFINITY, sink = sink_log2(logit);
+        const float M = fmaxf(m, sink), Mf = M == -INFINITY ? 0.f : M, e = ex2(m - Mf);
+        const float rows = l * e;
+        float z = rows, zr = r * e;
+        if (sink > -INFINITY) {
+          z += ex2(sink - Mf);
+          zr += ex2(sink - Mf);
+        }
+        fac = zr > 0.f || zr != zr ? e / zr : 0.f;  // no row and no sink: zeros
+        if (a.lse && live && blk == 0) a.lse[grow] = head_lse(Mf, z, rows, logit);
+      } else if (blk == 0) {
+        float* st = a.pstat + (slot * 2 + rank) * 192 + row;
+        st[0] = m;
+        st[64] = l;
+        st[128] = r;
+      }
+      const float f0 = mslot == -INFINITY ? 0.f : ex2(mslot - m);
+      const float2* rope = Y.rope[live ? grow / a.H - crow0 / a.H : 0];
+      uint16_t* out = a.out + (int64_t)grow * kDLat + kh * 128 + half * 64;
+#pragma unroll 1
+      for (int hh = 0; hh < 2; ++hh) {
+        const bool rot = whole && a.inv_freq && hh == 1 && blk == 3;
+#pragma unroll 1
+        for (int k = 0; k < 64; k += 16) {
+          uint32_t v[16];
+          tmem_ld16(tlane + 128 * hh + 64 * half + k, v);
+          tmem_ld_wait();
+          float o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(v[j]);
+          if (folded) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 q = part[(hh * 32 + (k >> 2) + j) * 128];
+              o[4 * j] = fmaf(q.x, f0, o[4 * j]);
+              o[4 * j + 1] = fmaf(q.y, f0, o[4 * j + 1]);
+              o[4 * j + 2] = fmaf(q.z, f0, o[4 * j + 2]);
+              o[4 * j + 3] = fmaf(q.w, f0, o[4 * j + 3]);
+            }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              part[(hh * 32 + (k >> 2) + j) * 128] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            continue;
+          }
+          uint32_t b[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float y0 = o[2 * j] * fac, y1 = o[2 * j + 1] * fac;
+            if (rot) {  // times e^{-i p theta}
+              const float2 cs = rope[(k >> 1) + j];
+              const float z = y0 * cs.x + y1 * cs.y;
+              y1 = y1 * cs.x - y0 * cs.y;
+              y0 = z;
+            }
+            b[j] = pack_bf16x2(y0, y1);
+          }
+          if (live) {
+            uint4* to = reinterpret_cast<uint4*>(out + hh * 256 + k);
+            to[0] = make_uint4(b[0], b[1], b[2], b[3]);
+            to[1] = make_uint4(b[4], b[5], b[6], b[7]);
+          }
+        }
+      }
+      tc_fence_before();
+      soft_sync();  // the sums and angles are read before P is written again
+    } while (walk_next(a, w));
+  } else if (work && warp == kWarpMma && rank == 0) {
+    // ================= products =================
+    const uint32_t lead = elect_lane();
+    const uint32_t id_s = idesc_bf16(128, 256, 0, 0), id_o = idesc_bf16(128, 256, 0, 1);
+    const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), p_d = sdesc_sw128(p_s, 16, 1024);
+    const uint64_t k_d = sdesc_sw128(ring, 16, 1024), v_d = sdesc_sw128(ring, 1024, 2048);
+    bool ok = true;
+    int c = 0, rev = 0, seg = 0;
+    auto scores = [&]() {
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
+        if (!ok) return;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            umma_pair_bf16(tmem + kColS + 128 * (c & 1), q_d + ((k * 8192 + s * 32) >> 4),
+                           k_d + ((k * kSlotBytes + s * 32) >> 4), id_s, k > 0 || s > 0);
+          umma_commit_pair(smem_u32(&X.empty[k]));
+        }
+        __syncwarp();
+      }
+      if (lead) umma_commit_pair(smem_u32(&X.s_full[c & 1]));
+      __syncwarp();
+      ++rev;
+      ++c;
+    };
+    do {
+      const int n = uniform(w.n);
+      ok = all_ok(wait_phase(X, X.q_full, (uint32_t)seg & 1));
+      tc_fence_after();
+      const int c0 = c;
+      if (ok) scores();
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n) scores();
+        if (i + 2 >= n && (i + 1 < n || n == 1)) {  // Q is free
+          if (lead) umma_commit_pair(smem_u32(&X.q_empty));
+          __syncwarp();
+        }
+        ok = ok && all_ok(wait_phase(X, X.p_full, (uint32_t)(c0 + i) & 1));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kSlots; ++k) {
+          ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              umma_pair_bf16(tmem + 128 * (k & 1), p_d + (((k >> 1) * 8192 + s * 32) >> 4),
+                             v_d + ((k * kSlotBytes + s * 4096) >> 4), id_o,
+                             (i & (kRun - 1)) > 0 || k > 1 || s > 0);
+            umma_commit_pair(smem_u32(&X.empty[k]));
+          }
+          __syncwarp();
+        }
+        if (lead) umma_commit_pair(smem_u32(&X.pv_done));
+        __syncwarp();
+        ++rev;
+      }
+      ++seg;
+    } while (ok && uniform(walk_next(a, w)) != 0);
+    // no product may still be running when the tensor memory is released, whatever happened above
+    if (lead) umma_commit_pair(smem_u32(&X.fin));
+    __syncwarp();
+    mbar_wait(smem_u32(&X.fin), 0, 100000000ull);
+  } else if (work && warp == kWarpLoad) {
+    // ================= loads =================
+    const uint64_t pol = policy_evict_normal();
+    const uint32_t q_full = dsmem_addr(smem_u32(&X.q_full), 0);
+    const int lg = 31 - __clz(a.box_rows);
+    bool ok = true;
+    int rev = 0, c = 0, seg = 0, n_last = 0;
+    // Eight slots, each in pieces of box_rows rows, one a lane: of `rows` rows from row `row0 + step
+    // (k / 2)` of the key tile on.
+    auto slots = [&](const Places& at, const CUtensorMap* map, bool values) {
+      const int pieces = (values ? 64 : 128) >> lg;
+#pragma unroll 1
+      for (int k = 0; k < kSlots; ++k) {
+        if (rev > 0) ok = ok && all_ok(wait_phase(X, X.empty[k], (uint32_t)(rev - 1) & 1));
+        if (!ok) return;
+        const int g = ((values ? 8 * (k >> 1) : 16 * (int)rank) + ((lane << lg) >> 3)) & 31;
+        const int32_t y = __shfl_sync(0xFFFFFFFFu, at.y, g), z = __shfl_sync(0xFFFFFFFFu, at.z, g);
+        const uint32_t full = dsmem_addr(smem_u32(&X.full[k]), 0);
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&X.full[k]), 2 * kSlotBytes);
+        __syncwarp();
+        if (lane < pieces)
+          tma_load_5d_pair(ring + k * kSlotBytes + ((uint32_t)lane << lg) * (values ? 256 : 128), map,
+                           values ? 4 * (k & 1) + 2 * (int)rank : k, y, z, full, pol);
+        __syncwarp();
+      }
+      ++rev;
+    };
+    do {
+      const ChunkTile& t = w.t;
+      int lo0, hi0, lo1, hi1;
+      tile_rows(a, t, lo0, hi0, lo1, hi1);
+      if (seg > 0)
+        ok = all_ok(wait_phase(X, X.q_empty, (uint32_t)(seg - 1) & 1,
+                               2000000000ull + 100000ull * (uint32_t)n_last));
+      if (!ok) break;
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&X.q_full), 2 * kQBytes);
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k)
+          tma_load_2d_pair(q_s + k * 8192, &qmap, 64 * k, t.row0 + (int)rank * 64, q_full, pol);
+      }
+      __syncwarp();
+      ++seg;
+      n_last = w.n;
+      const int64_t base = (int64_t)(t.k0 + w.unit) * kKeys;
+      Places cur, nxt = place_groups(a, t, base, lo0, hi1, lane, rank == 0);
+      auto keys = [&](int i) {
+        const uint32_t groups = __ballot_sync(0xFFFFFFFFu, nxt.good);
+        if (lane == 0) {
+          X.groups[c & 3] = groups;
+          mbar_arrive(smem_u32(&X.mask_full[c & 3]));
+        }
+        ++c;
+        slots(nxt, &kmap, false);
+      };
+      keys(0);
+      for (int i = 0; ok && i < w.n; ++i) {
+        cur = nxt;
+        if (i + 1 < w.n) {
+          nxt = place_groups(a, t, base + (int64_t)(i + 1) * kKeys, lo0, hi1, lane, rank == 0);
+          keys(i + 1);
+        }
+        if (ok) slots(cur, &vmap, true);
+      }
+    } while (ok && uniform(walk_next(a, w)) != 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (X.abort) {  // copies in flight land within microseconds
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    __syncthreads();
+  }
+  if (warp == kWarpMma) tmem_dealloc_pair(tmem, 512);
+}
+
+// ---- join ------------------------------------------------------------------------------
+//
+// A tile that pairs c0 .. c1 worked on: with M the largest running maximum (and the sink's logit) of
+// a row, out = sum 2^(m - M) O / Z.  Pair c0 + 1's CTAs do it (the first that began within the tile),
+// kJoin of them, a thread 16 bytes of every part at a time.  Bound by the parts' way from L2.
+constexpr int kJoin = 16, kMaxPairs = 76;
+
+__global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
+  __shared__ float wt[kMaxPairs][64];
+  __shared__ float red[3][4][64];
+  __shared__ float inv[64];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = blockIdx.x;
+  const ChunkShare s = a.share[c];
+  if (s.count <= 0 || s.unit == 0) return;
+  const ChunkTile t = a.tile[s.tile];
+  if (t.c0 + 1 != c) return;
+  const int tid = threadIdx.x, n = min(t.c1 - t.c0 + 1, kMaxPairs);
+  const int rank = blockIdx.y / (kJoin / 2);  // the CTA whose 64 rows these are
+  auto slot = [&](int i) -> int64_t { return (2 * (int64_t)(t.c0 + i) + (i == 0 ? 1 : 0)) * 2 + rank; };
+  const int row = tid & 63, quarter = tid >> 6, r = 64 * rank + row;
+  const int grow = t.row0 + min(r, t.rows - 1), h = grow % a.H;
+  const bool live = r < t.rows;
+  {
+    float m = -INFINITY;
+    for (int i = quarter; i < n; i += 4) {
+      const float x = a.pstat[slot(i) * 192 + row];
+      wt[i][row] = x;
+      m = fmaxf(m, x);
+    }
+    red[0][quarter][row] = m;
+    __syncthreads();
+    const float logit = a.sink ? a.sink[h] : -INFINITY, sink = sink_log2(logit);
+    float M = sink;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) M = fmaxf(M, red[0][k][row]);
+    const float Mf = M == -INFINITY ? 0.f : M;
+    float l = 0.f, z = 0.f;
+    for (int i = quarter; i < n; i += 4) {
+      const float e = ex2(wt[i][row] - Mf);
+      wt[i][row] = e;
+      l = fmaf(e, a.pstat[slot(i) * 192 + 64 + row], l);
+      z = fmaf(e, a.pstat[slot(i) * 192 + 128 + row], z);
+    }
+    red[1][quarter][row] = l;
+    red[2][quarter][row] = z;
+    __syncthreads();
+    if (quarter == 0) {
+      l = red[1][0][row] + red[1][1][row] + red[1][2][row] + red[1][3][row];
+      z = red[2][0][row] + red[2][1][row] + red[2][2][row] + red[2][3][row];
+      const float rows = l;
+      if (sink > -INFINITY) {
+        l += ex2(sink - Mf);
+        z += ex2(sink - Mf);
+      }
+      inv[row] = z > 0.f || z != z ? 1.f / z : 0.f;
+      if (a.lse && live && blockIdx.y % (kJoin / 2) == 0) a.lse[grow] = head_lse(Mf, l, rows, logit);
+    }
+    __syncthreads();
+  }
+  // 8192 float4 of this CTA's rows, columns by kJoin / 2 CTAs
+  for (int x = (blockIdx.y % (kJoin / 2)) * 256 + tid; x < 8192; x += 256 * (kJoin / 2)) {
+    const int L = x & 127, col = x >> 7;
+    const float4* p = reinterpret_cast<const float4*>(a.part) + col * 128 + L;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float4 v = p[slot(i) * 8192];
+      const float e = wt[i][row];
+      // (a part that saw nothing has weight zero and may hold anything finite)
+      o.x = fmaf(v.x, e, o.x);
+      o.y = fmaf(v.y, e, o.y);
+      o.z = fmaf(v.z, e, o.z);
+      o.w = fmaf(v.w, e, o.w);
+    }
+    const int d = (col >> 5) * 256 + (L >> 6) * 128 + ((col >> 4) & 1) * 64 + 4 * (col & 15);
+    const float f = inv[row];
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+    if (a.inv_freq && d >= kRopeDim0) {
+      const uint64_t pos = (uint64_t)(t.start + (grow / a.H - t.tok0));
+      float sn, cs;
+      sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), pos), &sn, &cs);
+      float z = o.x * cs + o.y * sn;
+      o.y = o.y * cs - o.x * sn;
+      o.x = z;
+      sincosf(rope_angle(rope_turn(a.inv_freq[((d - kRopeDim0) >> 1) + 1]), pos), &sn, &cs);
+      z = o.z * cs + o.w * sn;
+      o.w = o.w * cs - o.z * sn;
+      o.z = z;
+    }
+    if (live)
+      *reinterpret_cast<uint2*>(a.out + (int64_t)grow * kDLat + d) =
+          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  }
+}
 }  // namespace
 
 cudaError_t launch_paged_read(const PagedReadArgs& a, int sms, cudaStream_t s) {
@@ -175,8 +1095,46 @@ cudaError_t launch_paged_read(const PagedReadArgs& a, int sms, cudaStream_t s) {
                     dim3(kReadWarps * 32), 0, s, a);
 }
 
-cudaError_t launch_chunk_tokens(const ChunkArgs& a, int32_t* q_seq, int64_t* q_pos, cudaStream_t s) {
-  return launch_pdl(chunk_tokens_kernel, dim3((unsigned)((a.T + 7) / 8)), dim3(256), 0, s, a, q_seq, q_pos);
+int chunk_max_pairs() { return kMaxPairs; }
+int chunk_whole_keys() { return kWhole; }
+
+cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  CUtensorMap qm, km, vm;
+  if (!encode_rows_bf16(&qm, a.q, (uint64_t)a.T * a.H, kDLat, 64, 64)) return cudaErrorInvalidValue;
+  // a page (or all staged rows) as [8-row groups][8 dim blocks][8 rows][128 bytes]
+  const uint64_t groups = a.stage ? (uint64_t)a.stage_rows / 8 : (uint64_t)a.cache.page_rows / 8;
+  const uint64_t dims[5] = {128, 8, 8, groups, a.stage ? 1 : (uint64_t)a.cache.n_pages};
+  const uint64_t strides[4] = {1024, 128, 8192,
+                               a.stage ? groups * 8192 : (uint64_t)a.cache.page_stride};
+  const uint32_t kbox[5] = {128, 8, 1, (uint32_t)a.box_rows / 8, 1};
+  const uint32_t vbox[5] = {128, 8, 2, (uint32_t)a.box_rows / 8, 1};
+  const void* rows = a.stage ? (const void*)a.stage : (const void*)a.cache.data;
+  if (!encode_bytes(&km, rows, 5, dims, strides, kbox) || !encode_bytes(&vm, rows, 5, dims, strides, vbox))
+    return cudaErrorInvalidValue;
+  cudaError_t e = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+  if (e != cudaSuccess) return e;
+  if (a.stage) {
+    PagedReadArgs r{};
+    r.out = a.stage;
+    r.out_ld = kDLat;
+    r.T = (int)a.stage_rows;
+    r.row_end = a.stage_end;
+    r.cu_seqlens = a.stage_cu;
+    r.start_row = a.stage_first;
+    r.ratio = 1;
+    r.cache = a.cache;
+    r.cap_rows = a.cap_rows;
+    r.page_mul = a.page_mul;
+    r.page_shift = a.page_shift;
+    e = launch_paged_read(r, sms, s);
+    if (e != cudaSuccess) return e;
+  }
+  e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl_cluster(chunk_attn_kernel, dim3(2u * a.pairs), dim3(kThreads), kSmem, s, 2u, a, qm, km, vm);
+  if (e != cudaSuccess || !a.part) return e;
+  return launch_pdl(chunk_join_kernel, dim3((unsigned)a.pairs, kJoin), dim3(256), 0, s, a);
 }
 
 }  // namespace csa2

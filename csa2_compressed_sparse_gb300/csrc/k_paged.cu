@@ -14,8 +14,6 @@ CSA2_DEFINE_FAULT_FLAG(paged)
 namespace csa2 {
 namespace {
 
-constexpr float kLn2 = 0.6931471805599453f;
-
 // ================================ append ================================================
 //
 // A warp per token, kTok tokens at a time: a lane holds the 16-byte chunks `lane` (dims 8 l ..)
@@ -308,12 +306,6 @@ struct PagedCfg {
       kQBytes + kSlots * kSlotBytes + kPBytes + kScBytes + (int)sizeof(PagedAux);
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Wait for a phase; false once something in the CTA has given up.  The flag is read only while
 // the phase is incomplete: a read of shared memory takes some hundred cycles while the tensor
 // core's operand reads fill it, and the waits stand on the path from scores to values.
@@ -327,17 +319,6 @@ __device__ __forceinline__ bool wait_phase(PagedAux& X, uint64_t& bar, uint32_t 
   X.abort = 1;
   return false;
 }
-
-// One lane of the warp, and values that the compiler may take to be the same in all of it.
-__device__ __forceinline__ uint32_t elect_lane() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
-__device__ __forceinline__ bool all_ok(bool x) { return __all_sync(0xFFFFFFFFu, x); }
 
 // Four 8 x 8 matrices of 16-bit values: thread t holds (t / 4, 2 (t % 4) + {0, 1}) of each; lane
 // 8 i + r gives the address of row r of matrix i.  (No memory clobber: what it writes is read
@@ -370,24 +351,6 @@ __device__ __forceinline__ bool soft_any(bool pred) {
   return r != 0;
 }
 
-// Two fp32 lanes at once: a * b + c and a + b.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // 16 TMEM lanes x 32 columns: thread t receives lanes t / 4 and t / 4 + 8 of columns
 // 8 i + 2 (t % 4) + {0, 1} at r[4 i ..] (as tmem_ld_16x256b, four times).
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
@@ -407,25 +370,6 @@ __device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7])
       : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
 }
 
 // A box of a page's rows from group y of 8 rows on, dim blocks db and db + 1 (of 64), page z.
@@ -537,11 +481,6 @@ __device__ __forceinline__ void join_add(float (&acc)[8], const float4& x, const
 // A 32-bit store into shared memory of a CTA of the cluster.
 __device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
-}
-
-// ln Z of sums l (of rows and sink) under the maximum M; the sink itself where the rows' sum is 0.
-__device__ __forceinline__ float head_lse(float M, float l, float rows, float sink) {
-  return rows == 0.f ? sink : (M + __log2f(l)) * kLn2;
 }
 
 // A head's running maximum and sums over the parts of the softmax warps.
@@ -688,15 +627,6 @@ __device__ __forceinline__ void store_tile(const PagedAttnArgs& a, const PagedAu
     }
     __syncwarp();
   }
-}
-
-// Valid rows of the 64-row tile that begins at row r0, as bits.
-__device__ __forceinline__ uint64_t tile_mask(int64_t r0, int lo, int hi) {
-  const int64_t f = lo - r0, l = hi - r0;  // first valid, end
-  uint64_t m = l >= 64 ? ~0ull : l <= 0 ? 0ull : (1ull << l) - 1;
-  if (f >= 64) m = 0;
-  else if (f > 0) m &= ~0ull << f;
-  return m;
 }
 
 template <int kHp, int kMode, bool kDirect>
