@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
 //                one 64-row block of P.  The running maximum m moves only when a score exceeds it by
 //                2^64, so a tile's usual pass is one vote
 //   warp 8       issues all products (even CTA)
-//   warp 9       loads each tile's Q and all slots
+//   warps 9, 10  load the even and the odd slots, the first of them each tile's Q
 // The plan deals the key tiles of all tiles evenly to the pairs; a tile that several pairs work on is
 // joined from their parts by chunk_join_kernel.
 //
@@ -185,27 +185,43 @@ constexpr int kQRows = 128, kKeys = 256;
 constexpr int kSlotBytes = 16384, kSlots = 8;
 constexpr int kQBytes = 65536, kPBytes = 32768;
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
-constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 32 * 10;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kLoadWarps = 2, kThreads = 32 * (kWarpLoad + kLoadWarps);
 constexpr uint32_t kColS = 256;
 constexpr float kLazy = 64.0f;
 // Key tiles that O sums up in tensor memory (65536 rows; the tensor core cuts the low bits of its
 // running sums).  A longer segment is done in runs, which add up in fp32 in the pair's part.
 constexpr int kRun = 256;
 
+// A key tile of a pair's work, for the warps that do it; the loader writes them ahead.
+struct __align__(16) ChunkStep {
+  uint32_t groups;  // groups of eight rows that are on a page
+  int base;         // first cache row
+  int i;            // key tile of the segment, -1: no further one
+  int last;         // 1: the segment's last
+};
+// A segment: key tiles of a tile of queries.
+struct __align__(16) ChunkSegment {
+  int64_t start;
+  int row0, rows, tok0, clip;  // as in ChunkTile
+  int hi0, lo1;                // the first token's hi, the last one's lo
+  int whole;                   // all of the tile's key tiles
+  int slot;                    // its part
+};
+
 struct __align__(16) ChunkAux {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2];
   uint64_t p_full, pv_done;
-  uint64_t mask_full[4];
+  uint64_t step_full[4];
   uint64_t masked;        // both CTAs' softmax warps have flagged a masked tile's rows
   uint64_t landed;        // a flagged tile's values are in both CTAs
   uint64_t fin;
-  uint32_t groups[4];     // key tile c & 3: groups of eight rows that are on a page
+  ChunkStep step[4];      // of key tile c & 3 (three at most are in use)
+  ChunkSegment seg[4];    // of segment s & 3 (four)
   uint32_t flags[2][8];   // rows of a masked tile to be cleaned
   uint64_t turn[32];
-  float fac[64];
-  float top[4][64];
+  float top[4][64], sum[4][64];
   uint32_t tmem_slot;
   int abort;
 };
@@ -214,21 +230,25 @@ static_assert(kSmem <= 232448, "shared memory of a CTA");
 
 // In P's memory at a segment's end.
 struct ChunkEnd {
-  float l[4][64], r[4][64];
-  float2 rope[66][32];  // of the tokens of this CTA's rows
+  uint8_t stage[kSoftWarps][2048];  // 32 rows x 32 dims of the output
+  float2 rope[64][32];              // of the tokens of this CTA's rows
 };
 static_assert(sizeof(ChunkEnd) <= kPBytes, "it shares P's memory");
 
+// Wait for a phase; false once something in the CTA has given up.  kPair: one that threads of both CTAs
+// complete with what they wrote.
+template <bool kPair = false>
 __device__ __forceinline__ bool wait_phase(ChunkAux& X, uint64_t& bar, uint32_t parity,
                                            uint64_t limit_ns = 2000000000ull) {
   const uint32_t b = smem_u32(&bar);
-  if (mbar_try_wait_cluster(b, parity)) return true;
+  auto done = [&]() { return kPair ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity); };
+  if (done()) return true;
   const volatile int* abort = &X.abort;
   if (*abort) return false;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait_cluster(b, parity)) return true;
+      if (done()) return true;
     if (*abort) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
       raise_fault(kFaultTimeout);
@@ -301,6 +321,11 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* sums, int64_t* 
   const int64_t before = (warp ? sums[warp - 1] : 0) + y - x;
   __syncthreads();
   return before;
+}
+
+// x / y, mostly in 32 bits (a division in 64 takes four times as long).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
@@ -413,27 +438,31 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
       a.share[x] = ChunkShare{(int32_t)x, 0, t.kn};
       continue;
     }
-    t.c0 = (int)(((p + 1) * C - 1) / units);
-    t.c1 = (int)((e * C - 1) / units);
-    for (int64_t c = (p * C + units - 1) / units; c < C; ++c) {  // pairs that begin in this tile
-      const int64_t u = units * c / C;
-      if (u >= e) break;
-      if (u >= p) a.share[c] = ChunkShare{(int32_t)x, (int32_t)(u - p), units * (c + 1) / C - u};
+    t.c0 = (int)quotient((p + 1) * C - 1, units);
+    t.c1 = (int)quotient(e * C - 1, units);
+    for (int64_t c = t.c0; c <= t.c1; ++c) {  // pairs that begin in this tile
+      const int64_t u = quotient(units * c, C);
+      if (u >= p && u < e)
+        a.share[c] = ChunkShare{(int32_t)x, (int32_t)(u - p), quotient(units * (c + 1), C) - u};
     }
   }
 }
 
 // ---- attention -------------------------------------------------------------------------
 
-// A pair's walk over its segments: key tiles k .. k_end - 1 (of all) of a tile.
+// A pair's walk over its key tiles: i of n of the segment (tile, from key tile `unit` of it on).  The next
+// tile's record is read a segment ahead.
 struct ChunkWalk {
-  int64_t left;  // units from this segment on
-  int tile, unit, n;
-  ChunkTile t;
+  int64_t left;  // units behind this segment
+  int tile, unit, n, i;
+  ChunkTile t, next;
 };
-__device__ __forceinline__ void walk_fit(ChunkWalk& w) {
+__device__ __forceinline__ void walk_fit(const ChunkArgs& a, ChunkWalk& w) {
   const int rest = w.t.kn - w.unit;
   w.n = rest < w.left ? rest : (int)w.left;
+  w.left -= w.n;
+  w.i = 0;
+  if (w.left > 0) w.next = a.tile[w.tile + 1];
 }
 __device__ __forceinline__ bool walk_start(const ChunkArgs& a, int pair, ChunkWalk& w) {
   const ChunkShare s = a.share[pair];
@@ -442,15 +471,17 @@ __device__ __forceinline__ bool walk_start(const ChunkArgs& a, int pair, ChunkWa
   w.tile = s.tile;
   w.unit = s.unit;
   w.t = a.tile[w.tile];
-  walk_fit(w);
+  walk_fit(a, w);
   return true;
 }
+// On to the next key tile; false when there is none.
 __device__ __forceinline__ bool walk_next(const ChunkArgs& a, ChunkWalk& w) {
-  w.left -= w.n;
+  if (++w.i < w.n) return true;
   if (w.left <= 0) return false;
   w.unit = 0;
-  w.t = a.tile[++w.tile];
-  walk_fit(w);
+  ++w.tile;
+  w.t = w.next;
+  walk_fit(a, w);
   return true;
 }
 // What the tokens of a tile see: the first's lo, the last's hi.
@@ -511,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&X.s_full[i]), 1);
     mbar_init(smem_u32(&X.p_full), 2 * kSoftWarps);
     mbar_init(smem_u32(&X.pv_done), 1);
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&X.mask_full[i]), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&X.step_full[i]), 1);
     mbar_init(smem_u32(&X.masked), 2 * kSoftWarps);
     mbar_init(smem_u32(&X.landed), 1);
     mbar_init(smem_u32(&X.fin), 1);
@@ -533,38 +564,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, X.tmem_slot, 0);
-  ChunkWalk w;
-  const bool work = walk_start(a, pair, w);
+  const bool work = a.share[pair].count > 0;
 
   if (work && warp < kSoftWarps) {
     // ================= softmax, rescale, output =================
+    // (a wait that gave up is not acted on here: the loop's barriers need every thread)
     const int quad = warp & 3, half = warp >> 2;
     const int L = 32 * quad + lane, row = L & 63, kh = L >> 6, blk = 2 * kh + half;
     const uint32_t tlane = tmem + ((uint32_t)(32 * quad) << 16);
     const float sc2 = a.scale * kLog2e;
     const uint32_t p_full = dsmem_addr(smem_u32(&X.p_full), 0);
     const uint32_t peer_masked = dsmem_addr(smem_u32(&X.masked), rank ^ 1);
-    int c = 0;          // key tiles so far
-    int nmask = 0;      // masked ones
+    int nmask = 0;      // masked key tiles so far
     int nland = 0;      // flagged ones
-    int rev0 = 0;       // the ring's revolution where the segment begins
-    // (a wait that gave up is not acted on here: the loop's barriers need every thread)
-    do {
-      const ChunkTile& t = w.t;
-      int lo0, hi0, lo1, hi1, lo, hi;
-      tile_rows(a, t, lo0, hi0, lo1, hi1);
-      const int grow = t.row0 + min((int)rank * 64 + row, t.rows - 1);  // rows behind the last follow it
-      const int64_t pos = t.start + (grow / a.H - t.tok0);
-      token_rows(a, pos, t.clip, lo, hi);
-      const bool whole = t.c0 == t.c1;
-      float m = -INFINITY, mslot = -INFINITY;
-      float2 l2 = make_float2(0.f, 0.f), r2 = l2;  // unrounded, rounded
-      const int64_t slot = 2 * (int64_t)pair + (w.unit == 0 ? 1 : 0);
-      float4* part = reinterpret_cast<float4*>(a.part) + ((slot * 2 + rank) * 64 + 16 * half) * 128 + L;
-      for (int i = 0; i < w.n; ++i, ++c) {
-        const int64_t base = (int64_t)(t.k0 + w.unit + i) * kKeys;
+    int seg = 0;        // segments
+    // of the segment: bounds of its first and last token, of this thread's row; the running maximum,
+    // that of what the part holds, and the sums of P (unrounded, rounded)
+    int hi0 = 0, lo1 = 0, lo = 0, hi = 0;
+    float m = -INFINITY, mslot = -INFINITY;
+    float2 l2 = make_float2(0.f, 0.f), r2 = l2;
+    auto part_of = [&](int sl) {
+      return reinterpret_cast<float4*>(a.part) + (((int64_t)sl * 2 + rank) * 64 + 16 * half) * 128 + L;
+    };
+    for (int c = 0;; ++c) {
+      // (the loader ends the steps, too, when something has given up: all threads see the same end)
+      mbar_wait(smem_u32(&X.step_full[c & 3]), (uint32_t)(c >> 2) & 1, 60000000000ull);
+      const ChunkStep st = X.step[c & 3];
+      const bool have = st.i >= 0, first = st.i <= 0;
+      uint32_t pk[32];
+      bool masked = false;
+      // of the segment before, until its end is done
+      const float m_end = m, mslot_end = mslot;
+      const float2 l_end = l2, r_end = r2;
+      if (have) {
+        if (first) {
+          m = mslot = -INFINITY;
+          l2 = r2 = make_float2(0.f, 0.f);
+          const ChunkSegment& t = X.seg[seg & 3];
+          hi0 = t.hi0;
+          lo1 = t.lo1;
+          const int grow = t.row0 + min((int)rank * 64 + row, t.rows - 1);  // rows behind the last follow it
+          token_rows(a, t.start + (grow / a.H - t.tok0), t.clip, lo, hi);
+          ++seg;
+        }
         wait_phase(X, X.s_full[c & 1], (uint32_t)(c >> 1) & 1);
-        wait_phase(X, X.mask_full[c & 3], (uint32_t)(c >> 2) & 1);
         tc_fence_after();
         float2 x[32];
         {
@@ -579,12 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 16; ++j)
             x[16 + j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
         }
-        const uint32_t groups = X.groups[c & 3];
-        const bool masked = base < lo1 || base + kKeys > hi0 || groups != 0xFFFFFFFFu;  // the same in the pair
+        masked = st.base < lo1 || st.base + kKeys > hi0 || st.groups != 0xFFFFFFFFu;  // the same in the pair
         uint64_t seen = ~0ull;
         if (masked) {
-          seen = tile_mask(base + 64 * blk, lo, hi);
-          const uint32_t g8 = (groups >> (8 * blk)) & 0xFFu;
+          seen = tile_mask((int64_t)st.base + 64 * blk, lo, hi);
+          const uint32_t g8 = (st.groups >> (8 * blk)) & 0xFFu;
 #pragma unroll
           for (int g = 0; g < 8; ++g)
             if (!(g8 >> g & 1u)) seen &= ~(0xFFull << (8 * g));
@@ -605,8 +647,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        auto scaled = [&](int j, float nm) {
+          float2 y = fma2(x[j], make_float2(sc2, sc2), make_float2(nm, nm));
+          if (masked) {
+            if (!(seen >> (2 * j) & 1u)) y.x = -INFINITY;
+            if (!(seen >> (2 * j + 1) & 1u)) y.y = -INFINITY;
+          }
+          return y;
+        };
+        // The largest exponent of a row, of its four threads.
+        auto row_top = [&](float top) {
+          X.top[blk][row] = top;
+          soft_sync();
+          float mx = X.top[0][row];
+#pragma unroll
+          for (int k = 1; k < 4; ++k) mx = fmaxf(mx, X.top[k][row]);
+          return mx;
+        };
         // P = 2^(score - m), m the running maximum (none yet: 0)
-        uint32_t pk[32];
         float top;
         float2 ls, rs;
         auto weights = [&]() {
@@ -615,11 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ls = rs = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            float2 y = fma2(x[j], make_float2(sc2, sc2), make_float2(nm, nm));
-            if (masked) {
-              if (!(seen >> (2 * j) & 1u)) y.x = -INFINITY;
-              if (!(seen >> (2 * j + 1) & 1u)) y.y = -INFINITY;
-            }
+            float2 y = scaled(j, nm);
             top = fmaxf(top, fmaxf(y.x, y.y));
             y = make_float2(ex2(y.x), ex2(y.y));
             ls = add2(ls, y);
@@ -627,216 +681,238 @@ __global__ void __launch_bounds__(kThreads, 1)
             rs = add2(rs, make_float2(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xFFFF0000u)));
           }
         };
-        weights();
-        if (soft_any(top > kLazy || (m == -INFINITY && top > -INFINITY))) {
-          // a row's maximum moves: the largest exponent of its four threads; the weights are taken again
-          X.top[blk][row] = top;
-          soft_sync();
-          float mx = X.top[0][row];
+        if (first) {  // its own maximum, which the weights then need not move
+          top = -INFINITY;
 #pragma unroll
-          for (int k = 1; k < 4; ++k) mx = fmaxf(mx, X.top[k][row]);
-          float f = 1.f;
-          if (mx > kLazy || (m == -INFINITY && mx > -INFINITY)) {
-            f = m == -INFINITY ? 0.f : ex2(-mx);
-            m = m == -INFINITY ? mx : m + mx;
-            const float2 ff = make_float2(f, f), o = make_float2(0.f, 0.f);
-            l2 = fma2(l2, ff, o);
-            r2 = fma2(r2, ff, o);
+          for (int j = 0; j < 32; ++j) {
+            const float2 y = scaled(j, 0.f);
+            top = fmaxf(top, fmaxf(y.x, y.y));
           }
-          if (c > 0) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
-          tc_fence_after();
-          if ((i & (kRun - 1)) != 0 && __any_sync(0xFFFFFFFFu, f != 1.f)) {
-#pragma unroll 1
-            for (int k = 0; k < 128; k += 16) {
-              uint32_t v[16];
-              tmem_ld16(tlane + 128 * half + k, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-              tmem_st16(tlane + 128 * half + k, v);
-            }
-            tmem_st_wait();
-          }
+          m = row_top(top);
           weights();
           soft_sync();  // top is read by all
+        } else {
+          weights();
+          if (soft_any(top > kLazy || (m == -INFINITY && top > -INFINITY))) {
+            // a row's maximum moves; the weights are taken again
+            const float mx = row_top(top);
+            float f = 1.f;
+            if (mx > kLazy || (m == -INFINITY && mx > -INFINITY)) {
+              f = m == -INFINITY ? 0.f : ex2(-mx);
+              m = m == -INFINITY ? mx : m + mx;
+              const float2 ff = make_float2(f, f), o = make_float2(0.f, 0.f);
+              l2 = fma2(l2, ff, o);
+              r2 = fma2(r2, ff, o);
+            }
+            wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+            tc_fence_after();
+            if ((st.i & (kRun - 1)) != 0 && __any_sync(0xFFFFFFFFu, f != 1.f)) {
+#pragma unroll 1
+              for (int k = 0; k < 128; k += 16) {
+                uint32_t v[16];
+                tmem_ld16(tlane + 128 * half + k, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                tmem_st16(tlane + 128 * half + k, v);
+              }
+              tmem_st_wait();
+            }
+            weights();
+            soft_sync();  // top is read by all
+          }
         }
         l2 = add2(l2, ls);
         r2 = add2(r2, rs);
-        if (c > 0) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+      }
+      if (first && c > 0) {
+        // ---- the end of the segment before: its last products run while the weights above are taken ----
+        const ChunkSegment& t = X.seg[(seg - (have ? 2 : 1)) & 3];
+        const bool whole = t.whole != 0;
+        const int crow0 = t.row0 + (int)rank * 64, tok = crow0 / a.H;
+        const bool live = (int)rank * 64 + row < t.rows;
+        const int grow = live ? crow0 + row : t.row0, gtok = grow / a.H;
+        const int ntok = whole && a.inv_freq ? (crow0 + 63) / a.H - tok + 1 : 0;
+        float2 ang = make_float2(0.f, 0.f);
+        auto angle = [&](int k) {
+          float sn, cs;
+          sincosf(rope_angle(X.turn[k & 31], (uint64_t)(t.start + (tok + (k >> 5) - t.tok0))), &sn, &cs);
+          return make_float2(cs, sn);
+        };
+        if (tid < ntok * 32) ang = angle(tid);
+        X.top[blk][row] = l_end.x + l_end.y;
+        X.sum[blk][row] = r_end.x + r_end.y;
+        wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+        tc_fence_after();
+        if (tid < ntok * 32) Y.rope[tid >> 5][tid & 31] = ang;
+        for (int k = tid + kSoft; k < ntok * 32; k += kSoft) Y.rope[k >> 5][k & 31] = angle(k);
+        soft_sync();
+        float l = 0.f, r = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          st_shared16(p_s + blk * 8192 + sw128_off(row, k),
-                      make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]));
-        if (masked) {
-          // the flags of both CTAs; the other buffer's were read before this tile's votes
-          if (tid < 8) X.flags[(nmask & 1) ^ 1][tid] = 0;
-          soft_sync();
-          if (lane == 0) {
-            mbar_arrive_cluster(dsmem_addr(smem_u32(&X.masked), rank));
-            mbar_arrive_cluster(peer_masked);
+        for (int k = 0; k < 4; ++k) {
+          l += X.top[k][row];
+          r += X.sum[k][row];
+        }
+        float fac = 0.f;
+        if (whole) {
+          const float logit = a.sink ? a.sink[grow - gtok * a.H] : -INFINITY, sink = sink_log2(logit);
+          const float M = fmaxf(m_end, sink), Mf = M == -INFINITY ? 0.f : M, e = ex2(m_end - Mf);
+          const float rows = l * e;
+          float z = rows, zr = r * e;
+          if (sink > -INFINITY) {
+            z += ex2(sink - Mf);
+            zr += ex2(sink - Mf);
           }
-          wait_phase(X, X.masked, (uint32_t)nmask & 1);
-          uint32_t any = 0;
-          for (int k = 0; k < 8; ++k) any |= X.flags[nmask & 1][k];
-          if (any) {
-            // V(i) is revolution 2 i + 2 of the segment (the last one comes one earlier)
-            const uint32_t rev = (uint32_t)(rev0 + min(2 * i + 2, 2 * w.n - 1));
-            if (rank == 0) {
-              // (the next tile's scores are complete once its keys, one revolution earlier, are)
-              if (i + 1 < w.n) wait_phase(X, X.s_full[(c + 1) & 1], (uint32_t)((c + 1) >> 1) & 1);
-              for (int k = 0; k < kSlots; ++k) wait_phase(X, X.full[k], rev & 1);
-              if (tid == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&X.landed), 1));
-            } else {
-              wait_phase(X, X.landed, (uint32_t)nland & 1);
-            }
-            ++nland;
-            // row r's values: slots (r / 64, 0) and (r / 64, 1), group r % 64 / 8, two blocks of 64 dims
-            for (int r = warp; r < kKeys; r += kSoftWarps) {
-              if (!(X.flags[nmask & 1][r >> 5] >> (r & 31) & 1u)) continue;
-              const uint32_t at = ring + (uint32_t)((r >> 6) * 2 + (lane >> 4)) * kSlotBytes + ((r & 63) >> 3) * 2048 +
-                                  ((lane >> 3) & 1) * 1024 + (r & 7) * 128 + (lane & 7) * 16;
-              uint4 v = ld_shared16(at);
-              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
-                if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
-              }
-              st_shared16(at, v);
-            }
-          }
-          ++nmask;
+          fac = zr > 0.f || zr != zr ? e / zr : 0.f;  // no row and no sink: zeros
+          if (a.lse && live && blk == 0) a.lse[grow] = head_lse(Mf, z, rows, logit);
+        } else if (blk == 0) {
+          float* to = a.pstat + ((int64_t)t.slot * 2 + rank) * 192 + row;
+          to[0] = m_end;
+          to[64] = l;
+          to[128] = r;
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(p_full);
-        const bool last = i + 1 == w.n;
-        if (!last && ((i + 1) & (kRun - 1)) == 0) {
-          // a run's end: O joins what the part holds
-          wait_phase(X, X.pv_done, (uint32_t)c & 1);
-          tc_fence_after();
-          const float f = mslot == -INFINITY ? 0.f : ex2(mslot - m);
-          const bool first = i + 1 == kRun;
+        const float f0 = mslot_end == -INFINITY ? 0.f : ex2(mslot_end - m_end);
+        const bool folded = mslot_end != -INFINITY;
+        const float2* rope = Y.rope[live ? gtok - tok : 0];
+        const uint32_t stage = p_s + warp * 2048;
+        float4* part = part_of(t.slot);
+        // where the coalesced stores of this warp go: rows 32 (quad % 2) + .. of this CTA
+        const int srow = (int)rank * 64 + 32 * (quad & 1);
+        uint16_t* out = a.out + (int64_t)(t.row0 + srow) * kDLat + kh * 128 + half * 64;
 #pragma unroll 1
-          for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll 1
-            for (int k = 0; k < 64; k += 16) {
-              uint32_t v[16];
-              tmem_ld16(tlane + 128 * hh + 64 * half + k, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float4* to = part + (hh * 32 + (k >> 2) + j) * 128;
-                float4 o = first ? make_float4(0.f, 0.f, 0.f, 0.f) : *to;
-                o.x = o.x * f + __uint_as_float(v[4 * j]);
-                o.y = o.y * f + __uint_as_float(v[4 * j + 1]);
-                o.z = o.z * f + __uint_as_float(v[4 * j + 2]);
-                o.w = o.w * f + __uint_as_float(v[4 * j + 3]);
-                *to = o;
-              }
-            }
-          }
-          mslot = m;
-          tc_fence_before();
-        }
-      }
-      rev0 += 2 * w.n;
-      // ---- the segment's end ----
-      wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
-      tc_fence_after();
-      Y.l[blk][row] = l2.x + l2.y;
-      Y.r[blk][row] = r2.x + r2.y;
-      const bool folded = w.n > kRun;
-      const int crow0 = t.row0 + (int)rank * 64;
-      if (whole && a.inv_freq) {
-        const int64_t tok = crow0 / a.H;
-        const int n = (int)((crow0 + 63) / a.H - tok) + 1;
-        for (int k = tid; k < n * 32; k += kSoft) {
-          float s, cs;
-          sincosf(rope_angle(X.turn[k & 31], (uint64_t)(t.start + (tok + (k >> 5) - t.tok0))), &s, &cs);
-          Y.rope[k >> 5][k & 31] = make_float2(cs, s);
-        }
-      }
-      soft_sync();
-      float l = 0.f, r = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        l += Y.l[k][row];
-        r += Y.r[k][row];
-      }
-      const bool live = (int)rank * 64 + row < t.rows;
-      const int h = grow - grow / a.H * a.H;
-      float fac = 0.f;
-      if (whole) {
-        const float logit = a.sink ? a.sink[h] : -INFINITY, sink = sink_log2(logit);
-        const float M = fmaxf(m, sink), Mf = M == -INFINITY ? 0.f : M, e = ex2(m - Mf);
-        const float rows = l * e;
-        float z = rows, zr = r * e;
-        if (sink > -INFINITY) {
-          z += ex2(sink - Mf);
-          zr += ex2(sink - Mf);
-        }
-        fac = zr > 0.f || zr != zr ? e / zr : 0.f;  // no row and no sink: zeros
-        if (a.lse && live && blk == 0) a.lse[grow] = head_lse(Mf, z, rows, logit);
-      } else if (blk == 0) {
-        float* st = a.pstat + (slot * 2 + rank) * 192 + row;
-        st[0] = m;
-        st[64] = l;
-        st[128] = r;
-      }
-      const float f0 = mslot == -INFINITY ? 0.f : ex2(mslot - m);
-      const float2* rope = Y.rope[live ? grow / a.H - crow0 / a.H : 0];
-      uint16_t* out = a.out + (int64_t)grow * kDLat + kh * 128 + half * 64;
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {
-        const bool rot = whole && a.inv_freq && hh == 1 && blk == 3;
-#pragma unroll 1
-        for (int k = 0; k < 64; k += 16) {
-          uint32_t v[16];
-          tmem_ld16(tlane + 128 * hh + 64 * half + k, v);
+        for (int k = 0; k < 4; ++k) {  // 32 columns
+          const int hh = k >> 1, col = 32 * (k & 1);
+          uint32_t v[32];
+          tmem_ld32(tlane + 128 * hh + 64 * half + col, v);
           tmem_ld_wait();
-          float o[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(v[j]);
           if (folded) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 q = part[(hh * 32 + (k >> 2) + j) * 128];
-              o[4 * j] = fmaf(q.x, f0, o[4 * j]);
-              o[4 * j + 1] = fmaf(q.y, f0, o[4 * j + 1]);
-              o[4 * j + 2] = fmaf(q.z, f0, o[4 * j + 2]);
-              o[4 * j + 3] = fmaf(q.w, f0, o[4 * j + 3]);
+            for (int j = 0; j < 8; ++j) {
+              const float4 q = part[(hh * 32 + (col >> 2) + j) * 128];
+              v[4 * j] = __float_as_uint(fmaf(q.x, f0, __uint_as_float(v[4 * j])));
+              v[4 * j + 1] = __float_as_uint(fmaf(q.y, f0, __uint_as_float(v[4 * j + 1])));
+              v[4 * j + 2] = __float_as_uint(fmaf(q.z, f0, __uint_as_float(v[4 * j + 2])));
+              v[4 * j + 3] = __float_as_uint(fmaf(q.w, f0, __uint_as_float(v[4 * j + 3])));
             }
           }
           if (!whole) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              part[(hh * 32 + (k >> 2) + j) * 128] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)
+              part[(hh * 32 + (col >> 2) + j) * 128] =
+                  make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                              __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
             continue;
           }
-          uint32_t b[8];
+          const bool rot = ntok > 0 && hh == 1 && blk == 3;
+          uint32_t b[16];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float y0 = o[2 * j] * fac, y1 = o[2 * j + 1] * fac;
+          for (int j = 0; j < 16; ++j) {
+            float y0 = __uint_as_float(v[2 * j]) * fac, y1 = __uint_as_float(v[2 * j + 1]) * fac;
             if (rot) {  // times e^{-i p theta}
-              const float2 cs = rope[(k >> 1) + j];
+              const float2 cs = rope[(col >> 1) + j];
               const float z = y0 * cs.x + y1 * cs.y;
               y1 = y1 * cs.x - y0 * cs.y;
               y0 = z;
             }
             b[j] = pack_bf16x2(y0, y1);
           }
-          if (live) {
-            uint4* to = reinterpret_cast<uint4*>(out + hh * 256 + k);
-            to[0] = make_uint4(b[0], b[1], b[2], b[3]);
-            to[1] = make_uint4(b[4], b[5], b[6], b[7]);
+          // 32 rows of 64 bytes: chunk i of row r at i ^ (r / 2 % 4)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st_shared16(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
+                        make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]));
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int rr = 8 * j + (lane >> 2);
+            const uint4 o = ld_shared16(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+            if (srow + rr < t.rows)
+              __stcs(reinterpret_cast<uint4*>(out + (int64_t)rr * kDLat + hh * 256 + col) + (lane & 3), o);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        soft_sync();  // sums, angles and stages are read before P and the next sums are written
+      }
+      if (!have) break;
+      if (!first) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        st_shared16(p_s + blk * 8192 + sw128_off(row, k),
+                    make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]));
+      if (masked) {
+        // the flags of both CTAs; the other buffer's were read before this tile's votes
+        if (tid < 8) X.flags[(nmask & 1) ^ 1][tid] = 0;
+        soft_sync();
+        if (lane == 0) {
+          mbar_arrive_cluster(dsmem_addr(smem_u32(&X.masked), rank));
+          mbar_arrive_cluster(peer_masked);
+        }
+        wait_phase<true>(X, X.masked, (uint32_t)nmask & 1);
+        uint32_t any = 0;
+        for (int k = 0; k < 8; ++k) any |= X.flags[nmask & 1][k];
+        if (any) {
+          mbar_wait(smem_u32(&X.step_full[(c + 1) & 3]), (uint32_t)((c + 1) >> 2) & 1, 60000000000ull);
+          const bool ahead = X.step[(c + 1) & 3].i >= 0;  // another key tile follows
+          if (rank == 0) {
+            // V(c) is revolution 2 c + 2, the last one 2 c + 1.  (The next tile's scores are complete
+            // once its keys, one revolution earlier, are.)
+            if (ahead) wait_phase(X, X.s_full[(c + 1) & 1], (uint32_t)((c + 1) >> 1) & 1);
+            for (int k = 0; k < kSlots; ++k) wait_phase(X, X.full[k], ahead ? 0u : 1u);
+            if (tid == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&X.landed), 1));
+          } else {
+            wait_phase<true>(X, X.landed, (uint32_t)nland & 1);
+          }
+          ++nland;
+          // row r's values: slots (r / 64, 0) and (r / 64, 1), group r % 64 / 8, two blocks of 64 dims
+          for (int r = warp; r < kKeys; r += kSoftWarps) {
+            if (!(X.flags[nmask & 1][r >> 5] >> (r & 31) & 1u)) continue;
+            const uint32_t at = ring + (uint32_t)((r >> 6) * 2 + (lane >> 4)) * kSlotBytes + ((r & 63) >> 3) * 2048 +
+                                ((lane >> 3) & 1) * 1024 + (r & 7) * 128 + (lane & 7) * 16;
+            uint4 v = ld_shared16(at);
+            uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
+              if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
+            }
+            st_shared16(at, v);
           }
         }
+        ++nmask;
       }
+      fence_proxy_async_smem();
       tc_fence_before();
-      soft_sync();  // the sums and angles are read before P is written again
-    } while (walk_next(a, w));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(p_full);
+      if (!st.last && ((st.i + 1) & (kRun - 1)) == 0) {
+        // a run's end: O joins what the part holds
+        wait_phase(X, X.pv_done, (uint32_t)c & 1);
+        tc_fence_after();
+        const float f = mslot == -INFINITY ? 0.f : ex2(mslot - m);
+        const bool onto = st.i + 1 > kRun;
+        float4* part = part_of(X.seg[(seg - 1) & 3].slot);
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const int hh = k >> 2, col = 16 * (k & 3);
+          uint32_t v[16];
+          tmem_ld16(tlane + 128 * hh + 64 * half + col, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float4* to = part + (hh * 32 + (col >> 2) + j) * 128;
+            float4 o = onto ? *to : make_float4(0.f, 0.f, 0.f, 0.f);
+            o.x = fmaf(o.x, f, __uint_as_float(v[4 * j]));
+            o.y = fmaf(o.y, f, __uint_as_float(v[4 * j + 1]));
+            o.z = fmaf(o.z, f, __uint_as_float(v[4 * j + 2]));
+            o.w = fmaf(o.w, f, __uint_as_float(v[4 * j + 3]));
+            *to = o;
+          }
+        }
+        mslot = m;
+        tc_fence_before();
+      }
+    }
   } else if (work && warp == kWarpMma && rank == 0) {
     // ================= products =================
     const uint32_t lead = elect_lane();
@@ -844,12 +920,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), p_d = sdesc_sw128(p_s, 16, 1024);
     const uint64_t k_d = sdesc_sw128(ring, 16, 1024), v_d = sdesc_sw128(ring, 1024, 2048);
     bool ok = true;
-    int c = 0, rev = 0, seg = 0;
-    auto scores = [&]() {
+    int rev = 0;
+    auto values = [&](int c, int run) {  // of key tile c of this pair, the run's run-th
+      ok = ok && all_ok(wait_phase<true>(X, X.p_full, (uint32_t)c & 1));
+      if (!ok) return;
+      tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kSlots; ++k) {
         ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
         if (!ok) return;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            umma_pair_bf16(tmem + 128 * (k & 1), p_d + (((k >> 1) * 8192 + s * 32) >> 4),
+                           v_d + ((k * kSlotBytes + s * 4096) >> 4), id_o, run > 0 || k > 1 || s > 0);
+          umma_commit_pair(smem_u32(&X.empty[k]));
+        }
+        __syncwarp();
+      }
+      if (lead) umma_commit_pair(smem_u32(&X.pv_done));
+      __syncwarp();
+      ++rev;
+    };
+    int c = 0, seg = 0, run = 0;
+    while (ok) {
+      ok = all_ok(wait_phase(X, X.step_full[c & 3], (uint32_t)(c >> 2) & 1));
+      const int i = uniform(X.step[c & 3].i), last = uniform(X.step[c & 3].last);
+      if (!ok || i < 0) break;
+      if (i == 0) {
+        ok = all_ok(wait_phase(X, X.q_full, (uint32_t)seg & 1));
+        ++seg;
+      }
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
+        if (!ok) break;
         tc_fence_after();
         if (lead) {
 #pragma unroll
@@ -860,116 +966,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      if (lead) umma_commit_pair(smem_u32(&X.s_full[c & 1]));
+      if (!ok) break;
+      if (lead) {
+        umma_commit_pair(smem_u32(&X.s_full[c & 1]));
+        if (last) umma_commit_pair(smem_u32(&X.q_empty));
+      }
       __syncwarp();
       ++rev;
+      if (c > 0) values(c - 1, run);
+      run = i & (kRun - 1);
       ++c;
-    };
-    do {
-      const int n = uniform(w.n);
-      ok = all_ok(wait_phase(X, X.q_full, (uint32_t)seg & 1));
-      tc_fence_after();
-      const int c0 = c;
-      if (ok) scores();
-      for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n) scores();
-        if (i + 2 >= n && (i + 1 < n || n == 1)) {  // Q is free
-          if (lead) umma_commit_pair(smem_u32(&X.q_empty));
-          __syncwarp();
-        }
-        ok = ok && all_ok(wait_phase(X, X.p_full, (uint32_t)(c0 + i) & 1));
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < kSlots; ++k) {
-          ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (lead) {
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-              umma_pair_bf16(tmem + 128 * (k & 1), p_d + (((k >> 1) * 8192 + s * 32) >> 4),
-                             v_d + ((k * kSlotBytes + s * 4096) >> 4), id_o,
-                             (i & (kRun - 1)) > 0 || k > 1 || s > 0);
-            umma_commit_pair(smem_u32(&X.empty[k]));
-          }
-          __syncwarp();
-        }
-        if (lead) umma_commit_pair(smem_u32(&X.pv_done));
-        __syncwarp();
-        ++rev;
-      }
-      ++seg;
-    } while (ok && uniform(walk_next(a, w)) != 0);
+    }
+    if (ok) values(c - 1, run);
     // no product may still be running when the tensor memory is released, whatever happened above
     if (lead) umma_commit_pair(smem_u32(&X.fin));
     __syncwarp();
     mbar_wait(smem_u32(&X.fin), 0, 100000000ull);
-  } else if (work && warp == kWarpLoad) {
+  } else if (work && warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
     // ================= loads =================
     const uint64_t pol = policy_evict_normal();
-    const uint32_t q_full = dsmem_addr(smem_u32(&X.q_full), 0);
+    const int k0 = warp - kWarpLoad;  // this warp's slots: k0, k0 + kLoadWarps, ..
+    const uint32_t q_full = dsmem_addr(smem_u32(&X.q_full), 0), full = dsmem_addr(smem_u32(&X.full[0]), 0);
     const int lg = 31 - __clz(a.box_rows);
     bool ok = true;
     int rev = 0, c = 0, seg = 0, n_last = 0;
-    // Eight slots, each in pieces of box_rows rows, one a lane: of `rows` rows from row `row0 + step
-    // (k / 2)` of the key tile on.
+    int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
+    ChunkWalk w;
+    walk_start(a, pair, w);
+    // Eight slots, each in pieces of box_rows rows, one a lane.
     auto slots = [&](const Places& at, const CUtensorMap* map, bool values) {
-      const int pieces = (values ? 64 : 128) >> lg;
+      const int piece = lane << lg;
+      const bool mine = piece < (values ? 64 : 128);
+      const uint32_t dst = ring + (uint32_t)piece * (values ? 256 : 128);
+      int g = (16 * (int)rank + (piece >> 3)) & 31;
+      int32_t y = __shfl_sync(0xFFFFFFFFu, at.y, g), z = __shfl_sync(0xFFFFFFFFu, at.z, g);
 #pragma unroll 1
-      for (int k = 0; k < kSlots; ++k) {
+      for (int k = k0; k < kSlots; k += kLoadWarps) {
+        if (values) {
+          g = (8 * (k >> 1) + (piece >> 3)) & 31;
+          y = __shfl_sync(0xFFFFFFFFu, at.y, g);
+          z = __shfl_sync(0xFFFFFFFFu, at.z, g);
+        }
         if (rev > 0) ok = ok && all_ok(wait_phase(X, X.empty[k], (uint32_t)(rev - 1) & 1));
         if (!ok) return;
-        const int g = ((values ? 8 * (k >> 1) : 16 * (int)rank) + ((lane << lg) >> 3)) & 31;
-        const int32_t y = __shfl_sync(0xFFFFFFFFu, at.y, g), z = __shfl_sync(0xFFFFFFFFu, at.z, g);
-        const uint32_t full = dsmem_addr(smem_u32(&X.full[k]), 0);
         if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&X.full[k]), 2 * kSlotBytes);
-        __syncwarp();
-        if (lane < pieces)
-          tma_load_5d_pair(ring + k * kSlotBytes + ((uint32_t)lane << lg) * (values ? 256 : 128), map,
-                           values ? 4 * (k & 1) + 2 * (int)rank : k, y, z, full, pol);
+        if (mine)
+          tma_load_5d_pair(dst + k * kSlotBytes, map, values ? 4 * (k & 1) + 2 * (int)rank : k, y, z,
+                           full + 8 * k, pol);
         __syncwarp();
       }
       ++rev;
     };
-    do {
-      const ChunkTile& t = w.t;
-      int lo0, hi0, lo1, hi1;
-      tile_rows(a, t, lo0, hi0, lo1, hi1);
-      if (seg > 0)
-        ok = all_ok(wait_phase(X, X.q_empty, (uint32_t)(seg - 1) & 1,
-                               2000000000ull + 100000ull * (uint32_t)n_last));
-      if (!ok) break;
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&X.q_full), 2 * kQBytes);
+    // The places of the walk's key tile (a segment's first: with its bounds).
+    auto places = [&]() {
+      if (w.i == 0) tile_rows(a, w.t, lo0, hi0, lo1, hi1);
+      return place_groups(a, w.t, (int64_t)(w.t.k0 + w.unit + w.i) * kKeys, lo0, hi1, lane,
+                          rank == 0 && k0 == 0);
+    };
+    Places cur = places(), last = cur;
+    bool have = true;
+    while (ok && have) {
+      if (k0 == 0) {
+        if (w.i == 0) {
+          if (seg > 0)
+            ok = all_ok(wait_phase(X, X.q_empty, (uint32_t)(seg - 1) & 1,
+                                   2000000000ull + 100000ull * (uint32_t)n_last));
+          if (!ok) break;
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&X.q_full), 2 * kQBytes);
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          tma_load_2d_pair(q_s + k * 8192, &qmap, 64 * k, t.row0 + (int)rank * 64, q_full, pol);
-      }
-      __syncwarp();
-      ++seg;
-      n_last = w.n;
-      const int64_t base = (int64_t)(t.k0 + w.unit) * kKeys;
-      Places cur, nxt = place_groups(a, t, base, lo0, hi1, lane, rank == 0);
-      auto keys = [&](int i) {
-        const uint32_t groups = __ballot_sync(0xFFFFFFFFu, nxt.good);
+            for (int k = 0; k < 8; ++k)
+              tma_load_2d_pair(q_s + k * 8192, &qmap, 64 * k, w.t.row0 + (int)rank * 64, q_full, pol);
+          }
+          if (lane == 0)
+            X.seg[seg & 3] = ChunkSegment{w.t.start, w.t.row0, w.t.rows, w.t.tok0, w.t.clip, hi0, lo1,
+                                          w.t.c0 == w.t.c1, 2 * pair + (w.unit == 0 ? 1 : 0)};
+          __syncwarp();
+          ++seg;
+          n_last = w.n;
+        }
+        const uint32_t groups = __ballot_sync(0xFFFFFFFFu, cur.good);
         if (lane == 0) {
-          X.groups[c & 3] = groups;
-          mbar_arrive(smem_u32(&X.mask_full[c & 3]));
+          X.step[c & 3] = ChunkStep{groups, (w.t.k0 + w.unit + w.i) * kKeys, w.i, w.i + 1 == w.n};
+          mbar_arrive(smem_u32(&X.step_full[c & 3]));
         }
-        ++c;
-        slots(nxt, &kmap, false);
-      };
-      keys(0);
-      for (int i = 0; ok && i < w.n; ++i) {
-        cur = nxt;
-        if (i + 1 < w.n) {
-          nxt = place_groups(a, t, base + (int64_t)(i + 1) * kKeys, lo0, hi1, lane, rank == 0);
-          keys(i + 1);
-        }
-        if (ok) slots(cur, &vmap, true);
       }
-    } while (ok && uniform(walk_next(a, w)) != 0);
+      const Places now = cur;
+      have = uniform(walk_next(a, w)) != 0;
+      if (have) cur = places();  // (the table's entries arrive while the slots are filled)
+      slots(now, &kmap, false);
+      if (ok && c > 0) slots(last, &vmap, true);
+      last = now;
+      ++c;
+    }
+    if (k0 == 0 && lane == 0) {  // (after a wait that gave up, too)
+      X.step[c & 3] = ChunkStep{0u, 0, -1, 0};
+      mbar_arrive(smem_u32(&X.step_full[c & 3]));
+    }
+    if (ok) slots(last, &vmap, true);
   }
   tc_fence_before();
   __syncthreads();
@@ -988,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A tile that pairs c0 .. c1 worked on: with M the largest running maximum (and the sink's logit) of
 // a row, out = sum 2^(m - M) O / Z.  Pair c0 + 1's CTAs do it (the first that began within the tile),
 // kJoin of them, a thread 16 bytes of every part at a time.  Bound by the parts' way from L2.
-constexpr int kJoin = 16, kMaxPairs = 76;
+constexpr int kJoin = 64, kMaxPairs = 76;
 
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
   __shared__ float wt[kMaxPairs][64];
