@@ -915,6 +915,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (work && warp == kWarpMma && rank == 0) {
     // ================= products =================
+    // (loops over slots stay rolled: unrolled, their instructions crowd out the softmax', and 2048 tokens
+    // over 32768 rows take 6.0 ms in place of 5.1)
     const uint32_t lead = elect_lane();
     const uint32_t id_s = idesc_bf16(128, 256, 0, 0), id_o = idesc_bf16(128, 256, 0, 1);
     const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), p_d = sdesc_sw128(p_s, 16, 1024);
@@ -925,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && all_ok(wait_phase<true>(X, X.p_full, (uint32_t)c & 1));
       if (!ok) return;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < kSlots; ++k) {
         ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
         if (!ok) return;
@@ -952,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = all_ok(wait_phase(X, X.q_full, (uint32_t)seg & 1));
         ++seg;
       }
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < kSlots; ++k) {
         ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
         if (!ok) break;
@@ -1053,9 +1055,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Places now = cur;
       have = uniform(walk_next(a, w)) != 0;
-      if (have) cur = places();  // (the table's entries arrive while the slots are filled)
       slots(now, &kmap, false);
       if (ok && c > 0) slots(last, &vmap, true);
+      if (have) cur = places();  // (read while the slots issued last are still in use)
       last = now;
       ++c;
     }
