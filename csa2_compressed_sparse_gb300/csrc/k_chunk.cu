@@ -172,20 +172,21 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
 //                2^64, so a tile's usual pass is one vote
 //   warp 8       issues all products (even CTA)
 //   warps 9, 10  load the even and the odd slots, the first of them each tile's Q
+//   warp 11      cleans values that must not be read (below)
 // The plan deals the key tiles of all tiles evenly to the pairs; a tile that several pairs work on is
 // joined from their parts by chunk_join_kernel.
 //
 // A row that some tokens of a tile see and others do not may hold NaN or infinities, which must not
 // reach those others through 0 * NaN.  Such a row makes its scores non-finite for every query, so
-// where a key tile is masked for some row, a masked score that is not finite flags the cache row in
-// both CTAs, and its values lose their non-finite elements before the product (the tokens that see
-// the row have NaN weights).  Rows behind the last visible one are garbage and are treated so too.
+// where a key tile is masked for some row, a masked score that is not finite flags the cache row, and
+// the values of flagged rows lose their non-finite elements before the product (the tokens that see the
+// row have NaN weights).  Rows behind the last visible one are garbage and are treated so too.
 
 constexpr int kQRows = 128, kKeys = 256;
 constexpr int kSlotBytes = 16384, kSlots = 8;
 constexpr int kQBytes = 65536, kPBytes = 32768;
 constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
-constexpr int kWarpMma = 8, kWarpLoad = 9, kLoadWarps = 2, kThreads = 32 * (kWarpLoad + kLoadWarps);
+constexpr int kWarpMma = 8, kWarpLoad = 9, kLoadWarps = 2, kWarpClean = 11, kThreads = 32 * 12;
 constexpr uint32_t kColS = 256;
 constexpr float kLazy = 64.0f;
 // Key tiles that O sums up in tensor memory (65536 rows; the tensor core cuts the low bits of its
@@ -197,8 +198,9 @@ struct __align__(16) ChunkStep {
   uint32_t groups;  // groups of eight rows that are on a page
   int base;         // first cache row
   int i;            // key tile of the segment, -1: no further one
-  int last;         // 1: the segment's last
+  int kind;         // 1: the segment's last, 2: not all of its rows are seen by all tokens
 };
+enum : int { kStepLast = 1, kStepMasked = 2 };
 // A segment: key tiles of a tile of queries.
 struct __align__(16) ChunkSegment {
   int64_t start;
@@ -212,28 +214,21 @@ struct __align__(16) ChunkAux {
   uint64_t full[kSlots], empty[kSlots];
   uint64_t q_full, q_empty;
   uint64_t s_full[2];
-  uint64_t p_full, pv_done;
+  uint64_t p_full[4], p_free[4];  // P's blocks of 64 cache rows: written; read by their products
   uint64_t step_full[4];
-  uint64_t masked;        // both CTAs' softmax warps have flagged a masked tile's rows
-  uint64_t landed;        // a flagged tile's values are in both CTAs
+  uint64_t clean_req, clean_done;
   uint64_t fin;
   ChunkStep step[4];      // of key tile c & 3 (three at most are in use)
   ChunkSegment seg[4];    // of segment s & 3 (four)
-  uint32_t flags[2][8];   // rows of a masked tile to be cleaned
+  uint32_t flags[2][8];   // even CTA: rows of key tile c & 1 to be cleaned
+  uint32_t clean[8];      // rows to be cleaned now
   uint64_t turn[32];
   float top[4][64], sum[4][64];
   uint32_t tmem_slot;
-  int abort;
+  int abort, done;
 };
 constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kPBytes + (int)sizeof(ChunkAux);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
-
-// In P's memory at a segment's end.
-struct ChunkEnd {
-  uint8_t stage[kSoftWarps][2048];  // 32 rows x 32 dims of the output
-  float2 rope[64][32];              // of the tokens of this CTA's rows
-};
-static_assert(sizeof(ChunkEnd) <= kPBytes, "it shares P's memory");
 
 // Wait for a phase; false once something in the CTA has given up.  kPair: one that threads of both CTAs
 // complete with what they wrote.
@@ -270,6 +265,18 @@ __device__ __forceinline__ bool soft_any(bool pred) {
   return r != 0;
 }
 
+// 32 bytes to global memory, 16-byte aligned; in one store where they are a sector.
+__device__ __forceinline__ void store_sector(uint16_t* to, const uint32_t (&b)[8]) {
+  if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(b[0]), "r"(b[1]),
+                 "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(b[5]), "r"(b[6]), "r"(b[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(to)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+    reinterpret_cast<uint4*>(to)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+  }
+}
+
 // Rows lo .. hi - 1 that the token at position p sees, of at most clip; true if there were more.
 __device__ __forceinline__ bool token_rows(const ChunkArgs& a, int64_t p, int64_t clip, int& lo, int& hi) {
   int64_t h;
@@ -290,11 +297,12 @@ __device__ __forceinline__ bool token_rows(const ChunkArgs& a, int64_t p, int64_
 // ---- plan ------------------------------------------------------------------------------
 //
 // One CTA: the tiles of all sequences with their key tiles, the staged rows' places, and each pair's
-// share of the W units (key tiles).  Up to as many tiles as pairs, none longer than kWhole, go to a
-// pair each.  Otherwise pair c gets units W c / C .. W (c + 1) / C - 1, C as many pairs as leave each
-// kShare units or a tile.
+// share.  Up to as many tiles as pairs, none longer than kWhole, go to a pair each.  Otherwise the cost of
+// all tiles, 2 a key tile and kTileCost a tile (what begins and ends it takes as long as 1.5 key tiles), is
+// cut evenly: pair c begins at cost W c / C, C as many pairs as leave each kShare key tiles or a tile.  A cut
+// within the first kTileCost of a tile is one before it.
 constexpr int kPlanThreads = 1024;
-constexpr int kWhole = 6, kShare = 4;
+constexpr int kWhole = 6, kShare = 4, kTileCost = 3;
 
 // Exclusive prefix of x over the CTA's threads; *total gets the sum.
 __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* sums, int64_t* total) {
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
         t.kn = hi > lo ? (hi + kKeys - 1) / kKeys - t.k0 : 1;
         atomicMax(&longest, t.kn);
       }
-      const int64_t before = units + plan_scan(t.kn, sums, &total);
+      const int64_t before = units + plan_scan(x < here ? 2 * t.kn + kTileCost : 0, sums, &total);
       if (x < here && tiles + x < a.max_tiles) {
         a.tile[tiles + x] = t;
         a.prefix[tiles + x] = before;
@@ -426,24 +434,44 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
   __syncthreads();
   const int64_t n = min(tiles, (int64_t)a.max_tiles);
   const bool whole = n <= a.pairs && longest <= kWhole;
-  int64_t C = max(n, (units + kShare - 1) / kShare);
+  int64_t C = max(n, ((units - kTileCost * n) / 2 + kShare - 1) / kShare);
   C = C < a.pairs ? C : a.pairs;
   for (int64_t c = tid; c < a.pairs; c += kPlanThreads)
     if (c >= (whole ? n : C)) a.share[c] = ChunkShare{0, 0, 0};
+  // Where pair c begins, as key tiles from tile x on (before cost p): at most kn.
+  auto begin = [&](int64_t c, int64_t p) -> int64_t {
+    const int64_t u = quotient(units * c, C) - p - kTileCost;
+    return u > 0 ? u >> 1 : 0;
+  };
   for (int64_t x = tid; x < n; x += kPlanThreads) {
     ChunkTile& t = a.tile[x];
-    const int64_t p = a.prefix[x], e = p + t.kn;
+    const int64_t p = a.prefix[x], e = p + 2 * t.kn + kTileCost;
     if (whole) {
       t.c0 = t.c1 = (int)x;
       a.share[x] = ChunkShare{(int32_t)x, 0, t.kn};
       continue;
     }
-    t.c0 = (int)quotient((p + 1) * C - 1, units);
+    // pairs that begin at or before its first key tile, and before its end
+    t.c0 = (int)quotient((p + kTileCost + 2) * C - 1, units);
     t.c1 = (int)quotient(e * C - 1, units);
-    for (int64_t c = t.c0; c <= t.c1; ++c) {  // pairs that begin in this tile
-      const int64_t u = quotient(units * c, C);
-      if (u >= p && u < e)
-        a.share[c] = ChunkShare{(int32_t)x, (int32_t)(u - p), quotient(units * (c + 1), C) - u};
+    for (int64_t c = quotient(p * C + units - 1, units); c <= t.c1; ++c) {  // pairs whose cut is in this tile
+      // its end: where the next one begins, in this tile or a later one
+      const int64_t at = begin(c, p), cut = c + 1 < C ? quotient(units * (c + 1), C) : units;
+      int64_t count = -at;
+      if (cut < e) {
+        count += begin(c + 1, p);
+      } else {
+        int64_t lo = x, hi = n - 1;  // the last tile that begins at or before the cut
+        while (lo < hi) {
+          const int64_t m = (lo + hi + 1) >> 1;
+          if (a.prefix[m] <= cut) lo = m;
+          else hi = m - 1;
+        }
+        // key tiles from tile x to the cut
+        count += c + 1 < C ? (a.prefix[lo] - p - kTileCost * (lo - x)) / 2 + begin(c + 1, a.prefix[lo])
+                           : (units - p - kTileCost * (n - x)) / 2;
+      }
+      a.share[c] = ChunkShare{(int32_t)x, (int32_t)at, count};
     }
   }
 }
@@ -527,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t q_s = smem_u32(smem), ring = q_s + kQBytes, p_s = ring + kSlots * kSlotBytes;
   ChunkAux& X = *reinterpret_cast<ChunkAux*>(smem + kQBytes + kSlots * kSlotBytes + kPBytes);
-  ChunkEnd& Y = *reinterpret_cast<ChunkEnd*>(smem + kQBytes + kSlots * kSlotBytes);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1;
@@ -540,13 +567,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&X.q_full), 1);
     mbar_init(smem_u32(&X.q_empty), 1);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&X.s_full[i]), 1);
-    mbar_init(smem_u32(&X.p_full), 2 * kSoftWarps);
-    mbar_init(smem_u32(&X.pv_done), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&X.p_full[i]), 2 * kSoftWarps / 4);
+      mbar_init(smem_u32(&X.p_free[i]), 1);
+    }
     for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&X.step_full[i]), 1);
-    mbar_init(smem_u32(&X.masked), 2 * kSoftWarps);
-    mbar_init(smem_u32(&X.landed), 1);
+    mbar_init(smem_u32(&X.clean_req), 1);
+    mbar_init(smem_u32(&X.clean_done), 2);
     mbar_init(smem_u32(&X.fin), 1);
-    X.abort = 0;
+    X.abort = X.done = 0;
     mbar_fence_init();
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
@@ -573,16 +602,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int L = 32 * quad + lane, row = L & 63, kh = L >> 6, blk = 2 * kh + half;
     const uint32_t tlane = tmem + ((uint32_t)(32 * quad) << 16);
     const float sc2 = a.scale * kLog2e;
-    const uint32_t p_full = dsmem_addr(smem_u32(&X.p_full), 0);
-    const uint32_t peer_masked = dsmem_addr(smem_u32(&X.masked), rank ^ 1);
-    int nmask = 0;      // masked key tiles so far
-    int nland = 0;      // flagged ones
-    int seg = 0;        // segments
-    // of the segment: bounds of its first and last token, of this thread's row; the running maximum,
+    const uint32_t p_full = dsmem_addr(smem_u32(&X.p_full[blk]), 0);
+    const uint32_t flags = dsmem_addr(smem_u32(&X.flags[0][2 * blk]), 0);
+    int seg = 0;  // segments so far
+    // of the segment: what this thread's row sees; the running maximum,
     // that of what the part holds, and the sums of P (unrounded, rounded)
-    int hi0 = 0, lo1 = 0, lo = 0, hi = 0;
+    int lo = 0, hi = 0;
     float m = -INFINITY, mslot = -INFINITY;
     float2 l2 = make_float2(0.f, 0.f), r2 = l2;
+    float logit = -INFINITY;  // the row's sink
     auto part_of = [&](int sl) {
       return reinterpret_cast<float4*>(a.part) + (((int64_t)sl * 2 + rank) * 64 + 16 * half) * 128 + L;
     };
@@ -596,33 +624,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // of the segment before, until its end is done
       const float m_end = m, mslot_end = mslot;
       const float2 l_end = l2, r_end = r2;
+      const float logit_end = logit;
       if (have) {
         if (first) {
           m = mslot = -INFINITY;
           l2 = r2 = make_float2(0.f, 0.f);
           const ChunkSegment& t = X.seg[seg & 3];
-          hi0 = t.hi0;
-          lo1 = t.lo1;
           const int grow = t.row0 + min((int)rank * 64 + row, t.rows - 1);  // rows behind the last follow it
           token_rows(a, t.start + (grow / a.H - t.tok0), t.clip, lo, hi);
+          if (a.sink) logit = a.sink[grow % a.H];
           ++seg;
         }
         wait_phase(X, X.s_full[c & 1], (uint32_t)(c >> 1) & 1);
         tc_fence_after();
-        float2 x[32];
-        {
-          uint32_t v[32];
-          tmem_ld32(tlane + kColS + 128 * (c & 1) + 64 * half, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-          tmem_ld32(tlane + kColS + 128 * (c & 1) + 64 * half + 32, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            x[16 + j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-        }
-        masked = st.base < lo1 || st.base + kKeys > hi0 || st.groups != 0xFFFFFFFFu;  // the same in the pair
+        const uint32_t scores = tlane + kColS + 128 * (c & 1) + 64 * half;
+        masked = (st.kind & kStepMasked) != 0;
         uint64_t seen = ~0ull;
         if (masked) {
           seen = tile_mask((int64_t)st.base + 64 * blk, lo, hi);
@@ -630,25 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int g = 0; g < 8; ++g)
             if (!(g8 >> g & 1u)) seen &= ~(0xFFull << (8 * g));
-          // rows that must not be seen and whose scores are not finite
-          uint32_t bad[2] = {0u, 0u};
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (!(seen >> (2 * j) & 1u) && !(fabsf(x[j].x) <= FLT_MAX)) bad[j >> 4] |= 1u << (2 * (j & 15));
-            if (!(seen >> (2 * j + 1) & 1u) && !(fabsf(x[j].y) <= FLT_MAX)) bad[j >> 4] |= 2u << (2 * (j & 15));
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            bad[k] = __reduce_or_sync(0xFFFFFFFFu, bad[k]);
-            if (lane == 0 && bad[k]) {
-              const uint32_t at = smem_u32(&X.flags[nmask & 1][2 * blk + k]);
-              red_or_cluster(dsmem_addr(at, rank), bad[k]);
-              red_or_cluster(dsmem_addr(at, rank ^ 1), bad[k]);
-            }
-          }
         }
-        auto scaled = [&](int j, float nm) {
-          float2 y = fma2(x[j], make_float2(sc2, sc2), make_float2(nm, nm));
+        // Exponents of columns 2 j, 2 j + 1: v two of the scores.
+        auto scaled = [&](int j, const uint32_t* v, float nm) {
+          float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), make_float2(sc2, sc2),
+                          make_float2(nm, nm));
           if (masked) {
             if (!(seen >> (2 * j) & 1u)) y.x = -INFINITY;
             if (!(seen >> (2 * j + 1) & 1u)) y.y = -INFINITY;
@@ -671,9 +673,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float nm = m == -INFINITY ? 0.f : -m;
           top = -INFINITY;
           ls = rs = make_float2(0.f, 0.f);
+          uint32_t v[64];
+          tmem_ld32(scores, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_ld32(scores + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            float2 y = scaled(j, nm);
+            float2 y = scaled(j, v + 2 * j, nm);
             top = fmaxf(top, fmaxf(y.x, y.y));
             y = make_float2(ex2(y.x), ex2(y.y));
             ls = add2(ls, y);
@@ -681,20 +687,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             rs = add2(rs, make_float2(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xFFFF0000u)));
           }
         };
-        if (first) {  // its own maximum, which the weights then need not move
-          top = -INFINITY;
+        // a segment's first tile begins with its own maximum, which the weights then need not move
+        for (int pass = first ? 1 : 0;; ++pass) {
+          if (pass == 1 || masked) {
+            // the largest exponent; and rows that must not be seen and whose scores are not finite
+            uint32_t v[64], bad[2] = {0u, 0u};
+            tmem_ld32(scores, *reinterpret_cast<uint32_t(*)[32]>(v));
+            tmem_ld32(scores + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+            tmem_ld_wait();
+            const float nm = m == -INFINITY ? 0.f : -m;
+            top = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 y = scaled(j, 0.f);
-            top = fmaxf(top, fmaxf(y.x, y.y));
+            for (int j = 0; j < 32; ++j) {
+              const float2 y = scaled(j, v + 2 * j, nm);
+              top = fmaxf(top, fmaxf(y.x, y.y));
+              if (masked) {
+                if ((v[2 * j] & 0x7F800000u) == 0x7F800000u) bad[j >> 4] |= 1u << (2 * (j & 15));
+                if ((v[2 * j + 1] & 0x7F800000u) == 0x7F800000u) bad[j >> 4] |= 2u << (2 * (j & 15));
+              }
+            }
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                bad[k] = __reduce_or_sync(0xFFFFFFFFu, bad[k] & ~(uint32_t)(seen >> (32 * k)));
+                if (lane == 0 && bad[k]) red_or_cluster(flags + (c & 1) * 32 + k * 4, bad[k]);
+              }
+            }
           }
-          m = row_top(top);
-          weights();
-          soft_sync();  // top is read by all
-        } else {
-          weights();
-          if (soft_any(top > kLazy || (m == -INFINITY && top > -INFINITY))) {
-            // a row's maximum moves; the weights are taken again
+          if (pass == 1) {  // a row's maximum moves
             const float mx = row_top(top);
             float f = 1.f;
             if (mx > kLazy || (m == -INFINITY && mx > -INFINITY)) {
@@ -704,48 +724,63 @@ __global__ void __launch_bounds__(kThreads, 1)
               l2 = fma2(l2, ff, o);
               r2 = fma2(r2, ff, o);
             }
-            wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
-            tc_fence_after();
-            if ((st.i & (kRun - 1)) != 0 && __any_sync(0xFFFFFFFFu, f != 1.f)) {
+            if ((st.i & (kRun - 1)) != 0) {
+              wait_phase(X, X.p_free[3], (uint32_t)(c - 1) & 1);
+              tc_fence_after();
+              if (__any_sync(0xFFFFFFFFu, f != 1.f)) {
 #pragma unroll 1
-              for (int k = 0; k < 128; k += 16) {
-                uint32_t v[16];
-                tmem_ld16(tlane + 128 * half + k, v);
-                tmem_ld_wait();
+                for (int k = 0; k < 128; k += 16) {
+                  uint32_t v[16];
+                  tmem_ld16(tlane + 128 * half + k, v);
+                  tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-                tmem_st16(tlane + 128 * half + k, v);
+                  for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                  tmem_st16(tlane + 128 * half + k, v);
+                }
+                tmem_st_wait();
               }
-              tmem_st_wait();
             }
-            weights();
-            soft_sync();  // top is read by all
           }
+          weights();
+          if (pass == 1) {
+            soft_sync();  // top is read by all
+            break;
+          }
+          if (!soft_any(top > kLazy || (m == -INFINITY && top > -INFINITY))) break;
         }
         l2 = add2(l2, ls);
         r2 = add2(r2, rs);
       }
-      if (first && c > 0) {
-        // ---- the end of the segment before: its last products run while the weights above are taken ----
-        const ChunkSegment& t = X.seg[(seg - (have ? 2 : 1)) & 3];
-        const bool whole = t.whole != 0;
-        const int crow0 = t.row0 + (int)rank * 64, tok = crow0 / a.H;
-        const bool live = (int)rank * 64 + row < t.rows;
-        const int grow = live ? crow0 + row : t.row0, gtok = grow / a.H;
-        const int ntok = whole && a.inv_freq ? (crow0 + 63) / a.H - tok + 1 : 0;
-        float2 ang = make_float2(0.f, 0.f);
-        auto angle = [&](int k) {
-          float sn, cs;
-          sincosf(rope_angle(X.turn[k & 31], (uint64_t)(t.start + (tok + (k >> 5) - t.tok0))), &sn, &cs);
-          return make_float2(cs, sn);
-        };
-        if (tid < ntok * 32) ang = angle(tid);
+      // ---- the end of the segment before: O is read before the next products may start, and stored
+      // while they run ----
+      const ChunkSegment& e = X.seg[(seg - (have ? 2 : 1)) & 3];
+      // (what it needs of the record is read before the products start: the loader may then write it over)
+      const bool end = first && c > 0, store = end && e.whole;
+      const int wrow = (int)rank * 64 + 32 * (quad & 1);  // this warp's rows within the tile
+      // the output's rotation: lane i has the angles of pair i, of the first kTok tokens of this warp's rows
+      constexpr int kTok = 2;
+      float2 ang[kTok] = {};
+      int tok = 0, ntok = 0;
+      if (store && blk == 3 && a.inv_freq) {
+        tok = (e.row0 + wrow) / a.H;
+        ntok = (e.row0 + wrow + 31) / a.H - tok + 1;
+#pragma unroll
+        for (int k = 0; k < kTok; ++k)
+          if (k < ntok)
+            sincosf(rope_angle(X.turn[lane], (uint64_t)(e.start + (tok + k - e.tok0))), &ang[k].y, &ang[k].x);
+      }
+      if (c > 0) wait_phase(X, X.p_free[blk], (uint32_t)(c - 1) & 1);
+      if (have) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          st_shared16(p_s + blk * 8192 + sw128_off(row, k),
+                      make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]));
+      }
+      if (end) {
+        wait_phase(X, X.p_free[3], (uint32_t)(c - 1) & 1);
+        tc_fence_after();
         X.top[blk][row] = l_end.x + l_end.y;
         X.sum[blk][row] = r_end.x + r_end.y;
-        wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
-        tc_fence_after();
-        if (tid < ntok * 32) Y.rope[tid >> 5][tid & 31] = ang;
-        for (int k = tid + kSoft; k < ntok * 32; k += kSoft) Y.rope[k >> 5][k & 31] = angle(k);
         soft_sync();
         float l = 0.f, r = 0.f;
 #pragma unroll
@@ -753,141 +788,100 @@ __global__ void __launch_bounds__(kThreads, 1)
           l += X.top[k][row];
           r += X.sum[k][row];
         }
+        const bool live = (int)rank * 64 + row < e.rows;
         float fac = 0.f;
-        if (whole) {
-          const float logit = a.sink ? a.sink[grow - gtok * a.H] : -INFINITY, sink = sink_log2(logit);
-          const float M = fmaxf(m_end, sink), Mf = M == -INFINITY ? 0.f : M, e = ex2(m_end - Mf);
-          const float rows = l * e;
-          float z = rows, zr = r * e;
+        if (e.whole) {
+          const float sink = sink_log2(logit_end);
+          const float M = fmaxf(m_end, sink), Mf = M == -INFINITY ? 0.f : M, x = ex2(m_end - Mf);
+          const float rows = l * x;
+          float z = rows, zr = r * x;
           if (sink > -INFINITY) {
             z += ex2(sink - Mf);
             zr += ex2(sink - Mf);
           }
-          fac = zr > 0.f || zr != zr ? e / zr : 0.f;  // no row and no sink: zeros
-          if (a.lse && live && blk == 0) a.lse[grow] = head_lse(Mf, z, rows, logit);
+          fac = zr > 0.f || zr != zr ? x / zr : 0.f;  // no row and no sink: zeros
+          if (a.lse && live && blk == 0)
+            a.lse[e.row0 + (int)rank * 64 + row] = head_lse(Mf, z, rows, logit_end);
         } else if (blk == 0) {
-          float* to = a.pstat + ((int64_t)t.slot * 2 + rank) * 192 + row;
+          float* to = a.pstat + ((int64_t)e.slot * 2 + rank) * 192 + row;
           to[0] = m_end;
           to[64] = l;
           to[128] = r;
         }
+        __syncwarp();
         const float f0 = mslot_end == -INFINITY ? 0.f : ex2(mslot_end - m_end);
         const bool folded = mslot_end != -INFINITY;
-        const float2* rope = Y.rope[live ? gtok - tok : 0];
-        const uint32_t stage = p_s + warp * 2048;
-        float4* part = part_of(t.slot);
-        // where the coalesced stores of this warp go: rows 32 (quad % 2) + .. of this CTA
-        const int srow = (int)rank * 64 + 32 * (quad & 1);
-        uint16_t* out = a.out + (int64_t)(t.row0 + srow) * kDLat + kh * 128 + half * 64;
+        const int mytok = ntok ? (e.row0 + wrow + lane) / a.H - tok : 0;
+        // A lane has 32 columns of its row at a time; their 64 bytes go out as two whole sectors (stores of
+        // 16 bytes a row took prompts twice as long; through shared memory a tile's end took 2000 cycles more).
+        uint16_t* out = a.out + (int64_t)(e.row0 + (int)rank * 64 + row) * kDLat + kh * 128 + half * 64;
+        float4* to = part_of(e.slot);
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {  // 32 columns
-          const int hh = k >> 1, col = 32 * (k & 1);
+        for (int k = 0; k < 4; ++k, to += (k & 1 ? 8 : 24) * 128, out += k & 1 ? 32 : 224) {
           uint32_t v[32];
-          tmem_ld32(tlane + 128 * hh + 64 * half + col, v);
+          tmem_ld32(tlane + 128 * (k >> 1) + 64 * half + 32 * (k & 1), v);
           tmem_ld_wait();
-          if (folded) {
+          if (folded || !store) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float4 q = part[(hh * 32 + (col >> 2) + j) * 128];
-              v[4 * j] = __float_as_uint(fmaf(q.x, f0, __uint_as_float(v[4 * j])));
-              v[4 * j + 1] = __float_as_uint(fmaf(q.y, f0, __uint_as_float(v[4 * j + 1])));
-              v[4 * j + 2] = __float_as_uint(fmaf(q.z, f0, __uint_as_float(v[4 * j + 2])));
-              v[4 * j + 3] = __float_as_uint(fmaf(q.w, f0, __uint_as_float(v[4 * j + 3])));
+              float4 o = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                     __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+              if (folded) {
+                const float4 q = to[j * 128];
+                o.x = fmaf(q.x, f0, o.x);
+                o.y = fmaf(q.y, f0, o.y);
+                o.z = fmaf(q.z, f0, o.z);
+                o.w = fmaf(q.w, f0, o.w);
+              }
+              if (!store) to[j * 128] = o;
+              v[4 * j] = __float_as_uint(o.x);
+              v[4 * j + 1] = __float_as_uint(o.y);
+              v[4 * j + 2] = __float_as_uint(o.z);
+              v[4 * j + 3] = __float_as_uint(o.w);
+            }
+            if (!store) continue;
+          }
+          if (k >= 2) {  // pair 16 (k - 2) + j times e^{-i p theta}
+#pragma unroll 1
+            for (int n = 0; n < ntok; ++n) {
+              float2 an = n == 0 ? ang[0] : ang[1];
+              if (n >= kTok) sincosf(rope_angle(X.turn[lane], (uint64_t)(e.start + (tok + n - e.tok0))), &an.y, &an.x);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float cs = __shfl_sync(0xFFFFFFFFu, an.x, 16 * (k - 2) + j);
+                const float sn = __shfl_sync(0xFFFFFFFFu, an.y, 16 * (k - 2) + j);
+                const float y0 = __uint_as_float(v[2 * j]), y1 = __uint_as_float(v[2 * j + 1]);
+                if (mytok == n) {
+                  v[2 * j] = __float_as_uint(y0 * cs + y1 * sn);
+                  v[2 * j + 1] = __float_as_uint(y1 * cs - y0 * sn);
+                }
+              }
             }
           }
-          if (!whole) {
+          if (live) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              part[(hh * 32 + (col >> 2) + j) * 128] =
-                  make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                              __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-            continue;
-          }
-          const bool rot = ntok > 0 && hh == 1 && blk == 3;
-          uint32_t b[16];
+            for (int q = 0; q < 2; ++q) {
+              uint32_t b[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float y0 = __uint_as_float(v[2 * j]) * fac, y1 = __uint_as_float(v[2 * j + 1]) * fac;
-            if (rot) {  // times e^{-i p theta}
-              const float2 cs = rope[(col >> 1) + j];
-              const float z = y0 * cs.x + y1 * cs.y;
-              y1 = y1 * cs.x - y0 * cs.y;
-              y0 = z;
+              for (int j = 0; j < 8; ++j)
+                b[j] = pack_bf16x2(__uint_as_float(v[16 * q + 2 * j]) * fac, __uint_as_float(v[16 * q + 2 * j + 1]) * fac);
+              store_sector(out + 16 * q, b);
             }
-            b[j] = pack_bf16x2(y0, y1);
           }
-          // 32 rows of 64 bytes: chunk i of row r at i ^ (r / 2 % 4)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            st_shared16(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4),
-                        make_uint4(b[4 * j], b[4 * j + 1], b[4 * j + 2], b[4 * j + 3]));
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int rr = 8 * j + (lane >> 2);
-            const uint4 o = ld_shared16(stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-            if (srow + rr < t.rows)
-              __stcs(reinterpret_cast<uint4*>(out + (int64_t)rr * kDLat + hh * 256 + col) + (lane & 3), o);
-          }
-          __syncwarp();
+          __syncwarp();  // (what follows wants whole warps)
         }
+      }
+      if (have) {
+        fence_proxy_async_smem();
         tc_fence_before();
-        soft_sync();  // sums, angles and stages are read before P and the next sums are written
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_full);
       }
+      if (end) soft_sync();  // the sums are read before others are written
       if (!have) break;
-      if (!first) wait_phase(X, X.pv_done, (uint32_t)(c - 1) & 1);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        st_shared16(p_s + blk * 8192 + sw128_off(row, k),
-                    make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]));
-      if (masked) {
-        // the flags of both CTAs; the other buffer's were read before this tile's votes
-        if (tid < 8) X.flags[(nmask & 1) ^ 1][tid] = 0;
-        soft_sync();
-        if (lane == 0) {
-          mbar_arrive_cluster(dsmem_addr(smem_u32(&X.masked), rank));
-          mbar_arrive_cluster(peer_masked);
-        }
-        wait_phase<true>(X, X.masked, (uint32_t)nmask & 1);
-        uint32_t any = 0;
-        for (int k = 0; k < 8; ++k) any |= X.flags[nmask & 1][k];
-        if (any) {
-          mbar_wait(smem_u32(&X.step_full[(c + 1) & 3]), (uint32_t)((c + 1) >> 2) & 1, 60000000000ull);
-          const bool ahead = X.step[(c + 1) & 3].i >= 0;  // another key tile follows
-          if (rank == 0) {
-            // V(c) is revolution 2 c + 2, the last one 2 c + 1.  (The next tile's scores are complete
-            // once its keys, one revolution earlier, are.)
-            if (ahead) wait_phase(X, X.s_full[(c + 1) & 1], (uint32_t)((c + 1) >> 1) & 1);
-            for (int k = 0; k < kSlots; ++k) wait_phase(X, X.full[k], ahead ? 0u : 1u);
-            if (tid == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&X.landed), 1));
-          } else {
-            wait_phase<true>(X, X.landed, (uint32_t)nland & 1);
-          }
-          ++nland;
-          // row r's values: slots (r / 64, 0) and (r / 64, 1), group r % 64 / 8, two blocks of 64 dims
-          for (int r = warp; r < kKeys; r += kSoftWarps) {
-            if (!(X.flags[nmask & 1][r >> 5] >> (r & 31) & 1u)) continue;
-            const uint32_t at = ring + (uint32_t)((r >> 6) * 2 + (lane >> 4)) * kSlotBytes + ((r & 63) >> 3) * 2048 +
-                                ((lane >> 3) & 1) * 1024 + (r & 7) * 128 + (lane & 7) * 16;
-            uint4 v = ld_shared16(at);
-            uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((e[k] & 0x7F80u) == 0x7F80u) e[k] &= 0xFFFF0000u;
-              if ((e[k] & 0x7F800000u) == 0x7F800000u) e[k] &= 0x0000FFFFu;
-            }
-            st_shared16(at, v);
-          }
-        }
-        ++nmask;
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(p_full);
-      if (!st.last && ((st.i + 1) & (kRun - 1)) == 0) {
+      if (!(st.kind & kStepLast) && ((st.i + 1) & (kRun - 1)) == 0) {
         // a run's end: O joins what the part holds
-        wait_phase(X, X.pv_done, (uint32_t)c & 1);
+        wait_phase(X, X.p_free[3], (uint32_t)c & 1);
         tc_fence_after();
         const float f = mslot == -INFINITY ? 0.f : ex2(mslot - m);
         const bool onto = st.i + 1 > kRun;
@@ -913,43 +907,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
       }
     }
+    if (tid == 0) *reinterpret_cast<volatile int*>(&X.done) = 1;
   } else if (work && warp == kWarpMma && rank == 0) {
     // ================= products =================
-    // (loops over slots stay rolled: unrolled, their instructions crowd out the softmax', and 2048 tokens
-    // over 32768 rows take 6.0 ms in place of 5.1)
     const uint32_t lead = elect_lane();
     const uint32_t id_s = idesc_bf16(128, 256, 0, 0), id_o = idesc_bf16(128, 256, 0, 1);
     const uint64_t q_d = sdesc_sw128(q_s, 16, 1024), p_d = sdesc_sw128(p_s, 16, 1024);
     const uint64_t k_d = sdesc_sw128(ring, 16, 1024), v_d = sdesc_sw128(ring, 1024, 2048);
     bool ok = true;
     int rev = 0;
-    auto values = [&](int c, int run) {  // of key tile c of this pair, the run's run-th
-      ok = ok && all_ok(wait_phase<true>(X, X.p_full, (uint32_t)c & 1));
-      if (!ok) return;
-      tc_fence_after();
+    int cleaned = 0;
+    // The values of key tile c of this pair, the run's run-th.
+    auto values = [&](int c, int run, bool masked) {
+      if (masked) {  // every row is flagged that is to be
 #pragma unroll 1
-      for (int k = 0; k < kSlots; ++k) {
-        ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
-        if (!ok) return;
-        tc_fence_after();
-        if (lead) {
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            umma_pair_bf16(tmem + 128 * (k & 1), p_d + (((k >> 1) * 8192 + s * 32) >> 4),
-                           v_d + ((k * kSlotBytes + s * 4096) >> 4), id_o, run > 0 || k > 1 || s > 0);
-          umma_commit_pair(smem_u32(&X.empty[k]));
+        for (int k = 0; k < 4; ++k) ok = ok && all_ok(wait_phase<true>(X, X.p_full[k], (uint32_t)c & 1));
+        const uint32_t bad = lane < 8 && ok ? X.flags[c & 1][lane] : 0u;
+        if (__any_sync(0xFFFFFFFFu, bad != 0u)) {
+          // rows to be cleaned, by a warp of each CTA, once all of the tile's values are there
+#pragma unroll 1
+          for (int k = 0; k < kSlots; ++k) ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
+          if (lane < 8) {
+            X.flags[c & 1][lane] = 0u;
+            X.clean[lane] = bad;
+            st_cluster32(dsmem_addr(smem_u32(&X.clean[lane]), 1), bad);
+          }
+          __syncwarp();
+          if (lane < 2) mbar_arrive_cluster(dsmem_addr(smem_u32(&X.clean_req), lane));
+          ok = ok && all_ok(wait_phase<true>(X, X.clean_done, (uint32_t)cleaned & 1));
+          ++cleaned;
         }
-        __syncwarp();
       }
-      if (lead) umma_commit_pair(smem_u32(&X.pv_done));
-      __syncwarp();
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        ok = ok && all_ok(wait_phase<true>(X, X.p_full[b], (uint32_t)c & 1));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && all_ok(wait_phase(X, X.full[2 * b + h], (uint32_t)rev & 1));
+          if (!ok) return;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              umma_pair_bf16(tmem + 128 * h, p_d + ((b * 8192 + s * 32) >> 4),
+                             v_d + (((2 * b + h) * kSlotBytes + s * 4096) >> 4), id_o, run > 0 || b > 0 || s > 0);
+            umma_commit_pair(smem_u32(&X.empty[2 * b + h]));
+            if (h == 1) umma_commit_pair(smem_u32(&X.p_free[b]));
+          }
+          __syncwarp();
+        }
+      }
       ++rev;
     };
     int c = 0, seg = 0, run = 0;
-    while (ok) {
-      ok = all_ok(wait_phase(X, X.step_full[c & 3], (uint32_t)(c >> 2) & 1));
-      const int i = uniform(X.step[c & 3].i), last = uniform(X.step[c & 3].last);
-      if (!ok || i < 0) break;
+    bool masked = false;
+    // What key tile c is, read while the products of the one before are under way.
+    int i = 0, kind = 0;
+    auto step = [&]() {
+      ok = ok && all_ok(wait_phase(X, X.step_full[c & 3], (uint32_t)(c >> 2) & 1));
+      i = ok ? uniform(X.step[c & 3].i) : -1;
+      kind = uniform(X.step[c & 3].kind);
+    };
+    step();
+    while (i >= 0) {
       if (i == 0) {
         ok = all_ok(wait_phase(X, X.q_full, (uint32_t)seg & 1));
         ++seg;
@@ -971,20 +991,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (lead) {
         umma_commit_pair(smem_u32(&X.s_full[c & 1]));
-        if (last) umma_commit_pair(smem_u32(&X.q_empty));
+        if (kind & kStepLast) umma_commit_pair(smem_u32(&X.q_empty));
       }
       __syncwarp();
       ++rev;
-      if (c > 0) values(c - 1, run);
+      if (c > 0) values(c - 1, run, masked);
       run = i & (kRun - 1);
+      masked = (kind & kStepMasked) != 0;
       ++c;
+      step();
     }
-    if (ok) values(c - 1, run);
+    if (ok) values(c - 1, run, masked);
     // no product may still be running when the tensor memory is released, whatever happened above
     if (lead) umma_commit_pair(smem_u32(&X.fin));
     __syncwarp();
     mbar_wait(smem_u32(&X.fin), 0, 100000000ull);
-  } else if (work && warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
+  } else if (work && warp == kWarpClean) {
+    // ================= values that must not be read =================
+    for (uint32_t n = 0;;) {
+      // (a try_wait may sleep for microseconds, which would hold up the kernel's end)
+      if (!mbar_test_wait(smem_u32(&X.clean_req), n & 1)) {
+        if (*reinterpret_cast<volatile int*>(&X.done)) break;
+        __nanosleep(200);
+        continue;
+      }
+      mbar_try_wait_cluster(smem_u32(&X.clean_req), n & 1);  // (complete: for what the request brings)
+      // row r's values: slots (r / 64, 0) and (r / 64, 1), group r % 64 / 8, two blocks of 64 dims
+      for (int r = 0; r < kKeys; ++r) {
+        if (!(X.clean[r >> 5] >> (r & 31) & 1u)) continue;
+        const uint32_t at = ring + (uint32_t)((r >> 6) * 2 + (lane >> 4)) * kSlotBytes + ((r & 63) >> 3) * 2048 +
+                            ((lane >> 3) & 1) * 1024 + (r & 7) * 128 + (lane & 7) * 16;
+        uint4 v = ld_shared16(at);
+        uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if ((x[k] & 0x7F80u) == 0x7F80u) x[k] &= 0xFFFF0000u;
+          if ((x[k] & 0x7F800000u) == 0x7F800000u) x[k] &= 0x0000FFFFu;
+        }
+        st_shared16(at, v);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(dsmem_addr(smem_u32(&X.clean_done), 0));
+      ++n;
+    }
+  } else if (work && warp >= kWarpLoad) {
     // ================= loads =================
     const uint64_t pol = policy_evict_normal();
     const int k0 = warp - kWarpLoad;  // this warp's slots: k0, k0 + kLoadWarps, ..
@@ -1049,7 +1100,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t groups = __ballot_sync(0xFFFFFFFFu, cur.good);
         if (lane == 0) {
-          X.step[c & 3] = ChunkStep{groups, (w.t.k0 + w.unit + w.i) * kKeys, w.i, w.i + 1 == w.n};
+          const int at = (w.t.k0 + w.unit + w.i) * kKeys;
+          X.step[c & 3] = ChunkStep{groups, at, w.i,
+                                    (w.i + 1 == w.n ? kStepLast : 0) |
+                                        (at < lo1 || at + kKeys > hi0 || ~groups ? kStepMasked : 0)};
           mbar_arrive(smem_u32(&X.step_full[c & 3]));
         }
       }
@@ -1067,6 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok) slots(last, &vmap, true);
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   cluster_sync();

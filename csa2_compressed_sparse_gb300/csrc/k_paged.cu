@@ -478,11 +478,6 @@ __device__ __forceinline__ void join_add(float (&acc)[8], const float4& x, const
   acc[7] = fmaf(y.w, w.w, acc[7]);
 }
 
-// A 32-bit store into shared memory of a CTA of the cluster.
-__device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
-}
-
 // A head's running maximum and sums over the parts of the softmax warps.
 struct HeadSums {
   float m, l, r;  // maximum; sums of P, unrounded and rounded

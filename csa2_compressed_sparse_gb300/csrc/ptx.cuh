@@ -418,6 +418,11 @@ __device__ __forceinline__ void st_cluster16(uint32_t dst, uint4 v) {
                : "memory");
 }
 
+// A 32-bit store into shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster32(uint32_t dst, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
