@@ -583,16 +583,20 @@ def _heads(name, x, out, norm, norm_w, T, D, dev):
         if out is not None or norm_w is not None:
             raise ValueError(f"csa2: {name} is missing")
         return None
-    H = x.shape[1] if x.dim() == 3 else 0
-    for what, t in ((name, x), (f"{name}_out", out)):
-        if (t is None or t.dtype is not torch.bfloat16 or t.get_device() != dev or
-                t.shape != (T, H, D) or (t.numel() > 0 and t.stride(2) != 1)):
-            raise ValueError(f"csa2: {what} must be [{T}, H, {D}] bf16 with dense heads on cuda:{dev}")
-    head = [t.stride(1) if H > 1 else 0 for t in (x, out)]
-    token = [t.stride(0) if T > 1 else 0 for t in (x, out)]
-    return ctypes.byref(_HeadsC(x.data_ptr(), out.data_ptr(), token[0], head[0], token[1], head[1], H,
-                                1 if norm else 0,
-                                _arg(f"{name}_norm_w", norm_w, torch.float32, (D,), dev)))
+    shape = x.shape
+    H = shape[1] if len(shape) == 3 else 0
+    want = (T, H, D)
+    if (out is None or shape != want or out.shape != want or x.dtype is not torch.bfloat16 or
+            out.dtype is not torch.bfloat16 or x.get_device() != dev or out.get_device() != dev):
+        raise ValueError(f"csa2: {name} and {name}_out must be [{T}, H, {D}] bf16 on cuda:{dev}")
+    xs, os_ = x.stride(), out.stride()
+    if (xs[2] != 1 or os_[2] != 1) and T > 0 and H > 0 and D > 1:
+        raise ValueError(f"csa2: {name} and {name}_out must have dense heads")
+    return ctypes.byref(_HeadsC(x.data_ptr(), out.data_ptr(), xs[0] if T > 1 else 0,
+                                xs[1] if H > 1 else 0, os_[0] if T > 1 else 0, os_[1] if H > 1 else 0,
+                                H, 1 if norm else 0,
+                                _arg(f"{name}_norm_w", norm_w, torch.float32, (D,), dev)
+                                if norm_w is not None else None))
 
 
 def csa2_qk_norm_rope(q, q_out, pos, inv_freq, k=None, k_out=None, q_norm=True, k_norm=True,
@@ -601,13 +605,14 @@ def csa2_qk_norm_rope(q, q_out, pos, inv_freq, k=None, k_out=None, q_norm=True, 
     """RMSNorm of each head of q [T, H, D] and k [T, K, D] (k: optional), then the rotation of their
     positions pos [T] by inv_freq [n] in 2 n dims from rope_dim0 on (None: the last ones); inv_freq
     None is the norm alone.  Outputs may be the inputs."""
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("csa2: q must be [T, H, D]")
-    T, _, D = q.shape
+    T, _, D = shape
     dev = q.get_device()
     if dev < 0:
         raise ValueError("csa2: tensors must live on the GPU")
-    n = 0 if inv_freq is None else inv_freq.numel()
+    n = 0 if inv_freq is None else inv_freq.shape[0]
     if rope_dim0 is None:
         rope_dim0 = max(0, D - 2 * n)
     _call(lib().csa2_qk_norm_rope, dev, stream, _heads("q", q, q_out, q_norm, q_norm_w, T, D, dev),

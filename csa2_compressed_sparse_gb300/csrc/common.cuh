@@ -284,7 +284,7 @@ struct HeadsArgs {
   const float* inv_freq;  // [rope_dims / 2]
   int rope_dim0, rope_dims, halves;
   float factor;
-  int rows;               // heads of an item
+  int units;              // units of rows of an item
 };
 
 cudaError_t launch_compress(const CompressArgs& a, cudaStream_t s);

@@ -12,142 +12,150 @@ namespace {
 
 // ================================ read ==================================================
 //
-// The inverse of paged_append_kernel, laid out as it is: a warp per row, kTok rows at a time; a lane
-// holds the chunks `lane` (dims 8 l ..) and, below lane 24, 32 + lane (dims 256 + 8 l ..), and the
-// rotation pair 448 + 2 l, 449 + 2 l.  x = code * scale in fp32, rounded once to bf16 (exact for
-// FP8_E8M0 scales of 2^-124 to 2^119).  Bound by the bytes moved: 1024 or 528 read, 1024 written per row.
+// The inverse of paged_append_kernel.  A warp takes runs of 32 rows: first each lane finds where one of
+// them lies, then the rows are loaded kTok at a time, the next ones before these are written.  An FP8 lane
+// has dims 16 l .. of a row, one 16-byte load and two 16-byte stores; a bf16 lane the chunks l and 32 + l of
+// eight dims.  Lane i has the angle of rotation pair i, which the lanes of dims 448.. fetch.  x = code *
+// scale in fp32, rounded once to bf16 (exact for FP8_E8M0 scales of 2^-124 to 2^119).  Bound by the
+// bytes moved: 1024 or 528 read, 1024 written per row.
 
-constexpr int kReadWarps = 8;
-constexpr int kReadCtas = 6;
+constexpr int kReadWarps = 4;
 
 __device__ __forceinline__ float2 e4m3x2(uint32_t two) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
-// Eight codes times a scale, to bf16.
-__device__ __forceinline__ uint4 decode8(uint2 c, float s) {
-  uint32_t r[4];
-  const uint32_t w[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 v = e4m3x2(w[i]);
-    r[i] = pack_bf16x2(v.x * s, v.y * s);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
 __device__ __forceinline__ float e8m0_scale(uint32_t e) {  // 2^(e - 127); 255 is NaN
   return e == 0 ? __uint_as_float(0x00400000u) : e == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(e << 23);
 }
+__device__ __forceinline__ void turn_back(float& x0, float& x1, float c, float s) {  // times e^{-i p theta}
+  const float y = x0 * c + x1 * s;
+  x1 = x1 * c - x0 * s;
+  x0 = y;
+}
 
-template <int kTok>
-__global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadArgs a) {
+// What a lane loads of a row, and the row written from it.
+template <int kMode>
+struct RowPart {
+  uint4 a, b;   // bf16: two chunks; FP8: sixteen codes in a
+  uint32_t sc;  // FP8: the scale
+
+  __device__ __forceinline__ void load(const uint8_t* src, int lane) {
+    a = __ldcs(reinterpret_cast<const uint4*>(src) + lane);
+    if (kMode == 0) b = __ldcs(reinterpret_cast<const uint4*>(src) + 32 + lane);
+    if (kMode == 1) sc = __ldcs(reinterpret_cast<const uint32_t*>(src + 512) + (lane >> 3));
+    if (kMode == 2) sc = __ldcs(src + 512 + (lane >> 1));
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); sc = 0u; }
+  __device__ __forceinline__ void store(uint16_t* dst, int lane, bool back, float c, float s) const {
+    if (kMode == 0) {
+      uint4 w = b;
+      if (back) {
+        float y[8];
+        unpack_bf16x8(b, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float ci = __shfl_sync(0xFFFFFFFFu, c, 4 * (lane - 24) + i);
+          const float si = __shfl_sync(0xFFFFFFFFu, s, 4 * (lane - 24) + i);
+          turn_back(y[2 * i], y[2 * i + 1], ci, si);
+        }
+        if (lane >= 24)
+          w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                         pack_bf16x2(y[6], y[7]));
+      }
+      __stcs(reinterpret_cast<uint4*>(dst) + lane, a);
+      __stcs(reinterpret_cast<uint4*>(dst) + 32 + lane, w);
+    } else {
+      const float scale = kMode == 1 ? __uint_as_float(sc) : e8m0_scale(sc);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 y = e4m3x2(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
+        y.x *= scale;
+        y.y *= scale;
+        if (back) {
+          const float ci = __shfl_sync(0xFFFFFFFFu, c, 8 * (lane - 28) + i);
+          const float si = __shfl_sync(0xFFFFFFFFu, s, 8 * (lane - 28) + i);
+          if (lane >= 28) turn_back(y.x, y.y, ci, si);
+        }
+        o[i] = pack_bf16x2(y.x, y.y);
+      }
+      __stcs(reinterpret_cast<uint4*>(dst) + 2 * lane, make_uint4(o[0], o[1], o[2], o[3]));
+      __stcs(reinterpret_cast<uint4*>(dst) + 2 * lane + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    }
+  }
+};
+
+template <int kMode, int kTok>
+__global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadArgs a, int run) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * kReadWarps * kTok;
+  const int64_t step = (int64_t)gridDim.x * kReadWarps * run;
   const uint64_t turn = a.inv_freq ? rope_turn(a.inv_freq[lane]) : 0;
   const int64_t total = min((int64_t)a.T, (int64_t)a.cu_seqlens[a.cache.B]);
-  for (int64_t t = ((int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * kTok; t < total; t += step) {
-    // where the rows are
-    const uint8_t* src[kTok];
-    int64_t j[kTok];
-    bool zero[kTok];
-    int b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t, lane);
-    int64_t t0 = a.cu_seqlens[b], t1 = a.cu_seqlens[b + 1], first = a.start_row[b];
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      src[i] = nullptr;
-      zero[i] = false;
-      if (t + i >= total) continue;
-      if (i > 0 && t + i >= t1) {  // on to the row's sequence
-        b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t + i, lane);
-        t0 = a.cu_seqlens[b];
-        t1 = a.cu_seqlens[b + 1];
-        first = a.start_row[b];
-      }
-      j[i] = first + (t + i - t0);
-      zero[i] = a.row_end != nullptr;
-      if (a.row_end && j[i] >= a.row_end[b]) continue;
-      int32_t page = -1, row = 0;
-      if (j[i] >= 0 && j[i] < a.cap_rows) {
-        const int32_t lp = (int32_t)(__umulhi((uint32_t)j[i], a.page_mul) >> a.page_shift);
-        row = (int32_t)j[i] - lp * a.cache.page_rows;
-        page = a.cache.table[(int64_t)b * a.cache.table_ld + lp];
-      }
-      if (page < 0 || page >= a.cache.n_pages) {
-        if (lane == 0) raise_fault(kFaultBounds);
-        continue;
-      }
-      src[i] = a.cache.data + (int64_t)page * a.cache.page_stride +
-               (int64_t)row * (a.cache.dtype == 0 ? 1024 : 528);
-    }
-    uint4 c0[kTok], c1[kTok];
-    float x0[kTok], x1[kTok];
-    if (a.cache.dtype == 0) {
-      uint32_t pr[kTok];
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (!src[i]) continue;
-        c0[i] = __ldcs(reinterpret_cast<const uint4*>(src[i]) + lane);
-        if (lane < 24) c1[i] = __ldcs(reinterpret_cast<const uint4*>(src[i]) + 32 + lane);
-        pr[i] = __ldcs(reinterpret_cast<const uint32_t*>(src[i] + 2 * kRopeDim0) + lane);
-      }
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        x0[i] = __uint_as_float(pr[i] << 16);
-        x1[i] = __uint_as_float(pr[i] & 0xFFFF0000u);
-      }
-    } else {
-      uint2 d0[kTok], d1[kTok];
-      uint32_t pr[kTok];
-      float s0[kTok], s1[kTok], sr[kTok];
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (!src[i]) continue;
-        d0[i] = __ldcs(reinterpret_cast<const uint2*>(src[i]) + lane);
-        if (lane < 24) d1[i] = __ldcs(reinterpret_cast<const uint2*>(src[i] + 256) + lane);
-        pr[i] = __ldcs(reinterpret_cast<const uint16_t*>(src[i] + kRopeDim0) + lane);
-        if (a.cache.dtype == 1) {
-          const float* sc = reinterpret_cast<const float*>(src[i] + 512);
-          s0[i] = sc[lane >> 4];
-          s1[i] = sc[2 + (lane >> 4)];
-          sr[i] = sc[3];
-        } else {
-          const uint8_t* sc = src[i] + 512;
-          s0[i] = e8m0_scale(sc[lane >> 2]);
-          s1[i] = e8m0_scale(sc[8 + (lane >> 2)]);
-          sr[i] = e8m0_scale(sc[14 + (lane >> 4)]);
+  for (int64_t t = ((int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * run; t < total; t += step) {
+    // lane l: row t + l
+    const int n = (int)min(total - t, (int64_t)run);
+    const uint8_t* src = nullptr;
+    int64_t j = 0;
+    bool zero = false;
+    {
+      const int64_t tl = t + min(lane, n - 1);
+      int b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t, lane);
+      if (a.cu_seqlens[b + 1] <= tl) {  // in a later sequence
+        int hi = a.cache.B - 1;
+        for (++b; b < hi;) {
+          const int m = (b + hi + 1) >> 1;
+          if (a.cu_seqlens[m] <= tl) b = m;
+          else hi = m - 1;
         }
       }
-#pragma unroll
-      for (int i = 0; i < kTok; ++i) {
-        if (!src[i]) continue;
-        c0[i] = decode8(d0[i], s0[i]);
-        if (lane < 24) c1[i] = decode8(d1[i], s1[i]);
-        const float2 v = e4m3x2(pr[i]);
-        x0[i] = v.x * sr[i];
-        x1[i] = v.y * sr[i];
+      j = a.start_row[b] + (tl - a.cu_seqlens[b]);
+      zero = a.row_end != nullptr;
+      if (!zero || j < a.row_end[b]) {
+        int32_t page = -1, row = 0;
+        if (j >= 0 && j < a.cap_rows) {
+          const int32_t lp = (int32_t)(__umulhi((uint32_t)j, a.page_mul) >> a.page_shift);
+          row = (int32_t)j - lp * a.cache.page_rows;
+          page = a.cache.table[(int64_t)b * a.cache.table_ld + lp];
+        }
+        if (page < 0 || page >= a.cache.n_pages) {
+          if (lane < n) raise_fault(kFaultBounds);
+        } else {
+          src = a.cache.data + (int64_t)page * a.cache.page_stride + (int64_t)row * (kMode == 0 ? 1024 : 528);
+        }
       }
     }
+    __syncwarp();
+    const uint64_t p = (uint64_t)j * (uint64_t)a.ratio;
+    const bool skip = !src && !zero;  // the row of out is left as it is
+    RowPart<kMode> cur[kTok], nxt[kTok];
+    auto fetch = [&](RowPart<kMode>(&r)[kTok], int i0) {
 #pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      if (!src[i]) {
-        if (!zero[i]) continue;
-        c0[i] = c1[i] = make_uint4(0u, 0u, 0u, 0u);
-        x0[i] = x1[i] = 0.f;
+      for (int i = 0; i < kTok; ++i) {
+        const uint64_t at = __shfl_sync(0xFFFFFFFFu, (unsigned long long)src, (i0 + i) & 31);
+        if (at && i0 + i < n) r[i].load(reinterpret_cast<const uint8_t*>(at), lane);
+        else r[i].zero();
       }
-      if (a.inv_freq) {  // times e^{-i p theta}
-        float s, c;
-        sincosf(rope_angle(turn, (uint64_t)j[i] * (uint64_t)a.ratio), &s, &c);
-        const float y0 = x0[i] * c + x1[i] * s;
-        x1[i] = x1[i] * c - x0[i] * s;
-        x0[i] = y0;
+    };
+    fetch(cur, 0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kTok) {
+      if (i0 + kTok < n) fetch(nxt, i0 + kTok);
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) {
+        const uint64_t pi = __shfl_sync(0xFFFFFFFFu, (unsigned long long)p, (i0 + i) & 31);
+        const bool none = __shfl_sync(0xFFFFFFFFu, (int)skip, (i0 + i) & 31) != 0;
+        if (none || i0 + i >= n) continue;  // (the same in the warp)
+        float s = 0.f, c = 1.f;
+        if (a.inv_freq) sincosf(rope_angle(turn, pi), &s, &c);
+        cur[i].store(a.out + (t + i0 + i) * a.out_ld, lane, a.inv_freq != nullptr, c, s);
       }
-      uint16_t* dst = a.out + (t + i) * a.out_ld;
-      *(reinterpret_cast<uint4*>(dst) + lane) = c0[i];
-      if (lane < 24) *(reinterpret_cast<uint4*>(dst) + 32 + lane) = c1[i];
-      *(reinterpret_cast<uint32_t*>(dst + kRopeDim0) + lane) = pack_bf16x2(x0[i], x1[i]);
+#pragma unroll
+      for (int i = 0; i < kTok; ++i) cur[i] = nxt[i];
     }
   }
 }
@@ -1235,15 +1243,26 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
 }
 }  // namespace
 
+namespace {
+
+template <int kMode>
+cudaError_t launch_read(const PagedReadArgs& a, int sms, cudaStream_t s) {
+  // Runs of 32 rows a warp, shorter ones where those would leave SMs without work.
+  int run = 32;
+  while (run > 1 && (int64_t)a.T < (int64_t)sms * 16 * run) run >>= 1;
+  const int64_t need = ((int64_t)a.T + kReadWarps * run - 1) / (kReadWarps * run), most = (int64_t)sms * 32;
+  const dim3 grid((unsigned)(need < most ? need : most));
+  return run >= 4 ? launch_pdl(paged_read_kernel<kMode, 4>, grid, dim3(kReadWarps * 32), 0, s, a, run)
+                  : launch_pdl(paged_read_kernel<kMode, 1>, grid, dim3(kReadWarps * 32), 0, s, a, run);
+}
+
+}  // namespace
+
 cudaError_t launch_paged_read(const PagedReadArgs& a, int sms, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  if (a.T >= 8 * kReadWarps * sms) {
-    const int64_t need = (a.T + 4 * kReadWarps - 1) / (4 * kReadWarps), most = (int64_t)sms * kReadCtas;
-    return launch_pdl(paged_read_kernel<4>, dim3((unsigned)(need < most ? need : most)),
-                      dim3(kReadWarps * 32), 0, s, a);
-  }
-  return launch_pdl(paged_read_kernel<1>, dim3((unsigned)((a.T + kReadWarps - 1) / kReadWarps)),
-                    dim3(kReadWarps * 32), 0, s, a);
+  return a.cache.dtype == 0   ? launch_read<0>(a, sms, s)
+         : a.cache.dtype == 1 ? launch_read<1>(a, sms, s)
+                              : launch_read<2>(a, sms, s);
 }
 
 int chunk_max_pairs() { return kMaxPairs; }

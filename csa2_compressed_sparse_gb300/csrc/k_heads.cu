@@ -5,9 +5,11 @@
 // rotated, pair i by the angle p theta_i (the phase exact, as in the compressor) and scaled by
 // `factor`, rounded once to bf16.  Pairs are neighbours (2 i, 2 i + 1) or halves (i, i + R / 2).
 //
-// A group of kG lanes has a row, a lane kC 16-byte chunks of it (chunk lane + 32 c), so a warp
-// reads whole rows in order; kU rows a lane are loaded at once.  The angles of a lane's dims are
-// computed once per item, which is a token and up to `rows` of its heads.
+// A group of kG lanes has a row, a lane kC 16-byte chunks of it (chunk lane + 32 c), so a warp reads
+// whole rows in order.  A warp takes an item, a token's rows or a run of them, a row a lane at a time,
+// the next one loaded before this is written; the token's angles it computes once, through shared
+// memory.  Angular steps (64-bit floating point, of which an SM does two a cycle) are computed once a CTA.
+// Bound by the bytes moved.
 #include "common.cuh"
 #include "compress_dev.cuh"
 
@@ -15,20 +17,34 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kMaxPairs = 256;
 
-template <int kG, int kC, bool kHalf, int kU>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(HeadsArgs a) {
+// Two bf16 values in fp32, and back.
+__device__ __forceinline__ float2 wide2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// CTAs of an SM: halves of wide heads take more registers
+template <int kC, bool kHalf>
+constexpr int kCtas = kHalf && kC == 2 ? 2 : 4;
+
+template <int kG, int kC, bool kHalf>
+__global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf>) qk_norm_rope_kernel(HeadsArgs a) {
+  __shared__ uint64_t turn_s[kMaxPairs];
+  __shared__ __align__(16) float cs_s[kWarps][kMaxPairs], sn_s[kWarps][kMaxPairs];
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kRows = 32 / kG;          // rows side by side in a warp
-  constexpr int kPairs = kHalf ? 8 : 4;   // angles of a chunk
-  const int lane = threadIdx.x & 31, sub = lane / kG, l = lane % kG;
+  constexpr int kRows = 32 / kG;  // rows of a unit
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane / kG, l = lane % kG;
   const int half = a.rope_dims >> 1;
-  // a lane's chunks: first dim, whether it exists, whether it is rotated, and its pairs' steps
-  int dim[kC], mate[kC];
+  const float inv_d = 1.f / (float)a.D;
+  if (tid < half) turn_s[tid] = rope_turn(a.inv_freq[tid]);
+  __syncthreads();
+  // a lane's chunks: first dim, whether it exists, whether it is rotated, its pairs
+  int dim[kC], mate[kC], pair[kC];
   bool have[kC], rot[kC];
   float sign[kC];
-  uint64_t turn[kC][kPairs];
 #pragma unroll
   for (int c = 0; c < kC; ++c) {
     dim[c] = 8 * (l + 32 * c);
@@ -38,91 +54,110 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(HeadsArgs a) 
     // halves: the chunk with the other dims of the pairs; -x1 s for the first, + x0 s for the second
     mate[c] = dim[c] + (e < half ? half : -half);
     sign[c] = e < half ? -1.f : 1.f;
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i)
-      turn[c][i] = rot[c] ? rope_turn(a.inv_freq[kHalf ? (e < half ? e : e - half) + i : e / 2 + i]) : 0;
+    pair[c] = rot[c] ? (kHalf ? (e < half ? e : e - half) : e / 2) : 0;
   }
-  const int64_t nq = (a.q.H + a.rows - 1) / a.rows, nk = (a.k.H + a.rows - 1) / a.rows;
-  const int64_t items = (nq + nk) * a.T, step = (int64_t)gridDim.x * kWarps;
-  for (int64_t it = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t t = it / (nq + nk);
-    int64_t blk = it - t * (nq + nk);
-    const HeadSet& s = blk < nq ? a.q : a.k;
-    if (blk >= nq) blk -= nq;
-    const int h0 = (int)blk * a.rows, h1 = min(s.H, h0 + a.rows);
-    const uint16_t* x = s.x + t * s.x_token;
-    uint16_t* out = s.out + t * s.out_token;
-    const uint64_t p = a.rope_dims > 0 ? (uint64_t)a.pos[t] : 0;
-    float cs[kC][kPairs], sn[kC][kPairs], w[kC][8], wm[kC][8];
+  const int nq = (a.q.H + kRows - 1) / kRows, nk = (a.k.H + kRows - 1) / kRows;
+  const int blocks = (nq + nk + a.units - 1) / a.units;
+  const int64_t items = (int64_t)a.T * blocks, step = (int64_t)gridDim.x * kWarps;
+  for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items; it += step) {
+    const int64_t t = it / blocks;
+    const int u0 = (int)(it - t * blocks) * a.units, u1 = min(nq + nk, u0 + a.units);
+    uint4 v[kC], m[kHalf ? kC : 1], vn[kC], mn[kHalf ? kC : 1];
+    auto fetch = [&](int u, uint4(&x)[kC], uint4(&y)[kHalf ? kC : 1]) {
+      const bool q = u < nq;
+      const HeadSet& s = q ? a.q : a.k;
+      const int r = (q ? u : u - nq) * kRows + sub;
+      const uint16_t* src = s.x + t * s.x_token + r * s.x_head;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[c][i] = wm[c][i] = 1.f;
-      if (have[c] && s.norm_w) cdev::load8_f32(s.norm_w + dim[c], w[c]);
-      if (!rot[c]) continue;
-      if (kHalf && s.norm_w) cdev::load8_f32(s.norm_w + mate[c], wm[c]);
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        sincosf(rope_angle(turn[c][i], p), &sn[c][i], &cs[c][i]);
-        cs[c][i] *= a.factor;
-        sn[c][i] *= a.factor;
+      for (int c = 0; c < kC; ++c) {
+        x[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < s.H && have[c]) x[c] = __ldcs(reinterpret_cast<const uint4*>(src + dim[c]));
+        if (kHalf && r < s.H && rot[c]) y[kHalf ? c : 0] = *reinterpret_cast<const uint4*>(src + mate[c]);
       }
+    };
+    fetch(u0, v, m);
+    if (half > 0) {
+      const uint64_t p = (uint64_t)a.pos[t];
+      __syncwarp();  // the last token's angles are read
+      for (int i = lane; i < half; i += 32) {
+        float s, c;
+        sincosf(rope_angle(turn_s[i], p), &s, &c);
+        cs_s[warp][i] = c * a.factor;
+        sn_s[warp][i] = s * a.factor;
+      }
+      __syncwarp();
     }
-    for (int h = h0; h < h1; h += kRows * kU) {
-      uint4 v[kU][kC], m[kU][kHalf ? kC : 1];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int r = h + u * kRows + sub;
+    float2 w[kC][4], wm[kHalf ? kC : 1][4];  // the set's weights, of the lane's dims and their mates
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) {
+      const bool q = u < nq;
+      const HeadSet& s = q ? a.q : a.k;
+      const int r = (q ? u : u - nq) * kRows + sub;
+      uint16_t* out = s.out + t * s.out_token + r * s.out_head;
+      if (u + 1 < u1) fetch(u + 1, vn, mn);
+      if (u == u0 || u == nq) {
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-          v[u][c] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < h1 && have[c])
-            v[u][c] = __ldcs(reinterpret_cast<const uint4*>(x + r * s.x_head + dim[c]));
-          if (kHalf && r < h1 && rot[c])
-            m[u][c] = *reinterpret_cast<const uint4*>(x + r * s.x_head + mate[c]);
+          const bool use = have[c] && s.norm_w;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[c][k] = use ? *reinterpret_cast<const float2*>(s.norm_w + dim[c] + 2 * k) : make_float2(1.f, 1.f);
+            if (kHalf)
+              wm[kHalf ? c : 0][k] = use && rot[c] ? *reinterpret_cast<const float2*>(s.norm_w + mate[c] + 2 * k)
+                                                   : make_float2(1.f, 1.f);
+          }
         }
       }
       __syncwarp();  // every lane has its part of these rows: they may be written over in place
+      float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int r = h + u * kRows + sub;
-        float y[kC][8];
-        float ss = 0.f;
+      for (int c = 0; c < kC; ++c)
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-          unpack_bf16x8(v[u][c], y[c]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(y[c][i], y[c][i], ss);
+        for (int k = 0; k < 4; ++k) {
+          const float2 y = wide2(word(v[c], k));
+          ss = fma2(y, y, ss);
         }
+      float sum = ss.x + ss.y;
 #pragma unroll
-        for (int o = kG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float rstd = s.norm ? 1.0f / sqrtf(ss / (float)a.D + a.eps) : 1.f;
+      for (int o = kG / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      // (rsqrtf is within 2 units: 2^-22)
+      const float rstd = s.norm ? rsqrtf(fmaf(sum, inv_d, a.eps)) : 1.f;
+      const float2 rr = make_float2(rstd, rstd);
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
+      for (int c = 0; c < kC; ++c) {
+        float2 y[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[c][i] *= rstd * w[c][i];
-          if (rot[c]) {
-            if (kHalf) {
-              float z[8];
-              unpack_bf16x8(m[u][c], z);
+        for (int k = 0; k < 4; ++k) y[k] = mul2(mul2(wide2(word(v[c], k)), rr), w[c][k]);
+        if (rot[c]) {
+          const float4* cs = reinterpret_cast<const float4*>(&cs_s[warp][pair[c]]);
+          const float4* sn = reinterpret_cast<const float4*>(&sn_s[warp][pair[c]]);
+          if (kHalf) {
+            const float2 sg = make_float2(sign[c], sign[c]);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                y[c][i] = y[c][i] * cs[c][i] + sign[c] * (z[i] * (rstd * wm[c][i])) * sn[c][i];
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x0 = y[c][2 * i], x1 = y[c][2 * i + 1];
-                y[c][2 * i] = x0 * cs[c][i] - x1 * sn[c][i];
-                y[c][2 * i + 1] = x0 * sn[c][i] + x1 * cs[c][i];
-              }
+            for (int k = 0; k < 4; k += 2) {
+              const float4 co = cs[k >> 1], si = sn[k >> 1];
+              const float2 z0 = mul2(mul2(wide2(word(m[kHalf ? c : 0], k)), rr), wm[kHalf ? c : 0][k]);
+              const float2 z1 = mul2(mul2(wide2(word(m[kHalf ? c : 0], k + 1)), rr), wm[kHalf ? c : 0][k + 1]);
+              y[k] = fma2(mul2(z0, sg), make_float2(si.x, si.y), mul2(y[k], make_float2(co.x, co.y)));
+              y[k + 1] = fma2(mul2(z1, sg), make_float2(si.z, si.w), mul2(y[k + 1], make_float2(co.z, co.w)));
             }
-          }
-          if (r < h1 && have[c]) {
-            const uint4 o = make_uint4(pack_bf16x2(y[c][0], y[c][1]), pack_bf16x2(y[c][2], y[c][3]),
-                                       pack_bf16x2(y[c][4], y[c][5]), pack_bf16x2(y[c][6], y[c][7]));
-            __stcs(reinterpret_cast<uint4*>(out + r * s.out_head + dim[c]), o);
+          } else {
+            const float4 co = cs[0], si = sn[0];
+            const float cc[4] = {co.x, co.y, co.z, co.w}, sc[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              y[k] = make_float2(y[k].x * cc[k] - y[k].y * sc[k], y[k].x * sc[k] + y[k].y * cc[k]);
           }
         }
+        if (r < s.H && have[c])
+          __stcs(reinterpret_cast<uint4*>(out + dim[c]),
+                 make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                            pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y)));
+      }
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        v[c] = vn[c];
+        if (kHalf) m[kHalf ? c : 0] = mn[kHalf ? c : 0];
       }
     }
   }
@@ -130,18 +165,15 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(HeadsArgs a) 
 
 template <int kG, int kC, bool kHalf>
 cudaError_t launch_rows(HeadsArgs a, int sms, cudaStream_t s) {
-  constexpr int kU = 4, kRows = 32 / kG;
-  // heads of an item: as many as leave every SM some 32 warps' worth of items
-  const int64_t heads = (int64_t)a.q.H + a.k.H;
-  int rows = 16 * kRows;
-  while (rows > kRows && a.T * ((heads + rows - 1) / rows) < (int64_t)sms * 32) rows >>= 1;
-  a.rows = rows;
-  const int64_t items = a.T * (((int64_t)a.q.H + rows - 1) / rows + ((int64_t)a.k.H + rows - 1) / rows);
-  const int64_t need = (items + kWarps - 1) / kWarps, most = (int64_t)sms * 8;
-  const dim3 grid((unsigned)(need < most ? need : most));
-  if (rows >= kU * kRows)
-    return launch_pdl(qk_norm_rope_kernel<kG, kC, kHalf, kU>, grid, dim3(kWarps * 32), 0, s, a);
-  return launch_pdl(qk_norm_rope_kernel<kG, kC, kHalf, 1>, grid, dim3(kWarps * 32), 0, s, a);
+  constexpr int kRows = 32 / kG;
+  const int units = (a.q.H + kRows - 1) / kRows + (a.k.H + kRows - 1) / kRows;
+  // a token's rows to a warp, or as few of them as it takes to give each SM some 24 warps
+  a.units = units;
+  while (a.units > 1 && (int64_t)a.T * ((units + a.units - 1) / a.units) < (int64_t)sms * 24) a.units = (a.units + 1) / 2;
+  const int64_t items = (int64_t)a.T * ((units + a.units - 1) / a.units);
+  const int64_t need = (items + kWarps - 1) / kWarps, most = (int64_t)sms * kCtas<kC, kHalf>;
+  return launch_pdl(qk_norm_rope_kernel<kG, kC, kHalf>, dim3((unsigned)(need < most ? need : most)),
+                    dim3(kWarps * 32), 0, s, a);
 }
 
 template <int kG, int kC>
