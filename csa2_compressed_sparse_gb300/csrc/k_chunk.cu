@@ -48,40 +48,40 @@ struct RowPart {
     if (kMode == 2) sc = __ldcs(src + 512 + (lane >> 1));
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); sc = 0u; }
-  __device__ __forceinline__ void store(uint16_t* dst, int lane, bool back, float c, float s) const {
+  // ang: cosine and sine of the row's 32 rotation pairs, or null.
+  __device__ __forceinline__ void store(uint16_t* dst, int lane, const float2* ang) const {
     if (kMode == 0) {
       uint4 w = b;
-      if (back) {
+      if (ang && lane >= 24) {
         float y[8];
         unpack_bf16x8(b, y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float ci = __shfl_sync(0xFFFFFFFFu, c, 4 * (lane - 24) + i);
-          const float si = __shfl_sync(0xFFFFFFFFu, s, 4 * (lane - 24) + i);
-          turn_back(y[2 * i], y[2 * i + 1], ci, si);
+          const float2 g = ang[4 * (lane - 24) + i];
+          turn_back(y[2 * i], y[2 * i + 1], g.x, g.y);
         }
-        if (lane >= 24)
-          w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                         pack_bf16x2(y[6], y[7]));
+        w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                       pack_bf16x2(y[6], y[7]));
       }
       __stcs(reinterpret_cast<uint4*>(dst) + lane, a);
       __stcs(reinterpret_cast<uint4*>(dst) + 32 + lane, w);
     } else {
       const float scale = kMode == 1 ? __uint_as_float(sc) : e8m0_scale(sc);
+      const float2 f = make_float2(scale, scale);
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+      float2 y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = mul2(e4m3x2(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu), f);
+      if (ang && lane >= 28) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 g = ang[8 * (lane - 28) + i];
+          turn_back(y[i].x, y[i].y, g.x, g.y);
+        }
+      }
       uint32_t o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float2 y = e4m3x2(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
-        y.x *= scale;
-        y.y *= scale;
-        if (back) {
-          const float ci = __shfl_sync(0xFFFFFFFFu, c, 8 * (lane - 28) + i);
-          const float si = __shfl_sync(0xFFFFFFFFu, s, 8 * (lane - 28) + i);
-          if (lane >= 28) turn_back(y.x, y.y, ci, si);
-        }
-        o[i] = pack_bf16x2(y.x, y.y);
-      }
+      for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(y[i].x, y[i].y);
       __stcs(reinterpret_cast<uint4*>(dst) + 2 * lane, make_uint4(o[0], o[1], o[2], o[3]));
       __stcs(reinterpret_cast<uint4*>(dst) + 2 * lane + 1, make_uint4(o[4], o[5], o[6], o[7]));
     }
@@ -92,7 +92,8 @@ template <int kMode, int kTok>
 __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadArgs a, int run) {
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
+  __shared__ __align__(16) float2 ang_s[kReadWarps][kTok][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = (int64_t)gridDim.x * kReadWarps * run;
   const uint64_t turn = a.inv_freq ? rope_turn(a.inv_freq[lane]) : 0;
   const int64_t total = min((int64_t)a.T, (int64_t)a.cu_seqlens[a.cache.B]);
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
     }
     __syncwarp();
     const uint64_t p = (uint64_t)j * (uint64_t)a.ratio;
-    const bool skip = !src && !zero;  // the row of out is left as it is
+    const uint32_t skips = __ballot_sync(0xFFFFFFFFu, !src && !zero);  // rows of out that are left as they are
     RowPart<kMode> cur[kTok], nxt[kTok];
     auto fetch = [&](RowPart<kMode>(&r)[kTok], int i0) {
 #pragma unroll
@@ -145,14 +146,20 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += kTok) {
       if (i0 + kTok < n) fetch(nxt, i0 + kTok);
+      if (a.inv_freq) {
+        __syncwarp();  // the last rows' angles are read
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+          const uint64_t pi = __shfl_sync(0xFFFFFFFFu, (unsigned long long)p, (i0 + i) & 31);
+          sincosf(rope_angle(turn, pi), &ang_s[warp][i][lane].y, &ang_s[warp][i][lane].x);
+        }
+        __syncwarp();
+      }
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
-        const uint64_t pi = __shfl_sync(0xFFFFFFFFu, (unsigned long long)p, (i0 + i) & 31);
-        const bool none = __shfl_sync(0xFFFFFFFFu, (int)skip, (i0 + i) & 31) != 0;
+        const bool none = (skips >> ((i0 + i) & 31) & 1u) != 0;
         if (none || i0 + i >= n) continue;  // (the same in the warp)
-        float s = 0.f, c = 1.f;
-        if (a.inv_freq) sincosf(rope_angle(turn, pi), &s, &c);
-        cur[i].store(a.out + (t + i0 + i) * a.out_ld, lane, a.inv_freq != nullptr, c, s);
+        cur[i].store(a.out + (t + i0 + i) * a.out_ld, lane, a.inv_freq ? ang_s[warp][i] : nullptr);
       }
 #pragma unroll
       for (int i = 0; i < kTok; ++i) cur[i] = nxt[i];
@@ -1247,10 +1254,10 @@ namespace {
 
 template <int kMode>
 cudaError_t launch_read(const PagedReadArgs& a, int sms, cudaStream_t s) {
-  // Runs of 32 rows a warp, shorter ones where those would leave SMs without work.
-  int run = 32;
-  while (run > 1 && (int64_t)a.T < (int64_t)sms * 16 * run) run >>= 1;
-  const int64_t need = ((int64_t)a.T + kReadWarps * run - 1) / (kReadWarps * run), most = (int64_t)sms * 32;
+  // Runs of up to 32 rows, as many to each warp of a grid that stays (five CTAs an SM, by registers).
+  const int64_t warps = (int64_t)sms * 5 * kReadWarps, passes = ((int64_t)a.T + warps * 32 - 1) / (warps * 32);
+  const int run = (int)(((int64_t)a.T + warps * passes - 1) / (warps * passes));
+  const int64_t need = ((int64_t)a.T + kReadWarps * run - 1) / (kReadWarps * run), most = (int64_t)sms * 5;
   const dim3 grid((unsigned)(need < most ? need : most));
   return run >= 4 ? launch_pdl(paged_read_kernel<kMode, 4>, grid, dim3(kReadWarps * 32), 0, s, a, run)
                   : launch_pdl(paged_read_kernel<kMode, 1>, grid, dim3(kReadWarps * 32), 0, s, a, run);
