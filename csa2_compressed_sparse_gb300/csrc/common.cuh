@@ -216,6 +216,13 @@ struct PagedReadArgs {
   int page_shift;
 };
 
+// Division of x < 2^31 by d in 1 .. 2^16: with s = ceil(log2 d) and mul = ceil(2^(31 + s) / d), j mul exceeds
+// j 2^(31 + s) / d by less than 2^31, so the floor of j mul / 2^(31 + s) is exact.  shift = s - 1.
+struct Divide {
+  uint32_t mul;
+  int shift;
+};
+
 // A tile of a chunk's attention: 128 rows (token, head) of one sequence, and its key tiles.
 struct __align__(16) ChunkTile {
   int32_t seq, row0, rows;  // rows row0 .. row0 + rows - 1 of [T * H]
@@ -251,12 +258,15 @@ struct ChunkArgs {
   uint32_t page_mul;      // as in PagedAppendArgs
   int page_shift;
   int box_rows;           // rows per tensor copy
+  Divide by_ratio, by_heads;
+  int alone;              // no plan: pair c works on tile c
   int pairs;              // CTA pairs of the launch
   // workspace
   ChunkTile* tile;        // [max_tiles]
   int64_t* prefix;        // [max_tiles] units before each tile
   int max_tiles;
   ChunkShare* share;      // [pairs]
+  int32_t* split;         // [1 + pairs] how many tiles several pairs work on, and which
   float* part;            // [2 pairs][2 CTAs][64 float4 columns][128 lanes][4]
   float* pstat;           // [2 pairs][2 CTAs][m, l, r][64]
   // rows that are not read from their pages: staged as dense bf16 rows (stage null: none are)

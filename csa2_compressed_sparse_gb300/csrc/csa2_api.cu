@@ -620,6 +620,12 @@ csa2_status paged_args(const char* name, const csa2_paged* p, csa2::PagedCache* 
   return CSA2_OK;
 }
 
+csa2::Divide divide_by(int d) {
+  int lg = 0;
+  while ((1 << lg) < d) ++lg;
+  return {(uint32_t)((((uint64_t)1 << (31 + lg)) + d - 1) / d), lg - 1};
+}
+
 // Factor and shift of a division by page_rows: with s = ceil(log2 d) and mul = ceil(2^(31 + s) /
 // d), j mul exceeds j 2^(31 + s) / d by less than j <= 2^31 times 1, so the floor of
 // j mul / 2^(31 + s) is exact for j < 2^31.
@@ -850,7 +856,7 @@ namespace {
 
 // Workspace of csa2_paged_chunk_attn.
 struct ChunkWs {
-  size_t tile, prefix, share, part, pstat, stage, stage_cu, stage_first, stage_end, total;
+  size_t tile, prefix, share, split_list, part, pstat, stage, stage_cu, stage_first, stage_end, total;
   int max_tiles, pairs;
   bool split;      // a tile may need parts
   int64_t rows;    // staged
@@ -870,6 +876,7 @@ ChunkWs chunk_ws_layout(int T, int H, const csa2_paged& c, int64_t max_rows, int
   w.tile = o; o = up256(o + (size_t)tiles * sizeof(csa2::ChunkTile));
   w.prefix = o; o = up256(o + (size_t)tiles * 8);
   w.share = o; o = up256(o + (size_t)w.pairs * sizeof(csa2::ChunkShare));
+  w.split_list = o; o = up256(o + (size_t)(w.pairs + 1) * 4);
   if (w.split) {
     w.part = o; o = up256(o + (size_t)w.pairs * 2 * 128 * 512 * 4);
     w.pstat = o; o = up256(o + (size_t)w.pairs * 2 * 128 * 3 * 4);
@@ -936,11 +943,15 @@ csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_
   a.inv_freq = inv_freq;
   page_division(a.cache, &a.page_mul, &a.page_shift);
   a.pairs = w.pairs;
+  a.by_ratio = divide_by(ratio);
+  a.by_heads = divide_by(H);
+  a.alone = !w.split && w.rows == 0 && a.cache.B <= 256 ? 1 : 0;
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.tile = reinterpret_cast<csa2::ChunkTile*>(base + w.tile);
   a.prefix = reinterpret_cast<int64_t*>(base + w.prefix);
   a.max_tiles = w.max_tiles;
   a.share = reinterpret_cast<csa2::ChunkShare*>(base + w.share);
+  a.split = reinterpret_cast<int32_t*>(base + w.split_list);
   if (w.split) {
     a.part = reinterpret_cast<float*>(base + w.part);
     a.pstat = reinterpret_cast<float*>(base + w.pstat);

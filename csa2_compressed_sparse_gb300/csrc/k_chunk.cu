@@ -240,7 +240,7 @@ struct __align__(16) ChunkAux {
   uint64_t turn[32];
   float top[4][64], sum[4][64];
   uint32_t tmem_slot;
-  int abort, done;
+  int abort, done, work;
 };
 constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kPBytes + (int)sizeof(ChunkAux);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -292,11 +292,16 @@ __device__ __forceinline__ void store_sector(uint16_t* to, const uint32_t (&b)[8
   }
 }
 
+// x / d for x < 2^31 by the factor and shift of d (Divide): see there.
+__device__ __forceinline__ uint32_t divide(uint32_t x, const Divide& d) {
+  return d.shift < 0 ? x : __umulhi(x, d.mul) >> d.shift;
+}
+
 // Rows lo .. hi - 1 that the token at position p sees, of at most clip; true if there were more.
 __device__ __forceinline__ bool token_rows(const ChunkArgs& a, int64_t p, int64_t clip, int& lo, int& hi) {
   int64_t h;
   if (p < 0) h = 0;
-  else if (p < 0x7FFFFFFF) h = (uint32_t)(p + 1) / (uint32_t)a.ratio;
+  else if (p < 0x7FFFFFFF) h = divide((uint32_t)(p + 1), a.by_ratio);
   else h = (int64_t)min(((uint64_t)p + 1) / (uint64_t)a.ratio, (uint64_t)1 << 62);
   int64_t l = a.window > 0 && h > a.window ? h - a.window : 0;
   const bool over = h > clip;
@@ -316,7 +321,7 @@ __device__ __forceinline__ bool token_rows(const ChunkArgs& a, int64_t p, int64_
 // all tiles, 2 a key tile and kTileCost a tile (what begins and ends it takes as long as 1.5 key tiles), is
 // cut evenly: pair c begins at cost W c / C, C as many pairs as leave each kShare key tiles or a tile.  A cut
 // within the first kTileCost of a tile is one before it.
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kMaxPairs = 76;
 constexpr int kWhole = 6, kShare = 4, kTileCost = 3;
 
 // Exclusive prefix of x over the CTA's threads; *total gets the sum.
@@ -351,16 +356,41 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
   return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
+// Tile k of a sequence of `count` tokens from tok0 on, the first at position start; true if a token sees
+// more rows than it may.
+__device__ __forceinline__ bool make_tile(const ChunkArgs& a, ChunkTile& t, int seq, int tok0, int count, int64_t start,
+                                          int64_t off, int clip, int k) {
+  const int64_t rows = (int64_t)count * a.H - (int64_t)k * kQRows;
+  t.seq = seq;
+  t.rows = (int)min(rows, (int64_t)kQRows);
+  t.row0 = tok0 * a.H + k * kQRows;
+  t.tok0 = tok0;
+  t.start = start;
+  t.off = off;
+  t.clip = clip;
+  t.c0 = t.c1 = 0;
+  int lo, hi, y;
+  bool over = token_rows(a, start + (int)(divide(t.row0, a.by_heads) - tok0), clip, lo, y);
+  over |= token_rows(a, start + (int)(divide(t.row0 + t.rows - 1, a.by_heads) - tok0), clip, y, hi);
+  t.k0 = hi > lo ? lo / kKeys : 0;
+  t.kn = hi > lo ? (hi + kKeys - 1) / kKeys - t.k0 : 1;
+  return over;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
+  constexpr int kTiles = 4;  // of a thread at a time, at most
   __shared__ int64_t sums[32];
-  __shared__ int tile0[kPlanThreads + 1], tok0[kPlanThreads], count[kPlanThreads], clip[kPlanThreads];
+  __shared__ int tile0[kPlanThreads], tok0[kPlanThreads], count[kPlanThreads], clip[kPlanThreads];
   __shared__ int64_t off[kPlanThreads], start[kPlanThreads];
-  __shared__ int longest;
+  __shared__ int cut_tile[kMaxPairs + 1], cut_at[kMaxPairs + 1];
+  __shared__ int64_t cut_keys[kMaxPairs + 1];
+  __shared__ int longest, splits;
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x;
-  if (tid == 0) longest = 0;
+  if (tid == 0) longest = splits = 0;
   int64_t tiles = 0, units = 0, staged = 0;
+  int most = 0;
   const int B = a.cache.B;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -405,40 +435,38 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
     count[tid] = n;
     clip[tid] = c;
     start[tid] = s;
-    if (tid == 0) tile0[kPlanThreads] = (int)total;
     __syncthreads();
     const int here = (int)total;
-    for (int x0 = 0; x0 < here; x0 += kPlanThreads) {
-      const int x = x0 + tid;
-      ChunkTile t{};
-      if (x < here) {
-        int i = 0, e = kPlanThreads;  // the last sequence with tile0 <= x
-        while (e - i > 1) {
-          const int m = (i + e) >> 1;
-          if (tile0[m] <= x) i = m;
-          else e = m;
-        }
-        const int k = x - tile0[i];
-        const int64_t rows = (int64_t)count[i] * a.H - (int64_t)k * kQRows;
-        t.seq = b0 + i;
-        t.rows = (int)min(rows, (int64_t)kQRows);
-        t.row0 = tok0[i] * a.H + k * kQRows;
-        t.tok0 = tok0[i];
-        t.start = start[i];
-        t.off = off[i];
-        t.clip = clip[i];
-        int lo, hi, y;
-        bool over = token_rows(a, t.start + (t.row0 / a.H - t.tok0), t.clip, lo, y);
-        over |= token_rows(a, t.start + ((t.row0 + t.rows - 1) / a.H - t.tok0), t.clip, y, hi);
-        if (over && t.clip == a.cap_rows) raise_fault(kFaultBounds);
-        t.k0 = hi > lo ? lo / kKeys : 0;
-        t.kn = hi > lo ? (hi + kKeys - 1) / kKeys - t.k0 : 1;
-        atomicMax(&longest, t.kn);
+    const int per = here > kPlanThreads ? kTiles : 1;
+    for (int x0 = 0; x0 < here; x0 += per * kPlanThreads) {
+      const int x = x0 + per * tid;
+      int i = 0, e = kPlanThreads;  // the last sequence with tile0 <= x
+      while (e - i > 1) {
+        const int m = (i + e) >> 1;
+        if (tile0[m] <= x) i = m;
+        else e = m;
       }
-      const int64_t before = units + plan_scan(x < here ? 2 * t.kn + kTileCost : 0, sums, &total);
-      if (x < here && tiles + x < a.max_tiles) {
-        a.tile[tiles + x] = t;
-        a.prefix[tiles + x] = before;
+      int cost[kTiles], sum = 0;
+#pragma unroll
+      for (int q = 0; q < kTiles; ++q) {
+        cost[q] = 0;
+        if (q < per && x + q < here && tiles + x + q < a.max_tiles) {
+          while (i + 1 < kPlanThreads && tile0[i + 1] <= x + q) ++i;  // (past empty sequences)
+          ChunkTile t{};
+          if (make_tile(a, t, b0 + i, tok0[i], count[i], start[i], off[i], clip[i], x + q - tile0[i]) &&
+              clip[i] == a.cap_rows)
+            raise_fault(kFaultBounds);
+          a.tile[tiles + x + q] = t;
+          cost[q] = 2 * t.kn + kTileCost;
+          most = max(most, t.kn);
+        }
+        sum += cost[q];
+      }
+      int64_t before = units + plan_scan(sum, sums, &total);
+#pragma unroll
+      for (int q = 0; q < kTiles; ++q) {
+        if (cost[q]) a.prefix[tiles + x + q] = before;
+        before += cost[q];
       }
       units += total;
     }
@@ -446,49 +474,95 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
     __syncthreads();
   }
   if (a.stage && tid == 0) a.stage_cu[B] = (int32_t)min(staged, a.stage_rows);
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if ((tid & 31) == 0) atomicMax(&longest, most);
   __syncthreads();
   const int64_t n = min(tiles, (int64_t)a.max_tiles);
-  const bool whole = n <= a.pairs && longest <= kWhole;
+  if (n <= a.pairs && longest <= kWhole) {
+    if (tid < a.pairs) a.share[tid] = tid < n ? ChunkShare{tid, 0, a.tile[tid].kn} : ChunkShare{0, 0, 0};
+    if (tid == 0) a.split[0] = 0;
+    return;
+  }
   int64_t C = max(n, ((units - kTileCost * n) / 2 + kShare - 1) / kShare);
   C = C < a.pairs ? C : a.pairs;
-  for (int64_t c = tid; c < a.pairs; c += kPlanThreads)
-    if (c >= (whole ? n : C)) a.share[c] = ChunkShare{0, 0, 0};
-  // Where pair c begins, as key tiles from tile x on (before cost p): at most kn.
-  auto begin = [&](int64_t c, int64_t p) -> int64_t {
-    const int64_t u = quotient(units * c, C) - p - kTileCost;
-    return u > 0 ? u >> 1 : 0;
-  };
-  for (int64_t x = tid; x < n; x += kPlanThreads) {
-    ChunkTile& t = a.tile[x];
-    const int64_t p = a.prefix[x], e = p + 2 * t.kn + kTileCost;
-    if (whole) {
-      t.c0 = t.c1 = (int)x;
-      a.share[x] = ChunkShare{(int32_t)x, 0, t.kn};
-      continue;
-    }
-    // pairs that begin at or before its first key tile, and before its end
-    t.c0 = (int)quotient((p + kTileCost + 2) * C - 1, units);
-    t.c1 = (int)quotient(e * C - 1, units);
-    for (int64_t c = quotient(p * C + units - 1, units); c <= t.c1; ++c) {  // pairs whose cut is in this tile
-      // its end: where the next one begins, in this tile or a later one
-      const int64_t at = begin(c, p), cut = c + 1 < C ? quotient(units * (c + 1), C) : units;
-      int64_t count = -at;
-      if (cut < e) {
-        count += begin(c + 1, p);
-      } else {
-        int64_t lo = x, hi = n - 1;  // the last tile that begins at or before the cut
-        while (lo < hi) {
-          const int64_t m = (lo + hi + 1) >> 1;
-          if (a.prefix[m] <= cut) lo = m;
-          else hi = m - 1;
-        }
-        // key tiles from tile x to the cut
-        count += c + 1 < C ? (a.prefix[lo] - p - kTileCost * (lo - x)) / 2 + begin(c + 1, a.prefix[lo])
-                           : (units - p - kTileCost * (n - x)) / 2;
+  // Where each pair begins: the last tile that does at or before its cut, searched for in every so manieth
+  // tile's prefix first.
+  int64_t* sample = start;
+  const int64_t every = (n + kPlanThreads - 1) / kPlanThreads;
+  if (tid * every < n) sample[tid] = a.prefix[tid * every];
+  __syncthreads();
+  if (tid <= C) {
+    if (tid == C) {
+      cut_tile[tid] = (int)n;
+      cut_at[tid] = 0;
+      cut_keys[tid] = (units - kTileCost * n) / 2;
+    } else {
+      const int64_t u = quotient(units * tid, C);
+      int lo = 0, hi = (int)((n - 1) / every);
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (sample[m] <= u) lo = m;
+        else hi = m - 1;
       }
-      a.share[c] = ChunkShare{(int32_t)x, (int32_t)at, count};
+      int64_t x = lo * every, e = min(n, x + every) - 1;
+      while (x < e) {
+        const int64_t m = (x + e + 1) >> 1;
+        if (a.prefix[m] <= u) x = m;
+        else e = m - 1;
+      }
+      const int64_t p = a.prefix[x], at = u - p - kTileCost;
+      cut_tile[tid] = (int)x;
+      cut_at[tid] = at > 0 ? (int)(at >> 1) : 0;
+      cut_keys[tid] = (p - kTileCost * x) / 2 + cut_at[tid];
     }
   }
+  __syncthreads();
+  if (tid < a.pairs)
+    a.share[tid] = tid < C ? ChunkShare{cut_tile[tid], cut_at[tid], cut_keys[tid + 1] - cut_keys[tid]}
+                           : ChunkShare{0, 0, 0};
+  // the tiles that are cut, each by the first pair that begins within it
+  if (tid > 0 && tid < C && cut_at[tid] > 0 && !(cut_tile[tid - 1] == cut_tile[tid] && cut_at[tid - 1] > 0)) {
+    int last = tid;
+    while (last + 1 < C && cut_tile[last + 1] == cut_tile[tid]) ++last;
+    a.tile[cut_tile[tid]].c0 = tid - 1;
+    a.tile[cut_tile[tid]].c1 = last;
+    a.split[1 + atomicAdd(&splits, 1)] = cut_tile[tid];
+  }
+  __syncthreads();
+  if (tid == 0) a.split[0] = splits;
+}
+
+// Few short sequences: tile `pair` by a warp of its own, without a plan; false when there is none.  All lanes
+// get the tile.
+__device__ __forceinline__ bool plan_alone(const ChunkArgs& a, ChunkTile& t, int pair, int lane, bool report) {
+  int tiles = 0;
+  for (int b0 = 0; b0 < a.cache.B; b0 += 32) {
+    const int b = b0 + lane;
+    int tok0 = 0, n = 0;
+    if (b < a.cache.B) {
+      tok0 = min(max(a.cu_seqlens[b], 0), a.T);
+      n = max(0, min(a.cu_seqlens[b + 1], a.T) - tok0);
+    }
+    const int mine = (int)(((int64_t)n * a.H + kQRows - 1) / kQRows);
+    int to = mine;  // tiles of this and the sequences before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, to, o);
+      if (lane >= o) to += x;
+    }
+    const uint32_t here = __ballot_sync(0xFFFFFFFFu, tiles + to > pair);
+    if (here) {
+      const int l = __ffs(here) - 1;
+      const int first = tiles + __shfl_sync(0xFFFFFFFFu, to - mine, l);
+      const int seq = b0 + l;
+      if (make_tile(a, t, seq, __shfl_sync(0xFFFFFFFFu, tok0, l), __shfl_sync(0xFFFFFFFFu, n, l), a.start_pos[seq], 0,
+                    (int)a.cap_rows, pair - first) && report && lane == 0)
+        raise_fault(kFaultBounds);
+      return true;
+    }
+    tiles += __shfl_sync(0xFFFFFFFFu, to, 31);
+  }
+  return false;
 }
 
 // ---- attention -------------------------------------------------------------------------
@@ -507,7 +581,14 @@ __device__ __forceinline__ void walk_fit(const ChunkArgs& a, ChunkWalk& w) {
   w.i = 0;
   if (w.left > 0) w.next = a.tile[w.tile + 1];
 }
-__device__ __forceinline__ bool walk_start(const ChunkArgs& a, int pair, ChunkWalk& w) {
+__device__ __forceinline__ bool walk_start(const ChunkArgs& a, int pair, int lane, bool report, ChunkWalk& w) {
+  if (a.alone) {
+    w.left = 0;
+    w.tile = w.unit = w.i = 0;
+    if (!plan_alone(a, w.t, pair, lane, report)) return false;
+    w.n = w.t.kn;
+    return true;
+  }
   const ChunkShare s = a.share[pair];
   w.left = s.count;
   if (w.left <= 0) return false;
@@ -530,8 +611,8 @@ __device__ __forceinline__ bool walk_next(const ChunkArgs& a, ChunkWalk& w) {
 // What the tokens of a tile see: the first's lo, the last's hi.
 __device__ __forceinline__ void tile_rows(const ChunkArgs& a, const ChunkTile& t, int& lo0, int& hi0,
                                           int& lo1, int& hi1) {
-  token_rows(a, t.start + (t.row0 / a.H - t.tok0), t.clip, lo0, hi0);
-  token_rows(a, t.start + ((t.row0 + t.rows - 1) / a.H - t.tok0), t.clip, lo1, hi1);
+  token_rows(a, t.start + (int)(divide(t.row0, a.by_heads) - t.tok0), t.clip, lo0, hi0);
+  token_rows(a, t.start + (int)(divide(t.row0 + t.rows - 1, a.by_heads) - t.tok0), t.clip, lo1, hi1);
 }
 
 // Groups of eight rows of a key tile, one a lane: where each lies.
@@ -603,12 +684,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   griddep_wait();
   if (a.inv_freq && tid < 32) X.turn[tid] = rope_turn(a.inv_freq[tid]);
+  ChunkWalk w;  // the loaders'
+  if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
+    const bool any = walk_start(a, pair, lane, rank == 0 && warp == kWarpLoad, w);
+    if (warp == kWarpLoad && lane == 0) X.work = any;
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  const bool work = X.work != 0;
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, X.tmem_slot, 0);
-  const bool work = a.share[pair].count > 0;
 
   if (work && warp < kSoftWarps) {
     // ================= softmax, rescale, output =================
@@ -646,8 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           l2 = r2 = make_float2(0.f, 0.f);
           const ChunkSegment& t = X.seg[seg & 3];
           const int grow = t.row0 + min((int)rank * 64 + row, t.rows - 1);  // rows behind the last follow it
-          token_rows(a, t.start + (grow / a.H - t.tok0), t.clip, lo, hi);
-          if (a.sink) logit = a.sink[grow % a.H];
+          const int tok = (int)divide(grow, a.by_heads);
+          token_rows(a, t.start + (tok - t.tok0), t.clip, lo, hi);
+          if (a.sink) logit = a.sink[grow - tok * a.H];
           ++seg;
         }
         wait_phase(X, X.s_full[c & 1], (uint32_t)(c >> 1) & 1);
@@ -777,8 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 ang[kTok] = {};
       int tok = 0, ntok = 0;
       if (store && blk == 3 && a.inv_freq) {
-        tok = (e.row0 + wrow) / a.H;
-        ntok = (e.row0 + wrow + 31) / a.H - tok + 1;
+        tok = (int)divide(e.row0 + wrow, a.by_heads);
+        ntok = (int)divide(e.row0 + wrow + 31, a.by_heads) - tok + 1;
 #pragma unroll
         for (int k = 0; k < kTok; ++k)
           if (k < ntok)
@@ -826,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         const float f0 = mslot_end == -INFINITY ? 0.f : ex2(mslot_end - m_end);
         const bool folded = mslot_end != -INFINITY;
-        const int mytok = ntok ? (e.row0 + wrow + lane) / a.H - tok : 0;
+        const int mytok = ntok ? (int)divide(e.row0 + wrow + lane, a.by_heads) - tok : 0;
         // A lane has 32 columns of its row at a time; their 64 bytes go out as two whole sectors (stores of
         // 16 bytes a row took prompts twice as long; through shared memory a tile's end took 2000 cycles more).
         uint16_t* out = a.out + (int64_t)(e.row0 + (int)rank * 64 + row) * kDLat + kh * 128 + half * 64;
@@ -886,13 +973,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();  // (what follows wants whole warps)
         }
       }
+      // A block of P lets the first products overwrite O, whichever warps have read it: none is handed on
+      // before all have.  (The sums, too, are read before others are written.)
+      if (end) soft_sync();
       if (have) {
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(p_full);
       }
-      if (end) soft_sync();  // the sums are read before others are written
       if (!have) break;
       if (!(st.kind & kStepLast) && ((st.i + 1) & (kRun - 1)) == 0) {
         // a run's end: O joins what the part holds
@@ -920,6 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mslot = m;
         tc_fence_before();
+        soft_sync();  // (as above: the next block of P lets O be overwritten)
       }
     }
     if (tid == 0) *reinterpret_cast<volatile int*>(&X.done) = 1;
@@ -1059,8 +1149,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int rev = 0, c = 0, seg = 0, n_last = 0;
     int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
-    ChunkWalk w;
-    walk_start(a, pair, w);
     // Eight slots, each in pieces of box_rows rows, one a lane.
     auto slots = [&](const Places& at, const CUtensorMap* map, bool values) {
       const int piece = lane << lg;
@@ -1152,9 +1240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- join ------------------------------------------------------------------------------
 //
 // A tile that pairs c0 .. c1 worked on: with M the largest running maximum (and the sink's logit) of
-// a row, out = sum 2^(m - M) O / Z.  Pair c0 + 1's CTAs do it (the first that began within the tile),
-// kJoin of them, a thread 16 bytes of every part at a time.  Bound by the parts' way from L2.
-constexpr int kJoin = 64, kMaxPairs = 76;
+// a row, out = sum 2^(m - M) O / Z.  kJoin CTAs a tile, a thread 16 bytes of every part at a time.  Bound by
+// the parts' way from L2.
+constexpr int kJoin = 64;
 
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
   __shared__ float wt[kMaxPairs][64];
@@ -1162,13 +1250,10 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
   __shared__ float inv[64];
   griddep_launch_dependents();
   griddep_wait();
-  const int c = blockIdx.x;
-  const ChunkShare s = a.share[c];
-  if (s.count <= 0 || s.unit == 0) return;
-  const ChunkTile t = a.tile[s.tile];
-  if (t.c0 + 1 != c) return;
+  if ((int)blockIdx.y >= a.split[0]) return;
+  const ChunkTile t = a.tile[a.split[1 + blockIdx.y]];
   const int tid = threadIdx.x, n = min(t.c1 - t.c0 + 1, kMaxPairs);
-  const int rank = blockIdx.y / (kJoin / 2);  // the CTA whose 64 rows these are
+  const int rank = blockIdx.x / (kJoin / 2);  // the CTA whose 64 rows these are
   auto slot = [&](int i) -> int64_t { return (2 * (int64_t)(t.c0 + i) + (i == 0 ? 1 : 0)) * 2 + rank; };
   const int row = tid & 63, quarter = tid >> 6, r = 64 * rank + row;
   const int grow = t.row0 + min(r, t.rows - 1), h = grow % a.H;
@@ -1206,12 +1291,12 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
         z += ex2(sink - Mf);
       }
       inv[row] = z > 0.f || z != z ? 1.f / z : 0.f;
-      if (a.lse && live && blockIdx.y % (kJoin / 2) == 0) a.lse[grow] = head_lse(Mf, l, rows, logit);
+      if (a.lse && live && blockIdx.x % (kJoin / 2) == 0) a.lse[grow] = head_lse(Mf, l, rows, logit);
     }
     __syncthreads();
   }
   // 8192 float4 of this CTA's rows, columns by kJoin / 2 CTAs
-  for (int x = (blockIdx.y % (kJoin / 2)) * 256 + tid; x < 8192; x += 256 * (kJoin / 2)) {
+  for (int x = (blockIdx.x % (kJoin / 2)) * 256 + tid; x < 8192; x += 256 * (kJoin / 2)) {
     const int L = x & 127, col = x >> 7;
     const float4* p = reinterpret_cast<const float4*>(a.part) + col * 128 + L;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1289,7 +1374,8 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
   const void* rows = a.stage ? (const void*)a.stage : (const void*)a.cache.data;
   if (!encode_bytes(&km, rows, 5, dims, strides, kbox) || !encode_bytes(&vm, rows, 5, dims, strides, vbox))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+  cudaError_t e = cudaSuccess;
+  if (!a.alone) e = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   if (a.stage) {
     PagedReadArgs r{};
@@ -1311,7 +1397,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl_cluster(chunk_attn_kernel, dim3(2u * a.pairs), dim3(kThreads), kSmem, s, 2u, a, qm, km, vm);
   if (e != cudaSuccess || !a.part) return e;
-  return launch_pdl(chunk_join_kernel, dim3((unsigned)a.pairs, kJoin), dim3(256), 0, s, a);
+  return launch_pdl(chunk_join_kernel, dim3(kJoin, (unsigned)a.pairs), dim3(256), 0, s, a);
 }
 
 }  // namespace csa2
