@@ -861,6 +861,23 @@ struct ChunkWs {
   bool split;      // a tile may need parts
   int64_t rows;    // staged
 };
+// Rows that a tensor copy brings at once: the largest of 64, 32, 16, 8 dividing page_rows.
+int page_box(int page_rows) {
+  return page_rows % 64 == 0 ? 64 : page_rows % 32 == 0 ? 32 : page_rows % 16 == 0 ? 16 : 8;
+}
+
+// FP8 rows are staged as dense bf16 rows first: decoding a row once for all tiles that read it.  So are bf16
+// rows on small pages where a sequence has tiles enough to read them, as copies of 16 or 8 rows take the
+// loaders longer than the products take: us direct / staged, chunks of 8 sequences with 150 tiles each
+// 795 / 678 at 16-row pages and 1048 / 679 at 8-row ones (688 / 710 at 32), 24 with 31 tiles 536 / 509 and
+// 754 / 536, 8 with 8 tiles 149 / 161 and 193 / 164, 64 with 2 tiles 171 / 271 and 194 / 274.
+bool chunk_stages(int T, int H, const csa2_paged& c) {
+  if (c.dtype != CSA2_SWA_BF16) return true;
+  const int64_t seqs = c.B < T ? c.B : T, tiles = ((int64_t)T * H + 127) / 128;
+  const int box = page_box(c.page_rows);
+  return box == 8 ? tiles >= 4 * seqs : box == 16 ? tiles >= 24 * seqs : false;
+}
+
 ChunkWs chunk_ws_layout(int T, int H, const csa2_paged& c, int64_t max_rows, int64_t total_rows) {
   ChunkWs w{};
   // sequences with tokens; each may have an incomplete tile
@@ -881,7 +898,7 @@ ChunkWs chunk_ws_layout(int T, int H, const csa2_paged& c, int64_t max_rows, int
     w.part = o; o = up256(o + (size_t)w.pairs * 2 * 128 * 512 * 4);
     w.pstat = o; o = up256(o + (size_t)w.pairs * 2 * 128 * 3 * 4);
   }
-  if (c.dtype != CSA2_SWA_BF16) {
+  if (chunk_stages(T, H, c)) {
     // whole groups of eight rows of each sequence
     w.rows = ((total_rows + 7) & ~(int64_t)7) + 16 * seqs;
     w.stage = o; o = up256(o + (size_t)w.rows * 1024);
@@ -956,8 +973,7 @@ csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_
     a.part = reinterpret_cast<float*>(base + w.part);
     a.pstat = reinterpret_cast<float*>(base + w.pstat);
   }
-  a.box_rows = a.cache.page_rows % 64 == 0 ? 64 : a.cache.page_rows % 32 == 0 ? 32
-               : a.cache.page_rows % 16 == 0 ? 16 : 8;
+  a.box_rows = page_box(a.cache.page_rows);
   if (w.rows > 0) {
     a.box_rows = 64;
     a.stage = reinterpret_cast<uint16_t*>(base + w.stage);

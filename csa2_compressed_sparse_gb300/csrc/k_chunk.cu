@@ -220,7 +220,6 @@ enum : int { kStepLast = 1, kStepMasked = 2 };
 struct __align__(16) ChunkSegment {
   int64_t start;
   int row0, rows, tok0, clip;  // as in ChunkTile
-  int hi0, lo1;                // the first token's hi, the last one's lo
   int whole;                   // all of the tile's key tiles
   int slot;                    // its part
 };
@@ -581,8 +580,9 @@ __device__ __forceinline__ void walk_fit(const ChunkArgs& a, ChunkWalk& w) {
   w.i = 0;
   if (w.left > 0) w.next = a.tile[w.tile + 1];
 }
+template <bool kAlone>
 __device__ __forceinline__ bool walk_start(const ChunkArgs& a, int pair, int lane, bool report, ChunkWalk& w) {
-  if (a.alone) {
+  if (kAlone) {
     w.left = 0;
     w.tile = w.unit = w.i = 0;
     if (!plan_alone(a, w.t, pair, lane, report)) return false;
@@ -645,6 +645,9 @@ __device__ __forceinline__ Places place_groups(const ChunkArgs& a, const ChunkTi
   return p;
 }
 
+// kAlone: without a plan, pair c works on tile c (an instance of its own: with its code in the other, FP8
+// chunks of four sequences took 1071 us in place of 1043)
+template <bool kAlone>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.inv_freq && tid < 32) X.turn[tid] = rope_turn(a.inv_freq[tid]);
   ChunkWalk w;  // the loaders'
   if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
-    const bool any = walk_start(a, pair, lane, rank == 0 && warp == kWarpLoad, w);
+    const bool any = walk_start<kAlone>(a, pair, lane, rank == 0 && warp == kWarpLoad, w);
     if (warp == kWarpLoad && lane == 0) X.work = any;
   }
   tc_fence_before();
@@ -941,7 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[4 * j + 2] = __float_as_uint(o.z);
               v[4 * j + 3] = __float_as_uint(o.w);
             }
-            if (!store) continue;
+            if (!store) {
+              __syncwarp();
+              continue;
+            }
           }
           if (k >= 2) {  // pair 16 (k - 2) + j times e^{-i p theta}
 #pragma unroll 1
@@ -1195,7 +1201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d_pair(q_s + k * 8192, &qmap, 64 * k, w.t.row0 + (int)rank * 64, q_full, pol);
           }
           if (lane == 0)
-            X.seg[seg & 3] = ChunkSegment{w.t.start, w.t.row0, w.t.rows, w.t.tok0, w.t.clip, hi0, lo1,
+            X.seg[seg & 3] = ChunkSegment{w.t.start, w.t.row0, w.t.rows, w.t.tok0, w.t.clip,
                                           w.t.c0 == w.t.c1, 2 * pair + (w.unit == 0 ? 1 : 0)};
           __syncwarp();
           ++seg;
@@ -1393,9 +1399,10 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
     e = launch_paged_read(r, sms, s);
     if (e != cudaSuccess) return e;
   }
-  e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  auto kern = a.alone ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl_cluster(chunk_attn_kernel, dim3(2u * a.pairs), dim3(kThreads), kSmem, s, 2u, a, qm, km, vm);
+  e = launch_pdl_cluster(kern, dim3(2u * a.pairs), dim3(kThreads), kSmem, s, 2u, a, qm, km, vm);
   if (e != cudaSuccess || !a.part) return e;
   return launch_pdl(chunk_join_kernel, dim3(kJoin, (unsigned)a.pairs), dim3(256), 0, s, a);
 }

@@ -630,8 +630,9 @@ csa2_status csa2_paged_read(csa2_bf16* out, int64_t out_ld, int T, const int32_t
  *   max_rows     bound on hi, 0 .. 2^31 - 256; a larger hi, or one beyond the table, raises
  *                CSA2_EBOUNDS and is clipped
  *   total_rows   bound on the rows seen by all sequences together (each sequence's from its first
- *                token's lo to its last token's hi), 0 .. 2^30; with FP8 rows, more raise CSA2_EBOUNDS
- *                and are left out
+ *                token's lo to its last token's hi), 0 .. 2^30.  FP8 rows, and rows of pages that
+ *                are no multiple of 32, may be copied to the workspace first: more raise
+ *                CSA2_EBOUNDS and are left out then
  *   ratio, window, sink, scale, lse, inv_freq   as csa2_paged_attn
  *   ws           workspace of csa2_paged_chunk_attn_workspace_size(T, H, cache, max_rows,
  *                total_rows) bytes, 256-byte aligned; contents are scratch.  Calls that can overlap

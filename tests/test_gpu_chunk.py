@@ -434,6 +434,102 @@ def test_one_workspace_for_many_calls_in_a_row():
         c.check(only=range(0, 200, 7))
 
 
+# ---- long segments: tensor memory sums up 65536 rows at most, the rest joins in fp32 ----------
+
+@pytest.mark.parametrize("case", ["plain", "rising", "no_pages", "window"])
+def test_segments_longer_than_a_run(case):
+    """Eighty tiles of 300 key tiles and more each: those that one pair works on alone, and the longer parts
+    of those that two share, are done in runs."""
+    n = 90000 if case == "no_pages" else 80000
+    c = Case(30, BF16, 64, 64, [160], [n - 160], window=77000 if case == "window" else 0)
+    if case == "rising":  # the maximum moves in every run
+        x = decode(get(c.data, c.table, 0, 0, n), BF16).float()
+        put(c.data, c.table, 0, (x * torch.linspace(0.1, 20, n, device="cuda")[:, None]).bfloat16())
+    if case != "no_pages":
+        c.call().check(only=range(0, 160, 13))
+        return
+    gone = 1100 * 64  # the first run sees nothing at all
+    x = decode(get(c.data, c.table, 0, gone, n), BF16)
+    c.table[0, :1100] = -1
+    c.call()
+    assert status() == 4
+    p, lo, hi = c.seen(0)
+    for i in range(0, 160, 13):
+        check_tokens(c.out[i:i + 1], c.lse[i:i + 1], c.q[i:i + 1], x, lo[i:i + 1], hi[i:i + 1] - gone, c.sink,
+                     c.scale, p[i:i + 1], True, BF16)
+
+
+def test_runs_do_not_depend_on_the_run():
+    c = Case(31, BF16, 64, 64, [160], [70000]).call()
+    first, lse = c.out.clone(), c.lse.clone()
+    c.out.fill_(1)
+    c.ws.random_(0, 255)
+    c.call()
+    assert torch.equal(c.out, first) and torch.equal(c.lse, lse)
+
+
+# ---- every way to the rows: whole pages, pieces of 32, 16 and 8 rows, copied first -------------
+
+@pytest.mark.parametrize("page", [8, 24, 16, 48, 32, 96])
+@pytest.mark.parametrize("new", [[1, 3], [40, 2], [130, 50]])
+@pytest.mark.parametrize("window", [0, 90])
+def test_small_pages(page, new, window):
+    Case(page, BF16, 64, page, new, [700, 333], window=window, ratio=1 + (page == 48)).call().check()
+
+
+@pytest.mark.parametrize("dtype,page", [(BF16, 8), (BF16, 16), (S128, 64), (E8M0, 24)])
+def test_bad_pages_of_copied_rows(dtype, page):
+    c = Case(32, dtype, 64, page, [100], [300])
+    x = decode(get(c.data, c.table, 0, 0, 400), dtype)
+    c.table[0, 3] = c.data.shape[0]
+    c.table[0, 4] = -7
+    c.call()
+    assert status() == 4
+    p, lo, hi = c.seen(0)
+    there = hi.clamp(max=3 * page) + (hi - 5 * page).clamp(min=0)  # of the rows 0 .. hi - 1
+    check_tokens(c.out, c.lse, c.q, torch.cat([x[:3 * page], x[5 * page:]]), lo, there, c.sink, c.scale, p, True,
+                 dtype)
+
+
+@pytest.mark.parametrize("dtype,page", [(BF16, 8), (S128, 64)])
+def test_more_rows_than_announced_are_left_out(dtype, page):
+    """Room for the first sequence's rows and a few of the second's."""
+    c = Case(33, dtype, 64, page, [60, 70], [100, 900])
+    c.call(total_rows=200)
+    assert status() == 4
+    x = decode(get(c.data, c.table, 0, 0, 160), dtype)
+    p, lo, hi = c.seen(0)
+    check_tokens(c.out[:60], c.lse[:60], c.q[:60], x, lo, hi, c.sink, c.scale, p, True, dtype)
+    assert bool(c.out[60:].isfinite().all()) and bool((c.out[60:] != 5).any())
+    c.out.fill_(5)
+    c.call().check()
+
+
+@pytest.mark.parametrize("B", [3, 32, 33, 60, 256, 257, 300])
+def test_few_tokens_of_many_sequences(B):
+    """Up to 256 sequences the pairs find their own tiles, with empty sequences among the others."""
+    new = [0] * B
+    for i, b in enumerate(range(B - 1, 0, -max(1, B // 9))):
+        new[b] = 1 + i % 5
+    Case(B, BF16, 64, 64, new, [17 * b % 900 for b in range(B)], pad=2).call().check()
+
+
+@pytest.mark.parametrize("n,hist", [(40, 300), (2, 40000)])
+def test_outputs_at_odd_chunks(n, hist):
+    """16-byte aligned, not 32."""
+    c = Case(34, BF16, 64, 64, [n], [hist])
+    for name in ("q", "out"):
+        t = getattr(c, name)
+        whole = torch.full((t.numel() + 16,), 5.0, dtype=torch.bfloat16, device="cuda")
+        view = whole[8:-8].view(t.shape)
+        view.copy_(t)
+        setattr(c, name, view)
+        setattr(c, name + "_whole", whole)
+    assert c.out.data_ptr() % 32 == 16
+    c.call().check()
+    assert bool((c.out_whole[:8] == 5).all()) and bool((c.out_whole[-8:] == 5).all())
+
+
 # ================================ read =========================================================
 
 def read_case(seed, dtype, page, lens, first, back=False, ratio=1, pad=0, gap=0, stream=None, layers=0):

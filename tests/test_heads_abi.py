@@ -1,12 +1,14 @@
 """Refusals of csa2_qk_norm_rope, csa2_paged_read and csa2_paged_chunk_attn: argument errors are found on
 the host, before anything is launched (no GPU is touched here)."""
 import ctypes
+import types
 
 import pytest
 import torch
 
 import csa2_compressed_sparse_gb300 as csa2
 from test_paged_abi import BAD_CACHES, cache
+from test_paged_binding import On
 
 P = ctypes.c_void_p(4096)
 
@@ -138,3 +140,79 @@ def test_the_binding_checks_its_tensors():
         csa2.csa2_qk_norm_rope(x, x, torch.zeros(2, dtype=torch.int64), torch.zeros(8))
     with pytest.raises(ValueError, match=r"\[T, H, D\]"):
         csa2.csa2_qk_norm_rope(x[0], x[0], torch.zeros(2, dtype=torch.int64), torch.zeros(8))
+
+
+# ---- tensors of another device than the cache's (nothing is called) --------------------------
+
+@pytest.fixture
+def recorded(monkeypatch):
+    seen = []
+    monkeypatch.setattr(csa2, "_call", lambda fn, dev, stream, *args: seen.append((fn, dev)))
+    table = torch.empty((2, 8), dtype=torch.int32, device="meta")
+    data = torch.empty((16, 64, 512), dtype=torch.bfloat16, device="meta")
+    fake = types.SimpleNamespace(_dev=1, table=table, data=data, c=lambda: None, _c=types.SimpleNamespace(B=2))
+    return fake, seen
+
+
+def tensors(device, T=3, H=4):
+    return dict(q=On.of(device, T, H, 512, dtype=torch.bfloat16), cu_seqlens=On.of(device, 3, dtype=torch.int32),
+                start_pos=On.of(device, 2, dtype=torch.int64), out=On.of(device, T, H, 512, dtype=torch.bfloat16),
+                ws=On.of(device, 1024), sink=On.of(device, H, dtype=torch.float32),
+                lse=On.of(device, T, H, dtype=torch.float32), inv_freq=On.of(device, 32, dtype=torch.float32))
+
+
+def test_the_caches_device_is_called(recorded):
+    fake, seen = recorded
+    csa2.csa2_paged_chunk_attn(cache=fake, **tensors(1))
+    csa2.csa2_paged_read(On.of(1, 5, 512, dtype=torch.bfloat16), tensors(1)["cu_seqlens"], tensors(1)["start_pos"],
+                         fake)
+    assert [d for _, d in seen] == [1, 1]
+
+
+@pytest.mark.parametrize("name", ["q", "cu_seqlens", "start_pos", "out", "ws", "sink", "lse", "inv_freq"])
+@pytest.mark.parametrize("device", [-1, 0])
+def test_chunk_tensors_elsewhere_are_refused(recorded, name, device):
+    with pytest.raises(ValueError, match=name):
+        csa2.csa2_paged_chunk_attn(cache=recorded[0], **{**tensors(1), name: tensors(device)[name]})
+    assert not recorded[1]
+
+
+@pytest.mark.parametrize("name,shape,dtype", [
+    ("q", (3, 512), torch.bfloat16), ("q", (3, 4, 256), torch.bfloat16), ("q", (3, 4, 512), torch.float16),
+    ("out", (2, 4, 512), torch.bfloat16), ("cu_seqlens", (2,), torch.int32), ("cu_seqlens", (3,), torch.int64),
+    ("start_pos", (2,), torch.int32), ("lse", (3, 5), torch.float32), ("sink", (5,), torch.float32),
+    ("inv_freq", (31,), torch.float32),
+])
+def test_chunk_shapes_are_refused(recorded, name, shape, dtype):
+    with pytest.raises(ValueError, match=name):
+        csa2.csa2_paged_chunk_attn(cache=recorded[0], **{**tensors(1), name: On.of(1, *shape, dtype=dtype)})
+    assert not recorded[1]
+
+
+@pytest.mark.parametrize("name,t", [
+    ("out", On.of(0, 5, 512, dtype=torch.bfloat16)), ("out", On.of(1, 5, 256, dtype=torch.bfloat16)),
+    ("out", On.of(1, 5, 512, dtype=torch.float32)), ("cu_seqlens", On.of(-1, 3, dtype=torch.int32)),
+    ("cu_seqlens", On.of(1, 2, dtype=torch.int32)), ("start_row", On.of(0, 2, dtype=torch.int64)),
+    ("start_row", On.of(1, 3, dtype=torch.int64)), ("inv_freq", On.of(0, 32, dtype=torch.float32)),
+])
+def test_read_tensors_are_refused(recorded, name, t):
+    a = dict(out=On.of(1, 5, 512, dtype=torch.bfloat16), cu_seqlens=On.of(1, 3, dtype=torch.int32),
+             start_row=On.of(1, 2, dtype=torch.int64), inv_freq=On.of(1, 32, dtype=torch.float32))
+    with pytest.raises(ValueError, match=name):
+        csa2.csa2_paged_read(cache=recorded[0], **{**a, name: t})
+    assert not recorded[1]
+
+
+@pytest.mark.parametrize("name", ["q_out", "pos", "inv_freq", "k", "k_out", "q_norm_w", "k_norm_w"])
+@pytest.mark.parametrize("device", [-1, 0])
+def test_head_tensors_elsewhere_are_refused(recorded, name, device):
+    def all_on(d):
+        a = {n: On.of(d, 3, h, 128, dtype=torch.bfloat16) for n, h in
+             (("q", 4), ("q_out", 4), ("k", 2), ("k_out", 2))}
+        return {**a, "pos": On.of(d, 3, dtype=torch.int64), "inv_freq": On.of(d, 16, dtype=torch.float32),
+                "q_norm_w": On.of(d, 128, dtype=torch.float32), "k_norm_w": On.of(d, 128, dtype=torch.float32)}
+    csa2.csa2_qk_norm_rope(**all_on(1))
+    assert len(recorded[1]) == 1
+    with pytest.raises(ValueError, match=name.replace("_out", "")):
+        csa2.csa2_qk_norm_rope(**{**all_on(1), name: all_on(device)[name]})
+    assert len(recorded[1]) == 1
