@@ -204,6 +204,7 @@ struct PagedAttnArgs {
 struct PagedReadArgs {
   uint16_t* out;
   const int64_t* row_end; // or null; rows from row_end[b] on, and those on bad pages, become zeros
+  uint16_t* low;          // or null: what FP8_S128 rows lose when rounded, rounded itself, as rows of out
   int64_t out_ld;         // elements from row to row
   int T;
   const int32_t* cu_seqlens;
@@ -270,7 +271,8 @@ struct ChunkArgs {
   float* part;            // [2 pairs][2 CTAs][64 float4 columns][128 lanes][4]
   float* pstat;           // [2 pairs][2 CTAs][m, l, r][64]
   // rows that are not read from their pages: staged as dense bf16 rows (stage null: none are)
-  uint16_t* stage;        // [stage_rows][512]
+  uint16_t* stage;        // [key_parts][stage_rows][512]
+  int key_parts;          // 2: the keys are the sum of the staged rows and those of the second part
   int64_t stage_rows;
   int32_t* stage_cu;      // [B + 1]
   int64_t* stage_first;   // [B]

@@ -20,6 +20,7 @@ namespace {
 // bytes moved: 1024 or 528 read, 1024 written per row.
 
 constexpr int kReadWarps = 4;
+constexpr int read_ctas(int mode) { return mode == 0 ? 4 : 5; }  // an SM, by registers
 
 __device__ __forceinline__ float2 e4m3x2(uint32_t two) {
   uint32_t h;
@@ -48,8 +49,9 @@ struct RowPart {
     if (kMode == 2) sc = __ldcs(src + 512 + (lane >> 1));
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); sc = 0u; }
-  // ang: cosine and sine of the row's 32 rotation pairs, or null.
-  __device__ __forceinline__ void store(uint16_t* dst, int lane, const float2* ang) const {
+  // ang: cosine and sine of the row's 32 rotation pairs, or null.  low: where what the rounding leaves of
+  // FP8_S128 values goes (nothing of those that overflow), or null.
+  __device__ __forceinline__ void store(uint16_t* dst, int lane, const float2* ang, uint16_t* low) const {
     if (kMode == 0) {
       uint4 w = b;
       if (ang && lane >= 24) {
@@ -84,12 +86,21 @@ struct RowPart {
       for (int i = 0; i < 8; ++i) o[i] = pack_bf16x2(y[i].x, y[i].y);
       __stcs(reinterpret_cast<uint4*>(dst) + 2 * lane, make_uint4(o[0], o[1], o[2], o[3]));
       __stcs(reinterpret_cast<uint4*>(dst) + 2 * lane + 1, make_uint4(o[4], o[5], o[6], o[7]));
+      if (kMode == 1 && low) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float h0 = __uint_as_float(o[i] << 16), h1 = __uint_as_float(o[i] & 0xFFFF0000u);
+          o[i] = pack_bf16x2(isfinite(h0) ? y[i].x - h0 : 0.f, isfinite(h1) ? y[i].y - h1 : 0.f);
+        }
+        __stcs(reinterpret_cast<uint4*>(low) + 2 * lane, make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(reinterpret_cast<uint4*>(low) + 2 * lane + 1, make_uint4(o[4], o[5], o[6], o[7]));
+      }
     }
   }
 };
 
 template <int kMode, int kTok>
-__global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadArgs a, int run) {
+__global__ void __launch_bounds__(kReadWarps * 32, read_ctas(kMode)) paged_read_kernel(PagedReadArgs a, int run) {
   griddep_launch_dependents();
   griddep_wait();
   __shared__ __align__(16) float2 ang_s[kReadWarps][kTok][32];
@@ -159,7 +170,8 @@ __global__ void __launch_bounds__(kReadWarps * 32) paged_read_kernel(PagedReadAr
       for (int i = 0; i < kTok; ++i) {
         const bool none = (skips >> ((i0 + i) & 31) & 1u) != 0;
         if (none || i0 + i >= n) continue;  // (the same in the warp)
-        cur[i].store(a.out + (t + i0 + i) * a.out_ld, lane, a.inv_freq ? ang_s[warp][i] : nullptr);
+        const int64_t at = (t + i0 + i) * a.out_ld;
+        cur[i].store(a.out + at, lane, a.inv_freq ? ang_s[warp][i] : nullptr, a.low ? a.low + at : nullptr);
       }
 #pragma unroll
       for (int i = 0; i < kTok; ++i) cur[i] = nxt[i];
@@ -645,9 +657,10 @@ __device__ __forceinline__ Places place_groups(const ChunkArgs& a, const ChunkTi
   return p;
 }
 
-// kAlone: without a plan, pair c works on tile c (an instance of its own: with its code in the other, FP8
-// chunks of four sequences took 1071 us in place of 1043)
-template <bool kAlone>
+// kAlone: without a plan, pair c works on tile c.  kParts: of the keys.  (Instances of their own, as code that is
+// not used lies in the way of what is: with kAlone's in it, ragged chunks took 531 us in place of 509, with
+// kParts as a number 525.)
+template <bool kAlone, int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -1086,15 +1099,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seg;
       }
 #pragma unroll 1
-      for (int k = 0; k < kSlots; ++k) {
-        ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)rev & 1));
+      for (int n = 0; n < kSlots * kParts; ++n) {
+        const int k = kParts == 1 ? n : n & (kSlots - 1);
+        ok = ok && all_ok(wait_phase(X, X.full[k], (uint32_t)(kParts == 1 ? rev : rev + n / kSlots) & 1));
         if (!ok) break;
         tc_fence_after();
         if (lead) {
 #pragma unroll
           for (int s = 0; s < 4; ++s)
             umma_pair_bf16(tmem + kColS + 128 * (c & 1), q_d + ((k * 8192 + s * 32) >> 4),
-                           k_d + ((k * kSlotBytes + s * 32) >> 4), id_s, k > 0 || s > 0);
+                           k_d + ((k * kSlotBytes + s * 32) >> 4), id_s, n > 0 || s > 0);
           umma_commit_pair(smem_u32(&X.empty[k]));
         }
         __syncwarp();
@@ -1105,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kind & kStepLast) umma_commit_pair(smem_u32(&X.q_empty));
       }
       __syncwarp();
-      ++rev;
+      rev += kParts;
       if (c > 0) values(c - 1, run, masked);
       run = i & (kRun - 1);
       masked = (kind & kStepMasked) != 0;
@@ -1155,29 +1169,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int rev = 0, c = 0, seg = 0, n_last = 0;
     int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
-    // Eight slots, each in pieces of box_rows rows, one a lane.
+    // Eight slots (of keys in two parts: those of each), each in pieces of box_rows rows, one a lane.
     auto slots = [&](const Places& at, const CUtensorMap* map, bool values) {
+      const int count = values ? kSlots : kSlots * kParts;
       const int piece = lane << lg;
       const bool mine = piece < (values ? 64 : 128);
       const uint32_t dst = ring + (uint32_t)piece * (values ? 256 : 128);
       int g = (16 * (int)rank + (piece >> 3)) & 31;
       int32_t y = __shfl_sync(0xFFFFFFFFu, at.y, g), z = __shfl_sync(0xFFFFFFFFu, at.z, g);
 #pragma unroll 1
-      for (int k = k0; k < kSlots; k += kLoadWarps) {
+      for (int n = k0; n < count; n += kLoadWarps) {
+        const int k = kParts == 1 ? n : n & (kSlots - 1), r = kParts == 1 ? rev : rev + n / kSlots;
         if (values) {
           g = (8 * (k >> 1) + (piece >> 3)) & 31;
           y = __shfl_sync(0xFFFFFFFFu, at.y, g);
           z = __shfl_sync(0xFFFFFFFFu, at.z, g);
         }
-        if (rev > 0) ok = ok && all_ok(wait_phase(X, X.empty[k], (uint32_t)(rev - 1) & 1));
+        if (r > 0) ok = ok && all_ok(wait_phase(X, X.empty[k], (uint32_t)(r - 1) & 1));
         if (!ok) return;
         if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&X.full[k]), 2 * kSlotBytes);
         if (mine)
-          tma_load_5d_pair(dst + k * kSlotBytes, map, values ? 4 * (k & 1) + 2 * (int)rank : k, y, z,
+          tma_load_5d_pair(dst + k * kSlotBytes, map, values ? 4 * (k & 1) + 2 * (int)rank : k, y, kParts == 1 ? z : z + n / kSlots,
                            full + 8 * k, pol);
         __syncwarp();
       }
-      ++rev;
+      rev += kParts == 1 || values ? 1 : kParts;
     };
     // The places of the walk's key tile (a segment's first: with its bounds).
     auto places = [&]() {
@@ -1345,10 +1361,10 @@ namespace {
 
 template <int kMode>
 cudaError_t launch_read(const PagedReadArgs& a, int sms, cudaStream_t s) {
-  // Runs of up to 32 rows, as many to each warp of a grid that stays (five CTAs an SM, by registers).
-  const int64_t warps = (int64_t)sms * 5 * kReadWarps, passes = ((int64_t)a.T + warps * 32 - 1) / (warps * 32);
+  // Runs of up to 32 rows, as many to each warp of a grid that stays.
+  const int64_t most = (int64_t)sms * read_ctas(kMode), warps = most * kReadWarps, passes = ((int64_t)a.T + warps * 32 - 1) / (warps * 32);
   const int run = (int)(((int64_t)a.T + warps * passes - 1) / (warps * passes));
-  const int64_t need = ((int64_t)a.T + kReadWarps * run - 1) / (kReadWarps * run), most = (int64_t)sms * 5;
+  const int64_t need = ((int64_t)a.T + kReadWarps * run - 1) / (kReadWarps * run);
   const dim3 grid((unsigned)(need < most ? need : most));
   return run >= 4 ? launch_pdl(paged_read_kernel<kMode, 4>, grid, dim3(kReadWarps * 32), 0, s, a, run)
                   : launch_pdl(paged_read_kernel<kMode, 1>, grid, dim3(kReadWarps * 32), 0, s, a, run);
@@ -1372,7 +1388,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
   if (!encode_rows_bf16(&qm, a.q, (uint64_t)a.T * a.H, kDLat, 64, 64)) return cudaErrorInvalidValue;
   // a page (or all staged rows) as [8-row groups][8 dim blocks][8 rows][128 bytes]
   const uint64_t groups = a.stage ? (uint64_t)a.stage_rows / 8 : (uint64_t)a.cache.page_rows / 8;
-  const uint64_t dims[5] = {128, 8, 8, groups, a.stage ? 1 : (uint64_t)a.cache.n_pages};
+  const uint64_t dims[5] = {128, 8, 8, groups, a.stage ? (uint64_t)a.key_parts : (uint64_t)a.cache.n_pages};
   const uint64_t strides[4] = {1024, 128, 8192,
                                a.stage ? groups * 8192 : (uint64_t)a.cache.page_stride};
   const uint32_t kbox[5] = {128, 8, 1, (uint32_t)a.box_rows / 8, 1};
@@ -1387,6 +1403,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
     PagedReadArgs r{};
     r.out = a.stage;
     r.out_ld = kDLat;
+    r.low = a.key_parts == 2 ? a.stage + a.stage_rows * kDLat : nullptr;
     r.T = (int)a.stage_rows;
     r.row_end = a.stage_end;
     r.cu_seqlens = a.stage_cu;
@@ -1399,7 +1416,9 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
     e = launch_paged_read(r, sms, s);
     if (e != cudaSuccess) return e;
   }
-  auto kern = a.alone ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
+  auto kern = a.alone            ? chunk_attn_kernel<true, 1>
+              : a.key_parts == 1 ? chunk_attn_kernel<false, 1>
+                                 : chunk_attn_kernel<false, 2>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl_cluster(kern, dim3(2u * a.pairs), dim3(kThreads), kSmem, s, 2u, a, qm, km, vm);

@@ -1,8 +1,8 @@
 """Chunks of new tokens over the paged cache, and its rows read back, against their formulas in 64 bits.
 
-Tolerances, with those of test_gpu_paged.py for products, weights and lse.  FP8_S128 rows may be rounded
-to bf16 on the way (2^-8 of each value, which bf16 and FP8_E8M0 rows are exactly): a score is then off by
-a further 2^-8 scale sum |q x|, the output by a further 2^-8 of the mean of |x|.
+Tolerances, with those of test_gpu_paged.py for products, weights and lse.  FP8_S128 rows are rounded to
+bf16 on the way (which bf16 and FP8_E8M0 rows are exactly): as values once (2^-8: the output is off by a further
+2^-8 of the mean of |x|), as keys in two parts (2^-8 of 2^-8: a score by a further 2^-16 scale sum |q x|).
 Read back: code times scale in fp32 (2^-24), the rotation 2^-20 (|x0| + |x1|), then bf16's 2^-8."""
 import numpy as np
 import pytest
@@ -39,7 +39,7 @@ def check_tokens(out, lse, q, x, lo, hi, sink, scale, pos, rope, dtype):
     s = (scale * qd @ x.T).masked_fill(~seen, -np.inf)
     size = abs(scale) * (qd.abs() @ xa.T).masked_fill(~seen, 0.0)
     extra = 2.0 ** -8 if dtype == S128 else 0.0
-    tau = (512 * 2.0 ** -23 + extra) * (size.amax(1) if x.shape[0] else torch.zeros(n * H, device="cuda"))
+    tau = (512 * 2.0 ** -23 + extra ** 2) * (size.amax(1) if x.shape[0] else torch.zeros(n * H, device="cuda"))
     tau = tau.double()
     full = s if sink is None else torch.cat([s, sink.double().repeat(n)[:, None]], 1)
     z = torch.logsumexp(full, 1) if full.shape[1] else torch.full((n * H,), -np.inf, device="cuda",
@@ -147,6 +147,32 @@ def test_head_counts(dtype, H):
 @pytest.mark.parametrize("page", [8, 16, 24, 32, 48, 64, 72, 128, 256, 1000])
 def test_page_sizes(dtype, page):
     Case(page, dtype, 64, page, [7, 30], [650, 300]).call().check()
+
+
+def test_keys_of_codes_and_scales_are_not_rounded_once():
+    """FP8_S128 rows with scales of a full mantissa.  One row is seen and no sink, so lse is its score:
+    rounded once it would be some 2^-10 of sum |q x| off."""
+    c = Case(40, S128, 64, 64, [1], [0], sink=None, spread=1.2345678).call().check()
+    c2 = Case(41, S128, 64, 64, [1] * 30, [0] * 30, sink=None, spread=3.1).call().check()
+    for d in (c, c2):
+        for b in range(d.B):
+            x = decode(get(d.data, d.table, b, 0, 1), S128)[0]
+            s = d.q[b].double() @ x * d.scale
+            size = d.q[b].double().abs() @ x.abs() * d.scale
+            assert bool(((d.lse[b].double() - s).abs() <= (2.0 ** -16 + 512 * 2.0 ** -23) * size + 2.0 ** -19).all())
+
+
+def test_scales_at_the_ends_of_the_range():
+    """FP8_S128 rows whose values overflow bf16 when rounded give infinite scores, not others' NaN."""
+    c = Case(42, S128, 64, 64, [9], [300])
+    row = get(c.data, c.table, 0, 305, 306).clone()
+    row[0, 512:516] = torch.tensor([3.0e38], device="cuda").view(torch.uint8)
+    put(c.data, c.table, 0, row, first=305)
+    x = decode(get(c.data, c.table, 0, 0, 309), S128)
+    c.call()
+    torch.cuda.synchronize()
+    p, lo, hi = c.seen(0)
+    check_tokens(c.out[:5], c.lse[:5], c.q[:5], x[:305], lo[:5], hi[:5], c.sink, c.scale, p[:5], True, S128)
 
 
 @pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 63, 64, 65, 127, 128, 129])
