@@ -271,8 +271,8 @@ struct ChunkArgs {
   float* part;            // [2 pairs][2 CTAs][64 float4 columns][128 lanes][4]
   float* pstat;           // [2 pairs][2 CTAs][m, l, r][64]
   // rows that are not read from their pages: staged as dense bf16 rows (stage null: none are)
-  uint16_t* stage;        // [key_parts][stage_rows][512]
-  int key_parts;          // 2: the keys are the sum of the staged rows and those of the second part
+  uint16_t* stage;        // [parts][stage_rows][512]
+  int parts;              // 2: a row is the sum of both parts'
   int64_t stage_rows;
   int32_t* stage_cu;      // [B + 1]
   int64_t* stage_first;   // [B]

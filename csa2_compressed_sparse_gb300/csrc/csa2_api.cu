@@ -860,7 +860,7 @@ struct ChunkWs {
   int max_tiles, pairs;
   bool split;      // a tile may need parts
   int64_t rows;    // staged
-  int parts;       // of the keys
+  int parts;       // whose sum the staged rows are
 };
 // Rows that a tensor copy brings at once: the largest of 64, 32, 16, 8 dividing page_rows.
 int page_box(int page_rows) {
@@ -890,9 +890,9 @@ ChunkWs chunk_ws_layout(int T, int H, const csa2_paged& c, int64_t max_rows, int
   w.split = tiles > csa2::chunk_max_pairs() || keys > csa2::chunk_whole_keys();
   const int64_t most = w.split ? tiles * keys : tiles;
   w.pairs = (int)(most < csa2::chunk_max_pairs() ? most : csa2::chunk_max_pairs());
-  // A code of four bits times a scale of 24 is more than bf16 holds: the keys of FP8_S128 rows are staged in two
-  // parts, the value rounded and what that leaves, rounded (2^-16 of the value in all; in one part, 2^-8,
-  // lse came out 1e-5 off).  For the values one part does: out is rounded so itself.
+  // A code of four bits times a scale of 24 is more than bf16 holds: FP8_S128 rows are staged in two parts, the
+  // value rounded and what that leaves, rounded, 2^-16 off in all.  In one part lse came out 1e-5 off and out
+  // half as far again as that of bf16 rows; four chunks over 16000 rows took 1040 us in place of 2010.
   w.parts = c.dtype == CSA2_SWA_FP8_S128 ? 2 : 1;
   size_t o = 0;
   w.tile = o; o = up256(o + (size_t)tiles * sizeof(csa2::ChunkTile));
@@ -979,7 +979,7 @@ csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_
     a.pstat = reinterpret_cast<float*>(base + w.pstat);
   }
   a.box_rows = page_box(a.cache.page_rows);
-  a.key_parts = w.parts;
+  a.parts = w.parts;
   if (w.rows > 0) {
     a.box_rows = 64;
     a.stage = reinterpret_cast<uint16_t*>(base + w.stage);

@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(kReadWarps * 32, read_ctas(kMode)) paged_read_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = (int64_t)gridDim.x * kReadWarps * run;
   const uint64_t turn = a.inv_freq ? rope_turn(a.inv_freq[lane]) : 0;
-  const int64_t total = min((int64_t)a.T, (int64_t)a.cu_seqlens[a.cache.B]);
+  // (with row_end a key tile's length more, which a tile that ends there reads)
+  const int64_t total = min((int64_t)a.T, (int64_t)a.cu_seqlens[a.cache.B] + (a.row_end ? 256 : 0));
   for (int64_t t = ((int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * run; t < total; t += step) {
     // lane l: row t + l
     const int n = (int)min(total - t, (int64_t)run);
@@ -657,7 +658,7 @@ __device__ __forceinline__ Places place_groups(const ChunkArgs& a, const ChunkTi
   return p;
 }
 
-// kAlone: without a plan, pair c works on tile c.  kParts: of the keys.  (Instances of their own, as code that is
+// kAlone: without a plan, pair c works on tile c.  kParts: of a staged row.  (Instances of their own, as code that is
 // not used lies in the way of what is: with kAlone's in it, ragged chunks took 531 us in place of 509, with
 // kParts as a number 525.)
 template <bool kAlone, int kParts>
@@ -1063,25 +1064,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
+      for (int n = 0; n < 4 * kParts; ++n) {
+        const int b = n & 3;
         ok = ok && all_ok(wait_phase<true>(X, X.p_full[b], (uint32_t)c & 1));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          ok = ok && all_ok(wait_phase(X, X.full[2 * b + h], (uint32_t)rev & 1));
+          ok = ok && all_ok(wait_phase(X, X.full[2 * b + h], (uint32_t)(kParts == 1 ? rev : rev + n / 4) & 1));
           if (!ok) return;
           tc_fence_after();
           if (lead) {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
               umma_pair_bf16(tmem + 128 * h, p_d + ((b * 8192 + s * 32) >> 4),
-                             v_d + (((2 * b + h) * kSlotBytes + s * 4096) >> 4), id_o, run > 0 || b > 0 || s > 0);
+                             v_d + (((2 * b + h) * kSlotBytes + s * 4096) >> 4), id_o, run > 0 || n > 0 || s > 0);
             umma_commit_pair(smem_u32(&X.empty[2 * b + h]));
-            if (h == 1) umma_commit_pair(smem_u32(&X.p_free[b]));
+            if (h == 1 && n >= 4 * (kParts - 1)) umma_commit_pair(smem_u32(&X.p_free[b]));
           }
           __syncwarp();
         }
       }
-      ++rev;
+      rev += kParts;
     };
     int c = 0, seg = 0, run = 0;
     bool masked = false;
@@ -1169,9 +1171,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int rev = 0, c = 0, seg = 0, n_last = 0;
     int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;
-    // Eight slots (of keys in two parts: those of each), each in pieces of box_rows rows, one a lane.
+    // Eight slots of each part, each in pieces of box_rows rows, one a lane.
     auto slots = [&](const Places& at, const CUtensorMap* map, bool values) {
-      const int count = values ? kSlots : kSlots * kParts;
+      constexpr int count = kSlots * kParts;
       const int piece = lane << lg;
       const bool mine = piece < (values ? 64 : 128);
       const uint32_t dst = ring + (uint32_t)piece * (values ? 256 : 128);
@@ -1193,7 +1195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            full + 8 * k, pol);
         __syncwarp();
       }
-      rev += kParts == 1 || values ? 1 : kParts;
+      rev += kParts;
     };
     // The places of the walk's key tile (a segment's first: with its bounds).
     auto places = [&]() {
@@ -1388,7 +1390,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
   if (!encode_rows_bf16(&qm, a.q, (uint64_t)a.T * a.H, kDLat, 64, 64)) return cudaErrorInvalidValue;
   // a page (or all staged rows) as [8-row groups][8 dim blocks][8 rows][128 bytes]
   const uint64_t groups = a.stage ? (uint64_t)a.stage_rows / 8 : (uint64_t)a.cache.page_rows / 8;
-  const uint64_t dims[5] = {128, 8, 8, groups, a.stage ? (uint64_t)a.key_parts : (uint64_t)a.cache.n_pages};
+  const uint64_t dims[5] = {128, 8, 8, groups, a.stage ? (uint64_t)a.parts : (uint64_t)a.cache.n_pages};
   const uint64_t strides[4] = {1024, 128, 8192,
                                a.stage ? groups * 8192 : (uint64_t)a.cache.page_stride};
   const uint32_t kbox[5] = {128, 8, 1, (uint32_t)a.box_rows / 8, 1};
@@ -1403,7 +1405,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
     PagedReadArgs r{};
     r.out = a.stage;
     r.out_ld = kDLat;
-    r.low = a.key_parts == 2 ? a.stage + a.stage_rows * kDLat : nullptr;
+    r.low = a.parts == 2 ? a.stage + a.stage_rows * kDLat : nullptr;
     r.T = (int)a.stage_rows;
     r.row_end = a.stage_end;
     r.cu_seqlens = a.stage_cu;
@@ -1417,7 +1419,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   auto kern = a.alone            ? chunk_attn_kernel<true, 1>
-              : a.key_parts == 1 ? chunk_attn_kernel<false, 1>
+              : a.parts == 1 ? chunk_attn_kernel<false, 1>
                                  : chunk_attn_kernel<false, 2>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;

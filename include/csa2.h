@@ -624,8 +624,8 @@ csa2_status csa2_paged_read(csa2_bf16* out, int64_t out_ld, int T, const int32_t
  *     s_j = scale * <q[t][h], x_j>, lo <= j < hi;   Z = e^{sink[h]} + sum_j e^{s_j}
  *     out_h = sum_j e^{s_j} x_j / Z,   lse_h = ln Z
  * in fp32 sums of bf16 products, the weights e^{s_j - m} rounded to bf16 for the second.  FP8_S128
- * rows (code * scale) are rounded to bf16 as values, and as keys in two parts, 2^-16 of the value off;
- * rows of the other types are exact.
+ * rows (code * scale) are the sum of two bf16 parts, 2^-16 off, which doubles the work; rows of the
+ * other types are exact in one.
  *   q, out       [T][H][512] bf16;  T 0 .. 1048576;  H 1 .. 128
  *   cu_seqlens   [cache->B + 1] int32, non-decreasing, cu_seqlens[0] == 0; empty sequences are
  *                fine.  Tokens from cu_seqlens[B] on (a padded batch) keep their out and lse

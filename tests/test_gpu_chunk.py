@@ -1,8 +1,8 @@
 """Chunks of new tokens over the paged cache, and its rows read back, against their formulas in 64 bits.
 
 Tolerances, with those of test_gpu_paged.py for products, weights and lse.  FP8_S128 rows are rounded to
-bf16 on the way (which bf16 and FP8_E8M0 rows are exactly): as values once (2^-8: the output is off by a further
-2^-8 of the mean of |x|), as keys in two parts (2^-8 of 2^-8: a score by a further 2^-16 scale sum |q x|).
+bf16 in two parts on the way, 2^-8 of 2^-8 off (the others are exact in one): a score is off by a further
+2^-16 scale sum |q x|, the output by a further 2^-16 of the mean of |x|.
 Read back: code times scale in fp32 (2^-24), the rotation 2^-20 (|x0| + |x1|), then bf16's 2^-8."""
 import numpy as np
 import pytest
@@ -38,8 +38,8 @@ def check_tokens(out, lse, q, x, lo, hi, sink, scale, pos, rope, dtype):
     seen = ((j >= lo[:, None]) & (j < hi[:, None]))[:, None].expand(n, H, -1).reshape(n * H, -1)
     s = (scale * qd @ x.T).masked_fill(~seen, -np.inf)
     size = abs(scale) * (qd.abs() @ xa.T).masked_fill(~seen, 0.0)
-    extra = 2.0 ** -8 if dtype == S128 else 0.0
-    tau = (512 * 2.0 ** -23 + extra ** 2) * (size.amax(1) if x.shape[0] else torch.zeros(n * H, device="cuda"))
+    extra = 2.0 ** -16 if dtype == S128 else 0.0
+    tau = (512 * 2.0 ** -23 + extra) * (size.amax(1) if x.shape[0] else torch.zeros(n * H, device="cuda"))
     tau = tau.double()
     full = s if sink is None else torch.cat([s, sink.double().repeat(n)[:, None]], 1)
     z = torch.logsumexp(full, 1) if full.shape[1] else torch.full((n * H,), -np.inf, device="cuda",
@@ -149,7 +149,7 @@ def test_page_sizes(dtype, page):
     Case(page, dtype, 64, page, [7, 30], [650, 300]).call().check()
 
 
-def test_keys_of_codes_and_scales_are_not_rounded_once():
+def test_codes_times_scales_are_not_rounded_once():
     """FP8_S128 rows with scales of a full mantissa.  One row is seen and no sink, so lse is its score:
     rounded once it would be some 2^-10 of sum |q x| off."""
     c = Case(40, S128, 64, 64, [1], [0], sink=None, spread=1.2345678).call().check()
@@ -160,6 +160,8 @@ def test_keys_of_codes_and_scales_are_not_rounded_once():
             s = d.q[b].double() @ x * d.scale
             size = d.q[b].double().abs() @ x.abs() * d.scale
             assert bool(((d.lse[b].double() - s).abs() <= (2.0 ** -16 + 512 * 2.0 ** -23) * size + 2.0 ** -19).all())
+            # its weight is one: the output is the row (rotated back from position 0), rounded once
+            assert bool(((d.out[b].double() - x).abs() <= (2.0 ** -8 + 2.0 ** -16 + 2.0 ** -19) * x.abs()).all())
 
 
 def test_scales_at_the_ends_of_the_range():
