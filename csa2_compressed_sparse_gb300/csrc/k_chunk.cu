@@ -332,11 +332,14 @@ __device__ __forceinline__ bool token_rows(const ChunkArgs& a, int64_t p, int64_
 // share.  Up to as many tiles as pairs, none longer than kWhole, go to a pair each.  Otherwise the cost of
 // all tiles, 2 a key tile and kTileCost a tile (what begins and ends it takes as long as 1.5 key tiles), is
 // cut evenly: pair c begins at cost W c / C, C as many pairs as leave each kShare key tiles or a tile.  A cut
-// within the first kTileCost of a tile is one before it.
-constexpr int kPlanThreads = 1024, kMaxPairs = 76;
+// within the first kTileCost of a tile is one before it.  Up to kPlanFew tiles and sequences are planned by as
+// many threads, whose barriers are shorter (with the fewer CTAs of the join: 35 sequences of two tokens 40.1 ->
+// 36.5 us, 45 of eight 44.7 -> 40.4).
+constexpr int kPlanThreads = 1024, kPlanFew = 256, kMaxPairs = 76;
 constexpr int kWhole = 6, kShare = 4, kTileCost = 3;
 
 // Exclusive prefix of x over the CTA's threads; *total gets the sum.
+template <int kN>
 __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* sums, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t y = x;
@@ -348,7 +351,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t x, int64_t* sums, int64_t* 
   if (lane == 31) sums[warp] = y;
   __syncthreads();
   if (warp == 0) {
-    int64_t v = sums[lane];
+    int64_t v = lane < kN / 32 ? sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t z = __shfl_up_sync(0xFFFFFFFFu, v, o);
@@ -389,11 +392,12 @@ __device__ __forceinline__ bool make_tile(const ChunkArgs& a, ChunkTile& t, int 
   return over;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
+template <int kN>
+__global__ void __launch_bounds__(kN) chunk_plan_kernel(ChunkArgs a) {
   constexpr int kTiles = 4;  // of a thread at a time, at most
   __shared__ int64_t sums[32];
-  __shared__ int tile0[kPlanThreads], tok0[kPlanThreads], count[kPlanThreads], clip[kPlanThreads];
-  __shared__ int64_t off[kPlanThreads], start[kPlanThreads];
+  __shared__ int tile0[kN], tok0[kN], count[kN], clip[kN];
+  __shared__ int64_t off[kN], start[kN];
   __shared__ int cut_tile[kMaxPairs + 1], cut_at[kMaxPairs + 1];
   __shared__ int64_t cut_keys[kMaxPairs + 1];
   __shared__ int longest, splits;
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
   int64_t tiles = 0, units = 0, staged = 0;
   int most = 0;
   const int B = a.cache.B;
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < B; b0 += kN) {
     const int b = b0 + tid;
     int t0 = 0, n = 0, c = (int)a.cap_rows;
     int64_t s = 0, first = 0, len = 0, end = 0;
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
     }
     int64_t total = 0;
     if (a.stage) {
-      const int64_t at = staged + plan_scan(len, sums, &total);
+      const int64_t at = staged + plan_scan<kN>(len, sums, &total);
       if (at + len > a.stage_rows) {  // more rows than announced
         raise_fault(kFaultBounds);
         len = max((int64_t)0, a.stage_rows - at) & ~(int64_t)7;
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
       off[tid] = 0;
     }
     const int64_t nt = ((int64_t)n * a.H + kQRows - 1) / kQRows;
-    const int64_t mine = plan_scan(nt, sums, &total);
+    const int64_t mine = plan_scan<kN>(nt, sums, &total);
     tile0[tid] = (int)mine;
     tok0[tid] = t0;
     count[tid] = n;
@@ -449,10 +453,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
     start[tid] = s;
     __syncthreads();
     const int here = (int)total;
-    const int per = here > kPlanThreads ? kTiles : 1;
-    for (int x0 = 0; x0 < here; x0 += per * kPlanThreads) {
+    const int per = here > kN ? kTiles : 1;
+    for (int x0 = 0; x0 < here; x0 += per * kN) {
       const int x = x0 + per * tid;
-      int i = 0, e = kPlanThreads;  // the last sequence with tile0 <= x
+      int i = 0, e = kN;  // the last sequence with tile0 <= x
       while (e - i > 1) {
         const int m = (i + e) >> 1;
         if (tile0[m] <= x) i = m;
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
       for (int q = 0; q < kTiles; ++q) {
         cost[q] = 0;
         if (q < per && x + q < here && tiles + x + q < a.max_tiles) {
-          while (i + 1 < kPlanThreads && tile0[i + 1] <= x + q) ++i;  // (past empty sequences)
+          while (i + 1 < kN && tile0[i + 1] <= x + q) ++i;  // (past empty sequences)
           ChunkTile t{};
           if (make_tile(a, t, b0 + i, tok0[i], count[i], start[i], off[i], clip[i], x + q - tile0[i]) &&
               clip[i] == a.cap_rows)
@@ -474,7 +478,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
         }
         sum += cost[q];
       }
-      int64_t before = units + plan_scan(sum, sums, &total);
+      int64_t before = units + plan_scan<kN>(sum, sums, &total);
 #pragma unroll
       for (int q = 0; q < kTiles; ++q) {
         if (cost[q]) a.prefix[tiles + x + q] = before;
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(ChunkArgs a) {
   // Where each pair begins: the last tile that does at or before its cut, searched for in every so manieth
   // tile's prefix first.
   int64_t* sample = start;
-  const int64_t every = (n + kPlanThreads - 1) / kPlanThreads;
+  const int64_t every = (n + kN - 1) / kN;
   if (tid * every < n) sample[tid] = a.prefix[tid * every];
   __syncthreads();
   if (tid <= C) {
@@ -1266,7 +1270,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A tile that pairs c0 .. c1 worked on: with M the largest running maximum (and the sink's logit) of
 // a row, out = sum 2^(m - M) O / Z.  kJoin CTAs a tile, a thread 16 bytes of every part at a time.  Bound by
 // the parts' way from L2.
-constexpr int kJoin = 64;
+// At most kJoinFew tiles at a time after a small plan: a CTA without a tile takes its time, too.
+constexpr int kJoin = 64, kJoinFew = 16;
 
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
   __shared__ float wt[kMaxPairs][64];
@@ -1274,87 +1279,90 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs a) {
   __shared__ float inv[64];
   griddep_launch_dependents();
   griddep_wait();
-  if ((int)blockIdx.y >= a.split[0]) return;
-  const ChunkTile t = a.tile[a.split[1 + blockIdx.y]];
-  const int tid = threadIdx.x, n = min(t.c1 - t.c0 + 1, kMaxPairs);
-  const int rank = blockIdx.x / (kJoin / 2);  // the CTA whose 64 rows these are
-  auto slot = [&](int i) -> int64_t { return (2 * (int64_t)(t.c0 + i) + (i == 0 ? 1 : 0)) * 2 + rank; };
-  const int row = tid & 63, quarter = tid >> 6, r = 64 * rank + row;
-  const int grow = t.row0 + min(r, t.rows - 1), h = grow % a.H;
-  const bool live = r < t.rows;
-  {
-    float m = -INFINITY;
-    for (int i = quarter; i < n; i += 4) {
-      const float x = a.pstat[slot(i) * 192 + row];
-      wt[i][row] = x;
-      m = fmaxf(m, x);
-    }
-    red[0][quarter][row] = m;
-    __syncthreads();
-    const float logit = a.sink ? a.sink[h] : -INFINITY, sink = sink_log2(logit);
-    float M = sink;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) M = fmaxf(M, red[0][k][row]);
-    const float Mf = M == -INFINITY ? 0.f : M;
-    float l = 0.f, z = 0.f;
-    for (int i = quarter; i < n; i += 4) {
-      const float e = ex2(wt[i][row] - Mf);
-      wt[i][row] = e;
-      l = fmaf(e, a.pstat[slot(i) * 192 + 64 + row], l);
-      z = fmaf(e, a.pstat[slot(i) * 192 + 128 + row], z);
-    }
-    red[1][quarter][row] = l;
-    red[2][quarter][row] = z;
-    __syncthreads();
-    if (quarter == 0) {
-      l = red[1][0][row] + red[1][1][row] + red[1][2][row] + red[1][3][row];
-      z = red[2][0][row] + red[2][1][row] + red[2][2][row] + red[2][3][row];
-      const float rows = l;
-      if (sink > -INFINITY) {
-        l += ex2(sink - Mf);
-        z += ex2(sink - Mf);
+  const int tid = threadIdx.x, splits = a.split[0];
+  for (int y = blockIdx.y; y < splits; y += gridDim.y) {
+    const ChunkTile t = a.tile[a.split[1 + y]];
+    const int n = min(t.c1 - t.c0 + 1, kMaxPairs);
+    const int rank = blockIdx.x / (kJoin / 2);  // the CTA whose 64 rows these are
+    auto slot = [&](int i) -> int64_t { return (2 * (int64_t)(t.c0 + i) + (i == 0 ? 1 : 0)) * 2 + rank; };
+    const int row = tid & 63, quarter = tid >> 6, r = 64 * rank + row;
+    const int grow = t.row0 + min(r, t.rows - 1), h = grow % a.H;
+    const bool live = r < t.rows;
+    {
+      float m = -INFINITY;
+      for (int i = quarter; i < n; i += 4) {
+        const float x = a.pstat[slot(i) * 192 + row];
+        wt[i][row] = x;
+        m = fmaxf(m, x);
       }
-      inv[row] = z > 0.f || z != z ? 1.f / z : 0.f;
-      if (a.lse && live && blockIdx.x % (kJoin / 2) == 0) a.lse[grow] = head_lse(Mf, l, rows, logit);
+      red[0][quarter][row] = m;
+      __syncthreads();
+      const float logit = a.sink ? a.sink[h] : -INFINITY, sink = sink_log2(logit);
+      float M = sink;
+  #pragma unroll
+      for (int k = 0; k < 4; ++k) M = fmaxf(M, red[0][k][row]);
+      const float Mf = M == -INFINITY ? 0.f : M;
+      float l = 0.f, z = 0.f;
+      for (int i = quarter; i < n; i += 4) {
+        const float e = ex2(wt[i][row] - Mf);
+        wt[i][row] = e;
+        l = fmaf(e, a.pstat[slot(i) * 192 + 64 + row], l);
+        z = fmaf(e, a.pstat[slot(i) * 192 + 128 + row], z);
+      }
+      red[1][quarter][row] = l;
+      red[2][quarter][row] = z;
+      __syncthreads();
+      if (quarter == 0) {
+        l = red[1][0][row] + red[1][1][row] + red[1][2][row] + red[1][3][row];
+        z = red[2][0][row] + red[2][1][row] + red[2][2][row] + red[2][3][row];
+        const float rows = l;
+        if (sink > -INFINITY) {
+          l += ex2(sink - Mf);
+          z += ex2(sink - Mf);
+        }
+        inv[row] = z > 0.f || z != z ? 1.f / z : 0.f;
+        if (a.lse && live && blockIdx.x % (kJoin / 2) == 0) a.lse[grow] = head_lse(Mf, l, rows, logit);
+      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
-  // 8192 float4 of this CTA's rows, columns by kJoin / 2 CTAs
-  for (int x = (blockIdx.x % (kJoin / 2)) * 256 + tid; x < 8192; x += 256 * (kJoin / 2)) {
-    const int L = x & 127, col = x >> 7;
-    const float4* p = reinterpret_cast<const float4*>(a.part) + col * 128 + L;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float4 v = p[slot(i) * 8192];
-      const float e = wt[i][row];
-      // (a part that saw nothing has weight zero and may hold anything finite)
-      o.x = fmaf(v.x, e, o.x);
-      o.y = fmaf(v.y, e, o.y);
-      o.z = fmaf(v.z, e, o.z);
-      o.w = fmaf(v.w, e, o.w);
+    // 8192 float4 of this CTA's rows, columns by kJoin / 2 CTAs
+    for (int x = (blockIdx.x % (kJoin / 2)) * 256 + tid; x < 8192; x += 256 * (kJoin / 2)) {
+      const int L = x & 127, col = x >> 7;
+      const float4* p = reinterpret_cast<const float4*>(a.part) + col * 128 + L;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float4 v = p[slot(i) * 8192];
+        const float e = wt[i][row];
+        // (a part that saw nothing has weight zero and may hold anything finite)
+        o.x = fmaf(v.x, e, o.x);
+        o.y = fmaf(v.y, e, o.y);
+        o.z = fmaf(v.z, e, o.z);
+        o.w = fmaf(v.w, e, o.w);
+      }
+      const int d = (col >> 5) * 256 + (L >> 6) * 128 + ((col >> 4) & 1) * 64 + 4 * (col & 15);
+      const float f = inv[row];
+      o.x *= f;
+      o.y *= f;
+      o.z *= f;
+      o.w *= f;
+      if (a.inv_freq && d >= kRopeDim0) {
+        const uint64_t pos = (uint64_t)(t.start + (grow / a.H - t.tok0));
+        float sn, cs;
+        sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), pos), &sn, &cs);
+        float z = o.x * cs + o.y * sn;
+        o.y = o.y * cs - o.x * sn;
+        o.x = z;
+        sincosf(rope_angle(rope_turn(a.inv_freq[((d - kRopeDim0) >> 1) + 1]), pos), &sn, &cs);
+        z = o.z * cs + o.w * sn;
+        o.w = o.w * cs - o.z * sn;
+        o.z = z;
+      }
+      if (live)
+        *reinterpret_cast<uint2*>(a.out + (int64_t)grow * kDLat + d) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     }
-    const int d = (col >> 5) * 256 + (L >> 6) * 128 + ((col >> 4) & 1) * 64 + 4 * (col & 15);
-    const float f = inv[row];
-    o.x *= f;
-    o.y *= f;
-    o.z *= f;
-    o.w *= f;
-    if (a.inv_freq && d >= kRopeDim0) {
-      const uint64_t pos = (uint64_t)(t.start + (grow / a.H - t.tok0));
-      float sn, cs;
-      sincosf(rope_angle(rope_turn(a.inv_freq[(d - kRopeDim0) >> 1]), pos), &sn, &cs);
-      float z = o.x * cs + o.y * sn;
-      o.y = o.y * cs - o.x * sn;
-      o.x = z;
-      sincosf(rope_angle(rope_turn(a.inv_freq[((d - kRopeDim0) >> 1) + 1]), pos), &sn, &cs);
-      z = o.z * cs + o.w * sn;
-      o.w = o.w * cs - o.z * sn;
-      o.z = z;
-    }
-    if (live)
-      *reinterpret_cast<uint2*>(a.out + (int64_t)grow * kDLat + d) =
-          make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+    __syncthreads();  // wt and inv are read
   }
 }
 }  // namespace
@@ -1399,7 +1407,10 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
   if (!encode_bytes(&km, rows, 5, dims, strides, kbox) || !encode_bytes(&vm, rows, 5, dims, strides, vbox))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
-  if (!a.alone) e = launch_pdl(chunk_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+  if (!a.alone)
+    e = a.max_tiles <= kPlanFew && a.cache.B <= kPlanFew
+            ? launch_pdl(chunk_plan_kernel<kPlanFew>, dim3(1), dim3(kPlanFew), 0, s, a)
+            : launch_pdl(chunk_plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   if (a.stage) {
     PagedReadArgs r{};
@@ -1425,7 +1436,8 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, int sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl_cluster(kern, dim3(2u * a.pairs), dim3(kThreads), kSmem, s, 2u, a, qm, km, vm);
   if (e != cudaSuccess || !a.part) return e;
-  return launch_pdl(chunk_join_kernel, dim3(kJoin, (unsigned)a.pairs), dim3(256), 0, s, a);
+  const int few = a.max_tiles <= kPlanFew ? kJoinFew : a.pairs, y = a.max_tiles < few ? a.max_tiles : few;
+  return launch_pdl(chunk_join_kernel, dim3(kJoin, (unsigned)y), dim3(256), 0, s, a);
 }
 
 }  // namespace csa2
