@@ -167,11 +167,26 @@ template <int kG, int kC, bool kHalf>
 cudaError_t launch_rows(HeadsArgs a, int sms, cudaStream_t s) {
   constexpr int kRows = 32 / kG;
   const int units = (a.q.H + kRows - 1) / kRows + (a.k.H + kRows - 1) / kRows;
-  // a token's rows to a warp, or as few of them as it takes to give each SM some 24 warps
+  const int64_t most = (int64_t)sms * kCtas<kC, kHalf>, cap = most * kWarps;
+  // Much work goes in runs of which the GPU's warps take at least two each, the last ones as nearly at the same
+  // time as may be; what begins a run counts as a unit of 1 KiB, or three of fewer bytes.  Of 65 heads of 512,
+  // 5000 tokens took 173 us with a token's rows to a warp (one each, and 136 over) and take 123.
+  constexpr int kStart = kC == 2 ? 1 : 3;
+  int64_t best = INT64_MAX;
   a.units = units;
-  while (a.units > 1 && (int64_t)a.T * ((units + a.units - 1) / a.units) < (int64_t)sms * 24) a.units = (a.units + 1) / 2;
+  for (int blocks = 1; (int64_t)a.T * units >= 8 * cap && blocks <= 16 && blocks <= units; ++blocks) {
+    const int n = (units + blocks - 1) / blocks;
+    const int64_t rounds = ((int64_t)a.T * ((units + n - 1) / n) + cap - 1) / cap;
+    if (rounds > 1 && rounds * (n + kStart) < best) {
+      best = rounds * (n + kStart);
+      a.units = n;
+    }
+  }
+  // Otherwise: a token's rows to a warp, or as few of them as it takes to give each SM some 24 warps.
+  while (best == INT64_MAX && a.units > 1 && (int64_t)a.T * ((units + a.units - 1) / a.units) < (int64_t)sms * 24)
+    a.units = (a.units + 1) / 2;
   const int64_t items = (int64_t)a.T * ((units + a.units - 1) / a.units);
-  const int64_t need = (items + kWarps - 1) / kWarps, most = (int64_t)sms * kCtas<kC, kHalf>;
+  const int64_t need = (items + kWarps - 1) / kWarps;
   return launch_pdl(qk_norm_rope_kernel<kG, kC, kHalf>, dim3((unsigned)(need < most ? need : most)),
                     dim3(kWarps * 32), 0, s, a);
 }

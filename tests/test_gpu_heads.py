@@ -86,6 +86,21 @@ def test_tokens_and_heads(T, H, K, layout):
     run(T + H, T, H, K, 128, 64, layout)
 
 
+@pytest.mark.parametrize("T,H,K,D", [(40, 1023, 5, 512), (600, 64, 1, 512), (700, 129, 17, 512), (1500, 128, 1, 512),
+                                     (5000, 32, 8, 128), (3001, 30, 3, 64), (9000, 5, 0, 256)])
+@pytest.mark.parametrize("layout", [PAIRS, HALVES])
+def test_rows_dealt_to_warps(T, H, K, D, layout):
+    """However many rows a warp takes of a token, each is done once (in place a second time would show)."""
+    run(T, T, H, K, D, 64, layout)
+    import csa2_compressed_sparse_gb300 as csa2
+    x = torch.randn((T, H + K, D), device="cuda").bfloat16()
+    y, pos, f = torch.empty_like(x), torch.arange(T, device="cuda"), freq(32)
+    k = (x[:, H:], y[:, H:]) if K else (None, None)
+    csa2.csa2_qk_norm_rope(x[:, :H], y[:, :H], pos, f, k=k[0], k_out=k[1], layout=layout, factor=1.25)
+    csa2.csa2_qk_norm_rope(x[:, :H], x[:, :H], pos, f, k=k[0], k_out=k[0], layout=layout, factor=1.25)
+    assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("layout", [PAIRS, HALVES])
 @pytest.mark.parametrize("r0", [0, 8, 64, 320])
 def test_the_rotated_part_may_lie_anywhere(layout, r0):
