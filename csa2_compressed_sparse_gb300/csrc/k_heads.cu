@@ -9,7 +9,8 @@
 // whole rows in order.  A warp takes an item, a token's rows or a run of them, a row a lane at a time,
 // the next one loaded before this is written; the token's angles it computes once, through shared
 // memory.  Angular steps (64-bit floating point, of which an SM does two a cycle) are computed once a CTA.
-// Bound by the bytes moved.
+// Bound by the bytes moved: 4096 tokens of 65 heads of 512 take 102 us (5.3 of 6.8 TB/s; what is missing is
+// bytes in flight, a row and the next of each of 32 warps an SM), 64 tokens the launch and a chain of latencies (7 us).
 #include "common.cuh"
 #include "compress_dev.cuh"
 
