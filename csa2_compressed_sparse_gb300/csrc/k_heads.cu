@@ -9,8 +9,8 @@
 // whole rows in order.  A warp takes an item, a token's rows or a run of them, a row a lane at a time,
 // the next one loaded before this is written; the token's angles it computes once, through shared
 // memory.  Angular steps (64-bit floating point, of which an SM does two a cycle) are computed once a CTA.
-// Bound by the bytes moved: 4096 tokens of 65 heads of 512 take 102 us (5.3 of 6.8 TB/s; what is missing is
-// bytes in flight, a row and the next of each of 32 warps an SM), 64 tokens the launch and a chain of latencies (7 us).
+// Bound by the bytes moved: 4096 tokens of 65 heads of 512 take 98 us (5.6 of 6.8 TB/s; what is missing is
+// bytes in flight, a row and the next two of each of 24 warps an SM), 64 tokens the launch and a chain of latencies (7 us).
 #include "common.cuh"
 #include "compress_dev.cuh"
 
@@ -26,12 +26,13 @@ __device__ __forceinline__ float2 wide2(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// CTAs of an SM: halves of wide heads take more registers
-template <int kC, bool kHalf>
-constexpr int kCtas = kHalf && kC == 2 ? 2 : 4;
+// CTAs of an SM, by registers: halves of wide heads take more, and so do two rows ahead
+template <int kC, bool kHalf, bool kTwo>
+constexpr int kCtas = kC == 1 ? 4 : kHalf ? 2 : kTwo ? 3 : 4;
 
-template <int kG, int kC, bool kHalf>
-__global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf>) qk_norm_rope_kernel(HeadsArgs a) {
+// kTwo: the next two rows are loaded ahead, not one.
+template <int kG, int kC, bool kHalf, bool kTwo>
+__global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf, kTwo>) qk_norm_rope_kernel(HeadsArgs a) {
   __shared__ uint64_t turn_s[kMaxPairs];
   __shared__ __align__(16) float cs_s[kWarps][kMaxPairs], sn_s[kWarps][kMaxPairs];
   griddep_launch_dependents();
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf>) qk_norm_rope_ke
   for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items; it += step) {
     const int64_t t = it / blocks;
     const int u0 = (int)(it - t * blocks) * a.units, u1 = min(nq + nk, u0 + a.units);
-    uint4 v[kC], m[kHalf ? kC : 1], vn[kC], mn[kHalf ? kC : 1];
+    uint4 v[kC], m[kHalf ? kC : 1], vn[kC], mn[kHalf ? kC : 1], vf[kTwo ? kC : 1];
     auto fetch = [&](int u, uint4(&x)[kC], uint4(&y)[kHalf ? kC : 1]) {
       const bool q = u < nq;
       const HeadSet& s = q ? a.q : a.k;
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf>) qk_norm_rope_ke
       }
     };
     fetch(u0, v, m);
+    if (kTwo && u0 + 1 < u1) fetch(u0 + 1, vn, mn);
     if (half > 0) {
       const uint64_t p = (uint64_t)a.pos[t];
       __syncwarp();  // the last token's angles are read
@@ -95,7 +97,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf>) qk_norm_rope_ke
       const HeadSet& s = q ? a.q : a.k;
       const int r = (q ? u : u - nq) * kRows + sub;
       uint16_t* out = s.out + t * s.out_token + r * s.out_head;
-      if (u + 1 < u1) fetch(u + 1, vn, mn);
+      if constexpr (kTwo) {
+        if (u + 2 < u1) fetch(u + 2, vf, mn);
+      } else {
+        if (u + 1 < u1) fetch(u + 1, vn, mn);
+      }
       if (u == u0 || u == nq) {
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
@@ -158,6 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf>) qk_norm_rope_ke
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
         v[c] = vn[c];
+        if (kTwo) vn[c] = vf[kTwo ? c : 0];
         if (kHalf) m[kHalf ? c : 0] = mn[kHalf ? c : 0];
       }
     }
@@ -167,12 +174,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf>) qk_norm_rope_ke
 template <int kG, int kC, bool kHalf>
 cudaError_t launch_rows(HeadsArgs a, int sms, cudaStream_t s) {
   constexpr int kRows = 32 / kG;
+  // Much work on heads that fill a warp has two rows ahead (4096 tokens of 65 heads of 512 103 -> 98 us, 5000
+  // 127 -> 116, heads of 192 and 256 10 % less; little work took 13.8 in place of 13.0, narrower heads as long
+  // or up to 9 % longer, and so halves of any width, whose rows take twice the registers).
+  constexpr bool kTwo = kG == 32 && !kHalf;
   const int units = (a.q.H + kRows - 1) / kRows + (a.k.H + kRows - 1) / kRows;
-  const int64_t most = (int64_t)sms * kCtas<kC, kHalf>, cap = most * kWarps;
   // Much work goes in runs of which the GPU's warps take at least two each, the last ones as nearly at the same
   // time as may be; what begins a run counts as a unit of 1 KiB, or three of fewer bytes.  Of 65 heads of 512,
-  // 5000 tokens took 173 us with a token's rows to a warp (one each, and 136 over) and take 123.
+  // 5000 tokens took 173 us with a token's rows to a warp (one each, and 136 over) and 127 so.
   constexpr int kStart = kC == 2 ? 1 : 3;
+  const int64_t cap = (int64_t)sms * kCtas<kC, kHalf, kTwo> * kWarps;
   int64_t best = INT64_MAX;
   a.units = units;
   for (int blocks = 1; (int64_t)a.T * units >= 8 * cap && blocks <= 16 && blocks <= units; ++blocks) {
@@ -184,12 +195,14 @@ cudaError_t launch_rows(HeadsArgs a, int sms, cudaStream_t s) {
     }
   }
   // Otherwise: a token's rows to a warp, or as few of them as it takes to give each SM some 24 warps.
-  while (best == INT64_MAX && a.units > 1 && (int64_t)a.T * ((units + a.units - 1) / a.units) < (int64_t)sms * 24)
+  const bool much = best != INT64_MAX;
+  while (!much && a.units > 1 && (int64_t)a.T * ((units + a.units - 1) / a.units) < (int64_t)sms * 24)
     a.units = (a.units + 1) / 2;
   const int64_t items = (int64_t)a.T * ((units + a.units - 1) / a.units);
   const int64_t need = (items + kWarps - 1) / kWarps;
-  return launch_pdl(qk_norm_rope_kernel<kG, kC, kHalf>, dim3((unsigned)(need < most ? need : most)),
-                    dim3(kWarps * 32), 0, s, a);
+  const int64_t most = (int64_t)sms * (much ? kCtas<kC, kHalf, kTwo> : kCtas<kC, kHalf, false>);
+  return launch_pdl(much ? qk_norm_rope_kernel<kG, kC, kHalf, kTwo> : qk_norm_rope_kernel<kG, kC, kHalf, false>,
+                    dim3((unsigned)(need < most ? need : most)), dim3(kWarps * 32), 0, s, a);
 }
 
 template <int kG, int kC>

@@ -389,6 +389,16 @@ def test_positions_below_zero_see_nothing():
     c.call().check()
 
 
+@pytest.mark.parametrize("dtype,H", [(BF16, 64), (S128, 64), (E8M0, 3), (BF16, 128)])
+def test_no_rows_at_all(dtype, H):
+    """Bounds of zero: the first tokens of groups that are not complete, of one sequence or of hundreds."""
+    for B in (1, 300):
+        c = Case(50, dtype, H, 64, [2] * B, [0] * B, ratio=128)
+        assert c.max_rows == 0 and c.total == 0
+        c.call().check()
+        assert bool((c.out == 0).all()) and torch.equal(c.lse, c.sink.expand_as(c.lse))
+
+
 def test_positions_at_the_end_of_int64():
     c = Case(18, BF16, 64, 64, [2], [500])
     c.start.fill_(2 ** 63 - 2)
@@ -464,12 +474,12 @@ def test_one_workspace_for_many_calls_in_a_row():
 
 # ---- long segments: tensor memory sums up 65536 rows at most, the rest joins in fp32 ----------
 
-@pytest.mark.parametrize("case", ["plain", "rising", "no_pages", "window"])
+@pytest.mark.parametrize("case", ["plain", "rising", "no_pages", "window", "s128"])
 def test_segments_longer_than_a_run(case):
     """Eighty tiles of 300 key tiles and more each: those that one pair works on alone, and the longer parts
     of those that two share, are done in runs."""
     n = 90000 if case == "no_pages" else 80000
-    c = Case(30, BF16, 64, 64, [160], [n - 160], window=77000 if case == "window" else 0)
+    c = Case(30, S128 if case == "s128" else BF16, 64, 64, [160], [n - 160], window=77000 if case == "window" else 0)
     if case == "rising":  # the maximum moves in every run
         x = decode(get(c.data, c.table, 0, 0, n), BF16).float()
         put(c.data, c.table, 0, (x * torch.linspace(0.1, 20, n, device="cuda")[:, None]).bfloat16())
@@ -558,6 +568,14 @@ def test_outputs_at_odd_chunks(n, hist):
     assert bool((c.out_whole[:8] == 5).all()) and bool((c.out_whole[-8:] == 5).all())
 
 
+def test_queries_beyond_4_gib():
+    c = Case(51, BF16, 128, 64, [9, 35000], [0, 3], window=16, want_lse=False, rope=False)
+    assert c.q.numel() > 1 << 31
+    c.call().check(only=[0, 1, 8, 20000, 32760, 32768, 34990, 34998, 34999], at_most=1 << 24)
+    del c
+    torch.cuda.empty_cache()
+
+
 # ================================ read =========================================================
 
 def read_case(seed, dtype, page, lens, first, back=False, ratio=1, pad=0, gap=0, stream=None, layers=0):
@@ -609,6 +627,18 @@ def test_many_rows_read_back(dtype):
     read_case(2, dtype, 64, [30000, 1, 17, 0, 9000], [5, 0, 100, 0, 700], back=True, ratio=2, pad=3)
     read_case(3, dtype, 16, [40] * 300, [11] * 300, layers=2)
     read_case(4, dtype, 64, [1], [0])
+
+
+def test_rows_beyond_4_gib():
+    import csa2_compressed_sparse_gb300 as csa2
+    n, ld = 300000, 8192
+    data, table, _ = pool(np.random.default_rng(5), BF16, 64, [n])
+    x = torch.randn((n, 512), device="cuda").bfloat16()
+    put(data, table, 0, x)
+    whole = torch.full((n, ld), 9.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    csa2.csa2_paged_read(whole[:, :512], cu, torch.zeros(1, dtype=torch.int64, device="cuda"), paged(data, table, BF16))
+    assert torch.equal(whole[:, :512], x) and bool((whole[:, 512:520] == 9).all())
 
 
 def test_read_is_the_inverse_of_append():
