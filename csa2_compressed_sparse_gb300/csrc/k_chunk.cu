@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kReadWarps * 32, read_ctas(kMode)) paged_read_
 // reach those others through 0 * NaN.  Such a row makes its scores non-finite for every query, so
 // where a key tile is masked for some row, a masked score that is not finite flags the cache row, and
 // the values of flagged rows lose their non-finite elements before the product (the tokens that see the
-// row have NaN weights).  Rows behind the last visible one are garbage and are treated so too.
+// row have NaN weights).  Rows behind the last visible one are garbage and are treated so too.  Rows in two
+// parts lose the elements of the first; the second holds zeros there, and is finite everywhere.
 
 constexpr int kQRows = 128, kKeys = 256;
 constexpr int kSlotBytes = 16384, kSlots = 8;
