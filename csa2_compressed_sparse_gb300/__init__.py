@@ -604,7 +604,7 @@ def csa2_qk_norm_rope(q, q_out, pos, inv_freq, k=None, k_out=None, q_norm=True, 
                       factor=1.0, stream=None):
     """RMSNorm of each head of q [T, H, D] and k [T, K, D] (k: optional), then the rotation of their
     positions pos [T] by inv_freq [n] in 2 n dims from rope_dim0 on (None: the last ones); inv_freq
-    None is the norm alone.  Outputs may be the inputs."""
+    None is the norm alone.  Outputs may be the inputs, and the step's calls may take them directly."""
     shape = q.shape
     if len(shape) != 3:
         raise ValueError("csa2: q must be [T, H, D]")

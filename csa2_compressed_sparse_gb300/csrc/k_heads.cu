@@ -11,6 +11,9 @@
 // memory.  Angular steps (64-bit floating point, of which an SM does two a cycle) are computed once a CTA.
 // Bound by the bytes moved: 4096 tokens of 65 heads of 512 take 98 us (5.6 of 6.8 TB/s; what is missing is
 // bytes in flight, a row and the next two of each of 24 warps an SM), 64 tokens the launch and a chain of latencies (7 us).
+//
+// The attention of the sparse step reads its queries and window rows before its dependency wait, and this
+// kernel is what writes them: it lets no dependent start before its CTAs have ended.
 #include "common.cuh"
 #include "compress_dev.cuh"
 
@@ -35,7 +38,6 @@ template <int kG, int kC, bool kHalf, bool kTwo>
 __global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf, kTwo>) qk_norm_rope_kernel(HeadsArgs a) {
   __shared__ uint64_t turn_s[kMaxPairs];
   __shared__ __align__(16) float cs_s[kWarps][kMaxPairs], sn_s[kWarps][kMaxPairs];
-  griddep_launch_dependents();
   griddep_wait();
   constexpr int kRows = 32 / kG;  // rows of a unit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane / kG, l = lane % kG;
@@ -169,6 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas<kC, kHalf, kTwo>) qk_norm_r
       }
     }
   }
+  __threadfence();  // (what ends a CTA need not make its rows visible to what starts then)
 }
 
 template <int kG, int kC, bool kHalf>

@@ -506,7 +506,8 @@ __device__ __forceinline__ void red_or_cluster(uint32_t addr, uint32_t v) {
 // before its first write to global memory and before it reads what a kernel of the same
 // call, or a selection, key or plane before it, may still be writing.  The paged kernels
 // read nothing at all before it.  The kernels of the sparse step read the call inputs
-// that csa2.h lists before it, so that these loads overlap with the previous kernel too.
+// that csa2.h lists before it, so that these loads overlap with the previous kernel too;
+// qk_norm_rope_kernel, which may write them, lets nothing start before it has ended.
 __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

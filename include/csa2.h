@@ -15,10 +15,10 @@
  *     memory is caller-provided through the *_workspace_size queries.
  *   - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL = the legacy
  *     default stream).  No call synchronises except csa2_device_status().  Kernels are
- *     launched as programmatic dependents and let their own dependents start early: a
- *     call may begin while the kernel before it on the stream drains.  Outputs and
- *     workspace are written, and selections, candidates, keys, scores and planes read,
- *     only once that kernel has finished.
+ *     launched as programmatic dependents and, but for csa2_qk_norm_rope's, let their own
+ *     dependents start early: a call may begin while the kernel before it on the stream
+ *     drains.  Outputs and workspace are written, and selections, candidates, keys, scores
+ *     and planes read, only once that kernel has finished.
  *   - The calls on the paged cache (csa2_paged_*) and csa2_qk_norm_rope read everything else
  *     after it too, so stream order is all that their inputs need.
  *   - The calls of the sparse step (index, top-k, attention, and the compressor's tokens
@@ -27,7 +27,8 @@
  *     with cu_seqlens, and inv_freq.  They must not be written by a kernel that itself lets
  *     its dependents start early and that no other launch separates from the call.  That
  *     is any kernel of this library (an attention output taken as queries, a window filled
- *     by csa2_paged_append) and any other that triggers programmatic launches.  Between the
+ *     by csa2_paged_append or csa2_paged_read) except csa2_qk_norm_rope's, whose outputs the
+ *     step may take directly, and any other that triggers programmatic launches.  Between the
  *     two, a kernel launched without the programmatic attribute, a copy, or a wait for an
  *     event of another stream makes them complete; kernels that trigger nothing and
  *     copies are so by themselves.
@@ -669,7 +670,8 @@ csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_
  *   pos          [T] int64 (of any sign);  inv_freq [rope_dims / 2] fp32; neither is read with
  *                rope_dims 0 (a norm alone)
  *   rope_dim0, rope_dims   multiples of 8 (rope_dims of 16 with HALVES)
- *   factor       finite; it scales the rotated dims only */
+ *   factor       finite; it scales the rotated dims only
+ * The calls of the sparse step may follow directly on the stream and take what it wrote. */
 typedef enum { CSA2_ROPE_PAIRS = 0, CSA2_ROPE_HALVES = 1 } csa2_rope_layout;
 typedef struct {
   const csa2_bf16* x;

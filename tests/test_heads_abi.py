@@ -1,6 +1,7 @@
 """Refusals of csa2_qk_norm_rope, csa2_paged_read and csa2_paged_chunk_attn: argument errors are found on
 the host, before anything is launched (no GPU is touched here)."""
 import ctypes
+import os
 import types
 
 import pytest
@@ -216,3 +217,11 @@ def test_head_tensors_elsewhere_are_refused(recorded, name, device):
     with pytest.raises(ValueError, match=name.replace("_out", "")):
         csa2.csa2_qk_norm_rope(**{**all_on(1), name: all_on(device)[name]})
     assert len(recorded[1]) == 1
+
+
+def test_norm_rope_lets_no_kernel_start_before_it_ends():
+    """The sparse step reads queries and window rows before its dependency wait; the header says that it may
+    follow csa2_qk_norm_rope directly, so that kernel must not trigger its dependents."""
+    src = os.path.join(os.path.dirname(csa2.__file__), "csrc", "k_heads.cu")
+    with open(src) as f:
+        assert "griddep_launch_dependents" not in f.read()
