@@ -109,28 +109,30 @@ __global__ void __launch_bounds__(kReadWarps * 32, read_ctas(kMode)) paged_read_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t step = (int64_t)gridDim.x * kReadWarps * run;
   const uint64_t turn = a.inv_freq ? rope_turn(a.inv_freq[lane]) : 0;
-  // (with row_end a key tile's length more, which a tile that ends there reads)
-  const int64_t total = min((int64_t)a.T, (int64_t)a.cu_seqlens[a.cache.B] + (a.row_end ? 256 : 0));
+  const int64_t rows = a.cu_seqlens[a.cache.B];
+  // (with row_end a key tile's length of zeros more, which a tile that ends there reads)
+  const int64_t total = min((int64_t)a.T, rows + (a.row_end ? 256 : 0));
   for (int64_t t = ((int64_t)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * run; t < total; t += step) {
     // lane l: row t + l
     const int n = (int)min(total - t, (int64_t)run);
     const uint8_t* src = nullptr;
     int64_t j = 0;
-    bool zero = false;
+    const bool zero = a.row_end != nullptr;
     {
       const int64_t tl = t + min(lane, n - 1);
       int b = cdev::warp_find_seq(a.cu_seqlens, a.cache.B, t, lane);
-      if (a.cu_seqlens[b + 1] <= tl) {  // in a later sequence
-        int hi = a.cache.B - 1;
-        for (++b; b < hi;) {
-          const int m = (b + hi + 1) >> 1;
-          if (a.cu_seqlens[m] <= tl) b = m;
-          else hi = m - 1;
+      if (tl < rows) {  // (the rows behind the last sequence's are no sequence's)
+        if (a.cu_seqlens[b + 1] <= tl) {  // in a later sequence
+          int hi = a.cache.B - 1;
+          for (++b; b < hi;) {
+            const int m = (b + hi + 1) >> 1;
+            if (a.cu_seqlens[m] <= tl) b = m;
+            else hi = m - 1;
+          }
         }
+        j = a.start_row[b] + (tl - a.cu_seqlens[b]);
       }
-      j = a.start_row[b] + (tl - a.cu_seqlens[b]);
-      zero = a.row_end != nullptr;
-      if (!zero || j < a.row_end[b]) {
+      if (tl < rows && (!zero || j < a.row_end[b])) {
         int32_t page = -1, row = 0;
         if (j >= 0 && j < a.cap_rows) {
           const int32_t lp = (int32_t)(__umulhi((uint32_t)j, a.page_mul) >> a.page_shift);
