@@ -150,13 +150,15 @@ __device__ __forceinline__ void load_own(const CompressArgs& a, int64_t t, int l
 // Sequence of token t: the last b < B with cu[b] <= t (cu non-decreasing, cu[0] = 0),
 // found by the 32 lanes of a warp together: each round probes 32 evenly spaced entries
 // and keeps the span between the last probe at or below t and the next one, so B = 8192
-// takes three rounds of loads.
+// takes three rounds of loads.  Ordinary loads, as the kernel in front may write cu while this one is resident
+// (the copied rows' places, which chunk_plan_kernel makes; a caller's cu_seqlens): loads through the read-only
+// path may then bring what was there before, whatever they are ordered behind.
 __device__ __forceinline__ int warp_find_seq(const int32_t* cu, int B, int64_t t, int lane) {
   int lo = 0, hi = B - 1;
   while (hi > lo) {
     const int step = (hi - lo + 31) / 32;
     const int probe = min(hi, lo + step * (lane + 1));
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, (int64_t)__ldg(cu + probe) <= t);
+    const uint32_t m = __ballot_sync(0xFFFFFFFFu, (int64_t)cu[probe] <= t);
     if (m == 0u) {
       hi = lo + step - 1;
     } else {

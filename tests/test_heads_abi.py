@@ -225,3 +225,11 @@ def test_norm_rope_lets_no_kernel_start_before_it_ends():
     src = os.path.join(os.path.dirname(csa2.__file__), "csrc", "k_heads.cu")
     with open(src) as f:
         assert "griddep_launch_dependents" not in f.read()
+
+
+def test_the_search_for_a_sequence_does_not_read_around_the_dependency_wait():
+    """Its array may be written by the kernel in front while the reader is resident: no read-only loads."""
+    src = os.path.join(os.path.dirname(csa2.__file__), "csrc", "compress_dev.cuh")
+    with open(src) as f:
+        body = f.read().split("warp_find_seq(")[1].split("\n}")[0]
+    assert "cu[probe]" in body and "__ldg" not in body
