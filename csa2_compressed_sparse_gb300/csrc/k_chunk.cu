@@ -877,7 +877,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           weights();
           if (pass == 1) {
-            soft_sync();  // top is read by all
+            // all have read top, and have rescaled O: no block of P is handed on before
+            tc_fence_before();
+            soft_sync();
             break;
           }
           if (!soft_any(top > kLazy || (m == -INFINITY && top > -INFINITY))) break;
@@ -1010,7 +1012,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // A block of P lets the first products overwrite O, whichever warps have read it: none is handed on
       // before all have.  (The sums, too, are read before others are written.)
-      if (end) soft_sync();
+      if (end) {
+        tc_fence_before();
+        soft_sync();
+      }
       if (have) {
         fence_proxy_async_smem();
         tc_fence_before();

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from test_gpu_chunk import Case, status
-from test_gpu_paged import BF16, E8M0, S128
+from test_gpu_paged import BF16, DTYPES, E8M0, S128, put, quantised
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,26 @@ def test_copied_rows_of_calls_in_a_row(dtype, page):
         assert status() == 0
         for c, (out, lse) in zip(cases, first):
             assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("new,hist", [([40, 9, 128], [700, 1500, 0]), ([6] * 90, [300] * 90), ([3], [30000])])
+def test_maxima_that_move_in_every_key_tile(dtype, new, hist):
+    """Each key tile rescales what the tensor memory holds, and segments end while others begin: the warps
+    that hand a block of weights on are not those that rescaled or read all of it."""
+    c = Case(70, dtype, 64, 64, new, hist)
+    g = torch.Generator(device="cuda").manual_seed(70)
+    x = torch.randn((1, 512), generator=g, device="cuda")
+    c.q.copy_((x * (1 + 0.1 * torch.rand((c.T, 64, 1), generator=g, device="cuda"))).bfloat16())
+    for b, n in enumerate(c.rows):
+        top = 6.0 * -(-n // 256)  # scores of some 130 more from tile to tile: beyond 2^64 of a weight
+        r = x * torch.linspace(0, top, n, device="cuda")[:, None] + torch.randn((n, 512), generator=g, device="cuda")
+        put(c.data, c.table, b, quantised(r, dtype))
+    c.call().check(only=[0, 1, 2, 5, 31, 39, 64, 127])
+    out, lse = c.out.clone(), c.lse.clone()
+    for _ in range(6):
+        c.out.fill_(5)
+        c.lse.fill_(6)
+        c.call()
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    assert status() == 0
