@@ -217,8 +217,10 @@ __global__ void __launch_bounds__(kReadWarps * 32, read_ctas(kMode)) paged_read_
 // A row that some tokens of a tile see and others do not may hold NaN or infinities, which must not
 // reach those others through 0 * NaN.  Such a row makes its scores non-finite for every query, so
 // where a key tile is masked for some row, a masked score that is not finite flags the cache row, and
-// the values of flagged rows lose their non-finite elements before the product (the tokens that see the
-// row have NaN weights).  Rows behind the last visible one are garbage and are treated so too.  Rows in two
+// the values of flagged rows lose their non-finite elements before the product.  A token that sees the row
+// has a NaN weight and shows it all the same, unless its score is -inf: then the weight is 0, and
+// 0 times the elements that were lost is NaN in their dims (poison_outputs), as it is in a key tile that all
+// tokens see.  Rows behind the last visible one are garbage and are treated so too.  Rows in two
 // parts lose the elements of the first; the second holds zeros there, and is finite everywhere.
 
 constexpr int kQRows = 128, kKeys = 256;
@@ -246,6 +248,7 @@ struct __align__(16) ChunkSegment {
   int row0, rows, tok0, clip;  // as in ChunkTile
   int whole;                   // all of the tile's key tiles
   int slot;                    // its part
+  int seq;
 };
 
 struct __align__(16) ChunkAux {
@@ -264,6 +267,7 @@ struct __align__(16) ChunkAux {
   float top[4][64], sum[4][64];
   uint32_t tmem_slot;
   int abort, done, work;
+  int odd[2];             // of key tile c & 1: a token sees a row with a score that is not finite
 };
 constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kPBytes + (int)sizeof(ChunkAux);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -673,12 +677,102 @@ __device__ __forceinline__ Places place_groups(const ChunkArgs& a, const ChunkTi
   return p;
 }
 
+// Rows of block `blk` of a key tile that a token sees (they are on a page, and lo .. hi - 1).
+__device__ __forceinline__ uint64_t rows_seen(int base, uint32_t groups, int blk, int lo, int hi) {
+  uint64_t seen = tile_mask((int64_t)base + 64 * blk, lo, hi);
+  const uint32_t g8 = (groups >> (8 * blk)) & 0xFFu;
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    if (!(g8 >> g & 1u)) seen &= ~(0xFFull << (8 * g));
+  return seen;
+}
+
+// Those of them whose scores, in the 64 columns from `scores` on, are not finite, as bits for the token of row `row`.
+__device__ __forceinline__ void note_rows(ChunkAux& X, uint32_t scores, int base, uint32_t groups, int lo, int hi,
+                                          bool any, int blk, int row) {
+  uint64_t odd = 0;
+#pragma unroll 1
+  for (int k = 0; k < 64; k += 16) {
+    uint32_t v[16], w = 0;
+    __syncwarp();
+    tmem_ld16(scores + k, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w |= (v[j] & 0x7F800000u) == 0x7F800000u ? 1u << j : 0u;
+    odd |= (uint64_t)w << k;
+  }
+  odd = any ? odd & rows_seen(base, groups, blk, lo, hi) : 0;
+  X.top[blk][row] = __uint_as_float((uint32_t)odd);
+  X.sum[blk][row] = __uint_as_float((uint32_t)(odd >> 32));
+}
+
+// The O of such a token gets NaN in the dims in which one of these rows, of the key tile from row `base` on, is not
+// finite.  O is in the 64 columns from `o` and `o` + 128 on, dims d.. and d + 256 ...  By whole warps, hardly ever.
+__device__ __forceinline__ void poison_outputs(const ChunkArgs& a, const ChunkAux& X, int seq, int base, int row,
+                                               int d, uint32_t o) {
+  const int64_t off = a.stage ? a.stage_cu[seq] - a.stage_first[seq] : 0;
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    const int col = 16 * (k & 3), dim = d + 256 * (k >> 2) + col;
+    uint32_t gone = 0;  // columns
+#pragma unroll 1
+    for (int b = 0; b < 8; ++b) {
+      uint32_t bits = __float_as_uint((b & 1 ? X.sum : X.top)[b >> 1][row]);
+      for (; bits; bits &= bits - 1) {
+        const int64_t j = (int64_t)base + 32 * b + __ffs(bits) - 1;
+        const uint16_t* at;
+        if (a.stage) {
+          at = a.stage + (j + off) * kDLat;
+        } else {
+          const int32_t lp = (int32_t)(__umulhi((uint32_t)j, a.page_mul) >> a.page_shift);
+          at = reinterpret_cast<const uint16_t*>(a.cache.data + a.cache.table[(int64_t)seq * a.cache.table_ld + lp] *
+                                                                    a.cache.page_stride) +
+               (j - (int64_t)lp * a.cache.page_rows) * kDLat;
+        }
+        for (int i = 0; i < 16; ++i)
+          if ((at[dim + i] & 0x7F80u) == 0x7F80u) gone |= 1u << i;
+      }
+    }
+    if (__any_sync(0xFFFFFFFFu, gone != 0)) {
+      uint32_t v[16];
+      __syncwarp();
+      tmem_ld16(o + 128 * (k >> 2) + col, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (gone >> i & 1u) v[i] = 0x7FC00000u;
+      tmem_st16(o + 128 * (k >> 2) + col, v);
+      tmem_st_wait();
+    }
+  }
+}
+
+// What the softmax warps do with such a key tile c in place of handing on their blocks of P alone.  (A call of its
+// own: as two calls or inlined, 2048 tokens over 32768 rows, which never come here, took 2 to 6 % longer.)
+__device__ __noinline__ void poison_tile(const ChunkArgs& a, ChunkAux& X, int seg, int c, int base, uint32_t groups, int lo,
+                                         int hi, bool any, uint32_t tlane, uint32_t p_full) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp >> 2, L = 32 * (warp & 3) + lane;
+  const int row = L & 63, kh = L >> 6, blk = 2 * kh + half;
+  note_rows(X, tlane + kColS + 128 * (c & 1) + 64 * half, base, groups, lo, hi, any, blk, row);  // while they are there
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive_cluster(p_full);
+  soft_sync();
+  wait_phase(X, X.p_free[3], (uint32_t)c & 1);  // the values' products are done
+  tc_fence_after();
+  poison_outputs(a, X, X.seg[(seg - 1) & 3].seq, base, row, kh * 128 + half * 64, tlane + 64 * half);
+  tc_fence_before();
+  soft_sync();
+  if (threadIdx.x == 0) X.odd[c & 1] = 0;  // (set again by tile c + 2, barriers from here)
+}
+
 // kAlone: without a plan, pair c works on tile c.  kParts: of a staged row.  (Instances of their own, as code that is
 // not used lies in the way of what is: with kAlone's in it, ragged chunks took 531 us in place of 509, with
 // kParts as a number 525.)
 template <bool kAlone, int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_attn_kernel(ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
+    chunk_attn_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t q_s = smem_u32(smem), ring = q_s + kQBytes, p_s = ring + kSlots * kSlotBytes;
@@ -704,6 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&X.clean_done), 2);
     mbar_init(smem_u32(&X.fin), 1);
     X.abort = X.done = 0;
+    X.odd[0] = X.odd[1] = 0;
     mbar_fence_init();
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
@@ -754,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool have = st.i >= 0, first = st.i <= 0;
       uint32_t pk[32];
       bool masked = false;
+      bool poison = false;  // a thread sees a row with a score that is not finite
       // of the segment before, until its end is done
       const float m_end = m, mslot_end = mslot;
       const float2 l_end = l2, r_end = r2;
@@ -773,14 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t scores = tlane + kColS + 128 * (c & 1) + 64 * half;
         masked = (st.kind & kStepMasked) != 0;
-        uint64_t seen = ~0ull;
-        if (masked) {
-          seen = tile_mask((int64_t)st.base + 64 * blk, lo, hi);
-          const uint32_t g8 = (st.groups >> (8 * blk)) & 0xFFu;
-#pragma unroll
-          for (int g = 0; g < 8; ++g)
-            if (!(g8 >> g & 1u)) seen &= ~(0xFFull << (8 * g));
-        }
+        const uint64_t seen = masked ? rows_seen(st.base, st.groups, blk, lo, hi) : ~0ull;
         // Exponents of columns 2 j, 2 j + 1: v two of the scores.
         auto scaled = [&](int j, const uint32_t* v, float nm) {
           float2 y = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), make_float2(sc2, sc2),
@@ -843,6 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (masked) {
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
+                if (bad[k] & (uint32_t)(seen >> (32 * k))) *reinterpret_cast<volatile int*>(&X.odd[c & 1]) = 1;
                 bad[k] = __reduce_or_sync(0xFFFFFFFFu, bad[k] & ~(uint32_t)(seen >> (32 * k)));
                 if (lane == 0 && bad[k]) red_or_cluster(flags + (c & 1) * 32 + k * 4, bad[k]);
               }
@@ -886,6 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l2 = add2(l2, ls);
         r2 = add2(r2, rs);
+        if (masked) poison = *reinterpret_cast<volatile int*>(&X.odd[c & 1]) != 0;
       }
       // ---- the end of the segment before: O is read before the next products may start, and stored
       // while they run ----
@@ -1016,13 +1107,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         soft_sync();
       }
-      if (have) {
+      if (!have) break;
+      if (poison) {
+        poison_tile(a, X, seg, c, st.base, st.groups, lo, hi, l2.x + l2.y == l2.x + l2.y, tlane, p_full);
+      } else {
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(p_full);
       }
-      if (!have) break;
       if (!(st.kind & kStepLast) && ((st.i + 1) & (kRun - 1)) == 0) {
         // a run's end: O joins what the part holds
         wait_phase(X, X.p_free[3], (uint32_t)c & 1);
@@ -1240,7 +1333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0)
             X.seg[seg & 3] = ChunkSegment{w.t.start, w.t.row0, w.t.rows, w.t.tok0, w.t.clip,
-                                          w.t.c0 == w.t.c1, 2 * pair + (w.unit == 0 ? 1 : 0)};
+                                          w.t.c0 == w.t.c1, 2 * pair + (w.unit == 0 ? 1 : 0), w.t.seq};
           __syncwarp();
           ++seg;
           n_last = w.n;

@@ -627,6 +627,8 @@ csa2_status csa2_paged_read(csa2_bf16* out, int64_t out_ld, int T, const int32_t
  * in fp32 sums of bf16 products, the weights e^{s_j - m} rounded to bf16 for the second.  FP8_S128
  * rows (code * scale) are the sum of two bf16 parts, 2^-16 off, which doubles the work; rows of the
  * other types are exact in one.
+ * A row with NaN or infinities shows in the tokens that see it, as by the formula (0 times infinity
+ * is NaN, in the row's dims that hold one), and in no others.
  *   q, out       [T][H][512] bf16;  T 0 .. 1048576;  H 1 .. 128
  *   cu_seqlens   [cache->B + 1] int32, non-decreasing, cu_seqlens[0] == 0; empty sequences are
  *                fine.  Tokens from cu_seqlens[B] on (a padded batch) keep their out and lse
