@@ -792,6 +792,21 @@ csa2_status csa2_paged_read(csa2_bf16* out, int64_t out_ld, int T, const int32_t
 
 namespace {
 
+// Whether two of the runs of D elements at t * token + h * head, t < T, h < H, share an element (strides >= 0).
+bool rows_overlap(int T, int H, int D, int64_t token, int64_t head) {
+  if ((T > 1 && token < D) || (H > 1 && head < D)) return true;
+  if (T == 1 || H == 1) return false;
+  // one stride beyond all that the other spans: the usual layouts
+  typedef __int128 wide;
+  if (token >= (wide)head * (H - 1) + D || head >= (wide)token * (T - 1) + D) return false;
+  // otherwise the nearest token to each head
+  for (int h = 1; h < H; ++h) {
+    const wide to = (wide)head * h, most = T - 1, t = to / token < most ? to / token : most, past = to - t * token;
+    if (past < D || (t < most && token - past < D)) return true;
+  }
+  return false;
+}
+
 // Checks of one set of heads; fills *s.
 csa2_status head_args(const char* name, const char* which, const csa2_heads* h, int T, int D,
                       csa2::HeadSet* s) {
@@ -802,8 +817,7 @@ csa2_status head_args(const char* name, const char* which, const csa2_heads* h, 
   REQUIRE(h->x_token >= 0 && h->x_head >= 0 && h->out_token >= 0 && h->out_head >= 0 &&
               ((h->x_token | h->x_head | h->out_token | h->out_head) & 7) == 0,
           "%s: %s's strides must be multiples of 8, >= 0", name, which);
-  REQUIRE((h->H == 1 || h->out_head >= D) && (T == 1 || h->out_token >= D),
-          "%s: %s.out's heads or tokens overlap", name, which);
+  REQUIRE(!rows_overlap(T, h->H, D, h->out_token, h->out_head), "%s: %s.out's heads or tokens overlap", name, which);
   REQUIRE(aligned16(h->norm_w), "%s: %s.norm_w must be 16-byte aligned", name, which);
   s->x = h->x; s->out = h->out; s->x_token = h->x_token; s->x_head = h->x_head;
   s->out_token = h->out_token; s->out_head = h->out_head; s->H = h->H; s->norm = h->norm ? 1 : 0;

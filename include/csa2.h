@@ -666,7 +666,8 @@ csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_
  * for long contexts (YaRN) comes as inv_freq, its magnitude as factor.
  *   q, k         HOST structs (device pointers inside), either may be NULL; head h of token t is at
  *                x + t * x_token + h * x_head (elements, multiples of 8), D values side by side;
- *                out likewise.  out may be x with x's strides, and may not overlap it otherwise
+ *                out likewise, no two of its rows overlapping (checked).  out may be x with x's
+ *                strides, and may not overlap it otherwise (not checked)
  *   H            1 .. 1024;  norm_w [D] fp32, 16-byte aligned, or NULL (ones)
  *   D            a multiple of 8, 8 .. 512
  *   pos          [T] int64 (of any sign);  inv_freq [rope_dims / 2] fp32; neither is read with

@@ -233,3 +233,33 @@ def test_the_search_for_a_sequence_does_not_read_around_the_dependency_wait():
     with open(src) as f:
         body = f.read().split("warp_find_seq(")[1].split("\n}")[0]
     assert "cu[probe]" in body and "__ldg" not in body
+
+
+# ---- outputs whose rows overlap: D = 64 ------------------------------------------------------
+
+def overlaps(T, H, token, head, D=64):
+    """By the definition: two rows, of D elements each, that share one."""
+    at = sorted(t * token + h * head for t in range(T) for h in range(H))
+    return any(b - a < D for a, b in zip(at, at[1:]))
+
+
+STRIDES = [0, 8, 56, 64, 72, 96, 128, 136, 192, 256, 320, 328, 384, 448, 512, 640, 1024, 1 << 40]
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 7, 20])
+@pytest.mark.parametrize("H", [1, 2, 3, 6])
+def test_overlapping_outputs_are_refused(T, H):
+    """The odd pointer comes after the overlap in the order of the checks: nothing is ever launched here."""
+    for token in STRIDES:
+        for head in STRIDES:
+            h = heads(H=H, x_token=64 * H, x_head=64, out_token=token, out_head=head, norm_w=4100)
+            st, msg = norm_rope(q=h, T=T, D=64, r0=0, R=64)
+            assert st == 1 and (b"overlap" in msg) == overlaps(T, H, token, head), (token, head, msg)
+
+
+@pytest.mark.parametrize("token,head,bad", [
+    (512, 512, True), (512, 520, True), (32768, 512, False), (512, 1 << 62, False), (1 << 62, 512, False),
+    ((1 << 62) + 8, (1 << 62), True), (1 << 62, 1 << 62, True)])
+def test_overlaps_of_the_widest_strides(token, head, bad):
+    st, msg = norm_rope(q=heads(out_token=token, out_head=head, norm_w=4100), T=1 << 20)
+    assert st == 1 and (b"overlap" in msg) == bad
