@@ -602,14 +602,17 @@ def _heads(name, x, out, norm, norm_w, T, D, dev):
 def csa2_qk_norm_rope(q, q_out, pos, inv_freq, k=None, k_out=None, q_norm=True, k_norm=True,
                       q_norm_w=None, k_norm_w=None, eps=1e-6, rope_dim0=None, layout=ROPE_PAIRS,
                       factor=1.0, stream=None):
-    """RMSNorm of each head of q [T, H, D] and k [T, K, D] (k: optional), then the rotation of their
-    positions pos [T] by inv_freq [n] in 2 n dims from rope_dim0 on (None: the last ones); inv_freq
-    None is the norm alone.  Outputs may be the inputs, and the step's calls may take them directly."""
-    shape = q.shape
+    """RMSNorm of each head of q [T, H, D] and k [T, K, D] (one of them may be None), then the rotation
+    of their positions pos [T] by inv_freq [n] in 2 n dims from rope_dim0 on (None: the last ones);
+    inv_freq None is the norm alone.  Outputs may be the inputs, and the step's calls may take them directly."""
+    x = k if q is None else q
+    if x is None:
+        raise ValueError("csa2: q or k is required")
+    shape = x.shape
     if len(shape) != 3:
-        raise ValueError("csa2: q must be [T, H, D]")
+        raise ValueError(f"csa2: {'k' if q is None else 'q'} must be [T, H, D]")
     T, _, D = shape
-    dev = q.get_device()
+    dev = x.get_device()
     if dev < 0:
         raise ValueError("csa2: tensors must live on the GPU")
     n = 0 if inv_freq is None else inv_freq.shape[0]

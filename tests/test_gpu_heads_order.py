@@ -103,3 +103,29 @@ def test_queries_of_the_indexer(Q):
     for _ in range(5):
         got = chain(False)
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_keys_alone_are_as_with_queries(layout):
+    import csa2_compressed_sparse_gb300 as csa2
+    x = inputs(50, 7, 192, 1, 3)[0]
+    pos = torch.arange(50, device="cuda") * 1001
+    f = torch.tensor(160000.0 ** (-np.arange(32) / 32), dtype=torch.float32, device="cuda")
+    w = torch.linspace(0.5, 2, 192, device="cuda")
+    q, k, alone = torch.empty_like(x[:, :4]), torch.empty_like(x[:, 4:]), torch.empty_like(x[:, 4:])
+    csa2.csa2_qk_norm_rope(x[:, :4], q, pos, f, k=x[:, 4:], k_out=k, k_norm_w=w, layout=layout)
+    csa2.csa2_qk_norm_rope(None, None, pos, f, k=x[:, 4:], k_out=alone, k_norm_w=w, layout=layout)
+    assert torch.equal(k, alone)
+
+
+def test_rows_beyond_4_gib_are_normed_and_turned():
+    import csa2_compressed_sparse_gb300 as csa2
+    from test_gpu_heads import check, freq
+    T, H, D = 4200, 1024, 512  # 4.4 GB
+    x = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn((3, H, D), device="cuda").bfloat16()
+    last = x[-3:].clone()
+    pos, f = torch.arange(T, device="cuda"), freq(32)
+    csa2.csa2_qk_norm_rope(x, x, pos, f)
+    check(x[-3:], last, None, True, 1e-6, pos[-3:], f, D - 64, 0, 1.0)
+    assert bool((x[:-3] == 0).all())

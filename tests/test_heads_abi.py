@@ -263,3 +263,21 @@ def test_overlapping_outputs_are_refused(T, H):
 def test_overlaps_of_the_widest_strides(token, head, bad):
     st, msg = norm_rope(q=heads(out_token=token, out_head=head, norm_w=4100), T=1 << 20)
     assert st == 1 and (b"overlap" in msg) == bad
+
+
+# ---- keys alone, through the binding ---------------------------------------------------------
+
+def test_the_binding_takes_keys_alone(monkeypatch):
+    seen = []
+    monkeypatch.setattr(csa2, "_call", lambda fn, dev, stream, q, k, *args: seen.append((dev, q, k._obj.H, *args)))
+    a = dict(pos=On.of(1, 3, dtype=torch.int64), inv_freq=On.of(1, 16, dtype=torch.float32),
+             k=On.of(1, 3, 2, 128, dtype=torch.bfloat16), k_out=On.of(1, 3, 2, 128, dtype=torch.bfloat16))
+    csa2.csa2_qk_norm_rope(None, None, **a)
+    assert seen[0][:5] == (1, None, 2, 3, 128)
+    for kw, word in ((dict(k=None, k_out=None), "q or k"), (dict(q_out=a["k"]), "q is missing"),
+                     (dict(q_norm_w=On.of(1, 128, dtype=torch.float32)), "q is missing"), (dict(k_out=None), "k and k_out"),
+                     (dict(k=On.of(1, 3, 128, dtype=torch.bfloat16)), "k must be"),
+                     (dict(k_out=On.of(0, 3, 2, 128, dtype=torch.bfloat16)), "cuda:1")):
+        with pytest.raises(ValueError, match=word):
+            csa2.csa2_qk_norm_rope(None, **{"q_out": None, **a, **kw})
+    assert len(seen) == 1
