@@ -562,7 +562,8 @@ def csa2_paged_chunk_attn(q, cu_seqlens, start_pos, cache: Paged, out, ws=None, 
                           scale=512 ** -0.5, inv_freq=None, stream=None):
     """Attention of chunks q [T, H, 512], tokens cu_seqlens[b].. of sequence b from position
     start_pos[b] on, over the paged rows each token sees; max_rows bounds a sequence's rows and
-    total_rows those of all sequences together (None: what the page table can hold)."""
+    total_rows those of all sequences together (None: what the page table can hold).  FP8 rows, and
+    rows of small pages, take 1 or 2 KiB of workspace for each of total_rows: give a bound for them."""
     dev, B = cache._dev, cache._c.B
     if q.dim() != 3:
         raise ValueError("csa2: q must be [T, H, 512]")

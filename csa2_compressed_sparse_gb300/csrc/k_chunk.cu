@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kReadWarps * 32, read_ctas(kMode)) paged_read_
 //
 // A key tile takes 4096 cycles of products (an MMA of 128 x 256 x 16 by a pair 64, probed; with N = 128 it takes
 // 52) and about 5400 in all: reads of Q, P, K and V by the products and writes of the slots and P share an SM's
-// shared memory.  2048 tokens of 64 heads over 32768 rows take 5.1 to 5.4 ms, 1.6 to 1.7 PFLOP/s of 1.9
+// shared memory.  2048 tokens of 64 heads over 32768 rows take 5.0 to 5.5 ms, 1.57 to 1.7 PFLOP/s of 1.9
 // (1.70 is what a library's product of matrices sustains at the power limit).  The loops over slots are
 // rolled: unrolled, this took 6.0 ms, for the code of four kinds of warp then left the instruction cache.
 //
@@ -349,7 +349,7 @@ __device__ __forceinline__ bool token_rows(const ChunkArgs& a, int64_t p, int64_
 // cut evenly: pair c begins at cost W c / C, C as many pairs as leave each kShare key tiles or a tile.  A cut
 // within the first kTileCost of a tile is one before it.  Up to kPlanFew tiles and sequences are planned by as
 // many threads, whose barriers are shorter (with the fewer CTAs of the join: 35 sequences of two tokens 40.1 ->
-// 36.5 us, 45 of eight 44.7 -> 40.4).
+// 36.5 us, 45 of eight 44.7 -> 40.4).  kMaxPairs: a pair for each two of the GPU's 152 SMs.
 constexpr int kPlanThreads = 1024, kPlanFew = 256, kMaxPairs = 76;
 constexpr int kWhole = 6, kShare = 4, kTileCost = 3;
 
@@ -978,8 +978,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         r2 = add2(r2, rs);
         if (masked) poison = *reinterpret_cast<volatile int*>(&X.odd[c & 1]) != 0;
       }
-      // ---- the end of the segment before: O is read before the next products may start, and stored
-      // while they run ----
+      // ---- the end of the segment before: O is read and stored before the next values' products may
+      // start (those of scores run on) ----
       const ChunkSegment& e = X.seg[(seg - (have ? 2 : 1)) & 3];
       // (what it needs of the record is read before the products start: the loader may then write it over)
       const bool end = first && c > 0, store = end && e.whole;

@@ -13,7 +13,8 @@
 // bytes in flight, a row and the next two of each of 24 warps an SM), 64 tokens the launch and a chain of latencies (7 us).
 //
 // The attention of the sparse step reads its queries and window rows before its dependency wait, and this
-// kernel is what writes them: it lets no dependent start before its CTAs have ended.
+// kernel is what writes them: it lets no dependent start before its CTAs have ended (of calls in a row, 1001 tokens
+// of 65 heads of 128 take 14.7 us in place of 14.1, 4096 of 512 98.7 in place of 98.1).
 #include "common.cuh"
 #include "compress_dev.cuh"
 

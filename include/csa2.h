@@ -25,7 +25,7 @@
  *     in csa2_compress_index_topk) read some inputs before the kernel in front of them has
  *     finished: queries, sequence ids, positions and row bases, window rows, new tokens
  *     with cu_seqlens, and inv_freq.  They must not be written by a kernel that itself lets
- *     its dependents start early and that no other launch separates from the call.  That
+ *     its dependents start early, unless something named below lies between.  That
  *     is any kernel of this library (an attention output taken as queries, a window filled
  *     by csa2_paged_append or csa2_paged_read) except csa2_qk_norm_rope's, whose outputs the
  *     step may take directly, and any other that triggers programmatic launches.  Between the
@@ -637,12 +637,14 @@ csa2_status csa2_paged_read(csa2_bf16* out, int64_t out_ld, int T, const int32_t
  *                CSA2_EBOUNDS and is clipped
  *   total_rows   bound on the rows seen by all sequences together (each sequence's from its first
  *                token's lo to its last token's hi), 0 .. 2^30.  FP8 rows, and rows of pages that
- *                are no multiple of 32, may be copied to the workspace first: more raise
- *                CSA2_EBOUNDS and are left out then
+ *                are no multiple of 32, may be copied to the workspace first, where they take 1024
+ *                bytes each (FP8_S128: 2048) and groups of eight rows begin anew with each sequence.
+ *                Rows there is no room for raise CSA2_EBOUNDS and are left out; up to 16 rows a
+ *                sequence with tokens and 256 more than announced can find room, which is no error
  *   ratio, window, sink, scale, lse, inv_freq   as csa2_paged_attn
  *   ws           workspace of csa2_paged_chunk_attn_workspace_size(T, H, cache, max_rows,
- *                total_rows) bytes, 256-byte aligned; contents are scratch.  Calls that can overlap
- *                need one each. */
+ *                total_rows) bytes, 256-byte aligned; contents are scratch, of any value.  Calls
+ *                that can overlap need one each.  For copied rows its size follows total_rows. */
 size_t csa2_paged_chunk_attn_workspace_size(int T, int H, const csa2_paged* cache, int64_t max_rows,
                                             int64_t total_rows);
 csa2_status csa2_paged_chunk_attn(const csa2_bf16* q, int T, int H, const int32_t* cu_seqlens,
